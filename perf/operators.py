@@ -1,0 +1,437 @@
+"""Operators of token serving over a 4-bit paged cache: their cases, plain forms and calls.
+
+Three operators, used one after the other at every serving step:
+
+  tables   block tables, slot maps and positions of the step's new tokens, from the requests'
+           lengths before and after it; pages are taken from and returned to a pool
+  append   the step's K and V rows, rounded to 4 bits (E2M1 with one E4M3 scale per 16 channels)
+           and stored at their slots of the paged cache
+  attend   each new token's query heads over the cached keys up to its own position: all of them,
+           or those of the blocks it selected
+
+The cache is uint8 [pages, H, P / 16, 18 D]: a page holds P tokens, cut into strips of 16 tokens
+per KV head.  A strip is
+  K codes   [16 tokens][D / 2]            byte c / 2 of a token: channel c, low nibble when c is even
+  V codes   [D / 16 groups][16 tokens][8] byte c / 2 of a token in group g: channel 16 g + c
+  K scales  [16 tokens][D / 16]           E4M3
+  V scales  [D / 16][16 tokens]           E4M3
+and an element's value is code * scale * (its head's float32 scale).
+"""
+
+import math
+
+import torch
+
+own = False
+
+STEPS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)  # magnitudes of E2M1, by code
+
+
+# ---------------------------------------------------------------- cases
+
+def _tables(name, R, lo, hi, P, cap, mixed):
+    return {"name": name, "op": "tables", "R": R, "lo": lo, "hi": hi, "P": P, "max_tokens": cap, "mixed": mixed}
+
+
+def _append(name, T, H, D, P, dtype, pages):
+    return {"name": name, "op": "append", "T": T, "H": H, "D": D, "P": P, "dtype": dtype, "pages": pages}
+
+
+def _attend(name, R, n, lo, hi, HQ, H, D, S, BS, P, dtype):
+    return {"name": name, "op": "attend", "R": R, "n": n, "lo": lo, "hi": hi, "HQ": HQ, "H": H, "D": D, "S": S,
+            "BS": BS, "P": P, "dtype": dtype}
+
+
+def listed():
+    return [
+        # one decode step of a running batch: every request one token longer
+        _tables("tables decode 64", 64, 1, 32768, 64, 64, False),
+        # a step that mixes decodes, prefill chunks, rollbacks and finished requests
+        _tables("tables mixed 1024", 1024, 16, 8192, 64, 786432, True),
+        # the new rows of one decode step
+        _append("append decode 64", 64, 4, 128, 64, "bf16", 512),
+        # the rows of a long prompt (the MSA prefill's length)
+        _append("append prefill 32768", 32768, 4, 128, 64, "bf16", 640),
+        # float32 rows at a small head size, an odd count, small pages
+        _append("append f32 odd", 1021, 3, 64, 16, "f32", 96),
+        # one request, one token, the NSA selection: latency
+        _attend("selected NSA 1", 1, 1, 8192, 8192, 64, 4, 128, 16, 64, 64, "bf16"),
+        # a decode batch with the MSA selection at its prefill length
+        _attend("selected MSA 256", 256, 1, 24576, 32768, 64, 4, 128, 16, 128, 64, "bf16"),
+        # a few tokens of each request at once (drafted tokens), ragged lengths, small heads in float32
+        _attend("selected f32 drafts", 11, 3, 5, 4099, 12, 3, 64, 9, 32, 16, "f32"),
+        # a chunk of a prompt behind its cached prefix
+        _attend("selected chunk 2048", 4, 512, 4096, 16384, 64, 4, 128, 16, 64, 64, "bf16"),
+        # short full attention, few heads: latency
+        _attend("full short 8", 8, 1, 1, 600, 8, 2, 128, 0, 0, 32, "bf16"),
+        # one long context, every key
+        _attend("full long 1", 1, 1, 131072, 131072, 64, 4, 128, 0, 0, 64, "bf16"),
+        # a ragged decode batch, every key
+        _attend("full ragged 48", 48, 1, 64, 32768, 64, 8, 128, 0, 0, 128, "bf16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("tables", "append", "attend", "attend"))
+    P = rng.choice((16, 32, 64, 128))
+    if op == "tables":
+        R, hi, mixed = _log(rng, 1, 1024), _log(rng, 64, 8192), rng.random() < 0.5
+        lo = rng.randint(1, hi)
+        case = _tables("", R, lo, hi, P, 0, mixed)
+        total = sum(max(0, b - a) for a, b in _lengths(case))
+        case["max_tokens"] = total + rng.randint(0, 64)
+    elif op == "append":
+        T = _log(rng, 1, 32768)
+        H, D = rng.randint(1, 8), rng.choice((64, 128))
+        T = max(1, min(T, 32768 * 512 // (H * D)))
+        case = _append("", T, H, D, P, rng.choice(("bf16", "bf16", "f32")), T // P + 1 + rng.randint(1, 64))
+    else:
+        H, G, D = rng.randint(1, 8), rng.choice((1, 2, 3, 4, 6, 8, 16)), rng.choice((64, 128, 128))
+        R, n, hi = _log(rng, 1, 128), rng.choice((1, 1, 1, 2, 4, 7)), _log(rng, 16, 32768)
+        S, BS = rng.choice(((0, 0), (rng.randint(1, 24), rng.choice((16, 32, 64, 128)))))
+        R = max(1, min(R, (1 << 22) // (hi * H * n)))
+        lo = rng.randint(min(n, hi), hi)
+        case = _attend("", R, min(n, lo), lo, hi, H * G, H, D, S, BS, P, rng.choice(("bf16", "bf16", "bf16", "f32")))
+    del case["name"]
+    return case
+
+
+# ---------------------------------------------------------------- inputs
+
+def _ramp(R, lo, hi):
+    return [lo + (hi - lo) * i // max(1, R - 1) for i in range(R)]
+
+
+def _lengths(c):
+    """(before, after) of every request, in an order that the seed changes."""
+    got = []
+    for i, n in enumerate(_ramp(c["R"], c["lo"], c["hi"])):
+        kind = i % 8 if c["mixed"] else 7
+        got.append((n, 0) if kind == 0 else (0, n) if kind == 1 else (n, n - min(3, n)) if kind == 2
+                   else (n // 2, n) if kind == 3 else (n - 1, n))
+    return got
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _dtype(c):
+    return torch.float32 if c["dtype"] == "f32" else torch.bfloat16
+
+
+def _ints(v, dtype=torch.int32):
+    return torch.tensor(v, dtype=dtype, device="cuda")
+
+
+def _page_rows(lens, P, max_pages, ids):
+    """Block tables [R, max_pages] whose rows hold ceil(len / P) of the ids in turn, -1 behind them."""
+    pages = (lens.long() + P - 1) // P
+    first = torch.cumsum(pages, 0) - pages
+    col = torch.arange(max_pages, device="cuda")
+    at = (first[:, None] + col).clamp(max=ids.numel() - 1)
+    return torch.where(col < pages[:, None], ids[at], -1).int().contiguous()
+
+
+def _prepare_tables(c, seed):
+    g = _gen(seed)
+    pairs, P = _lengths(c), c["P"]
+    order = torch.randperm(c["R"], generator=g, device="cuda")
+    old, new = (_ints([p[k] for p in pairs])[order].contiguous() for k in (0, 1))
+    held, wanted = (sum(-(-p[k] // P) for p in pairs) for k in (0, 1))
+    n_pages = held + wanted + 8
+    max_pages = -(-c["hi"] // P)
+    ids = torch.randperm(n_pages, generator=g, device="cuda").int()
+    pool = torch.full((n_pages,), -1, dtype=torch.int32, device="cuda")
+    pool[:n_pages - held] = ids[held:]
+    R, cap = c["R"], c["max_tokens"]
+    s = dict(old=old, new=new, P=P, table=_page_rows(old, P, max_pages, ids), pool=pool, count=_ints([n_pages - held]),
+             count_out=_ints([0]), start=torch.zeros(R + 1, dtype=torch.int32, device="cuda"),
+             req=torch.zeros(cap, dtype=torch.int32, device="cuda"), pos=torch.zeros(cap, dtype=torch.int32, device="cuda"),
+             slots=torch.zeros(cap, dtype=torch.int64, device="cuda"))
+    return s
+
+
+def _prepare_append(c, seed):
+    g = _gen(seed)
+    T, H, D, P = c["T"], c["H"], c["D"], c["P"]
+    rows = torch.randn((T, 2 * H, D), generator=g, device="cuda")
+    rows[:, :H] *= 1 + 3 * torch.rand((1, 1, D), generator=g, device="cuda").pow(4)  # K: a few strong channels
+    rows[:, H:] *= 0.25
+    rows = rows.to(_dtype(c))  # K and V of a token side by side, as one projection gives them
+    pages = torch.randperm(c["pages"], generator=g, device="cuda")[: -(-(T + 5) // P)]
+    pos = torch.arange(T, device="cuda") + 5  # the first page is partly filled already
+    slots = pages[pos // P] * P + pos % P
+    kv = torch.rand((2, H), generator=g, device="cuda") * 0.2 + 0.05
+    cache = torch.zeros((c["pages"], H, P // 16, 18 * D), dtype=torch.uint8, device="cuda")
+    return dict(k=rows[:, :H], v=rows[:, H:], slots=slots.contiguous(), cache=cache, P=P, k_scale=kv[0].contiguous(),
+                v_scale=(kv[1] * 0.1).contiguous(), k_val=torch.zeros((T, H, D), dtype=rows.dtype, device="cuda"),
+                v_val=torch.zeros((T, H, D), dtype=rows.dtype, device="cuda"))
+
+
+def _bank(n, D, scale, g):
+    """n strips of N(0, 1) keys and values as the cache holds them."""
+    x = torch.randn((2, n, 16, D), generator=g, device="cuda")
+    codes, scales = _quantise(x, torch.full((1,), scale, device="cuda"))
+    k, v = _pack(codes)
+    v = v.view(n, 16, D // 16, 8).transpose(1, 2)
+    sk, sv = scales.view(torch.uint8)
+    return torch.cat([k.reshape(n, -1), v.reshape(n, -1), sk.reshape(n, -1), sv.transpose(1, 2).reshape(n, -1)], 1)
+
+
+def _prepare_attend(c, seed):
+    g = _gen(seed)
+    R, n, HQ, H, D, P = (c[x] for x in ("R", "n", "HQ", "H", "D", "P"))
+    T = R * n
+    lens = _ints(_ramp(R, c["lo"], c["hi"]))[torch.randperm(R, generator=g, device="cuda")].contiguous()
+    held, max_pages = sum(-(-x // P) for x in _ramp(R, c["lo"], c["hi"])), -(-c["hi"] // P)
+    ids = torch.randperm(held + 3, generator=g, device="cuda").int()
+    strips = _bank(2048, D, 0.125, g)
+    which = torch.randint(0, 2048, ((held + 3) * H * (P // 16),), generator=g, device="cuda")
+    s = dict(cache=strips[which].view(held + 3, H, P // 16, 18 * D), P=P, table=_page_rows(lens, P, max_pages, ids),
+             q=(2 * torch.randn((T, HQ, D), generator=g, device="cuda")).to(_dtype(c)), D=D, H=H, BS=c["BS"])
+    s["k_scale"] = s["v_scale"] = torch.full((H,), 0.125, device="cuda")
+    s["req"] = torch.arange(R, device="cuda").repeat_interleave(n).int()
+    s["pos"] = (lens.repeat_interleave(n) - n + torch.arange(n, device="cuda").repeat(R)).int()
+    s["blocks"] = s["counts"] = None
+    if c["S"]:  # a token's own block, and others before it drawn without replacement
+        BS, S = c["BS"], c["S"]
+        mine = (s["pos"] // BS).long()[:, None, None]
+        nblk = -(-c["hi"] // BS)
+        key = torch.rand((T, H, max(nblk, S)), generator=g, device="cuda")
+        at = torch.arange(key.shape[2], device="cuda")
+        key = torch.where(at < mine, key, -1.0).masked_fill(at == mine, 2.0)
+        got = key.topk(S, dim=2)
+        at = torch.where(got.values >= 0, got.indices, 1 << 30).sort(dim=2).values
+        s["counts"] = (got.values >= 0).sum(2).int().contiguous()
+        s["blocks"] = torch.where(at < 1 << 30, at, -1).int().contiguous()
+    return s
+
+
+def prepare(case, seed):
+    return {"tables": _prepare_tables, "append": _prepare_append, "attend": _prepare_attend}[case["op"]](case, seed)
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _quantise(x, head_scale):
+    """E2M1 codes [..., D] uint8 and E4M3 scales [..., D / 16] of x / head_scale.  A group's scale is its largest
+    magnitude / 6 rounded to E4M3; the codes are the nearest magnitudes of x / scale, ties to the even code."""
+    y = (x.float() * (1.0 / head_scale)).unflatten(-1, (-1, 16))
+    scale = (y.abs().amax(-1) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    s = scale.float().unsqueeze(-1)
+    a = torch.where(s > 0, y.abs() / s, 0.0).clamp(max=6.0)
+    code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int()
+            + (a >= 3.5).int() + (a > 5.0).int())
+    code = torch.where(y.signbit(), code + 8, code)
+    return code.to(torch.uint8).flatten(-2), scale
+
+
+def _pack(codes):
+    return codes[..., 0::2] | (codes[..., 1::2] << 4)
+
+
+def _value(codes):
+    return torch.tensor(STEPS + tuple(-x for x in STEPS), device="cuda")[codes.int()]
+
+
+def _unpack(b):
+    return torch.stack([_value(b & 15), _value(b >> 4)], -1).flatten(-2)
+
+
+def _plain_tables(s):
+    old, new, P, table = s["old"].long(), s["new"].long(), s["P"], s["table"]
+    before, after = (old + P - 1) // P, (new + P - 1) // P
+    col = torch.arange(table.shape[1], device="cuda")
+    count = s["count"].long()
+    give, take = (before - after).clamp(min=0), (after - before).clamp(min=0)
+    given, taken = give.sum(), take.sum()
+    at = given - 1 - (torch.cumsum(give, 0) - give)[:, None] - (col - after[:, None])  # the last page goes back first
+    back = (col >= after[:, None]) & (col < before[:, None])
+    stack = torch.cat([s["pool"], torch.zeros(table.numel() + 1, dtype=torch.int32, device="cuda")])
+    stack[torch.where(back, count + at, stack.numel() - 1)] = torch.where(back, table, 0)
+    at = count + given - 1 - (torch.cumsum(take, 0) - take)[:, None] - (col - before[:, None])
+    fresh = (col >= before[:, None]) & (col < after[:, None])
+    table = s["table"] = torch.where(fresh, stack[torch.where(fresh, at, 0)], table)
+    left = count + given - taken
+    i = torch.arange(s["pool"].numel(), device="cuda")
+    s["pool"] = torch.where((i >= count) & (i < left), stack[: s["pool"].numel()], s["pool"])
+    grown = (new - old).clamp(min=0)
+    start = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), torch.cumsum(grown, 0)])
+    i = torch.arange(s["slots"].numel(), device="cuda")
+    req = torch.searchsorted(start[1:], i, right=True)
+    live = i < start[-1]
+    req = torch.where(live, req, 0)
+    pos = old[req] + i - start[req]
+    slots = torch.where(live, table[req, torch.where(live, pos // P, 0)].long() * P + pos % P, -1)
+    return {"table": table, "pool": s["pool"], "count": left.int(), "start": start.int(),
+            "req": torch.where(live, req, -1).int(), "pos": torch.where(live, pos, -1).int(), "slots": slots}
+
+
+def _plain_append(s):
+    P, cache, slots = s["P"], s["cache"], s["slots"]
+    D = cache.shape[3] // 18
+    page, strip, t = slots // P, slots % P // 16, slots % 16
+    out = {}
+    for name, base in (("k", 0), ("v", 8 * D)):
+        codes, scales = _quantise(s[name], s[name + "_scale"][:, None])
+        codes_at, scales_at = cache[..., base:base + 8 * D], cache[..., 16 * D + base // 8:][..., :D]
+        groups = (D // 16, 16) if name == "v" else (16, D // 16)
+        codes_at, scales_at = codes_at.unflatten(3, groups + (8,)), scales_at.unflatten(3, groups)
+        if name == "v":
+            codes_at, scales_at = codes_at.transpose(3, 4), scales_at.transpose(3, 4)
+        codes_at[page, :, strip, t] = _pack(codes).unflatten(2, (-1, 8))
+        scales_at[page, :, strip, t] = scales.view(torch.uint8)
+        val = (_value(codes).unflatten(2, (-1, 16)) * scales.float()[..., None]).flatten(2)
+        out[name] = (val * s[name + "_scale"][:, None]).to(s[name].dtype)
+    return out
+
+
+def _plain_attend(s):
+    q, cache, P, H, D, BS = s["q"].float(), s["cache"], s["P"], s["H"], s["D"], s["BS"]
+    T, HQ = q.shape[:2]
+    req, pos = s["req"].long(), s["pos"].long()
+    if s["blocks"] is None:
+        first = torch.arange(0, s["table"].shape[1] * P, 16, device="cuda").expand(T, H, -1)
+        use = first <= pos[:, None, None]
+    else:
+        used = torch.arange(s["blocks"].shape[2], device="cuda") < s["counts"][:, :, None]
+        first = (s["blocks"].long()[..., None] * BS + torch.arange(0, BS, 16, device="cuda")).flatten(2)
+        use = used.repeat_interleave(BS // 16, dim=2) & (first <= pos[:, None, None])
+    first = torch.where(use, first, 0)
+    page = s["table"][req[:, None, None], first // P].long()
+    strip = cache[page, torch.arange(H, device="cuda")[:, None], first % P // 16]  # [T, H, n, 18 D]
+    kc, vc, ks, vs = strip.split([8 * D, 8 * D, D, D], dim=3)
+    k = _unpack(kc.unflatten(3, (16, D // 2))).unflatten(4, (-1, 16))
+    k = (k * ks.view(torch.float8_e4m3fn).float().unflatten(3, (16, D // 16))[..., None]).flatten(4)
+    v = _unpack(vc.unflatten(3, (D // 16, 16, 8)))
+    v = (v * vs.view(torch.float8_e4m3fn).float().unflatten(3, (D // 16, 16))[..., None]).transpose(3, 4).flatten(4)
+    k = k.flatten(2, 3) * s["k_scale"][:, None, None]
+    v = v.flatten(2, 3) * s["v_scale"][:, None, None]
+    seen = use.repeat_interleave(16, dim=2) & ((first[..., None] + torch.arange(16, device="cuda")).flatten(2)
+                                               <= pos[:, None, None])
+    x = torch.matmul(q.view(T, H, HQ // H, D), k.transpose(2, 3)) * D ** -0.5
+    x = x.masked_fill(~seen[:, :, None], -math.inf)
+    top = x.amax(-1, keepdim=True).clamp(min=torch.finfo(torch.float32).min)
+    p = (x - top).exp()
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p, v) / total.clamp(min=torch.finfo(torch.float32).tiny)
+    lse = (top + total.log()).squeeze(-1)
+    return {"out": o.view(T, HQ, D).to(s["q"].dtype), "lse": lse.view(T, HQ)}
+
+
+# ---------------------------------------------------------------- calls
+
+def run(state):
+    s = state
+    if own:
+        from block_sparse_attention_tile_gb300 import pipeline
+        if "old" in s:
+            pipeline.cache_tables(s["old"], s["new"], s["P"], s["table"], s["pool"], s["count"], s["slots"].numel(),
+                                  out=(s["count_out"], s["start"], s["req"], s["pos"], s["slots"]))
+            return {"table": s["table"], "pool": s["pool"], "count": s["count_out"], "start": s["start"],
+                    "req": s["req"], "pos": s["pos"], "slots": s["slots"]}
+        if "k_val" in s:
+            pipeline.cache_append(s["k"], s["v"], s["slots"], s["cache"], s["k_scale"], s["v_scale"],
+                                  values=(s["k_val"], s["v_val"]))
+            return {"k": s["k_val"], "v": s["v_val"]}
+        out, lse = pipeline.cache_attention(s["q"], s["cache"], s["table"], s["req"], s["pos"], s["k_scale"],
+                                            s["v_scale"], block_indices=s["blocks"], block_counts=s["counts"],
+                                            block_size=s["BS"])
+        return {"out": out, "lse": lse}
+    return (_plain_tables if "old" in s else _plain_append if "k_val" in s else _plain_attend)(s)
+
+
+# ---------------------------------------------------------------- work
+
+def work(case):
+    c = case
+    if c["op"] == "tables":
+        pairs = _lengths(c)
+        moved = sum(abs(-(-a // c["P"]) + b // -c["P"]) for a, b in pairs)
+        return {"bytes": 12 * c["R"] + 8 + 16 * c["max_tokens"] + 8 * moved, "flops": 0}
+    size = 4 if c["dtype"] == "f32" else 2
+    if c["op"] == "append":
+        rows = 2 * c["T"] * c["H"] * c["D"]
+        return {"bytes": rows * (2 * size + 0.5 + 1 / 16) + 8 * c["T"], "flops": 0}
+    H, D, n, S, BS = c["H"], c["D"], c["n"], c["S"], c["BS"]
+    keys = held = 0
+    for length in _ramp(c["R"], c["lo"], c["hi"]):
+        seen = [min(p + 1, (S - 1) * BS + p % BS + 1) if S else p + 1 for p in range(length - n, length)]
+        keys += sum(seen)
+        held += min(sum(seen), length)
+    T = c["R"] * n
+    return {"bytes": held * H * D * 18 / 16 + T * c["HQ"] * (2 * D * size + 4) + 4 * T * H * (S + 1),
+            "flops": 4 * keys * c["HQ"] * D}
+
+
+# ---------------------------------------------------------------- 64 bits
+
+def _nearest(x, grid):
+    """Indices into the ascending grid of the nearest values to x >= 0, ties to the even index, the last for more."""
+    up = torch.bucketize(x, grid).clamp(1, grid.numel() - 1)
+    lo, hi = x - grid[up - 1], grid[up] - x
+    return torch.where((hi < lo) | ((hi == lo) & (up % 2 == 0)), up, up - 1)
+
+
+def _e4m3():
+    return torch.tensor([m * 2.0 ** -9 for m in range(8)]
+                        + [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8)][:-1],
+                        dtype=torch.float64, device="cuda")
+
+
+def _exact_append(s):
+    steps, grid, got = torch.tensor(STEPS, dtype=torch.float64, device="cuda"), _e4m3(), {}
+    for name in ("k", "v"):
+        x, h = s[name].double(), s[name + "_scale"].double()[:, None, None]
+        y = x.unflatten(2, (-1, 16)) / h
+        scale = grid[_nearest(y.abs().amax(3) / 6, grid)][..., None]
+        code = _nearest((y.abs() / scale.clamp(min=1e-300)).clamp(max=6.0), steps)
+        got[name] = (steps[code] * y.sign() * scale * h).flatten(2)
+    return got
+
+
+def _exact_attend(c, s):
+    T, H, D, P, BS, HQ = s["q"].shape[0], s["H"], s["D"], s["P"], s["BS"], c["HQ"]
+    if T * H > 10000:
+        return None
+    sign = torch.tensor([x * m for x in (1, -1) for m in STEPS], dtype=torch.float64, device="cuda")
+    e4m3, G = torch.cat([_e4m3(), _e4m3()[:1] * math.nan, -_e4m3()]), HQ // H
+    out = torch.zeros((T, HQ, D), dtype=torch.float64, device="cuda")
+    lse = torch.full((T, HQ), -math.inf, dtype=torch.float64, device="cuda")
+    pos, req = s["pos"].tolist(), s["req"].tolist()
+    counts = s["counts"].tolist() if c["S"] else None
+    ch = torch.arange(D, device="cuda")
+    for t in range(T):
+        for h in range(H):
+            if c["S"]:
+                keys = (s["blocks"][t, h, :counts[t][h]].long()[:, None] * BS
+                        + torch.arange(BS, device="cuda")).flatten()
+                keys = keys[keys <= pos[t]]
+            else:
+                keys = torch.arange(pos[t] + 1, device="cuda")
+            strip = s["cache"][s["table"][req[t]][keys // P].long(), h, keys % P // 16].long()  # [keys, 18 D]
+            j = (keys % 16)[:, None]
+            kb, vb = strip.gather(1, j * (D // 2) + ch // 2), strip.gather(1, 8 * D + (ch // 16 * 16 + j) * 8 + ch % 16 // 2)
+            ks, vs = strip.gather(1, 16 * D + j * (D // 16) + ch // 16), strip.gather(1, 17 * D + ch // 16 * 16 + j)
+            shift = ch % 2 * 4
+            k = sign[kb >> shift & 15] * e4m3[ks] * s["k_scale"][h].double()
+            v = sign[vb >> shift & 15] * e4m3[vs] * s["v_scale"][h].double()
+            x = s["q"][t, h * G:(h + 1) * G].double() @ k.T / math.sqrt(D)
+            z = torch.logsumexp(x, 1)
+            out[t, h * G:(h + 1) * G] = torch.exp(x - z[:, None]) @ v
+            lse[t, h * G:(h + 1) * G] = z
+    return {"out": out, "lse": lse}
+
+
+def exact(case, seed):
+    if case["op"] == "tables":
+        return None
+    s = prepare(case, seed)
+    return _exact_append(s) if case["op"] == "append" else _exact_attend(case, s)
