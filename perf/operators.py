@@ -221,10 +221,12 @@ def prepare(case, seed):
 # ---------------------------------------------------------------- plain forms
 
 def _quantise(x, head_scale):
-    """E2M1 codes [..., D] uint8 and E4M3 scales [..., D / 16] of x / head_scale.  A group's scale is its largest
-    magnitude / 6 rounded to E4M3; the codes are the nearest magnitudes of x / scale, ties to the even code."""
+    """E2M1 codes [..., D] uint8 and E4M3 scales [..., D / 16] of y = x * (1 / head_scale), a float32 product.  A
+    group's scale is its largest magnitude / 6 rounded to E4M3; the codes are the magnitudes nearest to y / scale,
+    ties to the even code."""
     y = (x.float() * (1.0 / head_scale)).unflatten(-1, (-1, 16))
-    scale = (y.abs().amax(-1) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn)
+    six = torch.full((), 6.0, device="cuda")  # on the device: a division, not a product with a rounded 1 / 6
+    scale = (y.abs().amax(-1) / six).clamp(max=448.0).to(torch.float8_e4m3fn)
     s = scale.float().unsqueeze(-1)
     a = torch.where(s > 0, y.abs() / s, 0.0).clamp(max=6.0)
     code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int()
@@ -390,7 +392,8 @@ def _exact_append(s):
     steps, grid, got = torch.tensor(STEPS, dtype=torch.float64, device="cuda"), _e4m3(), {}
     for name in ("k", "v"):
         x, h = s[name].double(), s[name + "_scale"].double()[:, None, None]
-        y = x.unflatten(2, (-1, 16)) / h
+        # y is a float32 product with a float32 reciprocal by definition; everything after it is exact
+        y = (x.unflatten(2, (-1, 16)) * (1 / h).float().double()).float().double()
         scale = grid[_nearest(y.abs().amax(3) / 6, grid)][..., None]
         code = _nearest((y.abs() / scale.clamp(min=1e-300)).clamp(max=6.0), steps)
         got[name] = (steps[code] * y.sign() * scale * h).flatten(2)
