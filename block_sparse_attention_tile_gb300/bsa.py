@@ -15,11 +15,12 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libbsa.so")
 
-BSA_OK, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_ERR_CUDA, BSA_ERR_INDEX, BSA_ERR_TIMEOUT = range(6)
+BSA_OK, BSA_ERR_INVALID_ARG, BSA_ERR_UNSUPPORTED, BSA_ERR_CUDA, BSA_ERR_INDEX, BSA_ERR_TIMEOUT, \
+    BSA_ERR_CAPACITY = range(7)
 BSA_F32, BSA_BF16 = 0, 1
 
 STATUS_NAMES = {0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_UNSUPPORTED", 3: "BSA_ERR_CUDA",
-                4: "BSA_ERR_INDEX", 5: "BSA_ERR_TIMEOUT"}
+                4: "BSA_ERR_INDEX", 5: "BSA_ERR_TIMEOUT", 6: "BSA_ERR_CAPACITY"}
 
 
 class BsaError(RuntimeError):
@@ -69,6 +70,12 @@ _SIGS = {
     "bsa_permute_rows": (I, [P, P, I, I, I, I, I, P, I, P]),
     "bsa_coarse_attention": (I, [P, I64, P, I64, I, I, I, P, P]),
     "bsa_coarse_apply": (I, [P, I, P, P, I, I, I, I, P, P, I, I, I, P]),
+    "bsa_cache_bytes": (SZ, [I, I, I, I]),
+    "bsa_cache_tables_workspace": (SZ, [I]),
+    "bsa_cache_tables": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, P, I, P, SZ, P]),
+    "bsa_cache_append": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P]),
+    "bsa_cache_attention_workspace": (SZ, [I, I, I, I, I]),
+    "bsa_fwd_cache_tokens": (I, [P, I, I, I, I, I, I64, P, I, I, P, I, I, P, P, P, P, P, P, I, I, F, P, P, P, SZ, P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -302,3 +309,99 @@ def bsa_reblock_layout(q, k, BH, N, D, n_prefix, block, perm, workspace, ridge=1
 def bsa_permute_rows(src, dst, BH, N, D, n_prefix, perm, inverse=False, stream=None):
     _check(_lib.bsa_permute_rows(_ptr(src), _ptr(dst), _dtype(src), BH, N, D, n_prefix, _ptr(perm),
                                  1 if inverse else 0, _stream(stream)))
+
+
+# The cache entry points check what the C side cannot see (types, layouts, sizes
+# behind the pointers, devices) and run on the device of their tensors, whichever
+# is current.
+
+def _device_of(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("a CUDA tensor is needed")
+    return dev
+
+
+def _expect(name, t, dtype, numel, dev):
+    """Data pointer of a contiguous tensor of this type on this device with at least numel elements; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of at least %d elements on cuda:%d is needed, got %s %s on %s"
+                         % (name, dtype, numel, dev, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _rows(name, t, T, heads, D, dtype, dev):
+    """Data pointer and token stride of [T, heads, D] rows whose heads are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (T, heads, D):
+        raise ValueError("%s: a %s tensor [%d, %d, %d] on cuda:%d is needed, got %s %s on %s"
+                         % (name, dtype, T, heads, D, dev, t.dtype, tuple(t.shape), t.device))
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (heads > 1 and st[1] != D):
+        raise ValueError("%s: a token's heads must be contiguous, got strides %s" % (name, st))
+    return t.data_ptr(), st[0] if T > 1 else heads * D
+
+
+def _run_on(dev, stream, fn, args):
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, raw))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, raw))
+
+
+def bsa_cache_bytes(n_pages, H, page_size, D):
+    return _lib.bsa_cache_bytes(n_pages, H, page_size, D)
+
+
+def bsa_cache_tables_workspace(R):
+    return _lib.bsa_cache_tables_workspace(R)
+
+
+def bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, n_pages, pool_count,
+                     pool_count_out, query_start, token_req, token_pos, slots, max_tokens, workspace, stream=None):
+    dev, i32 = _device_of(block_table), torch.int32
+    _run_on(dev, stream, _lib.bsa_cache_tables, (
+        _expect("old_lens", old_lens, i32, R, dev), _expect("new_lens", new_lens, i32, R, dev), R, page_size,
+        _expect("block_table", block_table, i32, R * max_pages, dev), max_pages,
+        _expect("pool", pool, i32, n_pages, dev), n_pages, _expect("pool_count", pool_count, i32, 1, dev),
+        _expect("pool_count_out", pool_count_out, i32, 1, dev), _expect("query_start", query_start, i32, R + 1, dev),
+        _expect("token_req", token_req, i32, max_tokens, dev), _expect("token_pos", token_pos, i32, max_tokens, dev),
+        _expect("slots", slots, torch.int64, max_tokens, dev), max_tokens,
+        _expect("workspace", workspace, workspace.dtype, 0, dev), workspace.numel() * workspace.element_size()))
+
+
+def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=None, v_scale=None, k_val=None,
+                     v_val=None, stream=None):
+    dev, dt = _device_of(cache), k.dtype
+    kp, ks = _rows("k", k, T, H, D, dt, dev)
+    vp, vs = _rows("v", v, T, H, D, dt, dev)
+    _run_on(dev, stream, _lib.bsa_cache_append, (
+        kp, vp, _dtype(k), T, H, D, ks, vs, _expect("slots", slots, torch.int64, T, dev),
+        _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
+        _expect("k_scale", k_scale, torch.float32, H, dev), _expect("v_scale", v_scale, torch.float32, H, dev),
+        _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev)))
+
+
+def bsa_cache_attention_workspace(T, HQ, H, D, max_keys):
+    return _lib.bsa_cache_attention_workspace(T, HQ, H, D, max_keys)
+
+
+def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table, R, max_pages, token_req, token_pos,
+                         k_scale, v_scale, block_indices, block_counts, S, block_size, scale, out, lse=None,
+                         workspace=None, stream=None):
+    dev, dt, i32, f32 = _device_of(cache), q.dtype, torch.int32, torch.float32
+    qp, qs = _rows("q", q, T, HQ, D, dt, dev)
+    _run_on(dev, stream, _lib.bsa_fwd_cache_tokens, (
+        qp, _dtype(q), T, HQ, H, D, qs,
+        _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
+        _expect("block_table", block_table, i32, R * max_pages, dev), R, max_pages,
+        _expect("token_req", token_req, i32, T, dev), _expect("token_pos", token_pos, i32, T, dev),
+        _expect("k_scale", k_scale, f32, H, dev), _expect("v_scale", v_scale, f32, H, dev),
+        _expect("block_indices", block_indices, i32, T * H * S, dev),
+        _expect("block_counts", block_counts, i32, T * H, dev), S, block_size, scale,
+        _expect("out", out, dt, T * HQ * D, dev), _expect("lse", lse, f32, T * HQ, dev),
+        None if workspace is None else _expect("workspace", workspace, workspace.dtype, 0, dev),
+        0 if workspace is None else workspace.numel() * workspace.element_size()))

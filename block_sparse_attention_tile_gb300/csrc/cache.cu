@@ -1,0 +1,416 @@
+// The paged cache's tables (a12) and the write of new rows into it (a13).
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace bsa {
+
+// ---------------------------------------------------------------- a12 tables
+//
+// Exclusive sums over the requests of (new tokens, pages taken, pages given back)
+// place everything: token i of request r goes to row start[r] + i, its k-th new
+// page is page take[r] + k of the call, and so on.  The pool is a stack of free
+// pages: the call's given-back pages are pushed, last request's last page first, and its
+// new pages popped one by one.  Both are only index arithmetic on the "virtual
+// stack" pool[0 .. count) + given-back pages, so every new page is known without
+// waiting for any write of the call, and no two threads touch the same word.
+//
+// Nothing here computes; a small call is bound by the launch and the scan's
+// latency, a large one by the 16 bytes written per token.
+
+struct Tables {
+    const int32_t* old_lens;
+    int32_t* new_lens;
+    int R, P, max_pages, n_pages, max_tokens;
+    int32_t *table, *pool;
+    const int32_t* count;
+    int32_t *count_out, *start, *req, *pos;
+    int64_t* slots;
+    int* status;
+};
+
+// What the second half of the work needs of the scan: in shared memory when one
+// CTA does everything, in the workspace when a grid follows.
+struct Sums {
+    int32_t *start, *take, *give;  // R + 1 each
+    int ok, count, taken, given, total;
+};
+
+constexpr int kScanThreads = 1024;
+constexpr int kOneCtaTokens = 4096;  // up to here one CTA does all: 4 tokens a thread cost less than a second launch
+constexpr int kOneCtaRequests = 1024;
+
+__device__ __forceinline__ int pages_of(int len, int sh) { return (int)(((unsigned)len + (1u << sh) - 1) >> sh); }
+
+// The largest r in [0, R) with sums[r] <= i (sums ascending, sums[R] > i).
+__device__ __forceinline__ int owner(const int32_t* sums, int R, int i) {
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Page at a position of the virtual stack.
+__device__ __forceinline__ int stack_page(const Tables& a, const Sums& s, int sh, int at) {
+    if (at < s.count) return a.pool[at];
+    const int i = s.given - 1 - (at - s.count);
+    const int r = owner(s.give, a.R, i);
+    return a.table[(long long)r * a.max_pages + pages_of(a.new_lens[r], sh) + i - s.give[r]];
+}
+
+// Everything behind the scan, by `stride` threads: token rows, new table entries, pages pushed.
+__device__ void place(const Tables& a, const Sums& s, int sh, int tid, int stride) {
+    for (unsigned i = tid; i < (unsigned)a.max_tokens; i += stride) {
+        int req = -1, pos = -1;
+        int64_t slot = -1;
+        if (s.ok && i < (unsigned)s.total) {
+            req = owner(s.start, a.R, i);
+            const int old = a.old_lens[req], before = pages_of(old, sh);
+            pos = old + i - s.start[req];
+            const int j = pos >> sh;
+            const int page = j < before ? a.table[(long long)req * a.max_pages + j]
+                                        : stack_page(a, s, sh, s.count + s.given - 1 - (s.take[req] + j - before));
+            if ((unsigned)page < (unsigned)a.n_pages) slot = ((int64_t)page << sh) + (pos & (a.P - 1));
+            else raise_status(a.status, BSA_ERR_INDEX);
+        }
+        a.req[i] = req;
+        a.pos[i] = pos;
+        a.slots[i] = slot;
+    }
+    if (!s.ok) return;
+    for (unsigned i = tid; i < (unsigned)s.taken; i += stride) {
+        const int r = owner(s.take, a.R, i);
+        a.table[(long long)r * a.max_pages + pages_of(a.old_lens[r], sh) + i - s.take[r]] =
+            stack_page(a, s, sh, s.count + s.given - 1 - i);
+    }
+    const int pushed = s.given - s.taken;
+    for (int i = tid; i < pushed; i += stride) {  // pushed <= n_pages
+        const int page = stack_page(a, s, sh, s.count + i);
+        if ((unsigned)page >= (unsigned)a.n_pages) raise_status(a.status, BSA_ERR_INDEX);
+        a.pool[s.count + i] = page;
+    }
+}
+
+// One CTA: the three exclusive sums, the checks, the new count; with kAll the rest too.
+template <bool kAll>
+__global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int sh, int32_t* ws) {
+    extern __shared__ int32_t dyn[];
+    __shared__ long long part[3][32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Sums s;
+    s.start = kAll ? dyn : a.start;
+    s.take = kAll ? dyn + (a.R + 1) : ws + 8;
+    s.give = s.take + (a.R + 1);
+    if (tid == 0) bad = 0;
+    s.count = a.count[0];
+    __syncthreads();
+    // token sums in 64 bits: R requests of up to 2^31 tokens; page sums fit 32 (R * max_pages < 2^31)
+    long long run[3] = {0, 0, 0};
+    const long long longest = (long long)a.max_pages << sh;
+    for (int base = 0; base < a.R; base += kScanThreads) {
+        const int r = base + tid;
+        long long x[3] = {0, 0, 0};
+        if (r < a.R) {
+            const int o = a.old_lens[r], n = a.new_lens[r];
+            if (o < 0 || n < 0 || o > longest || n > longest) {
+                bad = 1;
+            } else {
+                const int before = pages_of(o, sh), after = pages_of(n, sh);
+                x[0] = max(0, n - o);
+                x[1] = max(0, after - before);
+                x[2] = max(0, before - after);
+            }
+        }
+        long long inc[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            inc[k] = x[k];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc[k], d);
+                if (lane >= d) inc[k] += y;
+            }
+            if (lane == 31) part[k][warp] = inc[k];
+        }
+        __syncthreads();
+        if (warp < 3) {
+            long long y = part[warp][lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long z = __shfl_up_sync(0xffffffffu, y, d);
+                if (lane >= d) y += z;
+            }
+            part[warp][lane] = y;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const long long before = run[k] + (warp ? part[k][warp - 1] : 0) + inc[k] - x[k];
+            if (r < a.R) (k == 0 ? s.start : k == 1 ? s.take : s.give)[r] = (int32_t)min(before, 0x7fffffffLL);
+            run[k] += part[k][31];
+        }
+        __syncthreads();
+    }
+    s.taken = (int)run[1];
+    s.given = (int)run[2];
+    s.total = (int)min(run[0], 0x7fffffffLL);
+    int code = BSA_OK;
+    if (bad || s.count < 0 || s.count > a.n_pages || (long long)s.count + s.given - s.taken > a.n_pages)
+        code = BSA_ERR_INDEX;
+    else if ((long long)s.count + s.given < s.taken || run[0] > a.max_tokens)
+        code = BSA_ERR_CAPACITY;
+    s.ok = code == BSA_OK;
+    if (tid == 0) {
+        s.start[a.R] = s.total;
+        s.take[a.R] = s.taken;
+        s.give[a.R] = s.given;
+        a.count_out[0] = s.ok ? s.count + s.given - s.taken : s.count;
+        if (!s.ok) raise_status(a.status, code);
+        if (!kAll) {
+            ws[0] = s.ok;
+            ws[1] = s.count;
+            ws[2] = s.taken;
+            ws[3] = s.given;
+            ws[4] = s.total;
+        }
+    }
+    __syncthreads();
+    if (!s.ok)
+        for (int r = tid; r < a.R; r += kScanThreads) a.new_lens[r] = a.old_lens[r];
+    if (kAll) {
+        for (int r = tid; r <= a.R; r += kScanThreads) a.start[r] = s.ok ? s.start[r] : 0;
+        place(a, s, sh, tid, kScanThreads);
+    } else if (!s.ok) {
+        for (int r = tid; r <= a.R; r += kScanThreads) a.start[r] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, int32_t* ws) {
+    Sums s;
+    s.start = a.start;
+    s.take = ws + 8;
+    s.give = s.take + (a.R + 1);
+    s.ok = ws[0];
+    s.count = ws[1];
+    s.taken = ws[2];
+    s.given = ws[3];
+    s.total = ws[4];
+    place(a, s, sh, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+// ---------------------------------------------------------------- a13 append
+//
+// A thread rounds one group of 16 channels of one token and head, for K and for V:
+//   y = x * (1 / head scale),  s = E4M3(max |y| / 6),  code = E2M1(y / s).
+// max / 6 and y / s are IEEE divisions: a quotient that is not a rounding border of
+// the short format is never moved onto one by the float32 rounding, so the codes are those of the
+// exact quotient.  A group that holds a NaN or an infinity is stored with the scale
+// NaN, so that it reads back as NaN instead of as a finite number.
+//
+// Bound by HBM: 2 bytes read and 9/16 written per element.
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void load16(const T* p, float* x) {
+    if constexpr (kVec && sizeof(T) == 2) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+            x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = a.z, x[4 * i + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = to_f32(p[i]);
+    }
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store16(T* p, const float* x) {
+    if constexpr (kVec && sizeof(T) == 2) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = from_f32<T>(x[i]);
+    }
+}
+
+// Codes (8 bytes) and scale byte of a group; x becomes the group's stored values.
+__device__ __forceinline__ uint2 quantise16(float* x, float head_scale, uint32_t* scale) {
+    const float inv = __fdiv_rn(1.f, head_scale);
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        x[i] *= inv;
+        top = fmaxf(top, fabsf(x[i]));
+        finite = finite && fabsf(x[i]) <= 3.402823466e38f;
+    }
+    uint32_t sb = finite ? f32_to_e4m3(__fdiv_rn(top, kE2M1Max)) : 0x7fu;
+    const float s = f16x2_to_f32(e4m3x2_to_f16x2(sb)).x;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // a scale of zero stores zeros (and keeps the signs)
+        const float a = s > 0.f ? __fdiv_rn(x[2 * i], s) : copysignf(0.f, x[2 * i]);
+        const float b = s > 0.f ? __fdiv_rn(x[2 * i + 1], s) : copysignf(0.f, x[2 * i + 1]);
+        const uint32_t two = f32x2_to_e2m1x2(a, b);
+        const float2 v = f16x2_to_f32(e2m1x2_to_f16x2(two));
+        w[i >> 2] |= two << (8 * (i & 3));
+        x[2 * i] = v.x * s * head_scale;  // v.x * s is exact
+        x[2 * i + 1] = v.y * s * head_scale;
+    }
+    *scale = sb;
+    return make_uint2(w[0], w[1]);
+}
+
+template <typename T, bool kVec, bool kValues>
+__global__ void __launch_bounds__(256) cache_append_kernel(
+    const T* __restrict__ k, const T* __restrict__ v, long long k_stride, long long v_stride, long long items, int H,
+    int D, const int64_t* __restrict__ slots, uint8_t* __restrict__ cache, long long n_slots, int sh,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, T* __restrict__ k_val, T* __restrict__ v_val,
+    int* status) {
+    const int ng = D / 16;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < items;
+         i += (long long)gridDim.x * blockDim.x) {
+        const int g = (int)(i % ng);
+        const int h = (int)(i / ng % H);
+        const long long t = i / ng / H;
+        const long long slot = slots[t];
+        if (slot < 0 || slot >= n_slots) {
+            if (slot != -1) raise_status(status, BSA_ERR_INDEX);
+            continue;
+        }
+        float kx[16], vx[16];
+        load16<T, kVec>(k + t * k_stride + h * D + g * 16, kx);
+        load16<T, kVec>(v + t * v_stride + h * D + g * 16, vx);
+        const float ks = k_scale ? k_scale[h] : 1.f, vs = v_scale ? v_scale[h] : 1.f;
+        uint32_t kb, vb;
+        const uint2 kc = quantise16(kx, ks, &kb), vc = quantise16(vx, vs, &vb);
+        const long long page = slot >> sh;
+        const int in = (int)(slot & ((1 << sh) - 1)), j = in & 15;
+        uint8_t* strip = cache + (((page * H + h) << (sh - 4)) + (in >> 4)) * strip_bytes(D);
+        *reinterpret_cast<uint2*>(strip + j * (D / 2) + g * 8) = kc;
+        *reinterpret_cast<uint2*>(strip + 8 * D + (g * 16 + j) * 8) = vc;
+        strip[16 * D + j * ng + g] = (uint8_t)kb;
+        strip[17 * D + g * 16 + j] = (uint8_t)vb;
+        if (kValues) {
+            const long long at = (t * H + h) * D + g * 16;
+            store16<T, kVec>(k_val + at, kx);
+            store16<T, kVec>(v_val + at, vx);
+        }
+    }
+}
+
+template <typename T>
+static bsa_status launch_append(const void* k, const void* v, long long ks, long long vs, int T_, int H, int D,
+                                const int64_t* slots, uint8_t* cache, long long n_slots, int sh, const float* k_scale,
+                                const float* v_scale, void* k_val, void* v_val, cudaStream_t st) {
+    const long long items = (long long)T_ * H * (D / 16);
+    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 1 << 20);
+    const uintptr_t bits = (uintptr_t)k | (uintptr_t)v | (uintptr_t)k_val | (uintptr_t)v_val |
+                           (uintptr_t)(ks * (long long)sizeof(T)) | (uintptr_t)(vs * (long long)sizeof(T));
+    const bool vec = (bits & 15) == 0;
+#define BSA_APPEND(V, W)                                                                                        \
+    cache_append_kernel<T, V, W><<<grid, 256, 0, st>>>((const T*)k, (const T*)v, ks, vs, items, H, D, slots, cache, \
+                                                       n_slots, sh, k_scale, v_scale, (T*)k_val, (T*)v_val,     \
+                                                       status_word())
+    if (vec) {
+        if (k_val) BSA_APPEND(true, true); else BSA_APPEND(true, false);
+    } else {
+        if (k_val) BSA_APPEND(false, true); else BSA_APPEND(false, false);
+    }
+#undef BSA_APPEND
+    return check_launch("cache_append_kernel");
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" {
+
+size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D) {
+    if (n_pages < 1 || H < 1 || !page_size_ok(page_size) || D < 16 || D > 128 || D % 16) return 0;
+    return (size_t)n_pages * H * (page_size / kStrip) * strip_bytes(D);
+}
+
+size_t bsa_cache_tables_workspace(int R) { return R < 1 ? 0 : (8 + 2 * ((size_t)R + 1)) * sizeof(int32_t); }
+
+bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
+                            int32_t* block_table, int max_pages, int32_t* pool, int n_pages,
+                            const int32_t* pool_count, int32_t* pool_count_out, int32_t* query_start,
+                            int32_t* token_req, int32_t* token_pos, int64_t* slots, int max_tokens, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    BSA_REQUIRE(old_lens && new_lens && block_table && pool && pool_count && pool_count_out && query_start,
+                "cache tables: null pointer");
+    BSA_REQUIRE(max_tokens == 0 || (token_req && token_pos && slots), "cache tables: null token arrays");
+    BSA_REQUIRE(R > 0 && R <= (1 << 20) && max_pages > 0 && n_pages > 0 && max_tokens >= 0 && max_tokens <= (1 << 30),
+                "cache tables: sizes out of range (R=%d max_pages=%d n_pages=%d max_tokens=%d)", R, max_pages, n_pages,
+                max_tokens);
+    BSA_REQUIRE(page_size_ok(page_size), "cache tables: page_size must be a power of two in 16..1024, got %d", page_size);
+    BSA_REQUIRE((long long)R * max_pages <= 0x7fffffffLL && (long long)max_pages * page_size <= 0x7fffffffLL,
+                "cache tables: R * max_pages and max_pages * page_size must be below 2^31");
+    BSA_REQUIRE(workspace && workspace_bytes >= bsa_cache_tables_workspace(R) && ((uintptr_t)workspace & 3) == 0,
+                "cache tables: workspace of %zu bytes needed", bsa_cache_tables_workspace(R));
+    cudaStream_t st = as_stream(stream);
+    const int sh = log2i(page_size);
+    Tables a{old_lens, new_lens, R, page_size, max_pages, n_pages, max_tokens, block_table, pool, pool_count,
+             pool_count_out, query_start, token_req, token_pos, slots, status_word()};
+    int32_t* ws = static_cast<int32_t*>(workspace);
+    if (R <= kOneCtaRequests && max_tokens <= kOneCtaTokens) {
+        cache_scan_kernel<true><<<1, kScanThreads, 3 * (R + 1) * sizeof(int32_t), st>>>(a, sh, ws);
+        return check_launch("cache_scan_kernel");
+    }
+    cache_scan_kernel<false><<<1, kScanThreads, 0, st>>>(a, sh, ws);
+    bsa_status rc = check_launch("cache_scan_kernel");
+    if (rc != BSA_OK) return rc;
+    const int work = std::max(max_tokens, R);
+    cache_place_kernel<<<std::min((work + 255) / 256, 152 * 8), 256, 0, st>>>(a, sh, ws);
+    return check_launch("cache_place_kernel");
+}
+
+bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D, int64_t k_stride,
+                            int64_t v_stride, const int64_t* slots, void* cache, int n_pages, int page_size,
+                            const float* k_scale, const float* v_scale, void* k_val, void* v_val, void* stream) {
+    BSA_REQUIRE(k && v && slots && cache, "cache append: null pointer");
+    BSA_REQUIRE((k_val == nullptr) == (v_val == nullptr), "cache append: k_val and v_val come together");
+    BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "cache append: dtype");
+    BSA_REQUIRE(T >= 0 && H > 0 && n_pages > 0, "cache append: sizes out of range (T=%d H=%d n_pages=%d)", T, H, n_pages);
+    BSA_REQUIRE(page_size_ok(page_size), "cache append: page_size must be a power of two in 16..1024, got %d", page_size);
+    BSA_REQUIRE(D >= 16 && D <= 128 && D % 16 == 0, "cache append: D must be a multiple of 16 up to 128, got %d", D);
+    BSA_REQUIRE(H <= (1 << 20) && (T <= 1 || (k_stride >= (int64_t)H * D && v_stride >= (int64_t)H * D)),
+                "cache append: a token's stride is below H * D");
+    BSA_REQUIRE(((uintptr_t)cache & 15) == 0, "cache append: the cache must be 16-byte aligned");
+    if (T == 0) return BSA_OK;
+    const long long n_slots = (long long)n_pages * page_size;
+    const int sh = log2i(page_size);
+    cudaStream_t st = as_stream(stream);
+    return dtype == BSA_F32
+               ? launch_append<float>(k, v, k_stride, v_stride, T, H, D, slots, (uint8_t*)cache, n_slots, sh, k_scale,
+                                      v_scale, k_val, v_val, st)
+               : launch_append<__nv_bfloat16>(k, v, k_stride, v_stride, T, H, D, slots, (uint8_t*)cache, n_slots, sh,
+                                              k_scale, v_scale, k_val, v_val, st);
+}
+
+}  // extern "C"

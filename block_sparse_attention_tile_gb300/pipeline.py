@@ -7,7 +7,7 @@ in Python.
 """
 
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -320,3 +320,120 @@ def effective_flops(hq, n, d, k, bk, batch=1):
 def ceil_div(a, b):
     return -(-a // b)
 
+
+
+# ---------------------------------------------------------------- token serving over the paged 4-bit cache
+
+class CacheStep(NamedTuple):
+    """What one serving step's tables hold: the pool's new count, each request's
+    first new token [R + 1], and each new token's request, position and slot
+    [max_tokens] (-1 behind the last)."""
+    pool_count: torch.Tensor
+    query_start: torch.Tensor
+    token_req: torch.Tensor
+    token_pos: torch.Tensor
+    slots: torch.Tensor
+
+
+def new_cache(n_pages, H, page_size, D, device="cuda"):
+    """An empty paged 4-bit cache, uint8 [n_pages, H, page_size / 16, 18 D]."""
+    if not bsa.bsa_cache_bytes(n_pages, H, page_size, D):
+        raise ValueError("no cache of %d pages of %d tokens, %d heads of %d channels" % (n_pages, page_size, H, D))
+    return torch.zeros((n_pages, H, page_size // 16, 18 * D), dtype=torch.uint8, device=device)
+
+
+def cache_tables(old_lens, new_lens, page_size, block_table, pool, pool_count, max_tokens, out=None):
+    """Block tables [R, max_pages] and page pool from old_lens to new_lens (both int32 [R]), in place, and the
+    step's new tokens.  A step that cannot be served sets new_lens back to old_lens.  ``out``: the five tensors of the result, to be written instead of new ones (its first may be
+    pool_count)."""
+    R, max_pages = block_table.shape
+    dev = block_table.device
+    if out is None:
+        tok = torch.empty((2, max_tokens), dtype=torch.int32, device=dev)
+        out = (torch.empty((1,), dtype=torch.int32, device=dev),
+               torch.empty((R + 1,), dtype=torch.int32, device=dev), tok[0], tok[1],
+               torch.empty((max_tokens,), dtype=torch.int64, device=dev))
+    ws = torch.empty((bsa.bsa_cache_tables_workspace(R) // 4,), dtype=torch.int32, device=dev)
+    bsa.bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, pool.shape[0], pool_count,
+                         *out, max_tokens, ws)
+    return CacheStep(*out)
+
+
+def cache_append(k, v, slots, cache, k_scale=None, v_scale=None, values=None):
+    """K and V rows [T, H, D] (token stride free) rounded to 4 bits into their slots of the cache.  ``values``: a
+    pair of [T, H, D] tensors that receive the rows as the cache holds them."""
+    T, H, D = k.shape
+    if cache.shape[1] != H or cache.shape[3] != 18 * D:
+        raise ValueError("cache %s does not hold %d heads of %d channels" % (tuple(cache.shape), H, D))
+    kv, vv = (None, None) if values is None else values
+    bsa.bsa_cache_append(k, v, T, H, D, slots, cache, cache.shape[0], cache.shape[2] * 16, k_scale, v_scale, kv, vv)
+
+
+def cache_attention(q, cache, block_table, token_req, token_pos, k_scale=None, v_scale=None, block_indices=None,
+                    block_counts=None, block_size=0, scale=None, need_lse=True):
+    """Query rows [T, HQ, D] of the given requests and positions over the cached keys up to each row's own position:
+    all of them, or with block_indices [T, H, S] / block_counts [T, H] those of the listed blocks.  Returns
+    (out [T, HQ, D], lse [T, HQ] or None); rows of tokens with request -1 are not written."""
+    T, HQ, D = q.shape
+    n_pages, H, strips, width = cache.shape
+    if width != 18 * D:
+        raise ValueError("cache %s does not hold %d channels" % (tuple(cache.shape), D))
+    R, max_pages = block_table.shape
+    S = 0 if block_indices is None else block_indices.shape[-1]
+    max_keys = S * block_size if S else max_pages * strips * 16
+    out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((T, HQ), dtype=torch.float32, device=q.device) if need_lse else None
+    nbytes = bsa.bsa_cache_attention_workspace(T, HQ, H, D, max_keys)
+    ws = torch.empty((nbytes // 4,), dtype=torch.float32, device=q.device) if nbytes else None
+    bsa.bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, strips * 16, block_table, R, max_pages, token_req,
+                             token_pos, k_scale, v_scale, block_indices, block_counts, S, block_size,
+                             D ** -0.5 if scale is None else scale, out, lse, ws)
+    return out, lse
+
+
+class TokenCache:
+    """One layer's paged 4-bit cache with its tables, for R requests.
+
+    A serving step is ``step`` (the tables, from the requests' new lengths),
+    ``append`` (the new tokens' K and V) and ``attend`` (their queries).  Several
+    layers can share the tables: give the first layer's cache as ``tables``."""
+
+    def __init__(self, R, n_pages, max_pages, H, D, page_size=64, k_scale=None, v_scale=None, device="cuda",
+                 tables=None):
+        self.page_size = page_size
+        self.cache = new_cache(n_pages, H, page_size, D, device)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self._own = tables is None
+        if self._own:
+            self.lens = torch.zeros((R,), dtype=torch.int32, device=device)
+            self.block_table = torch.full((R, max_pages), -1, dtype=torch.int32, device=device)
+            self.pool = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 on top
+            self.pool_count = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        else:
+            if tables.block_table.shape != (R, max_pages) or tables.page_size != page_size \
+                    or tables.pool.shape[0] != n_pages:
+                raise ValueError("the shared tables have other sizes")
+            self.lens, self.block_table = tables.lens, tables.block_table
+            self.pool, self.pool_count = tables.pool, tables.pool_count
+
+    def step(self, new_lens, max_tokens):
+        """The tables for new_lens int32 [R]; returns the CacheStep.  A step that cannot be served (too few
+        free pages, more than max_tokens new tokens: BSA_ERR_CAPACITY on the device status) has no tokens and
+        leaves tables and lengths as they were."""
+        if not self._own:
+            raise ValueError("these tables belong to another cache")
+        held = new_lens.clone()
+        R, dev = held.shape[0], held.device
+        tok = torch.empty((2, max_tokens), dtype=torch.int32, device=dev)
+        out = cache_tables(self.lens, held, self.page_size, self.block_table, self.pool, self.pool_count, max_tokens,
+                           out=(self.pool_count, torch.empty((R + 1,), dtype=torch.int32, device=dev), tok[0], tok[1],
+                                torch.empty((max_tokens,), dtype=torch.int64, device=dev)))
+        self.lens.copy_(held)
+        return out
+
+    def append(self, k, v, step, values=None):
+        cache_append(k, v, step.slots, self.cache, self.k_scale, self.v_scale, values)
+
+    def attend(self, q, step, block_indices=None, block_counts=None, block_size=0, scale=None, need_lse=True):
+        return cache_attention(q, self.cache, self.block_table, step.token_req, step.token_pos, self.k_scale,
+                               self.v_scale, block_indices, block_counts, block_size, scale, need_lse)

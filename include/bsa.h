@@ -5,8 +5,9 @@
  *   tile map -> mean pool -> E = Q_bar K_bar^T / sqrt(D) -> per-row TopK ->
  *   exact online-softmax attention over the selected key blocks,
  * plus the caller-routed GQA variant (NSA selected branch), the KV-outer
- * order (reverse index, partial pass, log-sum-exp combine) and the
- * exact-plus-summary variant.
+ * order (reverse index, partial pass, log-sum-exp combine), the
+ * exact-plus-summary variant, and token-by-token use of the GQA variant over a
+ * paged cache held in 4 bits.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -63,7 +64,8 @@ typedef enum {
     BSA_ERR_UNSUPPORTED = 2,
     BSA_ERR_CUDA = 3,
     BSA_ERR_INDEX = 4,   /* device: an index outside its range was skipped */
-    BSA_ERR_TIMEOUT = 5  /* device: a bounded wait expired; that tile was abandoned */
+    BSA_ERR_TIMEOUT = 5, /* device: a bounded wait expired; that tile was abandoned */
+    BSA_ERR_CAPACITY = 6 /* device: a call needed more than its pool or arrays hold; it changed nothing */
 } bsa_status;
 
 typedef enum { BSA_F32 = 0, BSA_BF16 = 1 } bsa_dtype;
@@ -75,8 +77,8 @@ int bsa_version(void);
 const char* bsa_last_error(void);
 
 /* Synchronises `stream`, then returns and clears the device status word of
- * the current device (BSA_OK, BSA_ERR_INDEX or BSA_ERR_TIMEOUT), or
- * BSA_ERR_CUDA if the synchronisation itself failed. */
+ * the current device (BSA_OK, BSA_ERR_INDEX, BSA_ERR_TIMEOUT or
+ * BSA_ERR_CAPACITY), or BSA_ERR_CUDA if the synchronisation itself failed. */
 bsa_status bsa_device_status(void* stream);
 
 /* The same two calls under the names of the interface the pages imply
@@ -453,6 +455,107 @@ bsa_status bsa_reblock_layout(const void* q, const void* k, bsa_dtype dtype, int
                               float* factor, void* workspace, size_t workspace_bytes, void* stream);
 bsa_status bsa_permute_rows(const void* src, void* dst, bsa_dtype dtype, int BH, int N, int D,
                             int n_prefix, const int32_t* perm, int inverse, void* stream);
+
+/* ------------------------------------------------------------------ a12 ---
+ * Paged 4-bit cache: the tables of a serving step.  Token-by-token use of the
+ * [NSA] / [MSA] selected branch needs earlier keys and values kept; here they
+ * are kept in pages of page_size tokens (a power of two, 16..1024), and request
+ * r's token at position p lies in page block_table[r][p / page_size], its slot
+ * being page * page_size + p % page_size.
+ *
+ * Cache layout: uint8 [n_pages][H][page_size / 16][18 * D], D a multiple of 16
+ * up to 128; bsa_cache_bytes gives the size (0 for sizes out of range).  The
+ * 18 * D bytes of a strip (16 consecutive tokens of one KV head) are
+ *   K codes  [16 tokens][D / 2]      V codes  [D / 16][16 tokens][8]
+ *   K scales [16 tokens][D / 16]     V scales [D / 16][16 tokens]
+ * codes E2M1, the even channel in the low nibble; scales E4M3, one per token and
+ * 16 consecutive channels.  An element is code * scale * its head's scale.
+ *
+ * bsa_cache_tables brings the tables from old_lens [R] to new_lens [R] (tokens
+ * held by each request before and after the step).  A request that grows across
+ * a page border takes pages, one that shrinks gives back those it no longer
+ * reaches (new length 0: all of them).  pool [n_pages] is a stack of free page
+ * ids, its first pool_count[0] entries valid: the given-back pages are pushed,
+ * the last request's last page first, then the new pages are popped in order of
+ * request and position, so that a call that shrinks what the last one grew
+ * restores the pool.  pool_count_out[0] is the new count (it may be pool_count).
+ * block_table [R, max_pages] is updated in place: entries behind a request's
+ * last page are left as they were.
+ * The step's new tokens (positions old .. new - 1 of each request that grew) are
+ * numbered in order of request and position: query_start [R + 1] holds the first
+ * number of each request and the total; token_req, token_pos and slots
+ * [max_tokens] hold each token's request, position and slot, and -1 behind the
+ * last (so a captured step of fixed size can run a smaller batch).
+ * All pointers [device]; slots is int64, the rest int32.  block_table and pool
+ * must not overlap the other arrays.  workspace: bsa_cache_tables_workspace(R)
+ * bytes, its contents meaningless between calls.
+ * A call that cannot be carried out changes neither table, pool nor count,
+ * writes zeros to query_start, -1 to the token arrays and old_lens to new_lens
+ * (which therefore always holds the lengths that the tables are for), and latches
+ * BSA_ERR_CAPACITY (too few free pages, more than max_tokens new tokens) or
+ * BSA_ERR_INDEX (a length outside [0, max_pages * page_size], a count outside
+ * the pool).  A page id outside [0, n_pages) met on the way latches
+ * BSA_ERR_INDEX and gives the slot -1. */
+size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D);
+size_t bsa_cache_tables_workspace(int R);
+bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
+                            int32_t* block_table, int max_pages, int32_t* pool, int n_pages,
+                            const int32_t* pool_count, int32_t* pool_count_out, int32_t* query_start,
+                            int32_t* token_req, int32_t* token_pos, int64_t* slots, int max_tokens,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ a13 ---
+ * Rounds new K and V rows to 4 bits and stores them at their slots.  For each
+ * group of 16 channels of a token and head, with g its head's scale:
+ *   y = x * (1 / g) in float32,  s = E4M3(max |y| / 6) (nearest even, at most
+ *   448),  code = E2M1(y / s) (nearest even, at most 6);  s = 0 stores zeros.
+ * A group holding a NaN or an infinity gets the scale NaN: it reads back as NaN.
+ * k, v: [device] [T, H, D] of `dtype`, a token's heads contiguous and tokens
+ * k_stride / v_stride elements apart (so slices of a fused projection need no
+ * copy).  slots: [device] int64 [T] as bsa_cache_tables writes them; -1 skips the
+ * token, any other value outside the cache skips it and latches BSA_ERR_INDEX.
+ * The slots of one call must be distinct (a slot given twice holds a mixture).
+ * cache: [device] 16-byte aligned.  k_scale, v_scale: [device] float [H],
+ * positive, or NULL for 1.
+ * k_val, v_val: [device] [T, H, D] of `dtype`, the values as stored (code * s * g,
+ * rounded once to `dtype`), so that a prefill can attend to what later steps
+ * will read; rows of skipped tokens are left as they were.  Both or neither. */
+bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D,
+                            int64_t k_stride, int64_t v_stride, const int64_t* slots, void* cache,
+                            int n_pages, int page_size, const float* k_scale, const float* v_scale,
+                            void* k_val, void* v_val, void* stream);
+
+/* ------------------------------------------------------------------ a14 ---
+ * bsa_fwd_qouter_tokens over the cache: query head hq of token t reads KV head
+ * hq / (HQ / H) of request token_req[t], the keys at positions 0 .. token_pos[t]
+ * (the token's own must have been appended), or, with block lists, those of them
+ * in the blocks block_indices[t, h, 0 .. block_counts[t, h]): positions
+ * idx * block_size + u.  As there, slots are read in any order, a block listed
+ * twice counts twice, and an index outside [0, ceil(max_pages * page_size /
+ * block_size)) or a count above S latches BSA_ERR_INDEX (the slot is skipped, the
+ * count clamped).  A page id outside [0, n_pages) latches BSA_ERR_INDEX and its
+ * keys are skipped.  A row with no visible key (a position of -1, an empty list)
+ * outputs 0 and LSE -inf.  Tokens with token_req -1 are padding: their rows of
+ * out and lse are left as they were; a request of R or more, or a position of
+ * max_pages * page_size or more, latches BSA_ERR_INDEX (the first is then treated as
+ * padding, the second as an empty row).
+ * Cache bytes of keys that no row sees are not looked at: they may be anything.
+ * q: [device] [T, HQ, D] of `dtype`, tokens q_stride elements apart; out: [device]
+ * contiguous [T, HQ, D] of `dtype`; lse: [device] float [T, HQ] or NULL.
+ * block_table: [device] int32 [R, max_pages]; token_req, token_pos: [device]
+ * int32 [T]; block_indices: [device] int32 [T, H, S], block_counts: [device]
+ * int32 [T, H], or both NULL for every key.  block_size: a multiple of 16.
+ * D a multiple of 16 up to 128.
+ * workspace: [device] bsa_cache_attention_workspace bytes, 16-byte aligned, its
+ * contents meaningless between calls; max_keys is the most keys that a row can
+ * see: S * block_size with lists, else max_pages * page_size. */
+size_t bsa_cache_attention_workspace(int T, int HQ, int H, int D, int max_keys);
+bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, int H, int D, int64_t q_stride,
+                                const void* cache, int n_pages, int page_size, const int32_t* block_table,
+                                int R, int max_pages, const int32_t* token_req, const int32_t* token_pos,
+                                const float* k_scale, const float* v_scale, const int32_t* block_indices,
+                                const int32_t* block_counts, int S, int block_size, float scale, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,6 +16,9 @@ float64 restatement of the definitions given on four pages:
   query) and the Reblock layout (second-moment metric, equal-capacity
   hierarchical partition).
 
+``cache.py`` restates the paged 4-bit cache (tables, rounding and storage, the
+NSA selected branch over it) from the definitions in ``include/bsa.h``.
+
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 ``--impl reference`` legs of ``bench.py`` may import this package.  The CUDA
 library never imports it, links it or calls it, and the two share no code: the
@@ -46,4 +49,7 @@ from .spark import bf16_round, reweight_anchor, reweight_summary, reweight_summa
 from .coarse import coarse_attention, coarse_output  # noqa: F401
 from .reblock import (  # noqa: F401
     second_moment, metric_factor, unit_features, split_node, partition, reblock_layout, attention_mass_recall,
+)
+from .cache import (  # noqa: F401
+    e4m3_value, quantise_group, code_value, empty_cache, store, load, cache_tables, cache_attention,
 )
