@@ -28,8 +28,9 @@ __global__ void __launch_bounds__(128) cache_attn_simt_kernel(CacheAttn a) {
     for (int n = 0; n < row.strips; ++n) {
         const int first = first_key(a, row, n, tid == 0);
         if (first < 0) continue;
-        const uint8_t* strip = strip_at(a, row, h, first, tid == 0);
-        if (!strip) continue;
+        const int index = strip_index(a, row, h, first, tid == 0);
+        if (index < 0) continue;
+        const uint8_t* strip = a.cache + (long long)index * strip_bytes(D);
         const int seen = min(kStrip, row.pos - first + 1);
         __syncthreads();
         for (int i = tid; i < kStrip * D; i += 128) {
@@ -89,6 +90,8 @@ static bsa_status simt_cache_attention(const CacheAttn& a, bsa_dtype dtype, cuda
     return check_launch("cache_attn_simt_kernel");
 }
 
+static bool on_tensor_cores(int D) { return D == 64 || D == 128; }
+
 }  // namespace bsa
 
 using namespace bsa;
@@ -96,8 +99,8 @@ using namespace bsa;
 extern "C" {
 
 size_t bsa_cache_attention_workspace(int T, int HQ, int H, int D, int max_keys) {
-    (void)T, (void)HQ, (void)H, (void)D, (void)max_keys;
-    return 0;
+    if (T < 1 || H < 1 || HQ < 1 || HQ % H || max_keys < 1 || !on_tensor_cores(D)) return 0;
+    return mma_cache_attention_workspace(T, HQ, H, D, max_keys);
 }
 
 bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, int H, int D, int64_t q_stride,
@@ -123,7 +126,11 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
                 "cache attention: block lists need S and block_size");
     if (block_indices && block_size % kStrip)
         return fail(BSA_ERR_UNSUPPORTED, "cache attention: block_size must be a multiple of 16, got %d", block_size);
-    (void)workspace, (void)workspace_bytes;
+    BSA_REQUIRE(((long long)n_pages * H << (log2i(page_size) - 4)) <= 0x7fffffffLL, "cache attention: too many strips");
+    const long long max_keys = block_indices ? (long long)S * block_size : (long long)max_pages * page_size;
+    const size_t need = bsa_cache_attention_workspace(T, HQ, H, D, (int)max_keys);
+    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 15) == 0),
+                "cache attention: a 16-byte aligned workspace of %zu bytes is needed", need);
     if (T == 0) return BSA_OK;
     CacheAttn a;
     a.q = q, a.T = T, a.HQ = HQ, a.H = H, a.D = D, a.q_stride = q_stride;
@@ -132,6 +139,7 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
     a.k_scale = k_scale, a.v_scale = v_scale, a.blocks = block_indices, a.counts = block_counts;
     a.S = block_indices ? S : 0, a.block_strips = block_indices ? block_size / kStrip : 0;
     a.scale_log2 = scale * kLog2e, a.out = out, a.lse = lse, a.status = status_word();
+    if (on_tensor_cores(D) && !force_simt()) return mma_cache_attention(a, dtype, max_keys, workspace, as_stream(stream));
     return simt_cache_attention(a, dtype, as_stream(stream));
 }
 

@@ -70,14 +70,19 @@ __device__ __forceinline__ int first_key(const CacheAttn& a, const Row& r, int n
     return first <= r.pos ? (int)first : -1;
 }
 
-// The strip's bytes, or null (and a latched error) when its page is none of the cache's.
-__device__ __forceinline__ const uint8_t* strip_at(const CacheAttn& a, const Row& r, int h, int first, bool report) {
+// Index of the strip in the cache, or -1 (and a latched error) when its page is none of the cache's.
+__device__ __forceinline__ int strip_index(const CacheAttn& a, const Row& r, int h, int first, bool report) {
     const int page = a.table[(long long)r.req * a.max_pages + (first >> a.sh)];
     if ((unsigned)page >= (unsigned)a.n_pages) {
         if (report) raise_status(a.status, BSA_ERR_INDEX);
-        return nullptr;
+        return -1;
     }
-    return a.cache + ((((long long)page * a.H + h) << (a.sh - 4)) + ((first & ((1 << a.sh) - 1)) >> 4)) * strip_bytes(a.D);
+    return ((page * a.H + h) << (a.sh - 4)) + ((first & ((1 << a.sh) - 1)) >> 4);
 }
+
+// The tensor-core kernel (D = 64 or 128).
+size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_keys);
+bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
+                               cudaStream_t st);
 
 }  // namespace bsa

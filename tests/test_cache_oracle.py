@@ -208,7 +208,10 @@ def test_append_refusals(bsa, change, word):
     (dict(D=8), "multiple of 16", 1), (dict(D=256), "multiple of 16", 1), (dict(qs=1023), "stride", 1),
     (dict(cache=17), "aligned", 1), (dict(idx=None), "together", 1), (dict(cnt=None), "together", 1),
     (dict(S=0), "block lists", 1), (dict(BS=0), "block lists", 1), (dict(S=1 << 20, BS=1 << 12), "block lists", 1),
-    (dict(max_pages=1 << 26), "2^31", 1), (dict(BS=24), "multiple of 16", 2),
+    (dict(max_pages=1 << 26), "2^31", 1), (dict(BS=24), "multiple of 16", 2), (dict(n_pages=1 << 29), "strips", 1),
+    (dict(ws=None, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
+    (dict(ws=24, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
+    (dict(ws_bytes=64, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
 ])
 def test_attention_refusals(bsa, change, word, status):
     assert bsa._lib.bsa_fwd_cache_tokens(*_args(ATTEND, **change)) == status

@@ -7,6 +7,9 @@ Tolerances, from the arithmetic (u = half a step relative to the value):
   - a float32 logit is off by at most (D + 8) 2^-24 B from its sum and 2^-22 B from q in two float16 parts (bf16 q
     is exact in one), so a weight by twice that, and by 2^-22 from exp2;
   - a weight is held in float16 (u = 2^-11) for bf16 outputs, in two float16 parts (2^-22) for float32 ones;
+  - float16's smallest step is 2^-24 and the tensor-core kernel holds 2^15 times each weight (relative to the row's
+    largest, itself at most 1), so no weight is held closer than half a step, 2^-25 2^-15 = 2^-40: F = 2^-40 sum_j
+    |v_j| more per channel (found where a row's only large weight meets a zero of V: o ~ 1e-21 there, A no larger);
   - sums over n keys add n 2^-24; the output's own rounding is u = 2^-8 |o| (bf16), 2^-24 |o| (float32).
   LSE: the logit's error, n 2^-24 + 2^-22 for the sum, 2^-24 |lse| for its rounding."""
 
@@ -335,7 +338,7 @@ def want_attend(c, scale=None):
     scale = D ** -0.5 if scale is None else scale
     T, HQ, _ = q.shape
     H, P = c["cache"].shape[1], c["cache"].shape[2] * 16
-    A, B, n = np.zeros_like(o), np.zeros((T, HQ)), np.zeros((T, HQ))
+    A, B, n, F = np.zeros_like(o), np.zeros((T, HQ)), np.zeros((T, HQ)), np.zeros_like(o)
     memo = {}
     for t in range(T):
         for h in range(H):
@@ -358,11 +361,12 @@ def want_attend(c, scale=None):
                 x = K @ q[t, r] * scale
                 p = np.exp(x - lse[t, r])
                 A[t, r] = p @ np.abs(V)
+                F[t, r] = 2.0 ** -40 * np.abs(V).sum(0)
                 B[t, r] = (np.abs(K) @ np.abs(q[t, r])).max() * abs(scale)
                 n[t, r] = len(keys)
     logit = B * ((D + 8) * 2.0 ** -24 + 2.0 ** -22)
     weight = 2 * logit + 2.0 ** -22 + n * 2.0 ** -24 + (2.0 ** -11 if bf16 else 2.0 ** -22)
-    tol = A * weight[..., None] + np.abs(o) * (2.0 ** -8 if bf16 else 2.0 ** -24) * 1.01
+    tol = F + A * weight[..., None] + np.abs(o) * (2.0 ** -8 if bf16 else 2.0 ** -24) * 1.01
     return o, lse, tol, logit + n * 2.0 ** -24 + 2.0 ** -22 + np.abs(np.where(np.isfinite(lse), lse, 0)) * 2.0 ** -24
 
 
