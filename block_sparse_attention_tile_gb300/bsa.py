@@ -9,6 +9,7 @@ names, and importing this module fails loudly when the library is missing.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -71,7 +72,7 @@ _SIGS = {
     "bsa_coarse_attention": (I, [P, I64, P, I64, I, I, I, P, P]),
     "bsa_coarse_apply": (I, [P, I, P, P, I, I, I, I, P, P, I, I, I, P]),
     "bsa_cache_bytes": (SZ, [I, I, I, I]),
-    "bsa_cache_tables_workspace": (SZ, [I]),
+    "bsa_cache_tables_workspace": (SZ, [I, I]),
     "bsa_cache_tables": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, P, I, P, SZ, P]),
     "bsa_cache_append": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P]),
     "bsa_cache_attention_workspace": (SZ, [I, I, I, I, I]),
@@ -326,10 +327,14 @@ def _expect(name, t, dtype, numel, dev):
     """Data pointer of a contiguous tensor of this type on this device with at least numel elements; None stays None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of at least %d elements on cuda:%d is needed, got %s %s on %s"
-                         % (name, dtype, numel, dev, t.dtype, tuple(t.shape), t.device))
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s: a contiguous %s tensor of at least %d elements on cuda:%d is needed, got %s %s on %s"
+                     % (name, dtype, numel, dev, t.dtype, tuple(t.shape), t.device))
+
+
+def _workspace(t, dev):
+    return (None, 0) if t is None else (_expect("workspace", t, t.dtype, 0, dev), t.numel() * t.element_size())
 
 
 def _rows(name, t, T, heads, D, dtype, dev):
@@ -345,7 +350,7 @@ def _rows(name, t, T, heads, D, dtype, dev):
 
 def _run_on(dev, stream, fn, args):
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         _check(fn(*args, raw))
     else:
         with torch.cuda.device(dev):
@@ -356,12 +361,13 @@ def bsa_cache_bytes(n_pages, H, page_size, D):
     return _lib.bsa_cache_bytes(n_pages, H, page_size, D)
 
 
-def bsa_cache_tables_workspace(R):
-    return _lib.bsa_cache_tables_workspace(R)
+@functools.lru_cache(maxsize=1024)
+def bsa_cache_tables_workspace(R, max_tokens):
+    return _lib.bsa_cache_tables_workspace(R, max_tokens)
 
 
 def bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, n_pages, pool_count,
-                     pool_count_out, query_start, token_req, token_pos, slots, max_tokens, workspace, stream=None):
+                     pool_count_out, query_start, token_req, token_pos, slots, max_tokens, workspace=None, stream=None):
     dev, i32 = _device_of(block_table), torch.int32
     _run_on(dev, stream, _lib.bsa_cache_tables, (
         _expect("old_lens", old_lens, i32, R, dev), _expect("new_lens", new_lens, i32, R, dev), R, page_size,
@@ -370,7 +376,7 @@ def bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, p
         _expect("pool_count_out", pool_count_out, i32, 1, dev), _expect("query_start", query_start, i32, R + 1, dev),
         _expect("token_req", token_req, i32, max_tokens, dev), _expect("token_pos", token_pos, i32, max_tokens, dev),
         _expect("slots", slots, torch.int64, max_tokens, dev), max_tokens,
-        _expect("workspace", workspace, workspace.dtype, 0, dev), workspace.numel() * workspace.element_size()))
+        *_workspace(workspace, dev)))
 
 
 def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=None, v_scale=None, k_val=None,
@@ -385,6 +391,7 @@ def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=No
         _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev)))
 
 
+@functools.lru_cache(maxsize=1024)
 def bsa_cache_attention_workspace(T, HQ, H, D, max_keys):
     return _lib.bsa_cache_attention_workspace(T, HQ, H, D, max_keys)
 
@@ -403,5 +410,4 @@ def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table,
         _expect("block_indices", block_indices, i32, T * H * S, dev),
         _expect("block_counts", block_counts, i32, T * H, dev), S, block_size, scale,
         _expect("out", out, dt, T * HQ * D, dev), _expect("lse", lse, f32, T * HQ, dev),
-        None if workspace is None else _expect("workspace", workspace, workspace.dtype, 0, dev),
-        0 if workspace is None else workspace.numel() * workspace.element_size()))
+        *_workspace(workspace, dev)))

@@ -39,6 +39,7 @@ struct Sums {
 constexpr int kScanThreads = 1024;
 constexpr int kOneCtaTokens = 4096;  // up to here one CTA does all: 4 tokens a thread cost less than a second launch
 constexpr int kOneCtaRequests = 1024;
+inline bool one_cta(int R, int max_tokens) { return R <= kOneCtaRequests && max_tokens <= kOneCtaTokens; }
 
 __device__ __forceinline__ int pages_of(int len, int sh) { return (int)(((unsigned)len + (1u << sh) - 1) >> sh); }
 
@@ -355,7 +356,9 @@ size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D) {
     return (size_t)n_pages * H * (page_size / kStrip) * strip_bytes(D);
 }
 
-size_t bsa_cache_tables_workspace(int R) { return R < 1 ? 0 : (8 + 2 * ((size_t)R + 1)) * sizeof(int32_t); }
+size_t bsa_cache_tables_workspace(int R, int max_tokens) {
+    return R < 1 || one_cta(R, max_tokens) ? 0 : (8 + 2 * ((size_t)R + 1)) * sizeof(int32_t);
+}
 
 bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
                             int32_t* block_table, int max_pages, int32_t* pool, int n_pages,
@@ -371,14 +374,15 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
     BSA_REQUIRE(page_size_ok(page_size), "cache tables: page_size must be a power of two in 16..1024, got %d", page_size);
     BSA_REQUIRE((long long)R * max_pages <= 0x7fffffffLL && (long long)max_pages * page_size <= 0x7fffffffLL,
                 "cache tables: R * max_pages and max_pages * page_size must be below 2^31");
-    BSA_REQUIRE(workspace && workspace_bytes >= bsa_cache_tables_workspace(R) && ((uintptr_t)workspace & 3) == 0,
-                "cache tables: workspace of %zu bytes needed", bsa_cache_tables_workspace(R));
+    const size_t need = bsa_cache_tables_workspace(R, max_tokens);
+    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 3) == 0),
+                "cache tables: a workspace of %zu bytes is needed", need);
     cudaStream_t st = as_stream(stream);
     const int sh = log2i(page_size);
     Tables a{old_lens, new_lens, R, page_size, max_pages, n_pages, max_tokens, block_table, pool, pool_count,
              pool_count_out, query_start, token_req, token_pos, slots, status_word()};
     int32_t* ws = static_cast<int32_t*>(workspace);
-    if (R <= kOneCtaRequests && max_tokens <= kOneCtaTokens) {
+    if (one_cta(R, max_tokens)) {
         cache_scan_kernel<true><<<1, kScanThreads, 3 * (R + 1) * sizeof(int32_t), st>>>(a, sh, ws);
         return check_launch("cache_scan_kernel");
     }

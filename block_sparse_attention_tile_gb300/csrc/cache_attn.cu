@@ -119,7 +119,7 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
     BSA_REQUIRE(D >= 16 && D <= 128 && D % 16 == 0, "cache attention: D must be a multiple of 16 up to 128, got %d", D);
     BSA_REQUIRE((long long)max_pages * page_size <= 0x7fffffffLL, "cache attention: max_pages * page_size must be below 2^31");
     BSA_REQUIRE(T <= 1 || q_stride >= (int64_t)HQ * D, "cache attention: a token's stride is below HQ * D");
-    BSA_REQUIRE(((uintptr_t)cache & 15) == 0, "cache attention: the cache must be 16-byte aligned");
+    BSA_REQUIRE((((uintptr_t)cache | (uintptr_t)out) & 15) == 0, "cache attention: cache and out must be 16-byte aligned");
     BSA_REQUIRE((block_indices == nullptr) == (block_counts == nullptr),
                 "cache attention: block_indices and block_counts come together");
     BSA_REQUIRE(!block_indices || (S > 0 && block_size > 0 && (long long)S * block_size <= 0x7fffffffLL),
@@ -129,8 +129,8 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
     BSA_REQUIRE(((long long)n_pages * H << (log2i(page_size) - 4)) <= 0x7fffffffLL, "cache attention: too many strips");
     const long long max_keys = block_indices ? (long long)S * block_size : (long long)max_pages * page_size;
     const size_t need = bsa_cache_attention_workspace(T, HQ, H, D, (int)max_keys);
-    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 15) == 0),
-                "cache attention: a 16-byte aligned workspace of %zu bytes is needed", need);
+    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 31) == 0),
+                "cache attention: a 32-byte aligned workspace of %zu bytes is needed", need);
     if (T == 0) return BSA_OK;
     CacheAttn a;
     a.q = q, a.T = T, a.HQ = HQ, a.H = H, a.D = D, a.q_stride = q_stride;

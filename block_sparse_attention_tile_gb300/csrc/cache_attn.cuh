@@ -31,8 +31,9 @@ struct Row {
     const int32_t* blocks;
 };
 
-__device__ __forceinline__ Row row_of(const CacheAttn& a, int t, int h, bool report) {
-    Row r{a.req[t], a.pos[t], 0, nullptr};
+// From the loaded request, position and (with lists) count; r.blocks is left null.
+__device__ __forceinline__ Row row_from(const CacheAttn& a, int req, int pos, int count, bool report) {
+    Row r{req, pos, 0, nullptr};
     if (r.req >= a.R) {
         if (report) raise_status(a.status, BSA_ERR_INDEX);
         r.req = -1;
@@ -47,14 +48,17 @@ __device__ __forceinline__ Row row_of(const CacheAttn& a, int t, int h, bool rep
         r.strips = (r.pos >> 4) + 1;
         return r;
     }
-    const long long at = (long long)t * a.H + h;
-    int n = a.counts[at];
-    if (n > a.S) {
+    if (count > a.S) {
         if (report) raise_status(a.status, BSA_ERR_INDEX);
-        n = a.S;
+        count = a.S;
     }
-    r.strips = max(n, 0) * a.block_strips;
-    r.blocks = a.blocks + at * a.S;
+    r.strips = max(count, 0) * a.block_strips;
+    return r;
+}
+__device__ __forceinline__ Row row_of(const CacheAttn& a, int t, int h, bool report) {
+    const long long at = (long long)t * a.H + h;
+    Row r = row_from(a, a.req[t], a.pos[t], a.blocks ? a.counts[at] : 0, report);
+    if (a.blocks) r.blocks = a.blocks + at * a.S;
     return r;
 }
 

@@ -1,13 +1,17 @@
 // Attention over the 4-bit paged cache (a14) on the tensor cores, D = 64 or 128.
 //
-// A row is one token's up to 16 query heads of one KV head.  Its strips (16 keys each,
-// one contiguous run of 18 D bytes) are dealt out in tiles of four: to the row's CTAs in
-// equal runs, within a CTA to its four warps in turn.  Every warp works alone until its
-// keys are done: it copies its tiles into a ring of its own (one bulk copy per strip),
-// keeps its own running maximum, sum and output, and meets the others only in the merge
-//   m = max m_w,   l = sum l_w 2^(m_w - m),   U = sum U_w 2^(m_w - m),   O = U / l
-// over the warps (shared memory), the CTAs of a cluster (distributed shared memory) and,
-// where a row is cut finer than a cluster, over the clusters (workspace, second kernel).
+// A row is one token's up to 16 query heads of one KV head.  Its strips (16 keys each, one
+// contiguous run of 18 D bytes) are taken in tiles of up to four.  Every warp works alone: it
+// copies its tiles into a ring of its own (one bulk copy per strip), keeps its own running
+// maximum, sum and output, and goes on to its next row without waiting for anyone, the first
+// tiles of which are in flight by then.  Which tiles a warp takes:
+//   stream  two CTAs of four warps an SM, every warp an equal run of the rows' tiles laid end to
+//           end (so a batch of ragged lengths is balanced to a tile); a row that is cut leaves
+//           parts (m, l, U) in the workspace, and a second kernel joins them:
+//             m = max m_i,   l = sum l_i 2^(m_i - m),   U = sum U_i 2^(m_i - m),   O = U / l;
+//   rows    so many rows that whole ones balance: a run of rows each;
+//   split   so few tiles that one launch counts: a cluster of up to 8 CTAs per row, joined through
+//           shared and distributed shared memory.
 //
 // Numbers.  code * scale is exact in float16, so K and V enter the products exactly.  A
 // row of q is scaled by the power of two that brings its largest magnitude to 2^14..2^15
@@ -22,8 +26,18 @@
 // of one key (one 16-byte load at D = 128), of V the D / 8 consecutive channels of four keys.
 // Codes become float16 with cvt (two per byte) and one multiplication by their scales;
 // V's codes are first paired along the keys, four logic instructions per 16 codes.
-// No converted value is ever written back to shared memory.
+// No converted value is ever written back to shared memory.  With more than 8 heads q and the
+// weights are the 16-row operand; with up to 8 (kNarrow) K and V are, q and the weights the
+// 8-column one (transposed in registers by movmatrix), which halves the products and the output's
+// registers.
+//
+// What bounds it: the issue slots.  mma.sync keeps a scheduler for about 8 cycles, during which
+// little else issues (measured: 32 mma with 64 cvt and 64 multiplications take 2 cycles per mma
+// plus 1/4 per other instruction on an SM, whatever the number of warps), so a tile of 64 keys at
+// D = 128 costs 256 + 1000 / 4 cycles wide and 128 + 850 / 4 narrow, against 400 for its bytes at
+// the measured copy bandwidth.
 #include <algorithm>
+#include <atomic>
 
 #include "cache_attn.cuh"
 #include "tc_ptx.cuh"
@@ -31,28 +45,40 @@
 namespace bsa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = 4;     // strips of a tile
-constexpr int kStages = 2;   // tiles of a warp's ring
+constexpr int kWarps = 4;    // of a CTA
+constexpr int kTile = 4;     // strips of a tile, at most
+constexpr int kStages = 3;   // tiles of a warp's ring
 constexpr uint64_t kWaitNs = 500ull * 1000 * 1000;
-constexpr float kWeightLog2 = 15.f;
+constexpr float kWeightLog2 = 11.f;  // weights are held 2^11 times, relative to a reference
+constexpr float kSlack = 4.f;        // that the running maximum may pass by 2^4 before it is moved
 
-struct Split {
-    int head_tiles;  // tiles of 16 query heads per KV head
-    int splits;      // CTAs of a row: clusters of a row times cluster size
-    int clusters;
-    float* part;     // [rows][clusters][16][D] when clusters > 1
-    float2* ml;      // [rows][clusters][16]
+enum Mode { kSplit, kStream, kRows };
+
+struct Plan {
+    int mode;
+    int head_tiles;   // tiles of 16 query heads per KV head
+    int tile_strips;  // strips of a tile, at most kTile
+    int splits;       // kSplit: CTAs of a row (the cluster)
+    int rows;
+    float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
+    float2* ml;       // [warps][2][rows of U]
+    int2* begun;      // [warps] the cut row that the warp began (-1: none) and in how many parts it is
 };
 
 // ---------------------------------------------------------------- pieces
 
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_zero(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Eight codes -> four float16 pairs, in byte order.
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t* out) {
@@ -82,31 +108,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-template <typename V> __device__ __forceinline__ V lds(uint32_t addr);
-template <> __device__ __forceinline__ uint4 lds<uint4>(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
+template <typename V> __device__ __forceinline__ V lds(const unsigned char* p) { return *reinterpret_cast<const V*>(p); }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
-template <> __device__ __forceinline__ uint2 lds<uint2>(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-template <> __device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-template <> __device__ __forceinline__ uint16_t lds<uint16_t>(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-template <> __device__ __forceinline__ uint8_t lds<uint8_t>(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return (uint8_t)v;
+template <int N> __device__ __forceinline__ void bar_sync(int id) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -139,7 +148,7 @@ __device__ __forceinline__ float weight_of(float2 part, float m) {
     return part.x == -INFINITY && part.y == 0.f ? 0.f : ptx::ex2(part.x - m);
 }
 
-// Waits for a tile; after kWaitNs latches BSA_ERR_TIMEOUT and gives up.
+// Waits for a phase; after kWaitNs latches BSA_ERR_TIMEOUT and gives up.
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* status) {
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait(bar, parity))
@@ -150,170 +159,270 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* statu
     return true;
 }
 
-// ---------------------------------------------------------------- shared memory
+// ---------------------------------------------------------------- shapes
 
-template <int D>
-struct Layout {
+template <int D, typename T, bool kNarrow>
+struct Shape {
+    static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;  // float16 parts of q and of the weights
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRows = kNarrow ? 8 : 16;
     static constexpr int kStripB = strip_bytes(D);
     static constexpr int kTileB = kTile * kStripB;
-    static constexpr int kRing = kWarps * kStages * kTileB;
-    // merge: four warps' U, rows padded so that a quarter warp's 16-byte stores meet no bank twice
-    static constexpr int kRow = D + 16;
-    static constexpr int kMerge = kWarps * 16 * kRow * 4;
-    static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
-    static constexpr int kBars = kBuf;                                // kWarps * kStages mbarriers
-    static constexpr int kFirst = kBars + kWarps * kStages * 8;       // first key of each strip of the ring
-    static constexpr int kML = kFirst + kWarps * kStages * kTile * 4; // (m, l) of each warp and row; then the CTA's
-    static constexpr int kBytes = kML + kWarps * 16 * 8;
-    static __device__ __forceinline__ int at(int row, int ch) { return row * kRow + ch + ch / (D / 4) * 4; }
+    // kSplit: U of each warp over the ring, rows padded so that a quarter warp's 16-byte stores meet no bank twice
+    static constexpr int kRowF = D + 16;
+    static constexpr int kRing = kWarps * kStages * kTileB, kU = kWarps * kRows * kRowF * 4;
+    static constexpr int kML = kRing > kU ? kRing : kU;           // (m, l) of each warp and row
+    static constexpr int kCML = kML + kWarps * kRows * 8;         // the CTA's
+    static constexpr int kMeta = kCML + kRows * 8;                // of each tile of the ring: 8 ints
+    static constexpr int kFull = kMeta + kWarps * kStages * 32;
+    static constexpr int kBytes = kFull + kWarps * kStages * 8;
+    static __device__ __forceinline__ int at(int row, int ch) { return row * kRowF + ch + ch / (D / 4) * 4; }
 };
 
-// ---------------------------------------------------------------- the kernel
+// Row number -> token, KV head, head tile and the walk over its keys.
+struct Where {
+    int t, h, heads, hq0;
+};
+__device__ __forceinline__ Where where(const CacheAttn& a, const Plan& p, int r) {
+    Where w;
+    const int tile_h = r % p.head_tiles, G = a.HQ / a.H;
+    w.h = r / p.head_tiles % a.H;
+    w.t = r / p.head_tiles / a.H;
+    w.heads = min(16, G - tile_h * 16);
+    w.hq0 = w.h * G + tile_h * 16;
+    return w;
+}
+// A row without keys still has an output to write (one empty tile); a padding row has none.
+__device__ __forceinline__ int tiles_of(const Row& r, const Plan& p) {
+    return r.req < 0 ? 0 : max(1, (r.strips + p.tile_strips - 1) / p.tile_strips);
+}
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 2) cache_attn_mma_kernel(CacheAttn a, Split sp) {
-    using L = Layout<D>;
-    constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;  // float16 parts of q and of the weights
-    constexpr int kSteps = D / 16;                  // k-steps of q K^T
-    constexpr int kCh = D / 8;                      // channels of a lane's V fragment, and n-tiles of U
-    extern __shared__ __align__(128) unsigned char smem[];
-    const uint32_t sbase = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x % sp.splits, row_tile = blockIdx.x / sp.splits;
-    const int tile_h = row_tile % sp.head_tiles, h = row_tile / sp.head_tiles % a.H, t = row_tile / sp.head_tiles / a.H;
-    const int G = a.HQ / a.H, heads = min(16, G - tile_h * 16), hq0 = h * G + tile_h * 16;
+// Flags of a tile.
+constexpr int kBegin = 1, kEnd = 2, kCarried = 4, kCut = 8;
 
-    const Row row = row_of(a, t, h, tid == 0);
-    if (row.req < 0) return;  // the whole cluster shares the row
+// The tiles of a warp, looked up eight at a time (lane 4 i + j: strip j of the batch's tile i), a
+// batch ahead of the first copy that needs it.
+struct Ahead {
+    bool have = false;
+    int next_row = 0, first_tile = 0;  // the row after the current one; where the run begins in its first row
+    int left = 0;                      // tiles (kRows: rows) behind the current row's
+    // the current row: tiles [lo, hi) of n are the warp's, the batch is [off, off + size), the tile held off + at
+    int row = 0, lo = 0, hi = 0, n = 0, off = 0, size = 0, at = 0;
+    int opened = 0;                    // kStream: set to hi when the row is begun here and cut
+    Row r;
+    int h = 0;
+    int first = -1, page = 0;  // the lane's strip: its first key (-1: none to see), its page as the table has it
 
-    const int tiles = (row.strips + kTile - 1) / kTile;
-    const int lo = (int)((long long)tiles * split / sp.splits), hi = (int)((long long)tiles * (split + 1) / sp.splits);
-    const int mine = max(0, (hi - lo - warp + kWarps - 1) / kWarps);
-
-    const uint32_t ring = sbase + warp * kStages * L::kTileB;
-    const uint32_t bars = sbase + L::kBars + warp * kStages * 8;
-    int* firsts = reinterpret_cast<int*>(smem + L::kFirst) + warp * kStages * kTile;
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) ptx::mbar_init(bars + s * 8, 1);
-        ptx::fence_mbar_init();
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __device__ __forceinline__ void next(const CacheAttn& a, const Plan& p, int lane, int elem) {
+        have = false;
+        if (++at < size) {
+            have = true;
+            return;
+        }
+        off += size, size = 0;
+        while (off == hi) {
+            if (left <= 0 || next_row >= p.rows) return;
+            row = next_row++;
+            const Where w = where(a, p, row);
+            h = w.h;
+            r = row_of(a, w.t, w.h, lane == 0);
+            n = tiles_of(r, p);
+            lo = off = min(n, first_tile);
+            first_tile = 0;
+            // the row's queries are needed a few tiles from now
+            const char* q = static_cast<const char*>(a.q) + ((long long)w.t * a.q_stride + (long long)w.hq0 * a.D) * elem;
+            for (int i = lane * 128; i < w.heads * a.D * elem; i += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+            if (p.mode == kRows) {
+                hi = n;
+                --left;
+            } else {
+                hi = min(n, off + left);
+                left -= hi - off;
+                if (p.mode == kStream && lo == 0 && hi < n) opened = hi;
+            }
+        }
+        size = min(8, hi - off), at = 0;
+        have = true;
+        const int tile = off + (lane >> 2), s = tile * p.tile_strips + (lane & 3);
+        first = -1;
+        if ((lane & 3) < p.tile_strips && tile < hi && s < r.strips) {
+            first = first_key(a, r, s, true);
+            if (first >= 0) page = a.table[(long long)r.req * a.max_pages + (first >> a.sh)];
+        }
     }
-    __syncwarp();
+    __device__ __forceinline__ int flags() const {
+        const int t = off + at;
+        return (t == lo ? kBegin : 0) | (t == hi - 1 ? kEnd : 0) | (lo > 0 ? kCarried : 0) | (lo > 0 || hi < n ? kCut : 0);
+    }
+};
 
-    // Lane i holds strip i % 4 of the warp's tile 8 b + i / 4: its first key (-1: none to see) and its place.
-    auto resolve = [&](int b, int& first, int& place) {
-        const int tile = lo + warp + (8 * b + (lane >> 2)) * kWarps, n = tile * kTile + (lane & 3);
-        first = -1, place = 0;
-        if (tile >= hi || n >= row.strips) return;
-        first = first_key(a, row, n, true);
-        if (first < 0) return;
-        place = strip_index(a, row, h, first, true);
-        if (place < 0) first = -1;
-    };
-    int first, place, next_first = -1, next_place = 0;
-    resolve(0, first, place);
-    auto issue = [&](int j) {
-        const int src = (j & 7) * 4 + c, stage = j % kStages;
-        const int f = __shfl_sync(0xffffffffu, first, src), p = __shfl_sync(0xffffffffu, place, src);
-        const uint32_t live = __ballot_sync(0xffffffffu, f >= 0) & 15u;
-        if (lane < 4) firsts[stage * kTile + lane] = f;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bars + stage * 8, __popc(live) * L::kStripB);
-        __syncwarp();
-        if (lane < 4 && f >= 0)
-            bulk_copy(ring + stage * L::kTileB + lane * L::kStripB, a.cache + (long long)p * L::kStripB, L::kStripB,
-                      bars + stage * 8);
-    };
-    for (int j = 0; j < kStages && j < mine; ++j) issue(j);
+// kStream: where each warp's run begins and how long it is.  The tiles of a group of rows that
+// share their keys' number are counted once: a token's without lists, a (token, head)'s with.
+constexpr int kScanGroups = 8192;
+__device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, int* sums, int warps, int id, Ahead& ahead,
+                                           long long& run_lo, long long& total) {
+    __shared__ int part[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int mult = a.blocks ? p.head_tiles : a.H * p.head_tiles, groups = p.rows / mult;
+    for (int g0 = tid; g0 < groups; g0 += 8 * kWarps * 32) {  // eight groups' loads at a time
+        int req[8], pos[8], count[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int g = min(g0 + i * kWarps * 32, groups - 1), t = a.blocks ? g / a.H : g;
+            req[i] = a.req[t], pos[i] = a.pos[t];
+            count[i] = a.blocks ? a.counts[g] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (g0 + i * kWarps * 32 < groups)
+                sums[g0 + i * kWarps * 32] = tiles_of(row_from(a, req[i], pos[i], count[i], blockIdx.x == 0), p);
+    }
+    __syncthreads();
+    const int per = (groups + kWarps * 32 - 1) / (kWarps * 32), g0 = min(groups, tid * per), g1 = min(groups, g0 + per);
+    int mine = 0;
+    for (int g = g0; g < g1; ++g) mine += sums[g];
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    int before = inc - mine, all = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        if (k < warp) before += part[k];
+        all += part[k];
+    }
+    for (int g = g0; g < g1; ++g) sums[g] = before += sums[g];
+    __syncthreads();
+    total = (long long)all * mult;  // below 2^31: checked by the host
+    run_lo = total * id / warps;
+    ahead.left = (int)(total * (id + 1) / warps - run_lo);
+    if (ahead.left > 0) {
+        int lo = 0, hi = groups - 1;  // the first group that ends behind run_lo
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if ((long long)sums[mid] * mult > run_lo) hi = mid; else lo = mid + 1;
+        }
+        const int base = lo ? sums[lo - 1] : 0, n = sums[lo] - base, in = (int)(run_lo - (long long)base * mult);
+        ahead.next_row = lo * mult + in / n;
+        ahead.first_tile = in % n;
+    }
+    // the sums lie in the ring: everyone has read them before the first copy lands there
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+}
 
-    // q: lane (g, c) holds channels c D/4 .. of rows g and g + 8
-    uint32_t qa[kTerms][kSteps][4];
-    float rs[2];
-    {
-        const T* q = static_cast<const T*>(a.q) + t * a.q_stride + (long long)hq0 * D + c * (D / 4);
-        const float ks = (a.k_scale ? a.k_scale[h] : 1.f) * a.scale_log2;
+// ---------------------------------------------------------------- a warp's part of a row
+
+template <int D, typename T, bool kNarrow>
+struct Part {
+    using S = Shape<D, T, kNarrow>;
+    static constexpr int kTerms = S::kTerms;
+    static constexpr int kSteps = D / 16;             // k-steps of q K^T
+    static constexpr int kCh = D / 8;                 // channels of a lane's V fragment
+    static constexpr int kQ = kNarrow ? 2 : 4;        // registers of q per k-step
+    static constexpr int kU = kNarrow ? kCh / 2 : kCh;  // accumulator tiles of U
+
+    // Two "rows" (query heads) per lane: wide g and g + 8, narrow 2 c and 2 c + 1.
+    uint32_t q[kTerms][kSteps][kQ];
+    float rs[2], m[2], u[kU][4];
+    float2 l[2];
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) m[r] = -INFINITY, l[r] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
+    }
+
+    // Channels c D/4 .. of rows g (and g + 8), each row scaled to 2^14 .. 2^15.
+    __device__ __forceinline__ void load_q(const CacheAttn& a, const Plan& p, int row, int g, int c) {
+        const Where w = where(a, p, row);
+        const T* base = static_cast<const T*>(a.q) + w.t * a.q_stride + (long long)w.hq0 * D + c * (D / 4);
+        const float ks = (a.k_scale ? a.k_scale[w.h] : 1.f) * a.scale_log2;
         const bool wide = (((uintptr_t)a.q | (uintptr_t)(a.q_stride * (long long)sizeof(T))) & 15) == 0;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = g + half * 8;
+        for (int half = 0; half < (kNarrow ? 1 : 2); ++half) {
+            const int r = min(g + half * 8, w.heads - 1);  // rows behind the last head repeat it and are not written
             float x[D / 4];
-            if (r < heads) {
-                const T* p = q + (long long)r * D;
-                if (wide) {
-                    constexpr int kPer = 16 / sizeof(T);
+            const T* p4 = base + (long long)r * D;
+            if (wide) {
+                constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-                    for (int i = 0; i < D / 4 / kPer; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int i = 0; i < D / 4 / kPer; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p4) + i);
+                    const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if constexpr (sizeof(T) == 2) {
-                                x[i * kPer + 2 * e] = __uint_as_float(w[e] << 16);
-                                x[i * kPer + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                            } else {
-                                x[i * kPer + e] = __uint_as_float(w[e]);
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (sizeof(T) == 2) {
+                            x[i * kPer + 2 * e] = __uint_as_float(b[e] << 16);
+                            x[i * kPer + 2 * e + 1] = __uint_as_float(b[e] & 0xffff0000u);
+                        } else {
+                            x[i * kPer + e] = __uint_as_float(b[e]);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) x[i] = to_f32(p[i]);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+                for (int i = 0; i < D / 4; ++i) x[i] = to_f32(p4[i]);
             }
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^(14 - floor(log2 top)), its exponent kept in range; zero, infinite and NaN rows stay as they are
+            // 2^(14 - floor(log2 top)), its exponent kept in range; zero, infinite and NaN rows stay as they
+            // are.  The sign of the logits' factor goes into q, so that rs is positive; at least the
+            // smallest normal, so that a scale of zero leaves masked logits at -inf.
             const int e = (int)(__float_as_uint(top) >> 23);
             const int up = e == 0 || e == 255 ? 0 : min(126, 14 + 127 - e);
-            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-            rs[half] = ks * __uint_as_float((uint32_t)(127 - up) << 23);
+            const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), ks);
+            rs[half] = fmaxf(fabsf(ks) * __uint_as_float((uint32_t)(127 - up) << 23), 1.17549435e-38f);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {
+                    const int at = kNarrow ? e2 : half + 2 * e2;
                     const float x0 = x[4 * s + 2 * e2] * f, x1 = x[4 * s + 2 * e2 + 1] * f;
-                    const uint32_t hi2 = pack_f16x2(x0, x1);
-                    qa[0][s][half + 2 * e2] = hi2;
+                    q[0][s][at] = pack_f16x2(x0, x1);
                     if constexpr (kTerms == 2) {
-                        const float2 b = f16x2_to_f32(hi2);
-                        qa[1][s][half + 2 * e2] = pack_f16x2(x0 - b.x, x1 - b.y);
+                        const float2 b = f16x2_to_f32(q[0][s][at]);
+                        q[1][s][at] = pack_f16x2(x0 - b.x, x1 - b.y);
                     }
                 }
         }
+        if constexpr (kNarrow) {  // the lane's logits are those of heads 2 c and 2 c + 1
+            const float mine = rs[0];
+            rs[0] = __shfl_sync(0xffffffffu, mine, c * 8);
+            rs[1] = __shfl_sync(0xffffffffu, mine, c * 8 + 4);
+        }
     }
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, u[kCh][4];
-#pragma unroll
-    for (int j = 0; j < kCh; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
-
-    bool alive = true;
-    for (int j = 0; j < mine; ++j) {
-        const int stage = j % kStages;
-        const uint32_t bar = bars + stage * 8, parity = (j / kStages) & 1, tile = ring + stage * L::kTileB;
-        if (!ptx::mbar_try_wait(bar, parity)) alive = wait_slow(bar, parity, a.status);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;  // nothing is issued any more; the copies in flight are waited for below
-        int fk[kTile];
-#pragma unroll
-        for (int i = 0; i < kTile; ++i) fk[i] = firsts[stage * kTile + i];
-
-        // ---- S = q K^T
-        float s[kTile][2][4];
+    // One tile: fk[i] the first key of strip i, -1 if the row sees none of it.  kWhole: the row sees every
+    // key of the four strips (all but a row's last tile, and lists' last blocks).
+    template <bool kWhole>
+    __device__ __forceinline__ void tile(const unsigned char* tile, const int* fk, int pos, int g, int c) {
+        // ---- S: [strip][keys g, g + 8 (narrow) or keys 2 c .. and 8 + 2 c .. (wide)]; s[i][n][2 r + e] in the wide
+        // form is key 8 n + 2 c + e of row r, s[i][n][r] in the narrow one key 8 n + g of row r
+        constexpr int kE = kNarrow ? 2 : 4;
+        float s[kTile][2][kE];
 #pragma unroll
         for (int i = 0; i < kTile; ++i) {
+            const unsigned char* strip = tile + i * S::kStripB;
+            if (!kWhole && fk[i] < 0) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-            if (fk[i] < 0) continue;
-            const uint32_t strip = tile + i * L::kStripB;
+                    for (int e = 0; e < kE; ++e) s[i][n][e] = -INFINITY;
+                continue;
+            }
+            uint32_t kf[2][D / 32][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int key = g + 8 * n;
@@ -332,96 +441,145 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 2) cache_att
                 }
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) {
-                    uint32_t b[4];
-                    unpack8(w[x], b);
-                    const uint32_t scale = sc[x * 2 / (D / 32)];
+                    unpack8(w[x], kf[n][x]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] = hmul2(b[e], scale);
-#pragma unroll
-                    for (int term = 0; term < kTerms; ++term) {
-                        mma(s[i][n], qa[term][2 * x], b[0], b[1]);
-                        mma(s[i][n], qa[term][2 * x + 1], b[2], b[3]);
-                    }
+                    for (int e = 0; e < 4; ++e) kf[n][x][e] = hmul2(kf[n][x][e], sc[x * 2 / (D / 32)]);
                 }
+            }
+            if constexpr (kNarrow) {
+                float d[4];
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t ka[4] = {kf[0][x][2 * y], kf[1][x][2 * y], kf[0][x][2 * y + 1], kf[1][x][2 * y + 1]};
+#pragma unroll
+                        for (int term = 0; term < kTerms; ++term) {
+                            const uint32_t* b = q[term][2 * x + y];
+                            if (x + y + term == 0) mma_zero(d, ka, b[0], b[1]);
+                            else mma(d, ka, b[0], b[1]);
+                        }
+                    }
+                s[i][0][0] = d[0], s[i][0][1] = d[1], s[i][1][0] = d[2], s[i][1][1] = d[3];
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int term = 0; term < kTerms; ++term) {
+                                if (x + y + term == 0) mma_zero(s[i][n], q[0][0], kf[n][0][0], kf[n][0][1]);
+                                else mma(s[i][n], q[term][2 * x + y], kf[n][x][2 * y], kf[n][x][2 * y + 1]);
+                            }
             }
         }
 
-        // ---- logits in base 2, masked; running maximum
-        float top[2] = {-INFINITY, -INFINITY};
+        if constexpr (!kWhole) {
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) {
-            const int seen = fk[i] < 0 ? -1 : row.pos - fk[i];  // the strip's last visible key
+            for (int i = 0; i < kTile; ++i)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = n * 8 + c * 2 + (e & 1);
-                    s[i][n][e] = key <= seen ? s[i][n][e] * rs[e >> 1] : -INFINITY;
-                    top[e >> 1] = fmaxf(top[e >> 1], s[i][n][e]);
-                }
+                    for (int e = 0; e < kE; ++e)
+                        if (fk[i] + n * 8 + (kNarrow ? g : c * 2 + (e & 1)) > pos) s[i][n][e] = -INFINITY;
         }
-        bool moved = false;
-        float base[2];
+
+        // ---- the reference moves when a logit passes it by more than kSlack: first a test without any exchange
+        float top[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            top[r] = fmaxf(top[r], m[r]);
-            moved = moved || top[r] != m[r];
-            base[r] = top[r] == -INFINITY ? 0.f : top[r] - kWeightLog2;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
+            if constexpr (kNarrow) {
+                top[r] = fmaxf(s[0][0][r], s[0][1][r]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float f = top[r] == -INFINITY ? 1.f : ptx::ex2(m[r] - top[r]);
-                l[r] *= f;
-                m[r] = top[r];
+                for (int i = 1; i < kTile; ++i) top[r] = ptx::fmax3(top[r], s[i][0][r], s[i][1][r]);
+            } else {
+                top[r] = fmaxf(s[0][0][2 * r], s[0][0][2 * r + 1]);
 #pragma unroll
-                for (int j2 = 0; j2 < kCh; ++j2) u[j2][2 * r] *= f, u[j2][2 * r + 1] *= f;
+                for (int i = 0; i < kTile; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        if (i + n > 0) top[r] = ptx::fmax3(top[r], s[i][n][2 * r], s[i][n][2 * r + 1]);
             }
         }
+        if (__any_sync(0xffffffffu, top[0] * rs[0] > m[0] + kSlack || top[1] * rs[1] > m[1] + kSlack)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                constexpr int d0 = kNarrow ? 4 : 1, d1 = kNarrow ? 32 : 4;
+#pragma unroll
+                for (int d = d0; d < d1; d *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
+                const float to = top[r] * rs[r];
+                const bool move = to > m[r] + kSlack;
+                const float f = move ? ptx::ex2(m[r] - to) : 1.f;
+                m[r] = move ? to : m[r];
+                l[r].x *= f, l[r].y *= f;
+#pragma unroll
+                for (int j = 0; j < kU; ++j) {
+                    if constexpr (kNarrow) u[j][r] *= f, u[j][2 + r] *= f;
+                    else u[j][2 * r] *= f, u[j][2 * r + 1] *= f;
+                }
+            }
+        }
+        float base[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) base[r] = m[r] == -INFINITY ? 0.f : kWeightLog2 - m[r];
 
         // ---- weights and U += P V
 #pragma unroll
         for (int i = 0; i < kTile; ++i) {
-            if (fk[i] < 0) continue;
-            uint32_t pa[kTerms][4];
+            if (!kWhole && fk[i] < 0) continue;
+            uint32_t pf[kTerms][kNarrow ? 2 : 4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = ptx::ex2(s[i][n][2 * r] - base[r]), p1 = ptx::ex2(s[i][n][2 * r + 1] - base[r]);
-                    l[r] += p0 + p1;
-                    const uint32_t two = pack_f16x2(p0, p1);
-                    pa[0][2 * n + r] = two;
+            for (int n = 0; n < 2; ++n) {
+                if constexpr (kNarrow) {
+                    float2 p = ptx::ffma2(make_float2(s[i][n][0], s[i][n][1]), make_float2(rs[0], rs[1]),
+                                          make_float2(base[0], base[1]));
+                    p.x = ptx::ex2(p.x), p.y = ptx::ex2(p.y);
+                    l[0] = ptx::fadd2(l[0], p);  // (row 0, row 1); l[1] is not used
+                    const uint32_t two = pack_f16x2(p.x, p.y);
+                    pf[0][n] = transpose8x8(two);
                     if constexpr (kTerms == 2) {
                         const float2 b = f16x2_to_f32(two);
-                        pa[1][2 * n + r] = pack_f16x2(p0 - b.x, p1 - b.y);
+                        pf[1][n] = transpose8x8(pack_f16x2(p.x - b.x, p.y - b.y));
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float2 p = ptx::ffma2(make_float2(s[i][n][2 * r], s[i][n][2 * r + 1]),
+                                              make_float2(rs[r], rs[r]), make_float2(base[r], base[r]));
+                        p.x = ptx::ex2(p.x), p.y = ptx::ex2(p.y);
+                        l[r] = ptx::fadd2(l[r], p);
+                        const uint32_t two = pack_f16x2(p.x, p.y);
+                        pf[0][2 * n + r] = two;
+                        if constexpr (kTerms == 2) {
+                            const float2 b = f16x2_to_f32(two);
+                            pf[1][2 * n + r] = pack_f16x2(p.x - b.x, p.y - b.y);
+                        }
                     }
                 }
-            const uint32_t strip = tile + i * L::kStripB;
+            }
+            const unsigned char* strip = tile + i * S::kStripB;
             const int grp = D == 128 ? g : g >> 1;
             uint32_t s0 = e4m3x2_to_f16x2(lds<uint16_t>(strip + 17 * D + grp * 16 + c * 2));
             uint32_t s1 = e4m3x2_to_f16x2(lds<uint16_t>(strip + 17 * D + grp * 16 + c * 2 + 8));
-            const int seen = row.pos - fk[i];
-            if (seen < kStrip - 1) {  // keys behind the position may hold anything
-                const int k0 = c * 2;
+            if constexpr (!kWhole) {  // keys behind the position may hold anything
+                const int k0 = c * 2, seen = pos - fk[i];
                 s0 &= (k0 <= seen ? 0xffffu : 0u) | (k0 + 1 <= seen ? 0xffff0000u : 0u);
                 s1 &= (k0 + 8 <= seen ? 0xffffu : 0u) | (k0 + 9 <= seen ? 0xffff0000u : 0u);
             }
-            // the codes of keys (2c, 2c + 1) and (2c + 8, 2c + 9): kCh / 8 words of each
+            // the codes of keys (2c, 2c + 1) and (2c + 8, 2c + 9): kCh / 8 words of each.  At D = 128 the groups
+            // of a quarter warp meet in the same banks; the second pass costs less than reordering registers.
             uint32_t va[2][2][kCh / 8];
-            if constexpr (D == 128) {
-                // odd groups read their halves in the other order: a quarter warp then meets no bank twice
-                const uint32_t at = strip + 8 * D + g * 128 + c * 16, flip = (g & 1) * 64;
-                const uint4 x = lds<uint4>(at + flip), y = lds<uint4>(at + 64 - flip);
-                const uint4 v0 = flip ? y : x, v1 = flip ? x : y;
-                va[0][0][0] = v0.x, va[0][0][1] = v0.y, va[0][1][0] = v0.z, va[0][1][1] = v0.w;
-                va[1][0][0] = v1.x, va[1][0][1] = v1.y, va[1][1][0] = v1.z, va[1][1][1] = v1.w;
-            } else {
-                const uint32_t at = strip + 8 * D + ((g >> 1) * 16 + c * 2) * 8 + (g & 1) * 4;
-                va[0][0][0] = lds<uint32_t>(at), va[0][1][0] = lds<uint32_t>(at + 8);
-                va[1][0][0] = lds<uint32_t>(at + 64), va[1][1][0] = lds<uint32_t>(at + 72);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if constexpr (D == 128) {
+                    const uint4 v = lds<uint4>(strip + 8 * D + g * 128 + half * 64 + c * 16);
+                    va[half][0][0] = v.x, va[half][0][1] = v.y, va[half][1][0] = v.z, va[half][1][1] = v.w;
+                } else {
+                    const unsigned char* at = strip + 8 * D + ((g >> 1) * 16 + half * 8 + c * 2) * 8 + (g & 1) * 4;
+                    va[half][0][0] = lds<uint32_t>(at), va[half][1][0] = lds<uint32_t>(at + 8);
+                }
             }
 #pragma unroll
             for (int w = 0; w < kCh / 8; ++w) {
@@ -433,214 +591,440 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 2) cache_att
                 unpack8(even, b1[0]);
                 unpack8(odd, b1[1]);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t v0 = hmul2(b0[x & 1][x >> 1], s0), v1 = hmul2(b1[x & 1][x >> 1], s1);
+                for (int x = 0; x < 4; ++x) {  // channels 2 x and 2 x + 1 of the lane's
+                    const uint32_t v[4] = {hmul2(b0[0][x], s0), hmul2(b0[1][x], s0), hmul2(b1[0][x], s1),
+                                           hmul2(b1[1][x], s1)};
 #pragma unroll
-                    for (int term = 0; term < kTerms; ++term) mma(u[w * 8 + x], pa[term], v0, v1);
+                    for (int term = 0; term < kTerms; ++term) {
+                        if constexpr (kNarrow) {
+                            mma(u[w * 4 + x], v, pf[term][0], pf[term][1]);
+                        } else {
+                            mma(u[w * 8 + 2 * x], pf[term], v[0], v[2]);
+                            mma(u[w * 8 + 2 * x + 1], pf[term], v[1], v[3]);
+                        }
+                    }
                 }
             }
         }
+    }
+
+    // Sums of the lane's rows, complete over the warp.
+    __device__ __forceinline__ void totals(float* sum) const {
+        if constexpr (kNarrow) sum[0] = l[0].x, sum[1] = l[0].y;
+        else sum[0] = l[0].x + l[0].y, sum[1] = l[1].x + l[1].y;
+        constexpr int d0 = kNarrow ? 4 : 1, d1 = kNarrow ? 32 : 4;
+#pragma unroll
+        for (int d = d0; d < d1; d *= 2) {
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
+            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], d);
+        }
+    }
+    // The lane's U as runs of kRun consecutive channels: run i of row r begins at channel ch(i).
+    static constexpr int kRun = kNarrow ? kCh : 2 * kCh;
+    static __device__ __forceinline__ int row_at(int r, int g, int c) { return kNarrow ? 2 * c + r : g + 8 * r; }
+    static __device__ __forceinline__ int ch_at(int g, int c) { return kNarrow ? g * kCh : c * 2 * kCh; }
+    __device__ __forceinline__ float at(int r, int i) const {  // i-th channel of the run
+        if constexpr (kNarrow) return u[i / 2][(i & 1) * 2 + r];
+        else return u[i % kCh][2 * r + i / kCh];
+    }
+};
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.f ? -INFINITY : (m - kWeightLog2 + log2f(l)) * kLn2;
+}
+// Four channels of a finished row.
+template <int D, typename T>
+__device__ __forceinline__ void write_out(const CacheAttn& a, const Where& w, int r, int ch, float4 x, float m, float l) {
+    if (r >= w.heads) return;
+    const long long at = (long long)w.t * a.HQ + w.hq0 + r;
+    const float f = l == 0.f ? 0.f : (a.v_scale ? a.v_scale[w.h] : 1.f) / l;
+    T v[4] = {from_f32<T>(x.x * f), from_f32<T>(x.y * f), from_f32<T>(x.z * f), from_f32<T>(x.w * f)};
+    T* o = static_cast<T*>(a.out) + at * D + ch;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(v);
+    else *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(v);
+    if (a.lse && ch == 0) a.lse[at] = lse_of(m, l);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D, typename T, bool kNarrow>
+__global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAttn a, Plan p) {
+    using S = Shape<D, T, kNarrow>;
+    using P = Part<D, T, kNarrow>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t full = sbase + S::kFull + warp * kStages * 8;
+    int* meta = reinterpret_cast<int*>(smem + S::kMeta) + warp * kStages * 8;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(full + i * 8, 1);
+        ptx::fence_mbar_init();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+
+    const int warps = gridDim.x * kWarps, id = blockIdx.x * kWarps + warp;
+    Ahead ahead;
+    long long run_hi = 0, total = 0;
+    // the next tile; a row that the run begins and does not end is told to the join: it has a part in every warp
+    // up to the one that holds its last tile, tile x being the last warp b's with total b / warps < x + 1
+    auto advance = [&] {
+        ahead.next(a, p, lane, sizeof(T));
+        if (ahead.opened) {
+            const long long end = run_hi - ahead.opened + ahead.n;
+            if (lane == 0) p.begun[id] = make_int2(ahead.row, (int)((end * warps + total - 1) / total) - id);
+            ahead.opened = 0;
+        }
+    };
+    if (p.mode == kStream) {
+        asm volatile("griddepcontrol.launch_dependents;");
+        find_start(a, p, reinterpret_cast<int*>(smem), warps, id, ahead, run_hi, total);
+        run_hi += ahead.left;
+        if (lane == 0) p.begun[id] = make_int2(-1, 0);
+        if (ahead.left == 0 && lane < S::kRows)  // an empty run inside a row that is cut around it
+            p.ml[(long long)id * 2 * S::kRows + lane] = make_float2(-INFINITY, 0.f);
+        advance();
+    } else if (p.mode == kRows) {
+        ahead.next_row = (int)((long long)p.rows * id / warps);
+        ahead.left = (int)((long long)p.rows * (id + 1) / warps) - ahead.next_row;
+        advance();
+    } else {
+        ahead.next_row = blockIdx.x / p.splits;
+        const Where w = where(a, p, ahead.next_row);
+        const Row r = row_of(a, w.t, w.h, tid == 0);
+        const int n = tiles_of(r, p), part = blockIdx.x % p.splits * kWarps + warp, parts = p.splits * kWarps;
+        if (n == 0) return;  // a padding row: the whole cluster leaves
+        ahead.first_tile = (int)((long long)n * part / parts);
+        ahead.left = (int)((long long)n * (part + 1) / parts) - ahead.first_tile;
+        if (ahead.left > 0) advance();
+    }
+
+    auto issue = [&](int stage) {
+        const bool mine = (lane >> 2) == ahead.at;
+        int first = mine ? ahead.first : -1;
+        if (first >= 0 && (unsigned)ahead.page >= (unsigned)a.n_pages) {
+            raise_status(a.status, BSA_ERR_INDEX);
+            first = -1;
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, first >= 0);
+        int* mt = meta + stage * 8;
+        if (mine) mt[lane & 3] = first;
+        if (lane == 0) {
+            mt[4] = ahead.row, mt[5] = ahead.r.pos, mt[6] = ahead.flags();
+            ptx::mbar_arrive_expect_tx(full + stage * 8, __popc(live) * S::kStripB);
+        }
         __syncwarp();
-        const int jn = j + kStages;
-        if (jn < mine) {
-            if ((jn & 7) == 0) first = next_first, place = next_place;
-            issue(jn);
-            if ((jn & 7) == 4) resolve((jn >> 3) + 1, next_first, next_place);
+        if (first >= 0) {
+            const int strip = ((ahead.page * a.H + ahead.h) << (a.sh - 4)) + ((first & ((1 << a.sh) - 1)) >> 4);
+            bulk_copy(sbase + (warp * kStages + stage) * S::kTileB + (lane & 3) * S::kStripB,
+                      a.cache + (long long)strip * S::kStripB, S::kStripB, full + stage * 8);
+        }
+    };
+
+    P part;
+    part.reset();
+    int issued = 0;
+    bool alive = true;
+    while (issued < kStages && ahead.have) {
+        issue(issued++);
+        advance();
+    }
+    for (int n = 0, stage = 0, parity = 0; n < issued; ++n) {
+        if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;  // nothing more is issued; the copies in flight are waited for below
+        const int4 fk4 = *reinterpret_cast<const int4*>(meta + stage * 8);
+        const int4 tag = *reinterpret_cast<const int4*>(meta + stage * 8 + 4);  // row, position, flags
+        const int fk[kTile] = {fk4.x, fk4.y, fk4.z, fk4.w};
+        if (tag.z & kBegin) {
+            part.reset();
+            part.load_q(a, p, tag.x, g, c);
+        }
+        const unsigned char* tile = smem + (warp * kStages + stage) * S::kTileB;
+        const int least = min(min(fk4.x, fk4.y), min(fk4.z, fk4.w)), most = max(max(fk4.x, fk4.y), max(fk4.z, fk4.w));
+        if (least >= 0 && most + kStrip - 1 <= tag.y) part.template tile<true>(tile, fk, tag.y, g, c);
+        else if (most >= 0) part.template tile<false>(tile, fk, tag.y, g, c);
+        __syncwarp();
+        if (ahead.have) {
+            issue(stage);
+            ++issued;
+            advance();
+        }
+        if (++stage == kStages) stage = 0, parity ^= 1;
+        if ((tag.z & kEnd) && p.mode != kSplit) {
+            float sum[2];
+            part.totals(sum);
+            const Where w = where(a, p, tag.x);
+            const float vs = a.v_scale ? a.v_scale[w.h] : 1.f;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = P::row_at(r, g, c), ch = P::ch_at(g, c);
+                const bool owner = kNarrow ? g == 0 : c == 0;
+                if (tag.z & kCut) {
+                    const long long to = ((long long)id * 2 + (tag.z & kCarried ? 0 : 1)) * S::kRows + row;
+                    if (owner) p.ml[to] = make_float2(part.m[r], sum[r]);
+#pragma unroll
+                    for (int i = 0; i < P::kRun; i += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = part.at(r, i + k);
+                        ptx::st_global_v8(p.part + to * D + ch + i, reinterpret_cast<const uint32_t*>(v));
+                    }
+                } else if (row < w.heads) {
+                    const long long to = (long long)w.t * a.HQ + w.hq0 + row;
+                    const float f = sum[r] == 0.f ? 0.f : vs / sum[r];
+                    T* o = static_cast<T*>(a.out) + to * D + ch;
+#pragma unroll
+                    for (int i = 0; i < P::kRun; i += 16 / (int)sizeof(T)) {
+                        T v[16 / sizeof(T)];
+#pragma unroll
+                        for (int k = 0; k < 16 / (int)sizeof(T); ++k) v[k] = from_f32<T>(part.at(r, i + k) * f);
+                        *reinterpret_cast<uint4*>(o + i) = *reinterpret_cast<const uint4*>(v);
+                    }
+                    if (a.lse && owner) a.lse[to] = lse_of(part.m[r], sum[r]);
+                }
+            }
         }
     }
     if (!alive)  // bounded too: let the copies of the ring land before the memory is given up
-        for (int s = 0; s < kStages; ++s) wait_slow(bars + s * 8, 0, a.status), wait_slow(bars + s * 8, 1, a.status);
+        for (int i = 0; i < kStages; ++i) wait_slow(full + i * 8, 0, a.status), wait_slow(full + i * 8, 1, a.status);
+    if (p.mode != kSplit) return;
 
-    // ---- merge the warps
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    float2* ml = reinterpret_cast<float2*>(smem + L::kML);
+    // ---- kSplit: join the CTA's warps, then the cluster's CTAs
     float* U = reinterpret_cast<float*>(smem);
-    if (c == 0) {
-        ml[warp * 16 + g] = make_float2(m[0], l[0]);
-        ml[warp * 16 + g + 8] = make_float2(m[1], l[1]);
-    }
-    __syncthreads();  // every warp is done with its ring
-    float cm[2], cl[2];
+    float2* ml = reinterpret_cast<float2*>(smem + S::kML);
+    float2* cml = reinterpret_cast<float2*>(smem + S::kCML);
+    float sum[2];
+    part.totals(sum);
+    const bool owner = kNarrow ? g == 0 : c == 0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        if (owner) ml[warp * S::kRows + P::row_at(r, g, c)] = make_float2(part.m[r], sum[r]);
+    __syncthreads();  // also: every warp is done with its ring
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        float2 w[kWarps];
-        cm[r] = -INFINITY, cl[r] = 0.f;
+        const int row = P::row_at(r, g, c), ch = P::ch_at(g, c);
+        float cm = -INFINITY, cl = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            w[k] = ml[k * 16 + g + 8 * r];
-            cm[r] = fmaxf(cm[r], w[k].x);
-        }
+        for (int k = 0; k < kWarps; ++k) cm = fmaxf(cm, ml[k * S::kRows + row].x);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) cl[r] += w[k].y * weight_of(w[k], cm[r]);
-        const float f = weight_of(make_float2(m[r], l[r]), cm[r]);
-        float* dst = U + warp * 16 * L::kRow;
+        for (int k = 0; k < kWarps; ++k) cl += ml[k * S::kRows + row].y * weight_of(ml[k * S::kRows + row], cm);
+        if (warp == 0 && owner) cml[row] = make_float2(cm, cl);
+        const float f = weight_of(make_float2(part.m[r], sum[r]), cm);
+        float* dst = U + warp * S::kRows * S::kRowF;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < kCh / 4; ++i) {
-                float4 v;
-                v.x = u[4 * i][2 * r + e] * f, v.y = u[4 * i + 1][2 * r + e] * f;
-                v.z = u[4 * i + 2][2 * r + e] * f, v.w = u[4 * i + 3][2 * r + e] * f;
-                *reinterpret_cast<float4*>(dst + L::at(g + 8 * r, (2 * c + e) * kCh + 4 * i)) = v;
-            }
+        for (int i = 0; i < P::kRun; i += 4)
+            *reinterpret_cast<float4*>(dst + S::at(row, ch + i)) =
+                make_float4(part.at(r, i) * f, part.at(r, i + 1) * f, part.at(r, i + 2) * f, part.at(r, i + 3) * f);
     }
     __syncthreads();
-    if (warp == 0 && c == 0) {
-        ml[g] = make_float2(cm[0], cl[0]);
-        ml[g + 8] = make_float2(cm[1], cl[1]);
-    }
-    const int csize = sp.splits / sp.clusters;
-    const uint32_t rank = csize > 1 ? cluster_rank() : 0;
-    constexpr int kVecs = 16 * D / 4;  // float4s of U
-    if (csize > 1) {
-        // the CTA's sum into the first warp's rows, where the others of the cluster read it
-#pragma unroll
-        for (int v = tid; v < kVecs; v += kWarps * 32) {
-            float4* p = reinterpret_cast<float4*>(U + L::at(v / (D / 4), v % (D / 4) * 4));
-            float4 x = p[0];
-#pragma unroll
-            for (int k = 1; k < kWarps; ++k) {
-                const float4 y = p[k * 4 * L::kRow];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            }
-            p[0] = x;
-        }
-        cluster_sync();
-    } else {
-        __syncthreads();
-    }
-    const float vs = a.v_scale ? a.v_scale[h] : 1.f;
-    const int cl_id = split / csize;
-    for (int v = rank * (kVecs / csize) + tid; v < (int)(rank + 1) * (kVecs / csize); v += kWarps * 32) {
+    const Where w = where(a, p, blockIdx.x / p.splits);
+    for (int v = tid; v < S::kRows * D / 4; v += kWarps * 32) {
         const int r = v / (D / 4), ch = v % (D / 4) * 4;
+        float4* src = reinterpret_cast<float4*>(U + S::at(r, ch));
+        float4 x = src[0];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) {
+            const float4 y = src[k * S::kRows * S::kRowF / 4];
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        if (p.splits > 1) src[0] = x;
+        else write_out<D, T>(a, w, r, ch, x, cml[r].x, cml[r].y);
+    }
+    if (p.splits == 1) return;
+    cluster_sync();
+    const int rank = (int)cluster_rank(), share = S::kRows * D / 4 / p.splits;
+    for (int v = rank * share + tid; v < (rank + 1) * share; v += kWarps * 32) {
+        const int r = v / (D / 4), ch = v % (D / 4) * 4;
+        const uint32_t at_ml = sbase + S::kCML + r * 8, at_u = sbase + S::at(r, ch) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm = -INFINITY, ll = 0.f;
-        if (csize > 1) {
-            const uint32_t mine_ml = sbase + L::kML + r * 8, mine_u = sbase + L::at(r, ch) * 4;
-            for (int k = 0; k < csize; ++k) mm = fmaxf(mm, ld_cluster2(at_rank(mine_ml, k)).x);
-            for (int k = 0; k < csize; ++k) {
-                const float2 w = ld_cluster2(at_rank(mine_ml, k));
-                const float f = weight_of(w, mm);
-                const float4 y = ld_cluster4(at_rank(mine_u, k));
-                ll += w.y * f;
-                x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
-            }
-        } else {
-            mm = ml[r].x, ll = ml[r].y;
-            const float4* p = reinterpret_cast<const float4*>(U + L::at(r, ch));
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float4 y = p[k * 4 * L::kRow];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            }
+        for (int k = 0; k < p.splits; ++k) mm = fmaxf(mm, ld_cluster2(at_rank(at_ml, k)).x);
+        for (int k = 0; k < p.splits; ++k) {
+            const float2 y = ld_cluster2(at_rank(at_ml, k));
+            const float f = weight_of(y, mm);
+            const float4 z = ld_cluster4(at_rank(at_u, k));
+            ll += y.y * f;
+            x.x += z.x * f, x.y += z.y * f, x.z += z.z * f, x.w += z.w * f;
         }
-        if (sp.clusters > 1) {
-            const long long at = ((long long)row_tile * sp.clusters + cl_id) * 16 + r;
-            *reinterpret_cast<float4*>(sp.part + at * D + ch) = x;
-            if (ch == 0) sp.ml[at] = make_float2(mm, ll);
-        } else if (r < heads) {
-            const long long at = (long long)t * a.HQ + hq0 + r;
-            const float f = ll == 0.f ? 0.f : vs / ll;
-            T* o = static_cast<T*>(a.out) + at * D + ch;
-            o[0] = from_f32<T>(x.x * f), o[1] = from_f32<T>(x.y * f);
-            o[2] = from_f32<T>(x.z * f), o[3] = from_f32<T>(x.w * f);
-            if (a.lse && ch == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm - kWeightLog2 + log2f(ll)) * kLn2;
-        }
+        write_out<D, T>(a, w, r, ch, x, mm, ll);
     }
-    if (csize > 1) cluster_sync();  // nobody leaves while others read its shared memory
+    cluster_sync();  // nobody leaves while others read its shared memory
 }
 
-// The rows' clusters joined: a warp per query head.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) cache_attn_join_kernel(CacheAttn a, Split sp) {
-    const int lane = threadIdx.x & 31, G = a.HQ / a.H;
-    const long long head = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (head >= (long long)a.T * a.HQ) return;
-    const int t = (int)(head / a.HQ), hq = (int)(head % a.HQ), h = hq / G, in = hq % G;
-    if (a.req[t] < 0 || a.req[t] >= a.R) return;
-    const long long at = (((long long)t * a.H + h) * sp.head_tiles + in / 16) * sp.clusters * 16 + in % 16;
-    constexpr int kPer = D / 32;
-    float mm = -INFINITY, ll = 0.f, x[kPer] = {};
-    for (int k = 0; k < sp.clusters; ++k) mm = fmaxf(mm, sp.ml[at + k * 16].x);
-    for (int k = 0; k < sp.clusters; ++k) {
-        const float2 w = sp.ml[at + k * 16];
-        const float f = weight_of(w, mm);
+// Joins the parts of the row that a warp of the stream began: its own and the following warps'.
+// A block takes 1 / gridDim.y of the row's heads; 512 / (D / 4 * heads) threads share the parts of four channels.
+template <int D, typename T, bool kNarrow>
+__global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan p) {
+    constexpr int kRows = Shape<D, T, kNarrow>::kRows, kVec = D / 4;
+    __shared__ float4 xs[512];
+    __shared__ float2 mls[512];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the stream's kernel still runs
+    const int2 begun = p.begun[blockIdx.x];
+    if (begun.x < 0) return;
+    const int heads = kRows / gridDim.y, lanes = 512 / kVec / heads;
+    const int v = threadIdx.x % kVec, r = threadIdx.x / kVec % heads, part = threadIdx.x / kVec / heads;
+    const int row = blockIdx.y * heads + r;
+    auto slot = [&](int k) { return ((long long)(blockIdx.x + k) * 2 + (k == 0)) * kRows + row; };
+    float mm = -INFINITY, ll = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = part; k0 < begun.y; k0 += 4 * lanes) {  // four parts' loads at a time
+        float2 w[4];
+        float4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = k0 + i * lanes;
+            w[i] = make_float2(-INFINITY, 0.f);
+            y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < begun.y) {
+                w[i] = p.ml[slot(k)];
+                y[i] = *reinterpret_cast<const float4*>(p.part + slot(k) * D + v * 4);
+            }
+        }
+        float top = fmaxf(fmaxf(mm, fmaxf(w[0].x, w[1].x)), fmaxf(w[2].x, w[3].x));
+        const float keep = weight_of(make_float2(mm, ll), top);
+        mm = top, ll *= keep;
+        x.x *= keep, x.y *= keep, x.z *= keep, x.w *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = weight_of(w[i], top);
+            ll += w[i].y * f;
+            if (f != 0.f) x.x += y[i].x * f, x.y += y[i].y * f, x.z += y[i].z * f, x.w += y[i].w * f;  // else no part: memory of no meaning
+        }
+    }
+    if (lanes == 1) {
+        write_out<D, T>(a, where(a, p, begun.x), row, v * 4, x, mm, ll);
+        return;
+    }
+    xs[threadIdx.x] = x;
+    mls[threadIdx.x] = make_float2(mm, ll);
+    __syncthreads();
+    if (part > 0) return;
+    const int step = kVec * heads;
+    float top = -INFINITY;
+    for (int k = 0; k < lanes; ++k) top = fmaxf(top, mls[threadIdx.x + k * step].x);
+    ll = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < lanes; ++k) {
+        const float2 w = mls[threadIdx.x + k * step];
+        const float4 y = xs[threadIdx.x + k * step];
+        const float f = weight_of(w, top);
         ll += w.y * f;
-        const float* p = sp.part + (at + k * 16) * D + lane * kPer;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] += p[i] * f;
+        x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
     }
-    const float f = ll == 0.f ? 0.f : (a.v_scale ? a.v_scale[h] : 1.f) / ll;
-    T* o = static_cast<T*>(a.out) + head * D + lane * kPer;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = from_f32<T>(x[i] * f);
-    if (a.lse && lane == 0) a.lse[head] = ll == 0.f ? -INFINITY : (mm - kWeightLog2 + log2f(ll)) * kLn2;
+    write_out<D, T>(a, where(a, p, begun.x), row, v * 4, x, top, ll);
 }
 
-constexpr int kSlots = 152 * 3;  // CTAs resident at once
+// ---------------------------------------------------------------- host
 
-// How a row is cut, from the sizes that the host knows.
-void plan(int T, int HQ, int H, long long max_keys, int* head_tiles, int* cluster, int* clusters) {
-    *head_tiles = (HQ / H + 15) / 16;
-    const long long rows = (long long)T * H * *head_tiles;
-    const long long tiles = (max_keys + kTile * kStrip - 1) / (kTile * kStrip);
-    const long long most = std::max<long long>(1, (tiles + kWarps - 1) / kWarps);  // a tile for every warp at least
-    const long long want = std::min(most, std::max<long long>(1, kSlots / std::max<long long>(rows, 1)));
-    int c = 1;
-    while (c < 8 && 2 * c <= want) c *= 2;
-    *cluster = c;
-    *clusters = (int)(want / c);
+constexpr int kSms = 152, kGrid = 2 * kSms;  // two CTAs an SM
+
+template <typename F>
+bool once_per_device(F f) {  // f(): whether it succeeded; called until it has, for each device
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return f();
+    if (done.load(std::memory_order_acquire) >> dev & 1) return true;
+    if (!f()) return false;
+    done.fetch_or(1ull << dev, std::memory_order_acq_rel);
+    return true;
 }
 
-template <int D, typename T>
-bsa_status launch(const CacheAttn& a, Split sp, int cluster, cudaStream_t st) {
-    using L = Layout<D>;
-    auto kern = cache_attn_mma_kernel<D, T>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    if (e != cudaSuccess) return fail(BSA_ERR_CUDA, "cache_attn_mma_kernel: %s", cudaGetErrorString(e));
+struct Sizes {
+    Plan plan;
+    int grid;
+    size_t part, ml, begun;  // workspace bytes
+};
+
+// How the work is cut, from the sizes that the host knows.
+Sizes cut(int T, int HQ, int H, int D, bool lists, long long max_keys) {
+    Sizes z = {};
+    Plan& p = z.plan;
+    const int G = HQ / H;
+    p.head_tiles = (G + 15) / 16;
+    const long long rows = (long long)T * H * p.head_tiles;
+    p.rows = (int)std::min<long long>(rows, 0x7fffffff);
+    p.tile_strips = kTile;
+    const long long strips = (max_keys + kStrip - 1) / kStrip, tiles = (strips + kTile - 1) / kTile;
+    if (rows * tiles <= kWarps * kGrid || (rows <= kGrid && strips <= 16)) {
+        // at most about a tile for every warp of the GPU: spread the strips over a cluster
+        p.mode = kSplit;
+        int s = 1;
+        while (s < 8 && rows * s * 2 <= kGrid && strips > kWarps * s) s *= 2;
+        p.splits = s;
+        while (p.tile_strips > 1 && strips <= (long long)s * kWarps * (p.tile_strips / 2)) p.tile_strips /= 2;
+        z.grid = (int)(rows * s);
+        return z;
+    }
+    const long long groups = lists ? (long long)T * H : T;
+    p.mode = groups <= kScanGroups && rows * (tiles + 1) <= 0x7fffffffLL ? kStream : kRows;
+    z.grid = kGrid;
+    if (p.mode == kStream) {
+        const size_t slots = (size_t)kGrid * kWarps * 2 * (G <= 8 ? 8 : 16);
+        z.part = slots * D * sizeof(float);
+        z.ml = slots * sizeof(float2);
+        z.begun = (size_t)kGrid * kWarps * sizeof(int2);
+    }
+    return z;
+}
+
+template <int D, typename T, bool kNarrow>
+bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
+    using S = Shape<D, T, kNarrow>;
+    auto kern = cache_attn_mma_kernel<D, T, kNarrow>;
+    if (!once_per_device([&] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) == cudaSuccess;
+        }))
+        return check_launch("cache_attn_mma_kernel: shared memory");
+    const Plan& p = z.plan;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.T * a.H * sp.head_tiles * sp.splits));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.gridDim = dim3((unsigned)z.grid);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.x = p.mode == kSplit ? p.splits : 1;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, kern, a, sp);
+    cfg.numAttrs = attr.val.clusterDim.x > 1 ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kern, a, p);
     bsa_status rc = check_launch("cache_attn_mma_kernel");
-    if (rc != BSA_OK || sp.clusters == 1) return rc;
-    const long long heads = (long long)a.T * a.HQ;
-    cache_attn_join_kernel<D, T><<<(unsigned)((heads + 3) / 4), 128, 0, st>>>(a, sp);
+    if (rc != BSA_OK || p.mode != kStream) return rc;
+    // parts of a row: about the warps per row; blocks take fewer heads, and share out the parts, where they are many
+    const int warps = kGrid * kWarps, parts = warps / p.rows;
+    const int fold = parts <= 4 ? 1 : parts <= 32 ? 4 : S::kRows;
+    cfg.gridDim = dim3(warps, fold);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 0;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, T, kNarrow>, a, p);
     return check_launch("cache_attn_join_kernel");
 }
 
 }  // namespace
 
 size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_keys) {
-    int head_tiles, cluster, clusters;
-    plan(T, HQ, H, max_keys, &head_tiles, &cluster, &clusters);
-    return clusters == 1 ? 0 : (size_t)T * H * head_tiles * clusters * 16 * (D + 2) * sizeof(float);
+    // with and without lists: the larger (a workspace is asked for before the lists are)
+    const Sizes x = cut(T, HQ, H, D, false, max_keys), y = cut(T, HQ, H, D, true, max_keys);
+    return std::max(x.part + x.ml + x.begun, y.part + y.ml + y.begun);
 }
 
 bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
                                cudaStream_t st) {
-    Split sp;
-    int cluster;
-    plan(a.T, a.HQ, a.H, max_keys, &sp.head_tiles, &cluster, &sp.clusters);
-    sp.splits = cluster * sp.clusters;
-    const long long rows = (long long)a.T * a.H * sp.head_tiles;
-    if (rows * sp.splits > 0x7fffffffLL) return fail(BSA_ERR_UNSUPPORTED, "cache attention: too many (token, head) rows");
-    sp.part = static_cast<float*>(workspace);
-    sp.ml = reinterpret_cast<float2*>(sp.part + (sp.clusters > 1 ? rows * sp.clusters * 16 * a.D : 0));
-    if (dtype == BSA_F32) return a.D == 128 ? launch<128, float>(a, sp, cluster, st) : launch<64, float>(a, sp, cluster, st);
-    return a.D == 128 ? launch<128, __nv_bfloat16>(a, sp, cluster, st) : launch<64, __nv_bfloat16>(a, sp, cluster, st);
+    if ((long long)a.T * a.H * ((a.HQ / a.H + 15) / 16) > 0x7fffffffLL)
+        return fail(BSA_ERR_UNSUPPORTED, "cache attention: too many (token, head) rows");
+    Sizes z = cut(a.T, a.HQ, a.H, a.D, a.blocks != nullptr, max_keys);
+    char* ws = static_cast<char*>(workspace);
+    z.plan.part = reinterpret_cast<float*>(ws);
+    z.plan.ml = reinterpret_cast<float2*>(ws + z.part);
+    z.plan.begun = reinterpret_cast<int2*>(ws + z.part + z.ml);
+    const bool narrow = a.HQ / a.H <= 8;
+#define BSA_CACHE_ATTN(D_, T_) (narrow ? launch<D_, T_, true>(a, z, st) : launch<D_, T_, false>(a, z, st))
+    if (dtype == BSA_F32) return a.D == 128 ? BSA_CACHE_ATTN(128, float) : BSA_CACHE_ATTN(64, float);
+    return a.D == 128 ? BSA_CACHE_ATTN(128, __nv_bfloat16) : BSA_CACHE_ATTN(64, __nv_bfloat16);
+#undef BSA_CACHE_ATTN
 }
 
 }  // namespace bsa

@@ -487,8 +487,9 @@ bsa_status bsa_permute_rows(const void* src, void* dst, bsa_dtype dtype, int BH,
  * [max_tokens] hold each token's request, position and slot, and -1 behind the
  * last (so a captured step of fixed size can run a smaller batch).
  * All pointers [device]; slots is int64, the rest int32.  block_table and pool
- * must not overlap the other arrays.  workspace: bsa_cache_tables_workspace(R)
- * bytes, its contents meaningless between calls.
+ * must not overlap the other arrays.  workspace: bsa_cache_tables_workspace
+ * bytes (0 for a small step: then it may be NULL), its contents meaningless
+ * between calls.
  * A call that cannot be carried out changes neither table, pool nor count,
  * writes zeros to query_start, -1 to the token arrays and old_lens to new_lens
  * (which therefore always holds the lengths that the tables are for), and latches
@@ -497,7 +498,7 @@ bsa_status bsa_permute_rows(const void* src, void* dst, bsa_dtype dtype, int BH,
  * the pool).  A page id outside [0, n_pages) met on the way latches
  * BSA_ERR_INDEX and gives the slot -1. */
 size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D);
-size_t bsa_cache_tables_workspace(int R);
+size_t bsa_cache_tables_workspace(int R, int max_tokens);
 bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
                             int32_t* block_table, int max_pages, int32_t* pool, int n_pages,
                             const int32_t* pool_count, int32_t* pool_count_out, int32_t* query_start,
@@ -541,12 +542,13 @@ bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T
  * padding, the second as an empty row).
  * Cache bytes of keys that no row sees are not looked at: they may be anything.
  * q: [device] [T, HQ, D] of `dtype`, tokens q_stride elements apart; out: [device]
- * contiguous [T, HQ, D] of `dtype`; lse: [device] float [T, HQ] or NULL.
+ * contiguous [T, HQ, D] of `dtype`, 16-byte aligned as the cache is; lse:
+ * [device] float [T, HQ] or NULL.
  * block_table: [device] int32 [R, max_pages]; token_req, token_pos: [device]
  * int32 [T]; block_indices: [device] int32 [T, H, S], block_counts: [device]
  * int32 [T, H], or both NULL for every key.  block_size: a multiple of 16.
  * D a multiple of 16 up to 128.
- * workspace: [device] bsa_cache_attention_workspace bytes, 16-byte aligned, its
+ * workspace: [device] bsa_cache_attention_workspace bytes, 32-byte aligned, its
  * contents meaningless between calls; max_keys is the most keys that a row can
  * see: S * block_size with lists, else max_pages * page_size. */
 size_t bsa_cache_attention_workspace(int T, int HQ, int H, int D, int max_keys);

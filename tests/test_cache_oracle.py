@@ -175,7 +175,7 @@ APPEND = dict(k=16, v=16, dtype=1, T=4, H=2, D=128, ks=256, vs=256, slots=16, ca
               v_scale=None, k_val=None, v_val=None, stream=None)
 ATTEND = dict(q=16, dtype=1, T=4, HQ=8, H=2, D=128, qs=1024, cache=16, n_pages=4, P=64, table=16, R=2, max_pages=4,
               req=16, pos=16, k_scale=None, v_scale=None, idx=16, cnt=16, S=4, BS=64, scale=0.1, out=16, lse=None,
-              ws=16, ws_bytes=1 << 40, stream=None)
+              ws=32, ws_bytes=1 << 40, stream=None)
 
 
 @pytest.mark.parametrize("change,word", [
@@ -184,7 +184,8 @@ ATTEND = dict(q=16, dtype=1, T=4, HQ=8, H=2, D=128, qs=1024, cache=16, n_pages=4
     (dict(max_tokens=(1 << 30) + 1), "sizes"),
     (dict(P=48), "power of two"), (dict(P=8), "power of two"), (dict(P=2048), "power of two"),
     (dict(R=1 << 16, max_pages=1 << 15), "2^31"), (dict(max_pages=1 << 26, R=1), "2^31"),
-    (dict(ws=None), "workspace"), (dict(ws_bytes=(8 + 2 * 5) * 4 - 1), "workspace"), (dict(ws=18), "workspace"),
+    (dict(ws=None, max_tokens=5000), "workspace"), (dict(ws_bytes=(8 + 2 * 5) * 4 - 1, max_tokens=5000), "workspace"),
+    (dict(ws=18, max_tokens=5000), "workspace"), (dict(ws=None, R=1025), "workspace"),
 ])
 def test_tables_refusals(bsa, change, word):
     assert bsa._lib.bsa_cache_tables(*_args(TABLES, **change)) == bsa.BSA_ERR_INVALID_ARG
@@ -206,11 +207,11 @@ def test_append_refusals(bsa, change, word):
     (dict(q=None), "null", 1), (dict(pos=None), "null", 1), (dict(out=None), "null", 1), (dict(dtype=2), "dtype", 1),
     (dict(HQ=7), "sizes", 1), (dict(T=-1), "sizes", 1), (dict(R=0), "sizes", 1), (dict(P=24), "power of two", 1),
     (dict(D=8), "multiple of 16", 1), (dict(D=256), "multiple of 16", 1), (dict(qs=1023), "stride", 1),
-    (dict(cache=17), "aligned", 1), (dict(idx=None), "together", 1), (dict(cnt=None), "together", 1),
+    (dict(cache=17), "aligned", 1), (dict(out=24), "aligned", 1), (dict(idx=None), "together", 1), (dict(cnt=None), "together", 1),
     (dict(S=0), "block lists", 1), (dict(BS=0), "block lists", 1), (dict(S=1 << 20, BS=1 << 12), "block lists", 1),
     (dict(max_pages=1 << 26), "2^31", 1), (dict(BS=24), "multiple of 16", 2), (dict(n_pages=1 << 29), "strips", 1),
     (dict(ws=None, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
-    (dict(ws=24, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
+    (dict(ws=16, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
     (dict(ws_bytes=64, idx=None, cnt=None, max_pages=1 << 12), "workspace", 1),
 ])
 def test_attention_refusals(bsa, change, word, status):
@@ -228,7 +229,7 @@ def test_sizes(bsa):
     assert bsa.bsa_cache_bytes(1 << 20, 8, 128, 128) == (1 << 20) * 8 * 8 * 2304  # past 32 bits
     for bad in ((0, 1, 64, 128), (1, 1, 24, 128), (1, 1, 64, 100), (1, 1, 64, 256)):
         assert bsa.bsa_cache_bytes(*bad) == 0
-    assert bsa.bsa_cache_tables_workspace(4) == (8 + 2 * 5) * 4
+    assert bsa.bsa_cache_tables_workspace(4, 5000) == (8 + 2 * 5) * 4 and bsa.bsa_cache_tables_workspace(4, 4096) == 0
 
 
 def test_binding_refuses_tensors_that_do_not_fit(bsa):

@@ -7,9 +7,10 @@ Tolerances, from the arithmetic (u = half a step relative to the value):
   - a float32 logit is off by at most (D + 8) 2^-24 B from its sum and 2^-22 B from q in two float16 parts (bf16 q
     is exact in one), so a weight by twice that, and by 2^-22 from exp2;
   - a weight is held in float16 (u = 2^-11) for bf16 outputs, in two float16 parts (2^-22) for float32 ones;
-  - float16's smallest step is 2^-24 and the tensor-core kernel holds 2^15 times each weight (relative to the row's
-    largest, itself at most 1), so no weight is held closer than half a step, 2^-25 2^-15 = 2^-40: F = 2^-40 sum_j
-    |v_j| more per channel (found where a row's only large weight meets a zero of V: o ~ 1e-21 there, A no larger);
+  - float16's smallest step is 2^-24 and the tensor-core kernel holds 2^11 times each weight relative to a reference
+    that is never above the row's largest logit, so no weight (the largest is at most 1) is held closer than half a
+    step, 2^-25 2^-11 = 2^-36: F = 2^-36 sum_j |v_j| more per channel (it shows where a row's only large weight meets
+    a zero of V: o ~ 1e-21 there, and A no larger);
   - sums over n keys add n 2^-24; the output's own rounding is u = 2^-8 |o| (bf16), 2^-24 |o| (float32).
   LSE: the logit's error, n 2^-24 + 2^-22 for the sum, 2^-24 |lse| for its rounding."""
 
@@ -361,7 +362,7 @@ def want_attend(c, scale=None):
                 x = K @ q[t, r] * scale
                 p = np.exp(x - lse[t, r])
                 A[t, r] = p @ np.abs(V)
-                F[t, r] = 2.0 ** -40 * np.abs(V).sum(0)
+                F[t, r] = 2.0 ** -36 * np.abs(V).sum(0)
                 B[t, r] = (np.abs(K) @ np.abs(q[t, r])).max() * abs(scale)
                 n[t, r] = len(keys)
     logit = B * ((D + 8) * 2.0 ** -24 + 2.0 ** -22)
