@@ -5,7 +5,7 @@
 // copies its tiles into a ring of its own (one bulk copy per strip), keeps its own running
 // maximum, sum and output, and goes on to its next row without waiting for anyone, the first
 // tiles of which are in flight by then.  Which tiles a warp takes:
-//   stream  two CTAs of four warps an SM, every warp an equal run of the rows' tiles laid end to
+//   stream  two or three CTAs of four warps an SM, every warp an equal run of the rows' tiles laid end to
 //           end (so a batch of ragged lengths is balanced to a tile); a row that is cut leaves
 //           parts (m, l, U) in the workspace, and a second kernel joins them:
 //             m = max m_i,   l = sum l_i 2^(m_i - m),   U = sum U_i 2^(m_i - m),   O = U / l;
@@ -47,7 +47,6 @@ namespace {
 
 constexpr int kWarps = 4;    // of a CTA
 constexpr int kTile = 4;     // strips of a tile, at most
-constexpr int kStages = 3;   // tiles of a warp's ring
 constexpr uint64_t kWaitNs = 500ull * 1000 * 1000;
 constexpr float kWeightLog2 = 11.f;  // weights are held 2^11 times, relative to a reference
 constexpr float kSlack = 4.f;        // that the running maximum may pass by 2^4 before it is moved
@@ -62,7 +61,7 @@ struct Plan {
     int rows;
     float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
     float2* ml;       // [warps][2][rows of U]
-    int2* begun;      // [warps] the cut row that the warp began (-1: none) and in how many parts it is
+    int2* begun;      // [rows] the warp that began a cut row and in how many parts it is (0: whole)
 };
 
 // ---------------------------------------------------------------- pieces
@@ -165,6 +164,8 @@ template <int D, typename T, bool kNarrow>
 struct Shape {
     static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;  // float16 parts of q and of the weights
     static constexpr int kThreads = kWarps * 32;
+    // CTAs of an SM and tiles of a warp's ring: what registers and shared memory hold
+    static constexpr int kBlocks = kNarrow ? 3 : 2, kStages = kNarrow ? 2 : 3;
     static constexpr int kRows = kNarrow ? 8 : 16;
     static constexpr int kStripB = strip_bytes(D);
     static constexpr int kTileB = kTile * kStripB;
@@ -208,7 +209,7 @@ struct Ahead {
     int left = 0;                      // tiles (kRows: rows) behind the current row's
     // the current row: tiles [lo, hi) of n are the warp's, the batch is [off, off + size), the tile held off + at
     int row = 0, lo = 0, hi = 0, n = 0, off = 0, size = 0, at = 0;
-    int opened = 0;                    // kStream: set to hi when the row is begun here and cut
+    bool opened = false;               // kStream: the row begins here
     Row r;
     int h = 0;
     int first = -1, page = 0;  // the lane's strip: its first key (-1: none to see), its page as the table has it
@@ -239,7 +240,7 @@ struct Ahead {
             } else {
                 hi = min(n, off + left);
                 left -= hi - off;
-                if (p.mode == kStream && lo == 0 && hi < n) opened = hi;
+                opened = opened || (lo == 0 && hi > 0);
             }
         }
         size = min(8, hi - off), at = 0;
@@ -648,9 +649,10 @@ __device__ __forceinline__ void write_out(const CacheAttn& a, const Where& w, in
 // ---------------------------------------------------------------- the kernel
 
 template <int D, typename T, bool kNarrow>
-__global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAttn a, Plan p) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) cache_attn_mma_kernel(CacheAttn a, Plan p) {
     using S = Shape<D, T, kNarrow>;
     using P = Part<D, T, kNarrow>;
+    constexpr int kStages = S::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -666,21 +668,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAtt
     const int warps = gridDim.x * kWarps, id = blockIdx.x * kWarps + warp;
     Ahead ahead;
     long long run_hi = 0, total = 0;
-    // the next tile; a row that the run begins and does not end is told to the join: it has a part in every warp
-    // up to the one that holds its last tile, tile x being the last warp b's with total b / warps < x + 1
+    // the next tile; the join is told of a row by the warp that begins it: a cut one (the run's last) has a part
+    // in every warp up to the one that holds its last tile, tile x being the last warp b's with
+    // total b / warps < x + 1
     auto advance = [&] {
         ahead.next(a, p, lane, sizeof(T));
-        if (ahead.opened) {
-            const long long end = run_hi - ahead.opened + ahead.n;
-            if (lane == 0) p.begun[id] = make_int2(ahead.row, (int)((end * warps + total - 1) / total) - id);
-            ahead.opened = 0;
+        if (p.mode == kStream && ahead.opened) {
+            const long long end = run_hi - ahead.hi + ahead.n;
+            const int parts = ahead.hi == ahead.n ? 0 : (int)((end * warps + total - 1) / total) - id;
+            if (lane == 0) p.begun[ahead.row] = make_int2(id, parts);
+            ahead.opened = false;
         }
     };
     if (p.mode == kStream) {
         asm volatile("griddepcontrol.launch_dependents;");
         find_start(a, p, reinterpret_cast<int*>(smem), warps, id, ahead, run_hi, total);
         run_hi += ahead.left;
-        if (lane == 0) p.begun[id] = make_int2(-1, 0);
         if (ahead.left == 0 && lane < S::kRows)  // an empty run inside a row that is cut around it
             p.ml[(long long)id * 2 * S::kRows + lane] = make_float2(-INFINITY, 0.f);
         advance();
@@ -729,17 +732,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAtt
         issue(issued++);
         advance();
     }
+    __syncwarp();
     for (int n = 0, stage = 0, parity = 0; n < issued; ++n) {
-        if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status);
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;  // nothing more is issued; the copies in flight are waited for below
         const int4 fk4 = *reinterpret_cast<const int4*>(meta + stage * 8);
         const int4 tag = *reinterpret_cast<const int4*>(meta + stage * 8 + 4);  // row, position, flags
-        const int fk[kTile] = {fk4.x, fk4.y, fk4.z, fk4.w};
-        if (tag.z & kBegin) {
+        if (tag.z & kBegin) {  // the row's queries, while its first tile is on its way
             part.reset();
             part.load_q(a, p, tag.x, g, c);
         }
+        if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status);
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;  // nothing more is issued; the copies in flight are waited for below
+        const int fk[kTile] = {fk4.x, fk4.y, fk4.z, fk4.w};
         const unsigned char* tile = smem + (warp * kStages + stage) * S::kTileB;
         const int least = min(min(fk4.x, fk4.y), min(fk4.z, fk4.w)), most = max(max(fk4.x, fk4.y), max(fk4.z, fk4.w));
         if (least >= 0 && most + kStrip - 1 <= tag.y) part.template tile<true>(tile, fk, tag.y, g, c);
@@ -750,6 +754,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAtt
             ++issued;
             advance();
         }
+        __syncwarp();
         if (++stage == kStages) stage = 0, parity ^= 1;
         if ((tag.z & kEnd) && p.mode != kSplit) {
             float sum[2];
@@ -839,7 +844,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAtt
         const uint32_t at_ml = sbase + S::kCML + r * 8, at_u = sbase + S::at(r, ch) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm = -INFINITY, ll = 0.f;
+#pragma unroll 8
         for (int k = 0; k < p.splits; ++k) mm = fmaxf(mm, ld_cluster2(at_rank(at_ml, k)).x);
+#pragma unroll 4
         for (int k = 0; k < p.splits; ++k) {
             const float2 y = ld_cluster2(at_rank(at_ml, k));
             const float f = weight_of(y, mm);
@@ -852,48 +859,50 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_mma_kernel(CacheAtt
     cluster_sync();  // nobody leaves while others read its shared memory
 }
 
-// Joins the parts of the row that a warp of the stream began: its own and the following warps'.
-// A block takes 1 / gridDim.y of the row's heads; 512 / (D / 4 * heads) threads share the parts of four channels.
+// Joins the parts of a cut row, those of the warp that began it and of the following ones.  A block
+// takes 1 / gridDim.y of the row's heads; 512 / (D / 4 * heads) threads share the parts of four channels.
 template <int D, typename T, bool kNarrow>
 __global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan p) {
     constexpr int kRows = Shape<D, T, kNarrow>::kRows, kVec = D / 4;
     __shared__ float4 xs[512];
     __shared__ float2 mls[512];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the stream's kernel still runs
+    const Where w = where(a, p, blockIdx.x);
+    const int req = a.req[w.t];
     const int2 begun = p.begun[blockIdx.x];
-    if (begun.x < 0) return;
+    if (req < 0 || req >= a.R || begun.y == 0) return;  // a padding row (never begun), or a whole one
     const int heads = kRows / gridDim.y, lanes = 512 / kVec / heads;
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec % heads, part = threadIdx.x / kVec / heads;
     const int row = blockIdx.y * heads + r;
-    auto slot = [&](int k) { return ((long long)(blockIdx.x + k) * 2 + (k == 0)) * kRows + row; };
+    auto slot = [&](int k) { return ((long long)(begun.x + k) * 2 + (k == 0)) * kRows + row; };
     float mm = -INFINITY, ll = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = part; k0 < begun.y; k0 += 4 * lanes) {  // four parts' loads at a time
-        float2 w[4];
+        float2 ml[4];
         float4 y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = k0 + i * lanes;
-            w[i] = make_float2(-INFINITY, 0.f);
+            ml[i] = make_float2(-INFINITY, 0.f);
             y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (k < begun.y) {
-                w[i] = p.ml[slot(k)];
+                ml[i] = p.ml[slot(k)];
                 y[i] = *reinterpret_cast<const float4*>(p.part + slot(k) * D + v * 4);
             }
         }
-        float top = fmaxf(fmaxf(mm, fmaxf(w[0].x, w[1].x)), fmaxf(w[2].x, w[3].x));
+        float top = fmaxf(fmaxf(mm, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
         const float keep = weight_of(make_float2(mm, ll), top);
         mm = top, ll *= keep;
         x.x *= keep, x.y *= keep, x.z *= keep, x.w *= keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float f = weight_of(w[i], top);
-            ll += w[i].y * f;
+            const float f = weight_of(ml[i], top);
+            ll += ml[i].y * f;
             if (f != 0.f) x.x += y[i].x * f, x.y += y[i].y * f, x.z += y[i].z * f, x.w += y[i].w * f;  // else no part: memory of no meaning
         }
     }
     if (lanes == 1) {
-        write_out<D, T>(a, where(a, p, begun.x), row, v * 4, x, mm, ll);
+        write_out<D, T>(a, w, row, v * 4, x, mm, ll);
         return;
     }
     xs[threadIdx.x] = x;
@@ -905,18 +914,18 @@ __global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan 
     for (int k = 0; k < lanes; ++k) top = fmaxf(top, mls[threadIdx.x + k * step].x);
     ll = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < lanes; ++k) {
-        const float2 w = mls[threadIdx.x + k * step];
+        const float2 part_ml = mls[threadIdx.x + k * step];
         const float4 y = xs[threadIdx.x + k * step];
-        const float f = weight_of(w, top);
-        ll += w.y * f;
+        const float f = weight_of(part_ml, top);
+        ll += part_ml.y * f;
         x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
     }
-    write_out<D, T>(a, where(a, p, begun.x), row, v * 4, x, top, ll);
+    write_out<D, T>(a, w, row, v * 4, x, top, ll);
 }
 
 // ---------------------------------------------------------------- host
 
-constexpr int kSms = 152, kGrid = 2 * kSms;  // two CTAs an SM
+constexpr int kSms = 152;
 
 template <typename F>
 bool once_per_device(F f) {  // f(): whether it succeeded; called until it has, for each device
@@ -940,16 +949,18 @@ Sizes cut(int T, int HQ, int H, int D, bool lists, long long max_keys) {
     Sizes z = {};
     Plan& p = z.plan;
     const int G = HQ / H;
+    const bool narrow = G <= 8;
+    const int grid = kSms * (narrow ? Shape<128, float, true>::kBlocks : Shape<128, float, false>::kBlocks);
     p.head_tiles = (G + 15) / 16;
     const long long rows = (long long)T * H * p.head_tiles;
     p.rows = (int)std::min<long long>(rows, 0x7fffffff);
     p.tile_strips = kTile;
     const long long strips = (max_keys + kStrip - 1) / kStrip, tiles = (strips + kTile - 1) / kTile;
-    if (rows * tiles <= kWarps * kGrid || (rows <= kGrid && strips <= 16)) {
+    if (rows * tiles <= kWarps * grid || (rows <= grid && strips <= 16)) {
         // at most about a tile for every warp of the GPU: spread the strips over a cluster
         p.mode = kSplit;
         int s = 1;
-        while (s < 8 && rows * s * 2 <= kGrid && strips > kWarps * s) s *= 2;
+        while (s < 8 && rows * s * 2 <= grid && strips > kWarps * s) s *= 2;
         p.splits = s;
         while (p.tile_strips > 1 && strips <= (long long)s * kWarps * (p.tile_strips / 2)) p.tile_strips /= 2;
         z.grid = (int)(rows * s);
@@ -957,12 +968,12 @@ Sizes cut(int T, int HQ, int H, int D, bool lists, long long max_keys) {
     }
     const long long groups = lists ? (long long)T * H : T;
     p.mode = groups <= kScanGroups && rows * (tiles + 1) <= 0x7fffffffLL ? kStream : kRows;
-    z.grid = kGrid;
+    z.grid = grid;
     if (p.mode == kStream) {
-        const size_t slots = (size_t)kGrid * kWarps * 2 * (G <= 8 ? 8 : 16);
+        const size_t slots = (size_t)grid * kWarps * 2 * (narrow ? 8 : 16);
         z.part = slots * D * sizeof(float);
         z.ml = slots * sizeof(float2);
-        z.begun = (size_t)kGrid * kWarps * sizeof(int2);
+        z.begun = (size_t)rows * sizeof(int2);
     }
     return z;
 }
@@ -991,9 +1002,8 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     bsa_status rc = check_launch("cache_attn_mma_kernel");
     if (rc != BSA_OK || p.mode != kStream) return rc;
     // parts of a row: about the warps per row; blocks take fewer heads, and share out the parts, where they are many
-    const int warps = kGrid * kWarps, parts = warps / p.rows;
-    const int fold = parts <= 4 ? 1 : parts <= 32 ? 4 : S::kRows;
-    cfg.gridDim = dim3(warps, fold);
+    const int parts = z.grid * kWarps / p.rows, fold = parts <= 4 ? 1 : parts <= 32 ? 4 : S::kRows;
+    cfg.gridDim = dim3(p.rows, fold);
     cfg.blockDim = dim3(512);
     cfg.dynamicSmemBytes = 0;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
