@@ -9,6 +9,8 @@
 //           end (so a batch of ragged lengths is balanced to a tile); a row that is cut leaves
 //           parts (m, l, U) in the workspace, and a second kernel joins them:
 //             m = max m_i,   l = sum l_i 2^(m_i - m),   U = sum U_i 2^(m_i - m),   O = U / l;
+//   units   many rows of about the same length: clusters of an SM's worth of CTAs share out the rows,
+//           whole, and the warps of a cluster its tiles; a cut row is joined inside its cluster, in one launch;
 //   rows    so many rows that whole ones balance: a run of rows each;
 //   split   so few tiles that one launch counts: a cluster of up to 8 CTAs per row, joined through
 //           shared and distributed shared memory.
@@ -58,6 +60,7 @@ struct Plan {
     int head_tiles;   // tiles of 16 query heads per KV head
     int tile_strips;  // strips of a tile, at most kTile
     int splits;       // kSplit: CTAs of a row (the cluster)
+    int unit;         // kStream: CTAs of a unit (their cluster), or 0
     int rows;
     float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
     float2* ml;       // [warps][2][rows of U]
@@ -165,7 +168,7 @@ struct Shape {
     static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;  // float16 parts of q and of the weights
     static constexpr int kThreads = kWarps * 32;
     // CTAs of an SM and tiles of a warp's ring: what registers and shared memory hold
-    static constexpr int kBlocks = kNarrow ? 3 : 2, kStages = kNarrow ? 2 : 3;
+    static constexpr int kBlocks = kNarrow && kTerms == 1 ? 3 : 2, kStages = kBlocks == 3 ? 2 : 3;
     static constexpr int kRows = kNarrow ? 8 : 16;
     static constexpr int kStripB = strip_bytes(D);
     static constexpr int kTileB = kTile * kStripB;
@@ -262,7 +265,7 @@ struct Ahead {
 // share their keys' number are counted once: a token's without lists, a (token, head)'s with.
 constexpr int kScanGroups = 8192;
 __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, int* sums, int warps, int id, Ahead& ahead,
-                                           long long& run_lo, long long& total) {
+                                           long long& base, long long& total, long long& run_hi) {
     __shared__ int part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mult = a.blocks ? p.head_tiles : a.H * p.head_tiles, groups = p.rows / mult;
@@ -300,18 +303,38 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
     for (int g = g0; g < g1; ++g) sums[g] = before += sums[g];
     __syncthreads();
     total = (long long)all * mult;  // below 2^31: checked by the host
-    run_lo = total * id / warps;
-    ahead.left = (int)(total * (id + 1) / warps - run_lo);
-    if (ahead.left > 0) {
-        int lo = 0, hi = groups - 1;  // the first group that ends behind run_lo
+    // the row that holds tile x, and the tile of the row it is
+    auto find = [&](long long x, int& row, int& tile, int& n) {
+        int lo = 0, hi = groups - 1;  // the first group that ends behind x
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if ((long long)sums[mid] * mult > run_lo) hi = mid; else lo = mid + 1;
+            if ((long long)sums[mid] * mult > x) hi = mid; else lo = mid + 1;
         }
-        const int base = lo ? sums[lo - 1] : 0, n = sums[lo] - base, in = (int)(run_lo - (long long)base * mult);
-        ahead.next_row = lo * mult + in / n;
-        ahead.first_tile = in % n;
+        const int before = lo ? sums[lo - 1] : 0, in = (int)(x - (long long)before * mult);
+        n = sums[lo] - before;
+        row = lo * mult + in / n;
+        tile = in % n;
+    };
+    base = 0;
+    if (p.unit) {  // the unit's share begins and ends with the row that begins at or behind an equal cut
+        const int units = gridDim.x / p.unit, u = blockIdx.x / p.unit;
+        long long ends[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            ends[k] = total * (u + k) / units;
+            int row, tile, n;
+            if (ends[k] < total) {
+                find(ends[k], row, tile, n);
+                if (tile) ends[k] += n - tile;
+            }
+        }
+        base = ends[0], total = ends[1] - ends[0];
     }
+    const long long run_lo = base + total * id / warps;
+    run_hi = base + total * (id + 1) / warps;
+    ahead.left = (int)(run_hi - run_lo);
+    int n;
+    if (ahead.left > 0) find(run_lo, ahead.next_row, ahead.first_tile, n);
     // the sums lie in the ring: everyone has read them before the first copy lands there
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
@@ -514,7 +537,8 @@ struct Part {
                 const bool move = to > m[r] + kSlack;
                 const float f = move ? ptx::ex2(m[r] - to) : 1.f;
                 m[r] = move ? to : m[r];
-                l[r].x *= f, l[r].y *= f;
+                if constexpr (kNarrow) (r ? l[0].y : l[0].x) *= f;  // l[0] holds both rows' sums
+                else l[r].x *= f, l[r].y *= f;
 #pragma unroll
                 for (int j = 0; j < kU; ++j) {
                     if constexpr (kNarrow) u[j][r] *= f, u[j][2 + r] *= f;
@@ -628,6 +652,10 @@ struct Part {
         if constexpr (kNarrow) return u[i / 2][(i & 1) * 2 + r];
         else return u[i % kCh][2 * r + i / kCh];
     }
+    __device__ __forceinline__ float& ref(int r, int i) {
+        if constexpr (kNarrow) return u[i / 2][(i & 1) * 2 + r];
+        else return u[i % kCh][2 * r + i / kCh];
+    }
 };
 
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -665,25 +693,26 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     }
     __syncwarp();
 
-    const int warps = gridDim.x * kWarps, id = blockIdx.x * kWarps + warp;
+    // the warps that share out the tiles: the grid's, or the unit's
+    const int id = blockIdx.x * kWarps + warp, warps = (p.unit ? p.unit : gridDim.x) * kWarps;
+    const int in_unit = p.unit ? id % warps : id;
     Ahead ahead;
-    long long run_hi = 0, total = 0;
-    // the next tile; the join is told of a row by the warp that begins it: a cut one (the run's last) has a part
-    // in every warp up to the one that holds its last tile, tile x being the last warp b's with
-    // total b / warps < x + 1
+    long long base = 0, total = 0, run_hi = 0;
+    int begun = 0;  // parts of the row that the run's end cuts, if the run holds its beginning
+    // the next tile; a cut row has a part in every warp up to the one that holds its last tile, tile x being the
+    // last warp b's with base + total b / warps < x + 1
     auto advance = [&] {
         ahead.next(a, p, lane, sizeof(T));
         if (p.mode == kStream && ahead.opened) {
-            const long long end = run_hi - ahead.hi + ahead.n;
-            const int parts = ahead.hi == ahead.n ? 0 : (int)((end * warps + total - 1) / total) - id;
-            if (lane == 0) p.begun[ahead.row] = make_int2(id, parts);
+            const long long end = run_hi - ahead.hi + ahead.n - base;
+            begun = ahead.hi == ahead.n ? 0 : (int)((end * warps + total - 1) / total) - in_unit;
+            if (!p.unit && lane == 0) p.begun[ahead.row] = make_int2(id, begun);
             ahead.opened = false;
         }
     };
     if (p.mode == kStream) {
-        asm volatile("griddepcontrol.launch_dependents;");
-        find_start(a, p, reinterpret_cast<int*>(smem), warps, id, ahead, run_hi, total);
-        run_hi += ahead.left;
+        if (!p.unit) asm volatile("griddepcontrol.launch_dependents;");
+        find_start(a, p, reinterpret_cast<int*>(smem), warps, in_unit, ahead, base, total, run_hi);
         if (ahead.left == 0 && lane < S::kRows)  // an empty run inside a row that is cut around it
             p.ml[(long long)id * 2 * S::kRows + lane] = make_float2(-INFINITY, 0.f);
         advance();
@@ -726,7 +755,30 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
 
     P part;
     part.reset();
-    int issued = 0;
+    const bool owner = kNarrow ? g == 0 : c == 0;
+    float sum[2];
+    // O = U / l of a row that is complete in the registers
+    auto finish = [&](int number) {
+        const Where w = where(a, p, number);
+        const float vs = a.v_scale ? a.v_scale[w.h] : 1.f;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = P::row_at(r, g, c);
+            if (row >= w.heads) continue;
+            const long long to = (long long)w.t * a.HQ + w.hq0 + row;
+            const float f = sum[r] == 0.f ? 0.f : vs / sum[r];
+            T* o = static_cast<T*>(a.out) + to * D + P::ch_at(g, c);
+#pragma unroll
+            for (int i = 0; i < P::kRun; i += 16 / (int)sizeof(T)) {
+                T v[16 / sizeof(T)];
+#pragma unroll
+                for (int k = 0; k < 16 / (int)sizeof(T); ++k) v[k] = from_f32<T>(part.at(r, i + k) * f);
+                *reinterpret_cast<uint4*>(o + i) = *reinterpret_cast<const uint4*>(v);
+            }
+            if (a.lse && owner) a.lse[to] = lse_of(part.m[r], sum[r]);
+        }
+    };
+    int issued = 0, last = -1;
     bool alive = true;
     while (issued < kStages && ahead.have) {
         issue(issued++);
@@ -757,51 +809,63 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
         __syncwarp();
         if (++stage == kStages) stage = 0, parity ^= 1;
         if ((tag.z & kEnd) && p.mode != kSplit) {
-            float sum[2];
             part.totals(sum);
-            const Where w = where(a, p, tag.x);
-            const float vs = a.v_scale ? a.v_scale[w.h] : 1.f;
+            if (!(tag.z & kCut)) {
+                finish(tag.x);
+            } else if (!p.unit || (tag.z & kCarried)) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = P::row_at(r, g, c), ch = P::ch_at(g, c);
-                const bool owner = kNarrow ? g == 0 : c == 0;
-                if (tag.z & kCut) {
-                    const long long to = ((long long)id * 2 + (tag.z & kCarried ? 0 : 1)) * S::kRows + row;
+                for (int r = 0; r < 2; ++r) {
+                    const long long to = ((long long)id * 2 + (tag.z & kCarried ? 0 : 1)) * S::kRows + P::row_at(r, g, c);
                     if (owner) p.ml[to] = make_float2(part.m[r], sum[r]);
 #pragma unroll
                     for (int i = 0; i < P::kRun; i += 8) {
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = part.at(r, i + k);
-                        ptx::st_global_v8(p.part + to * D + ch + i, reinterpret_cast<const uint32_t*>(v));
+                        ptx::st_global_v8(p.part + to * D + P::ch_at(g, c) + i, reinterpret_cast<const uint32_t*>(v));
                     }
-                } else if (row < w.heads) {
-                    const long long to = (long long)w.t * a.HQ + w.hq0 + row;
-                    const float f = sum[r] == 0.f ? 0.f : vs / sum[r];
-                    T* o = static_cast<T*>(a.out) + to * D + ch;
-#pragma unroll
-                    for (int i = 0; i < P::kRun; i += 16 / (int)sizeof(T)) {
-                        T v[16 / sizeof(T)];
-#pragma unroll
-                        for (int k = 0; k < 16 / (int)sizeof(T); ++k) v[k] = from_f32<T>(part.at(r, i + k) * f);
-                        *reinterpret_cast<uint4*>(o + i) = *reinterpret_cast<const uint4*>(v);
-                    }
-                    if (a.lse && owner) a.lse[to] = lse_of(part.m[r], sum[r]);
                 }
+            } else {
+                last = tag.x;  // the run's last row, begun here and cut: it stays in the registers
             }
         }
     }
     if (!alive)  // bounded too: let the copies of the ring land before the memory is given up
         for (int i = 0; i < kStages; ++i) wait_slow(full + i * 8, 0, a.status), wait_slow(full + i * 8, 1, a.status);
-    if (p.mode != kSplit) return;
+    if (p.mode != kSplit) {
+        if (!p.unit) return;
+        // ---- the cut rows of the unit: the warp that began one adds the following warps' parts
+        cluster_sync();
+        if (last < 0) return;
+        for (int k = 1; k < begun; ++k) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const long long from = (long long)(id + k) * 2 * S::kRows + P::row_at(r, g, c);
+                const float2 w = p.ml[from];
+                const float top = fmaxf(part.m[r], w.x), keep = weight_of(make_float2(part.m[r], sum[r]), top),
+                            f = weight_of(w, top);
+                part.m[r] = top;
+                sum[r] = sum[r] * keep + w.y * f;
+                const float4* src = reinterpret_cast<const float4*>(p.part + from * D + P::ch_at(g, c));
+#pragma unroll
+                for (int i = 0; i < P::kRun; i += 4) {
+                    const float4 y = src[i / 4];
+                    const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // no part, no weight: memory of no meaning
+                        part.ref(r, i + j) = f != 0.f ? fmaf(v[j], f, part.at(r, i + j) * keep) : part.at(r, i + j) * keep;
+                }
+            }
+        }
+        finish(last);
+        return;
+    }
 
     // ---- kSplit: join the CTA's warps, then the cluster's CTAs
     float* U = reinterpret_cast<float*>(smem);
     float2* ml = reinterpret_cast<float2*>(smem + S::kML);
     float2* cml = reinterpret_cast<float2*>(smem + S::kCML);
-    float sum[2];
     part.totals(sum);
-    const bool owner = kNarrow ? g == 0 : c == 0;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
         if (owner) ml[warp * S::kRows + P::row_at(r, g, c)] = make_float2(part.m[r], sum[r]);
@@ -945,12 +1009,13 @@ struct Sizes {
 };
 
 // How the work is cut, from the sizes that the host knows.
-Sizes cut(int T, int HQ, int H, int D, bool lists, long long max_keys) {
+Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys) {
     Sizes z = {};
     Plan& p = z.plan;
     const int G = HQ / H;
     const bool narrow = G <= 8;
-    const int grid = kSms * (narrow ? Shape<128, float, true>::kBlocks : Shape<128, float, false>::kBlocks);
+    const int grid = kSms * (!narrow ? Shape<128, float, false>::kBlocks : f32 ? Shape<128, float, true>::kBlocks
+                                                                               : Shape<128, __nv_bfloat16, true>::kBlocks);
     p.head_tiles = (G + 15) / 16;
     const long long rows = (long long)T * H * p.head_tiles;
     p.rows = (int)std::min<long long>(rows, 0x7fffffff);
@@ -970,10 +1035,15 @@ Sizes cut(int T, int HQ, int H, int D, bool lists, long long max_keys) {
     p.mode = groups <= kScanGroups && rows * (tiles + 1) <= 0x7fffffffLL ? kStream : kRows;
     z.grid = grid;
     if (p.mode == kStream) {
+        // Whole rows to units where that leaves none with much more than its share: lists' rows are about as long as
+        // one another.  A unit is what an SM holds: larger clusters do not tile the GPU (76 clusters of four CTAs ran
+        // in two rounds: 143 us for 256 tokens of 2048 selected keys, against 99 with the join).
+        const long long most = (rows + kSms - 1) / kSms;
+        if (most * kSms * 100 <= rows * 108 && (lists || most >= 64)) p.unit = grid / kSms;
         const size_t slots = (size_t)grid * kWarps * 2 * (narrow ? 8 : 16);
         z.part = slots * D * sizeof(float);
         z.ml = slots * sizeof(float2);
-        z.begun = (size_t)rows * sizeof(int2);
+        z.begun = p.unit ? 0 : (size_t)rows * sizeof(int2);
     }
     return z;
 }
@@ -994,13 +1064,13 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.mode == kSplit ? p.splits : 1;
+    attr.val.clusterDim.x = p.mode == kSplit ? p.splits : std::max(1, p.unit);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = attr.val.clusterDim.x > 1 ? 1 : 0;
     cudaLaunchKernelEx(&cfg, kern, a, p);
     bsa_status rc = check_launch("cache_attn_mma_kernel");
-    if (rc != BSA_OK || p.mode != kStream) return rc;
+    if (rc != BSA_OK || p.mode != kStream || p.unit) return rc;
     // parts of a row: about the warps per row; blocks take fewer heads, and share out the parts, where they are many
     const int parts = z.grid * kWarps / p.rows, fold = parts <= 4 ? 1 : parts <= 32 ? 4 : S::kRows;
     cfg.gridDim = dim3(p.rows, fold);
@@ -1016,16 +1086,19 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
 }  // namespace
 
 size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_keys) {
-    // with and without lists: the larger (a workspace is asked for before the lists are)
-    const Sizes x = cut(T, HQ, H, D, false, max_keys), y = cut(T, HQ, H, D, true, max_keys);
-    return std::max(x.part + x.ml + x.begun, y.part + y.ml + y.begun);
+    size_t most = 0;  // of both types, with and without lists: a workspace is asked for by sizes alone
+    for (int k = 0; k < 4; ++k) {
+        const Sizes z = cut(T, HQ, H, D, k & 1, k >> 1, max_keys);
+        most = std::max(most, z.part + z.ml + z.begun);
+    }
+    return most;
 }
 
 bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
                                cudaStream_t st) {
     if ((long long)a.T * a.H * ((a.HQ / a.H + 15) / 16) > 0x7fffffffLL)
         return fail(BSA_ERR_UNSUPPORTED, "cache attention: too many (token, head) rows");
-    Sizes z = cut(a.T, a.HQ, a.H, a.D, a.blocks != nullptr, max_keys);
+    Sizes z = cut(a.T, a.HQ, a.H, a.D, dtype == BSA_F32, a.blocks != nullptr, max_keys);
     char* ws = static_cast<char*>(workspace);
     z.plan.part = reinterpret_cast<float*>(ws);
     z.plan.ml = reinterpret_cast<float2*>(ws + z.part);

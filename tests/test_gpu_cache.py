@@ -409,11 +409,79 @@ ATTEND_CASES = [
 
 @pytest.mark.parametrize("case", ATTEND_CASES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c))
 def test_attention(lib, pl, case):
-    c = attend_case(sum(case[:-1]), *case[:7], case[7], case[8], case[9], case[10])
+    c = attend_case(sum(case[:-1]), *case)
     want = want_attend(c)
     check_attend(*attend(pl, c), want)
     set_force_simt(True)
     check_attend(*attend(pl, c), want)
+
+
+def test_attention_running_maximum_moves_per_row(lib, pl):
+    """Logits that grow along the keys, by other amounts in each head: every row's sum and output are rescaled by its
+    own factor, tile after tile, in one warp's run as well as in a split row."""
+    for dtype in (torch.float32, torch.bfloat16):
+        for D in (64, 128):
+            for HQ in (3, 8, 16):
+                for R, n in ((1, 700), (60, 1500)):
+                    c = attend_case(HQ, R, 1, n, n, HQ, 1, D, 64, 0, 0, dtype, scales=False)
+                    c["cache"][..., 16 * D:17 * D] = 0x30  # K scales 0.5, but growing with the position below
+                    for r in range(R):
+                        for p in range(n):
+                            c["cache"][c["table"][r, p // 64], 0, p % 64 // 16, 16 * D + p % 16 * (D // 16):
+                                       16 * D + (p % 16 + 1) * (D // 16)] = 0x20 + min(0x30, p * 0x30 // n)
+                    c["q"] = (c["q"].double() * torch.logspace(-1, 0.3, HQ, dtype=torch.float64)[:, None]).to(dtype)
+                    out, lse = attend(pl, c)
+                    pick = slice(0, 2)
+                    d = {**c, "q": c["q"][pick], "req": c["req"][pick], "pos": c["pos"][pick]}
+                    check_attend(out[pick], lse[pick], want_attend(d))
+
+
+# Batches that are cut in each of the ways the tensor-core kernel has (rows * tiles of 64 keys against its warps):
+# equal runs of tiles with a join behind them (ragged, full), whole rows to clusters (many rows with lists), whole
+# rows to warps (more rows than a start is searched for)
+BATCHES = [
+    # R, n, lo, hi, HQ, H, D, P, S, BS, dtype
+    (40, 1, 1, 830, 32, 4, 128, 64, 0, 0, torch.bfloat16),
+    (40, 1, 1, 830, 64, 4, 128, 16, 0, 0, torch.bfloat16),
+    (23, 2, 2, 900, 8, 4, 64, 32, 0, 0, torch.float32),
+    (3, 1, 9000, 30000, 40, 1, 64, 128, 0, 0, torch.bfloat16),
+    (2, 1, 20000, 60000, 3, 1, 128, 64, 0, 0, torch.float32),
+    (150, 2, 2, 700, 32, 4, 128, 64, 5, 64, torch.bfloat16),
+    (150, 2, 2, 700, 64, 4, 128, 32, 9, 32, torch.bfloat16),
+    (140, 3, 3, 600, 20, 4, 64, 16, 3, 128, torch.float32),
+    (70, 30, 30, 200, 8, 4, 64, 16, 6, 16, torch.bfloat16),
+    (70, 30, 30, 200, 36, 4, 64, 16, 6, 16, torch.float32),
+    (180, 30, 30, 100, 4, 2, 64, 16, 0, 0, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", BATCHES, ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c))
+def test_attention_batches(lib, pl, case):
+    c = attend_case(sum(case[:-1]), *case)
+    T = c["q"].shape[0]
+    rng = np.random.default_rng(T)
+    pad = rng.random(T) < (0.05 if T > 10 else 0)
+    c["req"] = np.where(pad, -1, c["req"])
+    out, lse = attend(pl, c)
+    again = attend(pl, c)
+    live = torch.as_tensor(~pad, device=DEV)
+    assert torch.equal(out[live], again[0][live]) and torch.equal(lse[live], again[1][live])  # fixed order of sums
+    pick = np.sort(rng.permutation(T)[:40 if case[3] < 2000 else 2])
+    d = {**c, "q": c["q"][pick], "req": c["req"][pick], "pos": c["pos"][pick]}
+    if c["idx"] is not None:
+        d["idx"], d["cnt"] = c["idx"][pick], c["cnt"][pick]
+    pick = torch.as_tensor(pick, device=DEV)
+    check_attend(out[pick], lse[pick], want_attend(d))
+    # every row against the CUDA-core kernel: each is within its own tolerance of the exact row, bf16 outputs within
+    # two roundings (2 * 2^-8 |o|) and both kernels' weights (2^-11 A, A <= sum p |v| <= max |v|)
+    set_force_simt(True)
+    o2, l2 = attend(pl, c)
+    both = live[:, None] & torch.isfinite(l2)
+    assert torch.equal(both, live[:, None] & torch.isfinite(lse))
+    a, b = out.float()[both], o2.float()[both]
+    u = 2.0 ** -8 if c["q"].dtype == torch.bfloat16 else 2.0 ** -14
+    assert (a - b).norm() <= 2 * u * b.norm()
+    assert (lse - l2)[both].abs().max() <= 2.0 ** -14 * (1 + l2[both].abs().max())
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
