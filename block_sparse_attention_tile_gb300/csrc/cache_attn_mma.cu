@@ -59,7 +59,10 @@ struct Plan {
     int mode;
     int head_tiles;   // tiles of 16 query heads per KV head
     int tile_strips;  // strips of a tile, at most kTile
+    int tile_log2;
     int splits;       // kSplit: CTAs of a row (the cluster)
+    int G;            // query heads per KV head
+    unsigned long long inv_H;  // ceil(2^32 / H): g / H = g * inv_H >> 32 for g * H below 2^32
     int unit;         // kStream: CTAs of a unit (their cluster), or 0
     int rows;
     float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
@@ -189,16 +192,17 @@ struct Where {
 };
 __device__ __forceinline__ Where where(const CacheAttn& a, const Plan& p, int r) {
     Where w;
-    const int tile_h = r % p.head_tiles, G = a.HQ / a.H;
-    w.h = r / p.head_tiles % a.H;
-    w.t = r / p.head_tiles / a.H;
-    w.heads = min(16, G - tile_h * 16);
-    w.hq0 = w.h * G + tile_h * 16;
+    unsigned tile_h = 0, th = r;
+    if (p.head_tiles > 1) th = (unsigned)r / (unsigned)p.head_tiles, tile_h = r - th * p.head_tiles;
+    w.t = th / (unsigned)a.H;
+    w.h = th - w.t * a.H;
+    w.heads = min(16, p.G - (int)tile_h * 16);
+    w.hq0 = w.h * p.G + tile_h * 16;
     return w;
 }
 // A row without keys still has an output to write (one empty tile); a padding row has none.
 __device__ __forceinline__ int tiles_of(const Row& r, const Plan& p) {
-    return r.req < 0 ? 0 : max(1, (r.strips + p.tile_strips - 1) / p.tile_strips);
+    return r.req < 0 ? 0 : max(1, (r.strips + p.tile_strips - 1) >> p.tile_log2);
 }
 
 // Flags of a tile.
@@ -265,7 +269,7 @@ struct Ahead {
 // share their keys' number are counted once: a token's without lists, a (token, head)'s with.
 constexpr int kScanGroups = 8192;
 __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, int* sums, int warps, int id, Ahead& ahead,
-                                           long long& base, long long& total, long long& run_hi) {
+                                           int& base, int& total, int& run_hi) {
     __shared__ int part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mult = a.blocks ? p.head_tiles : a.H * p.head_tiles, groups = p.rows / mult;
@@ -273,7 +277,7 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
         int req[8], pos[8], count[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int g = min(g0 + i * kWarps * 32, groups - 1), t = a.blocks ? g / a.H : g;
+            const int g = min(g0 + i * kWarps * 32, groups - 1), t = a.blocks ? (int)(g * p.inv_H >> 32) : g;
             req[i] = a.req[t], pos[i] = a.pos[t];
             count[i] = a.blocks ? a.counts[g] : 0;
         }
@@ -302,26 +306,27 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
     }
     for (int g = g0; g < g1; ++g) sums[g] = before += sums[g];
     __syncthreads();
-    total = (long long)all * mult;  // below 2^31: checked by the host
+    total = all * mult;  // below 2^31: checked by the host
     // the row that holds tile x, and the tile of the row it is
-    auto find = [&](long long x, int& row, int& tile, int& n) {
+    auto find = [&](int x, int& row, int& tile, int& n) {
         int lo = 0, hi = groups - 1;  // the first group that ends behind x
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if ((long long)sums[mid] * mult > x) hi = mid; else lo = mid + 1;
+            if (sums[mid] * mult > x) hi = mid; else lo = mid + 1;
         }
-        const int before = lo ? sums[lo - 1] : 0, in = (int)(x - (long long)before * mult);
+        const int before = lo ? sums[lo - 1] : 0, in = x - before * mult;
         n = sums[lo] - before;
-        row = lo * mult + in / n;
-        tile = in % n;
+        const int whole = (unsigned)in / (unsigned)n;
+        row = lo * mult + whole;
+        tile = in - whole * n;
     };
     base = 0;
     if (p.unit) {  // the unit's share begins and ends with the row that begins at or behind an equal cut
         const int units = gridDim.x / p.unit, u = blockIdx.x / p.unit;
-        long long ends[2];
+        int ends[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            ends[k] = total * (u + k) / units;
+            ends[k] = (int)((long long)total * (u + k) / units);
             int row, tile, n;
             if (ends[k] < total) {
                 find(ends[k], row, tile, n);
@@ -330,9 +335,11 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
         }
         base = ends[0], total = ends[1] - ends[0];
     }
-    const long long run_lo = base + total * id / warps;
-    run_hi = base + total * (id + 1) / warps;
-    ahead.left = (int)(run_hi - run_lo);
+    // total id / warps in 32 bits: total = q warps + rest
+    const unsigned q = (unsigned)total / (unsigned)warps, rest = (unsigned)total - q * warps;
+    const unsigned run_lo = base + q * id + rest * id / warps;
+    run_hi = base + q * (id + 1) + rest * (id + 1) / warps;
+    ahead.left = run_hi - run_lo;
     int n;
     if (ahead.left > 0) find(run_lo, ahead.next_row, ahead.first_tile, n);
     // the sums lie in the ring: everyone has read them before the first copy lands there
@@ -374,31 +381,41 @@ struct Part {
 #pragma unroll
         for (int half = 0; half < (kNarrow ? 1 : 2); ++half) {
             const int r = min(g + half * 8, w.heads - 1);  // rows behind the last head repeat it and are not written
-            float x[D / 4];
-            const T* p4 = base + (long long)r * D;
-            if (wide) {
-                constexpr int kPer = 16 / sizeof(T);
+            const T* row_q = base + (long long)r * D;
+            float x[D / 4], top;
+            uint32_t pair[sizeof(T) == 2 ? D / 8 : 1];
+            if constexpr (sizeof(T) == 2) {
+                if (wide) {
 #pragma unroll
-                for (int i = 0; i < D / 4 / kPer; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p4) + i);
-                    const uint32_t b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (sizeof(T) == 2) {
-                            x[i * kPer + 2 * e] = __uint_as_float(b[e] << 16);
-                            x[i * kPer + 2 * e + 1] = __uint_as_float(b[e] & 0xffff0000u);
-                        } else {
-                            x[i * kPer + e] = __uint_as_float(b[e]);
-                        }
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row_q) + i);
+                        pair[4 * i] = v.x, pair[4 * i + 1] = v.y, pair[4 * i + 2] = v.z, pair[4 * i + 3] = v.w;
                     }
+                } else {
+                    const uint16_t* e = reinterpret_cast<const uint16_t*>(row_q);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) pair[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
                 }
+                // magnitudes of bf16 order as integers do; NaN is above infinity
+                uint32_t most = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) most = __vmaxu2(most, pair[i] & 0x7fff7fffu);
+                top = __uint_as_float(max(most << 16, most & 0xffff0000u));
             } else {
+                if (wide) {
 #pragma unroll
-                for (int i = 0; i < D / 4; ++i) x[i] = to_f32(p4[i]);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const float4 v = __ldg(reinterpret_cast<const float4*>(row_q) + i);
+                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i) x[i] = to_f32(row_q[i]);
+                }
+                top = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
             }
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^(14 - floor(log2 top)), its exponent kept in range; zero, infinite and NaN rows stay as they
@@ -412,8 +429,13 @@ struct Part {
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {
-                    const int at = kNarrow ? e2 : half + 2 * e2;
-                    const float x0 = x[4 * s + 2 * e2] * f, x1 = x[4 * s + 2 * e2 + 1] * f;
+                    const int at = kNarrow ? e2 : half + 2 * e2, i = 4 * s + 2 * e2;
+                    float x0, x1;
+                    if constexpr (sizeof(T) == 2) {
+                        x0 = __uint_as_float(pair[i / 2] << 16) * f, x1 = __uint_as_float(pair[i / 2] & 0xffff0000u) * f;
+                    } else {
+                        x0 = x[i] * f, x1 = x[i + 1] * f;
+                    }
                     q[0][s][at] = pack_f16x2(x0, x1);
                     if constexpr (kTerms == 2) {
                         const float2 b = f16x2_to_f32(q[0][s][at]);
@@ -697,14 +719,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     const int id = blockIdx.x * kWarps + warp, warps = (p.unit ? p.unit : gridDim.x) * kWarps;
     const int in_unit = p.unit ? id % warps : id;
     Ahead ahead;
-    long long base = 0, total = 0, run_hi = 0;
+    int base = 0, total = 0, run_hi = 0;
     int begun = 0;  // parts of the row that the run's end cuts, if the run holds its beginning
     // the next tile; a cut row has a part in every warp up to the one that holds its last tile, tile x being the
     // last warp b's with base + total b / warps < x + 1
     auto advance = [&] {
         ahead.next(a, p, lane, sizeof(T));
         if (p.mode == kStream && ahead.opened) {
-            const long long end = run_hi - ahead.hi + ahead.n - base;
+            const long long end = (long long)run_hi - ahead.hi + ahead.n - base;
             begun = ahead.hi == ahead.n ? 0 : (int)((end * warps + total - 1) / total) - in_unit;
             if (!p.unit && lane == 0) p.begun[ahead.row] = make_int2(id, begun);
             ahead.opened = false;
@@ -778,6 +800,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
             if (a.lse && owner) a.lse[to] = lse_of(part.m[r], sum[r]);
         }
     };
+    // a lane's values of row r of a part, eight channels together, runs of eight 256 floats apart
+    auto unit_part = [&](int of, int r, int ln) {
+        return p.part + (long long)of * 2 * S::kRows * D + r * (S::kRows * D / 2) + ln * 8;
+    };
     int issued = 0, last = -1;
     bool alive = true;
     while (issued < kStages && ahead.have) {
@@ -817,12 +843,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
                 for (int r = 0; r < 2; ++r) {
                     const long long to = ((long long)id * 2 + (tag.z & kCarried ? 0 : 1)) * S::kRows + P::row_at(r, g, c);
                     if (owner) p.ml[to] = make_float2(part.m[r], sum[r]);
+                    // a unit's part is read back lane by lane, the others' row by row
+                    float* dst = p.unit ? unit_part(id, r, lane) : p.part + to * D + P::ch_at(g, c);
+                    const int step = p.unit ? 32 : 1;
 #pragma unroll
                     for (int i = 0; i < P::kRun; i += 8) {
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = part.at(r, i + k);
-                        ptx::st_global_v8(p.part + to * D + P::ch_at(g, c) + i, reinterpret_cast<const uint32_t*>(v));
+                        ptx::st_global_v8(dst + i * step, reinterpret_cast<const uint32_t*>(v));
                     }
                 }
             } else {
@@ -841,15 +870,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const long long from = (long long)(id + k) * 2 * S::kRows + P::row_at(r, g, c);
-                const float2 w = p.ml[from];
+                const float2 w = __ldcg(p.ml + from);
                 const float top = fmaxf(part.m[r], w.x), keep = weight_of(make_float2(part.m[r], sum[r]), top),
                             f = weight_of(w, top);
                 part.m[r] = top;
                 sum[r] = sum[r] * keep + w.y * f;
-                const float4* src = reinterpret_cast<const float4*>(p.part + from * D + P::ch_at(g, c));
+                const float* src = unit_part(id + k, r, lane);
 #pragma unroll
                 for (int i = 0; i < P::kRun; i += 4) {
-                    const float4 y = src[i / 4];
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src + i / 8 * 256 + i % 8));
                     const float v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // no part, no weight: memory of no meaning
@@ -1019,7 +1048,10 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
     p.head_tiles = (G + 15) / 16;
     const long long rows = (long long)T * H * p.head_tiles;
     p.rows = (int)std::min<long long>(rows, 0x7fffffff);
+    p.G = G;
+    p.inv_H = (0x100000000ull + H - 1) / H;
     p.tile_strips = kTile;
+    p.tile_log2 = 2;
     const long long strips = (max_keys + kStrip - 1) / kStrip, tiles = (strips + kTile - 1) / kTile;
     if (rows * tiles <= kWarps * grid || (rows <= grid && strips <= 16)) {
         // at most about a tile for every warp of the GPU: spread the strips over a cluster
@@ -1027,7 +1059,7 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
         int s = 1;
         while (s < 8 && rows * s * 2 <= grid && strips > kWarps * s) s *= 2;
         p.splits = s;
-        while (p.tile_strips > 1 && strips <= (long long)s * kWarps * (p.tile_strips / 2)) p.tile_strips /= 2;
+        while (p.tile_strips > 1 && strips <= (long long)s * kWarps * (p.tile_strips / 2)) p.tile_strips /= 2, --p.tile_log2;
         z.grid = (int)(rows * s);
         return z;
     }
