@@ -240,7 +240,7 @@ struct Ahead {
             // the row's queries are needed a few tiles from now
             const char* q = static_cast<const char*>(a.q) + ((long long)w.t * a.q_stride + (long long)w.hq0 * a.D) * elem;
             for (int i = lane * 128; i < w.heads * a.D * elem; i += 32 * 128)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
             if (p.mode == kRows) {
                 hi = n;
                 --left;
@@ -273,46 +273,49 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
     __shared__ int part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mult = a.blocks ? p.head_tiles : a.H * p.head_tiles, groups = p.rows / mult;
-    for (int g0 = tid; g0 < groups; g0 += 8 * kWarps * 32) {  // eight groups' loads at a time
-        int req[8], pos[8], count[8];
+    int all = 0;
+    for (int g0 = 0; g0 < groups; g0 += 8 * kWarps * 32) {  // eight consecutive groups a thread
+        int v[8], req[8], pos[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int g = min(g0 + i * kWarps * 32, groups - 1), t = a.blocks ? (int)(g * p.inv_H >> 32) : g;
+            const int g = min(g0 + tid * 8 + i, groups - 1), t = a.blocks ? (int)(g * p.inv_H >> 32) : g;
             req[i] = a.req[t], pos[i] = a.pos[t];
-            count[i] = a.blocks ? a.counts[g] : 0;
+            v[i] = a.blocks ? a.counts[g] : 0;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (g0 + i * kWarps * 32 < groups)
-                sums[g0 + i * kWarps * 32] = tiles_of(row_from(a, req[i], pos[i], count[i], blockIdx.x == 0), p);
-    }
-    __syncthreads();
-    const int per = (groups + kWarps * 32 - 1) / (kWarps * 32), g0 = min(groups, tid * per), g1 = min(groups, g0 + per);
-    int mine = 0;
-    for (int g = g0; g < g1; ++g) mine += sums[g];
-    int inc = mine;
+        for (int i = 0; i < 8; ++i) {
+            v[i] = g0 + tid * 8 + i < groups ? tiles_of(row_from(a, req[i], pos[i], v[i], blockIdx.x == 0), p) : 0;
+            if (i) v[i] += v[i - 1];
+        }
+        int inc = v[7];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-    }
-    if (lane == 31) part[warp] = inc;
-    __syncthreads();
-    int before = inc - mine, all = 0;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        if (lane == 31) part[warp] = inc;
+        __syncthreads();
+        int before = all + inc - v[7];
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        if (k < warp) before += part[k];
-        all += part[k];
+        for (int k = 0; k < kWarps; ++k) {
+            if (k < warp) before += part[k];
+            all += part[k];
+        }
+        int4* to = reinterpret_cast<int4*>(sums + g0 + tid * 8);
+        to[0] = make_int4(before + v[0], before + v[1], before + v[2], before + v[3]);
+        to[1] = make_int4(before + v[4], before + v[5], before + v[6], before + v[7]);
+        __syncthreads();
     }
-    for (int g = g0; g < g1; ++g) sums[g] = before += sums[g];
-    __syncthreads();
     total = all * mult;  // below 2^31: checked by the host
-    // the row that holds tile x, and the tile of the row it is
+    // the row that holds tile x, and the tile of the row it is: the warp cuts the groups in 32 until one is left
     auto find = [&](int x, int& row, int& tile, int& n) {
-        int lo = 0, hi = groups - 1;  // the first group that ends behind x
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (sums[mid] * mult > x) hi = mid; else lo = mid + 1;
+        int lo = 0, len = groups;  // the first group that ends behind x is in [lo, lo + len)
+        while (len > 1) {
+            const int step = (len + 31) >> 5, at = lo + lane * step, end = min(at + step, lo + len);
+            const uint32_t behind = __ballot_sync(0xffffffffu, at < lo + len && sums[max(end, 1) - 1] * mult > x);
+            const int pick = lo + (__ffs(behind) - 1) * step;
+            len = min(step, lo + len - pick);
+            lo = pick;
         }
         const int before = lo ? sums[lo - 1] : 0, in = x - before * mult;
         n = sums[lo] - before;
