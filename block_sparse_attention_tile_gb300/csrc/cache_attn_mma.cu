@@ -375,49 +375,52 @@ struct Part {
             for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
     }
 
-    // Channels c D/4 .. of rows g (and g + 8), each row scaled to 2^14 .. 2^15.
-    __device__ __forceinline__ void load_q(const CacheAttn& a, const Plan& p, int row, int g, int c) {
+    // The lane's queries as they lie in memory, channels c D/4 .. of rows g (and g + 8): fetched ahead of their use.
+    static constexpr int kHalves = kNarrow ? 1 : 2, kRaw = D / 4 * sizeof(T) / 4;
+    struct Raw {
+        uint32_t w[kHalves][kRaw];
+        float ks;
+    };
+    static __device__ __forceinline__ void fetch_q(Raw& raw, const CacheAttn& a, const Plan& p, int row, int g, int c) {
         const Where w = where(a, p, row);
         const T* base = static_cast<const T*>(a.q) + w.t * a.q_stride + (long long)w.hq0 * D + c * (D / 4);
-        const float ks = (a.k_scale ? a.k_scale[w.h] : 1.f) * a.scale_log2;
         const bool wide = (((uintptr_t)a.q | (uintptr_t)(a.q_stride * (long long)sizeof(T))) & 15) == 0;
+        raw.ks = (a.k_scale ? a.k_scale[w.h] : 1.f) * a.scale_log2;
 #pragma unroll
-        for (int half = 0; half < (kNarrow ? 1 : 2); ++half) {
+        for (int half = 0; half < kHalves; ++half) {
             const int r = min(g + half * 8, w.heads - 1);  // rows behind the last head repeat it and are not written
-            const T* row_q = base + (long long)r * D;
-            float x[D / 4], top;
-            uint32_t pair[sizeof(T) == 2 ? D / 8 : 1];
-            if constexpr (sizeof(T) == 2) {
-                if (wide) {
+            const T* src = base + (long long)r * D;
+            if (wide) {
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row_q) + i);
-                        pair[4 * i] = v.x, pair[4 * i + 1] = v.y, pair[4 * i + 2] = v.z, pair[4 * i + 3] = v.w;
-                    }
-                } else {
-                    const uint16_t* e = reinterpret_cast<const uint16_t*>(row_q);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) pair[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
+                for (int i = 0; i < kRaw / 4; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    raw.w[half][4 * i] = v.x, raw.w[half][4 * i + 1] = v.y;
+                    raw.w[half][4 * i + 2] = v.z, raw.w[half][4 * i + 3] = v.w;
                 }
+            } else if constexpr (sizeof(T) == 2) {
+                const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+                for (int i = 0; i < kRaw; ++i) raw.w[half][i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRaw; ++i) raw.w[half][i] = __float_as_uint(to_f32(src[i]));
+            }
+        }
+    }
+    // Each row scaled to 2^14 .. 2^15 and rounded to (or split into) float16.
+    __device__ __forceinline__ void convert_q(const Raw& raw, int c) {
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+            float top = 0.f;
+            if constexpr (sizeof(T) == 2) {
                 // magnitudes of bf16 order as integers do; NaN is above infinity
                 uint32_t most = 0;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) most = __vmaxu2(most, pair[i] & 0x7fff7fffu);
+                for (int i = 0; i < kRaw; ++i) most = __vmaxu2(most, raw.w[half][i] & 0x7fff7fffu);
                 top = __uint_as_float(max(most << 16, most & 0xffff0000u));
             } else {
-                if (wide) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const float4 v = __ldg(reinterpret_cast<const float4*>(row_q) + i);
-                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) x[i] = to_f32(row_q[i]);
-                }
-                top = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+                for (int i = 0; i < kRaw; ++i) top = fmaxf(top, fabsf(__uint_as_float(raw.w[half][i])));
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -426,8 +429,8 @@ struct Part {
             // smallest normal, so that a scale of zero leaves masked logits at -inf.
             const int e = (int)(__float_as_uint(top) >> 23);
             const int up = e == 0 || e == 255 ? 0 : min(126, 14 + 127 - e);
-            const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), ks);
-            rs[half] = fmaxf(fabsf(ks) * __uint_as_float((uint32_t)(127 - up) << 23), 1.17549435e-38f);
+            const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), raw.ks);
+            rs[half] = fmaxf(fabsf(raw.ks) * __uint_as_float((uint32_t)(127 - up) << 23), 1.17549435e-38f);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -435,9 +438,10 @@ struct Part {
                     const int at = kNarrow ? e2 : half + 2 * e2, i = 4 * s + 2 * e2;
                     float x0, x1;
                     if constexpr (sizeof(T) == 2) {
-                        x0 = __uint_as_float(pair[i / 2] << 16) * f, x1 = __uint_as_float(pair[i / 2] & 0xffff0000u) * f;
+                        const uint32_t w = raw.w[half][i / 2];
+                        x0 = __uint_as_float(w << 16) * f, x1 = __uint_as_float(w & 0xffff0000u) * f;
                     } else {
-                        x0 = x[i] * f, x1 = x[i + 1] * f;
+                        x0 = __uint_as_float(raw.w[half][i]) * f, x1 = __uint_as_float(raw.w[half][i + 1]) * f;
                     }
                     q[0][s][at] = pack_f16x2(x0, x1);
                     if constexpr (kTerms == 2) {
@@ -809,17 +813,24 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     };
     int issued = 0, last = -1;
     bool alive = true;
-    while (issued < kStages && ahead.have) {
-        issue(issued++);
-        advance();
+    {
+        typename P::Raw raw;  // the first row's queries while its first tiles are looked up
+        if (ahead.have) P::fetch_q(raw, a, p, ahead.row, g, c);
+        while (issued < kStages && ahead.have) {
+            issue(issued++);
+            advance();
+        }
+        __syncwarp();
+        if (issued) part.convert_q(raw, c);
     }
-    __syncwarp();
     for (int n = 0, stage = 0, parity = 0; n < issued; ++n) {
         const int4 fk4 = *reinterpret_cast<const int4*>(meta + stage * 8);
         const int4 tag = *reinterpret_cast<const int4*>(meta + stage * 8 + 4);  // row, position, flags
-        if (tag.z & kBegin) {  // the row's queries, while its first tile is on its way
+        if ((tag.z & kBegin) && n) {  // the row's queries, while its first tile is on its way
             part.reset();
-            part.load_q(a, p, tag.x, g, c);
+            typename P::Raw raw;
+            P::fetch_q(raw, a, p, tag.x, g, c);
+            part.convert_q(raw, c);
         }
         if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status);
         alive = __all_sync(0xffffffffu, alive);
