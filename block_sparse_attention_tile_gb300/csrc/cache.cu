@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "cache.cuh"
+#include "tc_ptx.cuh"
 
 namespace bsa {
 
@@ -206,80 +207,101 @@ __global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, int3
 //
 // A thread rounds one group of 16 channels of one token and head, for K and for V:
 //   y = x * (1 / head scale),  s = E4M3(max |y| / 6),  code = E2M1(y / s).
-// max / 6 and y / s are IEEE divisions: a quotient that is not a rounding border of
-// the short format is never moved onto one by the float32 rounding, so the codes are those of the
-// exact quotient.  A group that holds a NaN or an infinity is stored with the scale
-// NaN, so that it reads back as NaN instead of as a finite number.
+// Both quotients are rounded once, to float32 (max / 6 by the division instruction's routine, y / s
+// by Markstein's three steps from the rounded reciprocal of s): a quotient that is not a border of the short format is
+// never moved onto one by that, because a float32 next to a product of border and scale leaves a quotient more than
+// half a step away, so the codes are those of the exact quotient.  The largest |y| is the product of the largest |x|
+// (products round monotonically), found on the inputs' bits: bf16 in pairs, and a group that
+// holds a NaN or an infinity shows there.  It is stored with the scale NaN, so that it reads back as NaN and not as
+// a finite number.
 //
-// Bound by HBM: 2 bytes read and 9/16 written per element.
+// Per element: 2 bytes read and 9/16 written (and 2 for the values), and about 10 instructions: at 16.8M
+// elements a tensor HBM and the issue slots bind about equally.
+
+// Sixteen elements as they lie in memory.
+template <typename T> struct Group { uint32_t w[4 * sizeof(T)]; };
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T* p, float* x) {
-    if constexpr (kVec && sizeof(T) == 2) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ Group<T> load16(const T* p) {
+    Group<T> x;
+    if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            x.w[4 * i] = a.x, x.w[4 * i + 1] = a.y, x.w[4 * i + 2] = a.z, x.w[4 * i + 3] = a.w;
         }
-    } else if constexpr (kVec) {
+    } else if constexpr (sizeof(T) == 2) {
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
-            x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = a.z, x[4 * i + 3] = a.w;
-        }
+        for (int i = 0; i < 8; ++i) x.w[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32(p[i]);
+        for (int i = 0; i < 16; ++i) x.w[i] = __float_as_uint(to_f32(p[i]));
     }
+    return x;
 }
-
+template <typename T>
+__device__ __forceinline__ float element(const Group<T>& x, int i) {
+    if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? x.w[i / 2] & 0xffff0000u : x.w[i / 2] << 16);
+    else return __uint_as_float(x.w[i]);
+}
 template <typename T, bool kVec>
 __device__ __forceinline__ void store16(T* p, const float* x) {
-    if constexpr (kVec && sizeof(T) == 2) {
-        uint32_t w[8];
+    if constexpr (kVec) {
+        uint32_t w[4 * sizeof(T)];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int i = 0; i < (int)(4 * sizeof(T)); ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                w[i] = __float_as_uint(x[i]);
+            }
         }
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) ptx::st_global_v8(p + i * 32 / sizeof(T), w + 8 * i);
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) p[i] = from_f32<T>(x[i]);
     }
 }
 
-// Codes (8 bytes) and scale byte of a group; x becomes the group's stored values.
-__device__ __forceinline__ uint2 quantise16(float* x, float head_scale, uint32_t* scale) {
+// Codes (8 bytes) and scale byte of a group; with kValues x becomes the group's stored values.
+template <typename T, bool kValues>
+__device__ __forceinline__ uint2 quantise16(const Group<T>& g, float head_scale, uint32_t* scale, float* x) {
     const float inv = __fdiv_rn(1.f, head_scale);
-    float top = 0.f;
-    bool finite = true;
+    uint32_t most = 0;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        x[i] *= inv;
-        top = fmaxf(top, fabsf(x[i]));
-        finite = finite && fabsf(x[i]) <= 3.402823466e38f;
+        for (int i = 0; i < 8; ++i) most = __vmaxu2(most, g.w[i] & 0x7fff7fffu);
+        most = max(most << 16, most & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = max(most, g.w[i] & 0x7fffffffu);
     }
-    uint32_t sb = finite ? f32_to_e4m3(__fdiv_rn(top, kE2M1Max)) : 0x7fu;
-    const float s = f16x2_to_f32(e4m3x2_to_f16x2(sb)).x;
+    const float top = __uint_as_float(most) * inv;
+    const bool finite = most < 0x7f800000u && top <= 3.402823466e38f;
+    const uint32_t sb = finite ? f32_to_e4m3(__fdiv_rn(top, kE2M1Max)) : 0x7fu;
+    const uint32_t s16 = e4m3x2_to_f16x2(sb | sb << 8);  // (s, s)
+    const float s = f16x2_to_f32(s16).x, r = s > 0.f ? __frcp_rn(s) : 0.f;  // a scale of zero stores zeros
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // a scale of zero stores zeros (and keeps the signs)
-        const float a = s > 0.f ? __fdiv_rn(x[2 * i], s) : copysignf(0.f, x[2 * i]);
-        const float b = s > 0.f ? __fdiv_rn(x[2 * i + 1], s) : copysignf(0.f, x[2 * i + 1]);
-        const uint32_t two = f32x2_to_e2m1x2(a, b);
-        const float2 v = f16x2_to_f32(e2m1x2_to_f16x2(two));
+        float q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float y = element<T>(g, 2 * i + k) * inv, q0 = y * r;
+            q[k] = fmaf(fmaf(-q0, s, y), r, q0);
+        }
+        const uint32_t two = f32x2_to_e2m1x2(q[0], q[1]);
         w[i >> 2] |= two << (8 * (i & 3));
-        x[2 * i] = v.x * s * head_scale;  // v.x * s is exact
-        x[2 * i + 1] = v.y * s * head_scale;
+        if constexpr (kValues) {
+            const uint32_t c = e2m1x2_to_f16x2(two);
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&s16));
+            const float2 f = __half22float2(v);  // code * s is exact in float16
+            x[2 * i] = f.x * head_scale;
+            x[2 * i + 1] = f.y * head_scale;
+        }
     }
     *scale = sb;
     return make_uint2(w[0], w[1]);
@@ -287,39 +309,33 @@ __device__ __forceinline__ uint2 quantise16(float* x, float head_scale, uint32_t
 
 template <typename T, bool kVec, bool kValues>
 __global__ void __launch_bounds__(256) cache_append_kernel(
-    const T* __restrict__ k, const T* __restrict__ v, long long k_stride, long long v_stride, long long items, int H,
+    const T* __restrict__ k, const T* __restrict__ v, long long k_stride, long long v_stride, unsigned items, int H,
     int D, const int64_t* __restrict__ slots, uint8_t* __restrict__ cache, long long n_slots, int sh,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale, T* __restrict__ k_val, T* __restrict__ v_val,
     int* status) {
-    const int ng = D / 16;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < items;
-         i += (long long)gridDim.x * blockDim.x) {
-        const int g = (int)(i % ng);
-        const int h = (int)(i / ng % H);
-        const long long t = i / ng / H;
+    const unsigned ng = D / 16;
+    for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < items; i += gridDim.x * blockDim.x) {
+        const unsigned row = i / ng, t = row / (unsigned)H;
+        const int g = (int)(i - row * ng), h = (int)(row - t * H);
         const long long slot = slots[t];
         if (slot < 0 || slot >= n_slots) {
             if (slot != -1) raise_status(status, BSA_ERR_INDEX);
             continue;
         }
-        float kx[16], vx[16];
-        load16<T, kVec>(k + t * k_stride + h * D + g * 16, kx);
-        load16<T, kVec>(v + t * v_stride + h * D + g * 16, vx);
+        const Group<T> kx = load16<T, kVec>(k + t * k_stride + h * D + g * 16);
+        const Group<T> vx = load16<T, kVec>(v + t * v_stride + h * D + g * 16);
         const float ks = k_scale ? k_scale[h] : 1.f, vs = v_scale ? v_scale[h] : 1.f;
-        uint32_t kb, vb;
-        const uint2 kc = quantise16(kx, ks, &kb), vc = quantise16(vx, vs, &vb);
-        const long long page = slot >> sh;
+        const long long page = slot >> sh, at = (long long)i * 16;
         const int in = (int)(slot & ((1 << sh) - 1)), j = in & 15;
         uint8_t* strip = cache + (((page * H + h) << (sh - 4)) + (in >> 4)) * strip_bytes(D);
-        *reinterpret_cast<uint2*>(strip + j * (D / 2) + g * 8) = kc;
-        *reinterpret_cast<uint2*>(strip + 8 * D + (g * 16 + j) * 8) = vc;
-        strip[16 * D + j * ng + g] = (uint8_t)kb;
-        strip[17 * D + g * 16 + j] = (uint8_t)vb;
-        if (kValues) {
-            const long long at = (t * H + h) * D + g * 16;
-            store16<T, kVec>(k_val + at, kx);
-            store16<T, kVec>(v_val + at, vx);
-        }
+        float x[16];
+        uint32_t byte;
+        *reinterpret_cast<uint2*>(strip + j * (D / 2) + g * 8) = quantise16<T, kValues>(kx, ks, &byte, x);
+        strip[16 * D + j * ng + g] = (uint8_t)byte;
+        if (kValues) store16<T, kVec>(k_val + at, x);
+        *reinterpret_cast<uint2*>(strip + 8 * D + (g * 16 + j) * 8) = quantise16<T, kValues>(vx, vs, &byte, x);
+        strip[17 * D + g * 16 + j] = (uint8_t)byte;
+        if (kValues) store16<T, kVec>(v_val + at, x);
     }
 }
 
@@ -328,10 +344,11 @@ static bsa_status launch_append(const void* k, const void* v, long long ks, long
                                 const int64_t* slots, uint8_t* cache, long long n_slots, int sh, const float* k_scale,
                                 const float* v_scale, void* k_val, void* v_val, cudaStream_t st) {
     const long long items = (long long)T_ * H * (D / 16);
-    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 1 << 20);
-    const uintptr_t bits = (uintptr_t)k | (uintptr_t)v | (uintptr_t)k_val | (uintptr_t)v_val |
-                           (uintptr_t)(ks * (long long)sizeof(T)) | (uintptr_t)(vs * (long long)sizeof(T));
-    const bool vec = (bits & 15) == 0;
+    if (items > (1LL << 31)) return fail(BSA_ERR_UNSUPPORTED, "cache append: too many rows (T=%d H=%d D=%d)", T_, H, D);
+    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 1 << 20);  // i stays below 2^32
+    const uintptr_t in = (uintptr_t)k | (uintptr_t)v | (uintptr_t)(ks * (long long)sizeof(T)) |
+                         (uintptr_t)(vs * (long long)sizeof(T)), out = (uintptr_t)k_val | (uintptr_t)v_val;
+    const bool vec = (in & 15) == 0 && (out & 31) == 0;
 #define BSA_APPEND(V, W)                                                                                        \
     cache_append_kernel<T, V, W><<<grid, 256, 0, st>>>((const T*)k, (const T*)v, ks, vs, items, H, D, slots, cache, \
                                                        n_slots, sh, k_scale, v_scale, (T*)k_val, (T*)v_val,     \

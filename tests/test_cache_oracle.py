@@ -219,6 +219,11 @@ def test_attention_refusals(bsa, change, word, status):
     assert word in bsa.bsa_last_error()
 
 
+def test_append_of_too_many_rows(bsa):
+    change = dict(T=(1 << 31) - 1, H=64, D=128, ks=64 * 128, vs=64 * 128)
+    assert bsa._lib.bsa_cache_append(*_args(APPEND, **change)) == bsa.BSA_ERR_UNSUPPORTED
+
+
 def test_an_empty_step_needs_no_launch(bsa):
     assert bsa._lib.bsa_cache_append(*_args(APPEND, T=0)) == bsa.BSA_OK
     assert bsa._lib.bsa_fwd_cache_tokens(*_args(ATTEND, T=0)) == bsa.BSA_OK
