@@ -284,23 +284,22 @@ __device__ __forceinline__ uint2 quantise16(const Group<T>& g, float head_scale,
     const uint32_t sb = finite ? f32_to_e4m3(__fdiv_rn(top, kE2M1Max)) : 0x7fu;
     const uint32_t s16 = e4m3x2_to_f16x2(sb | sb << 8);  // (s, s)
     const float s = f16x2_to_f32(s16).x, r = s > 0.f ? __frcp_rn(s) : 0.f;  // a scale of zero stores zeros
+    // two at a time; adding -0 leaves a product as it is
+    const float2 inv2 = make_float2(inv, inv), r2 = make_float2(r, r), s2 = make_float2(-s, -s), none = make_float2(-0.f, -0.f);
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float q[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float y = element<T>(g, 2 * i + k) * inv, q0 = y * r;
-            q[k] = fmaf(fmaf(-q0, s, y), r, q0);
-        }
-        const uint32_t two = f32x2_to_e2m1x2(q[0], q[1]);
+        const float2 y = ptx::ffma2(make_float2(element<T>(g, 2 * i), element<T>(g, 2 * i + 1)), inv2, none);
+        const float2 q0 = ptx::ffma2(y, r2, none), q = ptx::ffma2(ptx::ffma2(q0, s2, y), r2, q0);
+        const uint32_t two = f32x2_to_e2m1x2(q.x, q.y);
         w[i >> 2] |= two << (8 * (i & 3));
         if constexpr (kValues) {
             const uint32_t c = e2m1x2_to_f16x2(two);
             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&s16));
             const float2 f = __half22float2(v);  // code * s is exact in float16
-            x[2 * i] = f.x * head_scale;
-            x[2 * i + 1] = f.y * head_scale;
+            const float2 z = ptx::ffma2(f, make_float2(head_scale, head_scale), none);
+            x[2 * i] = z.x;
+            x[2 * i + 1] = z.y;
         }
     }
     *scale = sb;
