@@ -28,12 +28,14 @@ struct Tables {
     int32_t *count_out, *start, *req, *pos;
     int64_t* slots;
     int* status;
+    bool wide;  // the token arrays are 16-byte aligned
 };
 
 // What the second half of the work needs of the scan: in shared memory when one
 // CTA does everything, in the workspace when a grid follows.
 struct Sums {
     int32_t *start, *take, *give;  // R + 1 each
+    const int32_t *old_lens, *new_lens;
     int ok, count, taken, given, total;
 };
 
@@ -59,36 +61,65 @@ __device__ __forceinline__ int stack_page(const Tables& a, const Sums& s, int sh
     if (at < s.count) return a.pool[at];
     const int i = s.given - 1 - (at - s.count);
     const int r = owner(s.give, a.R, i);
-    return a.table[(long long)r * a.max_pages + pages_of(a.new_lens[r], sh) + i - s.give[r]];
+    return a.table[(long long)r * a.max_pages + pages_of(s.new_lens[r], sh) + i - s.give[r]];
 }
 
-// Everything behind the scan, by `stride` threads: token rows, new table entries, pages pushed.
-__device__ void place(const Tables& a, const Sums& s, int sh, int tid, int stride) {
-    for (unsigned i = tid; i < (unsigned)a.max_tokens; i += stride) {
-        int req = -1, pos = -1;
-        int64_t slot = -1;
-        if (s.ok && i < (unsigned)s.total) {
-            req = owner(s.start, a.R, i);
-            const int old = a.old_lens[req], before = pages_of(old, sh);
-            pos = old + i - s.start[req];
-            const int j = pos >> sh;
-            const int page = j < before ? a.table[(long long)req * a.max_pages + j]
-                                        : stack_page(a, s, sh, s.count + s.given - 1 - (s.take[req] + j - before));
-            if ((unsigned)page < (unsigned)a.n_pages) slot = ((int64_t)page << sh) + (pos & (a.P - 1));
-            else raise_status(a.status, BSA_ERR_INDEX);
+// Token rows, kPer consecutive ones a thread: one where each is likely to be another request's (a decode step), four
+// where they mostly share request and page and the 16 bytes written for each count.
+template <int kPer>
+__device__ void place_tokens(const Tables& a, const Sums& s, int sh, unsigned tid, unsigned stride) {
+    const unsigned live = s.ok ? s.total : 0, most = a.max_tokens;
+    for (unsigned i0 = tid * kPer; i0 < most; i0 += stride * kPer) {
+        int req[kPer], pos[kPer];
+        int64_t slot[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) req[k] = pos[k] = -1, slot[k] = -1;
+        if (i0 < live) {
+            int r = owner(s.start, a.R, i0), end = s.start[r + 1], old = s.old_lens[r], held = -1, page = 0;
+            int p = old + (int)i0 - s.start[r];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                if (i0 + k >= live) break;
+                if ((int)i0 + k >= end) {  // the next request with new tokens
+                    while (s.start[r + 1] <= (int)i0 + k) ++r;
+                    end = s.start[r + 1], p = old = s.old_lens[r], held = -1;
+                }
+                const int j = p >> sh;
+                if (j != held) {
+                    const int before = pages_of(old, sh);
+                    page = j < before ? a.table[(long long)r * a.max_pages + j]
+                                      : stack_page(a, s, sh, s.count + s.given - 1 - (s.take[r] + j - before));
+                    held = j;
+                }
+                req[k] = r, pos[k] = p;
+                if ((unsigned)page < (unsigned)a.n_pages) slot[k] = ((int64_t)page << sh) + (p & (a.P - 1));
+                else raise_status(a.status, BSA_ERR_INDEX);
+                ++p;
+            }
         }
-        a.req[i] = req;
-        a.pos[i] = pos;
-        a.slots[i] = slot;
+        if (kPer == 4 && a.wide && i0 + 4 <= most) {
+            *reinterpret_cast<int4*>(a.req + i0) = make_int4(req[0], req[1 % kPer], req[2 % kPer], req[3 % kPer]);
+            *reinterpret_cast<int4*>(a.pos + i0) = make_int4(pos[0], pos[1 % kPer], pos[2 % kPer], pos[3 % kPer]);
+            reinterpret_cast<longlong2*>(a.slots + i0)[0] = make_longlong2(slot[0], slot[1 % kPer]);
+            reinterpret_cast<longlong2*>(a.slots + i0)[1] = make_longlong2(slot[2 % kPer], slot[3 % kPer]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                if (i0 + k < most) a.req[i0 + k] = req[k], a.pos[i0 + k] = pos[k], a.slots[i0 + k] = slot[k];
+        }
     }
+}
+
+// New table entries and pages pushed.
+__device__ void place_pages(const Tables& a, const Sums& s, int sh, unsigned tid, unsigned stride) {
     if (!s.ok) return;
     for (unsigned i = tid; i < (unsigned)s.taken; i += stride) {
         const int r = owner(s.take, a.R, i);
-        a.table[(long long)r * a.max_pages + pages_of(a.old_lens[r], sh) + i - s.take[r]] =
+        a.table[(long long)r * a.max_pages + pages_of(s.old_lens[r], sh) + i - s.take[r]] =
             stack_page(a, s, sh, s.count + s.given - 1 - i);
     }
     const int pushed = s.given - s.taken;
-    for (int i = tid; i < pushed; i += stride) {  // pushed <= n_pages
+    for (int i = (int)tid; i < pushed; i += (int)stride) {  // pushed <= n_pages
         const int page = stack_page(a, s, sh, s.count + i);
         if ((unsigned)page >= (unsigned)a.n_pages) raise_status(a.status, BSA_ERR_INDEX);
         a.pool[s.count + i] = page;
@@ -102,10 +133,12 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
     __shared__ long long part[3][32];
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
     Sums s;
     s.start = kAll ? dyn : a.start;
     s.take = kAll ? dyn + (a.R + 1) : ws + 8;
     s.give = s.take + (a.R + 1);
+    s.old_lens = a.old_lens, s.new_lens = a.new_lens;
     if (tid == 0) bad = 0;
     s.count = a.count[0];
     __syncthreads();
@@ -184,23 +217,46 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
         for (int r = tid; r < a.R; r += kScanThreads) a.new_lens[r] = a.old_lens[r];
     if (kAll) {
         for (int r = tid; r <= a.R; r += kScanThreads) a.start[r] = s.ok ? s.start[r] : 0;
-        place(a, s, sh, tid, kScanThreads);
+        place_tokens<1>(a, s, sh, tid, kScanThreads);
+        place_pages(a, s, sh, tid, kScanThreads);
     } else if (!s.ok) {
         for (int r = tid; r <= a.R; r += kScanThreads) a.start[r] = 0;
     }
 }
 
-__global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, int32_t* ws) {
+// The rest of a large step: blocks of tokens, then blocks of pages.  kShared: the sums and lengths are copied to shared
+// memory first, where the ten or so dependent steps of a search cost a tenth of what they cost in L2.
+constexpr int kSharedRequests = 2400;  // 5 * (R + 1) ints in 48 KB
+constexpr int kPageBlocks = 32;
+
+template <bool kShared>
+__global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, const int32_t* ws) {
+    extern __shared__ int32_t dyn[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the scan still runs
     Sums s;
     s.start = a.start;
-    s.take = ws + 8;
+    s.take = const_cast<int32_t*>(ws) + 8;
     s.give = s.take + (a.R + 1);
+    s.old_lens = a.old_lens, s.new_lens = a.new_lens;
     s.ok = ws[0];
     s.count = ws[1];
     s.taken = ws[2];
     s.given = ws[3];
     s.total = ws[4];
-    place(a, s, sh, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+    if (kShared) {
+        const int n = a.R + 1;
+        for (int r = threadIdx.x; r < n; r += 256) {
+            const int l = min(r, a.R - 1);
+            const int v[5] = {s.start[r], s.take[r], s.give[r], s.old_lens[l], s.new_lens[l]};
+#pragma unroll
+            for (int k = 0; k < 5; ++k) dyn[k * n + r] = v[k];
+        }
+        s.start = dyn, s.take = dyn + n, s.give = dyn + 2 * n, s.old_lens = dyn + 3 * n, s.new_lens = dyn + 4 * n;
+        __syncthreads();
+    }
+    const int blocks = gridDim.x - kPageBlocks, b = blockIdx.x;
+    if (b < blocks) place_tokens<4>(a, s, sh, b * 256 + threadIdx.x, blocks * 256);
+    else place_pages(a, s, sh, (b - blocks) * 256 + threadIdx.x, kPageBlocks * 256);
 }
 
 // ---------------------------------------------------------------- a13 append
@@ -396,7 +452,8 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
     cudaStream_t st = as_stream(stream);
     const int sh = log2i(page_size);
     Tables a{old_lens, new_lens, R, page_size, max_pages, n_pages, max_tokens, block_table, pool, pool_count,
-             pool_count_out, query_start, token_req, token_pos, slots, status_word()};
+             pool_count_out, query_start, token_req, token_pos, slots, status_word(),
+             (((uintptr_t)token_req | (uintptr_t)token_pos | (uintptr_t)slots) & 15) == 0};
     int32_t* ws = static_cast<int32_t*>(workspace);
     if (one_cta(R, max_tokens)) {
         cache_scan_kernel<true><<<1, kScanThreads, 3 * (R + 1) * sizeof(int32_t), st>>>(a, sh, ws);
@@ -405,8 +462,17 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
     cache_scan_kernel<false><<<1, kScanThreads, 0, st>>>(a, sh, ws);
     bsa_status rc = check_launch("cache_scan_kernel");
     if (rc != BSA_OK) return rc;
-    const int work = std::max(max_tokens, R);
-    cache_place_kernel<<<std::min((work + 255) / 256, 152 * 8), 256, 0, st>>>(a, sh, ws);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = std::min(max_tokens / 1024 + 1, 152 * 4 - kPageBlocks) + kPageBlocks;
+    cfg.blockDim = 256;
+    cfg.dynamicSmemBytes = R <= kSharedRequests ? 5 * (R + 1) * sizeof(int32_t) : 0;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, R <= kSharedRequests ? cache_place_kernel<true> : cache_place_kernel<false>, a, sh, (const int32_t*)ws);
     return check_launch("cache_place_kernel");
 }
 
