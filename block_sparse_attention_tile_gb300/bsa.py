@@ -72,7 +72,7 @@ _SIGS = {
     "bsa_coarse_attention": (I, [P, I64, P, I64, I, I, I, P, P]),
     "bsa_coarse_apply": (I, [P, I, P, P, I, I, I, I, P, P, I, I, I, P]),
     "bsa_cache_bytes": (SZ, [I, I, I, I]),
-    "bsa_cache_tables_workspace": (SZ, [I, I]),
+    "bsa_cache_tables_workspace": (SZ, [I]),
     "bsa_cache_tables": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, P, I, P, SZ, P]),
     "bsa_cache_append": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P]),
     "bsa_cache_attention_workspace": (SZ, [I, I, I, I, I]),
@@ -362,8 +362,8 @@ def bsa_cache_bytes(n_pages, H, page_size, D):
 
 
 @functools.lru_cache(maxsize=1024)
-def bsa_cache_tables_workspace(R, max_tokens):
-    return _lib.bsa_cache_tables_workspace(R, max_tokens)
+def bsa_cache_tables_workspace(R):
+    return _lib.bsa_cache_tables_workspace(R)
 
 
 def bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, n_pages, pool_count,

@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
     asm volatile("griddepcontrol.launch_dependents;");
     Sums s;
     s.start = kAll ? dyn : a.start;
-    s.take = kAll ? dyn + (a.R + 1) : ws + 8;
-    s.give = s.take + (a.R + 1);
+    s.take = kAll ? dyn + (a.R + 1) : ws ? ws + 8 : nullptr;  // without a workspace nobody asks for these sums
+    s.give = s.take ? s.take + (a.R + 1) : nullptr;
     s.old_lens = a.old_lens, s.new_lens = a.new_lens;
     if (tid == 0) bad = 0;
     s.count = a.count[0];
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const long long before = run[k] + (warp ? part[k][warp - 1] : 0) + inc[k] - x[k];
-            if (r < a.R) (k == 0 ? s.start : k == 1 ? s.take : s.give)[r] = (int32_t)min(before, 0x7fffffffLL);
+            if (r < a.R && (k == 0 || s.take)) (k == 0 ? s.start : k == 1 ? s.take : s.give)[r] = (int32_t)min(before, 0x7fffffffLL);
             run[k] += part[k][31];
         }
         __syncthreads();
@@ -200,11 +200,10 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
     s.ok = code == BSA_OK;
     if (tid == 0) {
         s.start[a.R] = s.total;
-        s.take[a.R] = s.taken;
-        s.give[a.R] = s.given;
+        if (s.take) s.take[a.R] = s.taken, s.give[a.R] = s.given;
         a.count_out[0] = s.ok ? s.count + s.given - s.taken : s.count;
         if (!s.ok) raise_status(a.status, code);
-        if (!kAll) {
+        if (!kAll && ws) {
             ws[0] = s.ok;
             ws[1] = s.count;
             ws[2] = s.taken;
@@ -224,35 +223,73 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
     }
 }
 
-// The rest of a large step: blocks of tokens, then blocks of pages.  kShared: the sums and lengths are copied to shared
-// memory first, where the ten or so dependent steps of a search cost a tenth of what they cost in L2.
+// The rest of a large step: blocks of tokens, then blocks of pages.  kShared: every block sums the lengths again, into
+// shared memory, where the ten or so dependent steps of a search cost a tenth of what they cost in L2 (and which needs
+// no workspace).  It can, because the scan has set new_lens back where the call cannot be carried out: then nothing
+// grows or shrinks, and every token row is -1.
 constexpr int kSharedRequests = 2400;  // 5 * (R + 1) ints in 48 KB
 constexpr int kPageBlocks = 32;
 
 template <bool kShared>
 __global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, const int32_t* ws) {
     extern __shared__ int32_t dyn[];
+    __shared__ int part[3][8];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the scan still runs
     Sums s;
-    s.start = a.start;
-    s.take = const_cast<int32_t*>(ws) + 8;
-    s.give = s.take + (a.R + 1);
-    s.old_lens = a.old_lens, s.new_lens = a.new_lens;
-    s.ok = ws[0];
-    s.count = ws[1];
-    s.taken = ws[2];
-    s.given = ws[3];
-    s.total = ws[4];
     if (kShared) {
-        const int n = a.R + 1;
-        for (int r = threadIdx.x; r < n; r += 256) {
-            const int l = min(r, a.R - 1);
-            const int v[5] = {s.start[r], s.take[r], s.give[r], s.old_lens[l], s.new_lens[l]};
-#pragma unroll
-            for (int k = 0; k < 5; ++k) dyn[k * n + r] = v[k];
-        }
+        const int n = a.R + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         s.start = dyn, s.take = dyn + n, s.give = dyn + 2 * n, s.old_lens = dyn + 3 * n, s.new_lens = dyn + 4 * n;
+        const int left = a.count_out[0], per = (a.R + 255) / 256, r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+        int sum[3] = {0, 0, 0}, before[3], all[3] = {0, 0, 0};
+        for (int r = tid; r < a.R; r += 256) {
+            dyn[3 * n + r] = a.old_lens[r];
+            dyn[4 * n + r] = a.new_lens[r];
+        }
         __syncthreads();
+        auto add = [&](int r) {
+            const int o = s.old_lens[r], w = s.new_lens[r], b = pages_of(o, sh), e = pages_of(w, sh);
+            sum[0] += max(0, w - o), sum[1] += max(0, e - b), sum[2] += max(0, b - e);
+        };
+        for (int r = r0; r < r1; ++r) add(r);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            int inc = sum[k];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += y;
+            }
+            if (lane == 31) part[k][warp] = inc;
+            before[k] = inc - sum[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w < warp) before[k] += part[k][w];
+                all[k] += part[k][w];
+            }
+            sum[k] = before[k];
+        }
+        for (int r = r0; r < r1; ++r) {
+            s.start[r] = sum[0], s.take[r] = sum[1], s.give[r] = sum[2];
+            add(r);
+        }
+        if (tid == 0) s.start[a.R] = all[0], s.take[a.R] = all[1], s.give[a.R] = all[2];
+        s.ok = 1, s.total = all[0], s.taken = all[1], s.given = all[2];
+        s.count = left - s.given + s.taken;  // before the call
+        __syncthreads();
+    } else {
+        s.start = a.start;
+        s.take = const_cast<int32_t*>(ws) + 8;
+        s.give = s.take + (a.R + 1);
+        s.old_lens = a.old_lens, s.new_lens = a.new_lens;
+        s.ok = ws[0];
+        s.count = ws[1];
+        s.taken = ws[2];
+        s.given = ws[3];
+        s.total = ws[4];
     }
     const int blocks = gridDim.x - kPageBlocks, b = blockIdx.x;
     if (b < blocks) place_tokens<4>(a, s, sh, b * 256 + threadIdx.x, blocks * 256);
@@ -428,8 +465,8 @@ size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D) {
     return (size_t)n_pages * H * (page_size / kStrip) * strip_bytes(D);
 }
 
-size_t bsa_cache_tables_workspace(int R, int max_tokens) {
-    return R < 1 || one_cta(R, max_tokens) ? 0 : (8 + 2 * ((size_t)R + 1)) * sizeof(int32_t);
+size_t bsa_cache_tables_workspace(int R) {
+    return R <= kSharedRequests ? 0 : (8 + 2 * ((size_t)R + 1)) * sizeof(int32_t);
 }
 
 bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
@@ -446,7 +483,7 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
     BSA_REQUIRE(page_size_ok(page_size), "cache tables: page_size must be a power of two in 16..1024, got %d", page_size);
     BSA_REQUIRE((long long)R * max_pages <= 0x7fffffffLL && (long long)max_pages * page_size <= 0x7fffffffLL,
                 "cache tables: R * max_pages and max_pages * page_size must be below 2^31");
-    const size_t need = bsa_cache_tables_workspace(R, max_tokens);
+    const size_t need = bsa_cache_tables_workspace(R);
     BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 3) == 0),
                 "cache tables: a workspace of %zu bytes is needed", need);
     cudaStream_t st = as_stream(stream);
@@ -454,7 +491,7 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
     Tables a{old_lens, new_lens, R, page_size, max_pages, n_pages, max_tokens, block_table, pool, pool_count,
              pool_count_out, query_start, token_req, token_pos, slots, status_word(),
              (((uintptr_t)token_req | (uintptr_t)token_pos | (uintptr_t)slots) & 15) == 0};
-    int32_t* ws = static_cast<int32_t*>(workspace);
+    int32_t* ws = need ? static_cast<int32_t*>(workspace) : nullptr;
     if (one_cta(R, max_tokens)) {
         cache_scan_kernel<true><<<1, kScanThreads, 3 * (R + 1) * sizeof(int32_t), st>>>(a, sh, ws);
         return check_launch("cache_scan_kernel");

@@ -353,7 +353,7 @@ def cache_tables(old_lens, new_lens, page_size, block_table, pool, pool_count, m
         out = (torch.empty((1,), dtype=torch.int32, device=dev),
                torch.empty((R + 1,), dtype=torch.int32, device=dev), tok[0], tok[1],
                torch.empty((max_tokens,), dtype=torch.int64, device=dev))
-    nbytes = bsa.bsa_cache_tables_workspace(R, max_tokens)
+    nbytes = bsa.bsa_cache_tables_workspace(R)
     ws = torch.empty((nbytes // 4,), dtype=torch.int32, device=dev) if nbytes else None
     bsa.bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, pool.shape[0], pool_count,
                          *out, max_tokens, ws)

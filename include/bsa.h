@@ -488,7 +488,7 @@ bsa_status bsa_permute_rows(const void* src, void* dst, bsa_dtype dtype, int BH,
  * last (so a captured step of fixed size can run a smaller batch).
  * All pointers [device]; slots is int64, the rest int32.  block_table and pool
  * must not overlap the other arrays.  workspace: bsa_cache_tables_workspace
- * bytes (0 for a small step: then it may be NULL), its contents meaningless
+ * bytes (0 for up to 2400 requests: then it may be NULL), its contents meaningless
  * between calls.
  * A call that cannot be carried out changes neither table, pool nor count,
  * writes zeros to query_start, -1 to the token arrays and old_lens to new_lens
@@ -498,7 +498,7 @@ bsa_status bsa_permute_rows(const void* src, void* dst, bsa_dtype dtype, int BH,
  * the pool).  A page id outside [0, n_pages) met on the way latches
  * BSA_ERR_INDEX and gives the slot -1. */
 size_t bsa_cache_bytes(int n_pages, int H, int page_size, int D);
-size_t bsa_cache_tables_workspace(int R, int max_tokens);
+size_t bsa_cache_tables_workspace(int R);
 bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, int page_size,
                             int32_t* block_table, int max_pages, int32_t* pool, int n_pages,
                             const int32_t* pool_count, int32_t* pool_count_out, int32_t* query_start,

@@ -184,8 +184,8 @@ ATTEND = dict(q=16, dtype=1, T=4, HQ=8, H=2, D=128, qs=1024, cache=16, n_pages=4
     (dict(max_tokens=(1 << 30) + 1), "sizes"),
     (dict(P=48), "power of two"), (dict(P=8), "power of two"), (dict(P=2048), "power of two"),
     (dict(R=1 << 16, max_pages=1 << 15), "2^31"), (dict(max_pages=1 << 26, R=1), "2^31"),
-    (dict(ws=None, max_tokens=5000), "workspace"), (dict(ws_bytes=(8 + 2 * 5) * 4 - 1, max_tokens=5000), "workspace"),
-    (dict(ws=18, max_tokens=5000), "workspace"), (dict(ws=None, R=1025), "workspace"),
+    (dict(ws=None, R=2401), "workspace"), (dict(ws_bytes=(8 + 2 * 2402) * 4 - 1, R=2401), "workspace"),
+    (dict(ws=18, R=2401), "workspace"),
 ])
 def test_tables_refusals(bsa, change, word):
     assert bsa._lib.bsa_cache_tables(*_args(TABLES, **change)) == bsa.BSA_ERR_INVALID_ARG
@@ -234,7 +234,7 @@ def test_sizes(bsa):
     assert bsa.bsa_cache_bytes(1 << 20, 8, 128, 128) == (1 << 20) * 8 * 8 * 2304  # past 32 bits
     for bad in ((0, 1, 64, 128), (1, 1, 24, 128), (1, 1, 64, 100), (1, 1, 64, 256)):
         assert bsa.bsa_cache_bytes(*bad) == 0
-    assert bsa.bsa_cache_tables_workspace(4, 5000) == (8 + 2 * 5) * 4 and bsa.bsa_cache_tables_workspace(4, 4096) == 0
+    assert bsa.bsa_cache_tables_workspace(2401) == (8 + 2 * 2402) * 4 and bsa.bsa_cache_tables_workspace(2400) == 0
 
 
 def test_binding_refuses_tensors_that_do_not_fit(bsa):

@@ -97,7 +97,8 @@ def check_tables(step, t, want, new, old):
 @pytest.mark.parametrize("R,P,max_pages,kind,extra", [
     (1, 16, 1, "decode", 0), (1, 16, 4, "prefill", 5), (3, 16, 3, "mixed", 7), (64, 64, 20, "decode", 0),
     (64, 64, 20, "decode", 13), (33, 32, 9, "mixed", 1), (40, 1024, 2, "finish", 3), (257, 16, 5, "mixed", 100),
-    (1024, 16, 3, "decode", 1), (1025, 16, 3, "mixed", 0), (37, 128, 40, "prefill", 2), (2500, 16, 4, "mixed", 9),
+    (1024, 16, 3, "decode", 1), (1025, 16, 3, "mixed", 0), (37, 128, 40, "prefill", 2), (2500, 16, 4, "mixed", 9), (2400, 32, 5, "mixed", 3),
+    (300, 16, 70, "prefill", 0), (60, 16, 300, "mixed", 5000), (1, 1024, 9, "prefill", 1),
     (700, 64, 17, "mixed", 30), (90, 16, 600, "finish", 1),
 ])
 @pytest.mark.parametrize("alias", [False, True])
@@ -110,7 +111,7 @@ def test_tables(lib, pl, R, P, max_pages, kind, extra, alias):
     check_tables(step, t, want, new, old)
 
 
-@pytest.mark.parametrize("R", [5, 1500])
+@pytest.mark.parametrize("R", [5, 1500, 2600])
 @pytest.mark.parametrize("what", ["pages", "tokens", "negative", "long", "count", "overflow"])
 def test_tables_refuse_as_a_whole(lib, pl, R, what):
     P, max_pages = 16, 4
