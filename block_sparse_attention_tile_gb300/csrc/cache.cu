@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kScanThreads) cache_scan_kernel(Tables a, int 
     __shared__ long long part[3][32];
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
+    if (!kAll) asm volatile("griddepcontrol.launch_dependents;");
     Sums s;
     s.start = kAll ? dyn : a.start;
     s.take = kAll ? dyn + (a.R + 1) : ws ? ws + 8 : nullptr;  // without a workspace nobody asks for these sums

@@ -65,6 +65,8 @@ struct Plan {
     unsigned long long inv_H;  // ceil(2^32 / H): g / H = g * inv_H >> 32 for g * H below 2^32
     int unit;         // kStream: CTAs of a unit (their cluster), or 0
     int rows;
+    int warps;        // kStream: of the grid
+    int stall;        // tests only: a tile of each warp that is never copied (-1: none), waits end after 1 ms
     float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
     float2* ml;       // [warps][2][rows of U]
     int2* begun;      // [rows] the warp that began a cut row and in how many parts it is (0: whole)
@@ -153,11 +155,11 @@ __device__ __forceinline__ float weight_of(float2 part, float m) {
     return part.x == -INFINITY && part.y == 0.f ? 0.f : ptx::ex2(part.x - m);
 }
 
-// Waits for a phase; after kWaitNs latches BSA_ERR_TIMEOUT and gives up.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* status) {
+// Waits for a phase; after kWaitNs (1 ms in the test of this) latches BSA_ERR_TIMEOUT and gives up.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* status, int stall) {
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait(bar, parity))
-        if (ptx::globaltimer() - t0 > kWaitNs) {
+        if (ptx::globaltimer() - t0 > (stall >= 0 ? 1000000ull : kWaitNs)) {
             raise_status(status, BSA_ERR_TIMEOUT);
             return false;
         }
@@ -760,6 +762,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
         if (ahead.left > 0) advance();
     }
 
+    int issued = 0, last = -1;
     auto issue = [&](int stage) {
         const bool mine = (lane >> 2) == ahead.at;
         int first = mine ? ahead.first : -1;
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
             ptx::mbar_arrive_expect_tx(full + stage * 8, __popc(live) * S::kStripB);
         }
         __syncwarp();
-        if (first >= 0) {
+        if (first >= 0 && issued != p.stall) {
             const int strip = ((ahead.page * a.H + ahead.h) << (a.sh - 4)) + ((first & ((1 << a.sh) - 1)) >> 4);
             bulk_copy(sbase + (warp * kStages + stage) * S::kTileB + (lane & 3) * S::kStripB,
                       a.cache + (long long)strip * S::kStripB, S::kStripB, full + stage * 8);
@@ -811,13 +814,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     auto unit_part = [&](int of, int r, int ln) {
         return p.part + (long long)of * 2 * S::kRows * D + r * (S::kRows * D / 2) + ln * 8;
     };
-    int issued = 0, last = -1;
     bool alive = true;
     {
         typename P::Raw raw;  // the first row's queries while its first tiles are looked up
         if (ahead.have) P::fetch_q(raw, a, p, ahead.row, g, c);
         while (issued < kStages && ahead.have) {
-            issue(issued++);
+            issue(issued);
+            ++issued;
             advance();
         }
         __syncwarp();
@@ -832,7 +835,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
             P::fetch_q(raw, a, p, tag.x, g, c);
             part.convert_q(raw, c);
         }
-        if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status);
+        if (!ptx::mbar_try_wait(full + stage * 8, parity)) alive = wait_slow(full + stage * 8, parity, a.status, p.stall);
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;  // nothing more is issued; the copies in flight are waited for below
         const int fk[kTile] = {fk4.x, fk4.y, fk4.z, fk4.w};
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
         }
     }
     if (!alive)  // bounded too: let the copies of the ring land before the memory is given up
-        for (int i = 0; i < kStages; ++i) wait_slow(full + i * 8, 0, a.status), wait_slow(full + i * 8, 1, a.status);
+        for (int i = 0; i < kStages; ++i) wait_slow(full + i * 8, 0, a.status, p.stall), wait_slow(full + i * 8, 1, a.status, p.stall);
     if (p.mode != kSplit) {
         if (!p.unit) return;
         // ---- the cut rows of the unit: the warp that began one adds the following warps' parts
@@ -977,7 +980,9 @@ __global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan 
     const Where w = where(a, p, blockIdx.x);
     const int req = a.req[w.t];
     const int2 begun = p.begun[blockIdx.x];
-    if (req < 0 || req >= a.R || begun.y == 0) return;  // a padding row (never begun), or a whole one
+    if (req < 0 || req >= a.R) return;  // a padding row is never begun
+    // nothing to join of a whole row; after an expired wait a row may not have been begun: then this is any number
+    if ((unsigned)begun.x >= (unsigned)p.warps || begun.y <= 0 || begun.y > p.warps - begun.x) return;
     const int heads = kRows / gridDim.y, lanes = 512 / kVec / heads;
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec % heads, part = threadIdx.x / kVec / heads;
     const int row = blockIdx.y * heads + r;
@@ -1102,7 +1107,9 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) == cudaSuccess;
         }))
         return check_launch("cache_attn_mma_kernel: shared memory");
-    const Plan& p = z.plan;
+    Plan p = z.plan;
+    p.warps = z.grid * kWarps;
+    p.stall = test_stall_tile();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)z.grid);
     cfg.blockDim = dim3(S::kThreads);

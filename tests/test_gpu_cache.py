@@ -14,6 +14,8 @@ Tolerances, from the arithmetic (u = half a step relative to the value):
   - sums over n keys add n 2^-24; the output's own rounding is u = 2^-8 |o| (bf16), 2^-24 |o| (float32).
   LSE: the logit's error, n 2^-24 + 2^-22 for the sum, 2^-24 |lse| for its rounding."""
 
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -604,6 +606,25 @@ def test_attention_propagates_nan_and_infinity_that_a_row_sees(lib, pl):
         assert o3[1, 3].isnan().all() and l3[1, 3].isnan() and torch.equal(o3[1, :3], out[1, :3])
 
 
+@pytest.mark.parametrize("stall", [0, 2])
+@pytest.mark.parametrize("case", [BATCHES[0], BATCHES[1], BATCHES[5], BATCHES[6], ATTEND_CASES[9], ATTEND_CASES[15]],
+                         ids=["join-8", "join-16", "units-8", "units-16", "split-lists", "split"])
+def test_attention_expired_wait_is_reported_and_recovers(lib, pl, case, stall):
+    """A tile that is never copied: its wait runs out (after 1 ms under the switch), the kernel latches
+    BSA_ERR_TIMEOUT and ends, also where other warps and the join look for its parts; the next call is as before."""
+    c = attend_case(sum(case[:-1]), *case)
+    want = attend(pl, c)
+    os.environ["BSA_TEST_STALL_TILE"] = str(stall)
+    try:
+        attend(pl, c)
+    finally:
+        os.environ.pop("BSA_TEST_STALL_TILE")
+    status = lib.bsa_device_status()
+    assert status == lib.BSA_ERR_TIMEOUT or (stall > 0 and status == lib.BSA_OK)  # not every warp has a third tile
+    out, lse = attend(pl, c)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype,D,P", [(torch.bfloat16, 128, 64), (torch.float32, 64, 16)])
@@ -697,8 +718,38 @@ def test_a_captured_step_replays_with_new_lengths(lib, pl):
         assert torch.equal(eager.cache, graph.cache) and torch.equal(eager.block_table, graph.block_table)
 
 
+@pytest.mark.parametrize("case", [BATCHES[0], BATCHES[1], BATCHES[6]], ids=["join-8", "join-16", "units"])
+def test_captured_batches_replay(lib, pl, case):
+    """Large batches captured (the join behind its kernel, the clusters) and replayed over other positions, twice,
+    beside a second graph of the same call: equal to eager calls."""
+    c = attend_case(sum(case[:-1]), *case)
+    f = torch.float32
+    d = dict(q=c["q"].to(DEV), cache=dev(c["cache"], torch.uint8), table=dev(c["table"]), req=dev(c["req"]),
+             pos=dev(c["pos"]), ks=dev(c["ks"], f), vs=dev(c["vs"], f), idx=None if c["idx"] is None else dev(c["idx"]),
+             cnt=None if c["cnt"] is None else dev(c["cnt"]))
+
+    def go():
+        return pl.cache_attention(d["q"], d["cache"], d["table"], d["req"], d["pos"], d["ks"], d["vs"], d["idx"], d["cnt"],
+                                  c["BS"])
+
+    go()
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            got.append(go())
+    for shift in (0, 3, 40):
+        d["pos"].copy_(dev(np.maximum(c["pos"] - shift, -1)))
+        want = go()
+        for g, (out, lse) in zip(graphs, got):
+            out.zero_(), lse.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_calls_on_two_streams_do_not_disturb_each_other(lib, pl):
-    cases = [attend_case(30 + i, 4, 1, 300, 800, 16, 2, 128, 64, 0, 0, torch.bfloat16) for i in range(2)]
+    cases = [attend_case(30 + i, R, 1, 300, 800, 16, 2, 128, 64, 0, 0, torch.bfloat16) for i, R in ((0, 4), (1, 70))]
     want = [want_attend(c) for c in cases]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
