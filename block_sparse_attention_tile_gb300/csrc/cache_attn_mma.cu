@@ -970,12 +970,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
 }
 
 // Joins the parts of a cut row, those of the warp that began it and of the following ones.  A block
-// takes 1 / gridDim.y of the row's heads; 512 / (D / 4 * heads) threads share the parts of four channels.
+// takes 1 / gridDim.y of the row's heads; blockDim / (D / 4 * heads) threads share the parts of four channels.
 template <int D, typename T, bool kNarrow>
-__global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan p) {
+__global__ void __launch_bounds__(1024) cache_attn_join_kernel(CacheAttn a, Plan p) {
     constexpr int kRows = Shape<D, T, kNarrow>::kRows, kVec = D / 4;
-    __shared__ float4 xs[512];
-    __shared__ float2 mls[512];
+    __shared__ float4 xs[1024];
+    __shared__ float2 mls[1024];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the stream's kernel still runs
     const Where w = where(a, p, blockIdx.x);
     const int req = a.req[w.t];
@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(512) cache_attn_join_kernel(CacheAttn a, Plan 
     if (req < 0 || req >= a.R) return;  // a padding row is never begun
     // nothing to join of a whole row; after an expired wait a row may not have been begun: then this is any number
     if ((unsigned)begun.x >= (unsigned)p.warps || begun.y <= 0 || begun.y > p.warps - begun.x) return;
-    const int heads = kRows / gridDim.y, lanes = 512 / kVec / heads;
+    const int heads = kRows / gridDim.y, lanes = blockDim.x / kVec / heads;
     const int v = threadIdx.x % kVec, r = threadIdx.x / kVec % heads, part = threadIdx.x / kVec / heads;
     const int row = blockIdx.y * heads + r;
     auto slot = [&](int k) { return ((long long)(begun.x + k) * 2 + (k == 0)) * kRows + row; };
@@ -1127,7 +1127,7 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     // parts of a row: about the warps per row; blocks take fewer heads, and share out the parts, where they are many
     const int parts = z.grid * kWarps / p.rows, fold = parts <= 4 ? 1 : parts <= 32 ? 4 : S::kRows;
     cfg.gridDim = dim3(p.rows, fold);
-    cfg.blockDim = dim3(512);
+    cfg.blockDim = dim3(fold == S::kRows ? 1024 : 512);
     cfg.dynamicSmemBytes = 0;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
