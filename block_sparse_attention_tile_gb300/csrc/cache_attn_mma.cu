@@ -18,10 +18,11 @@
 // Numbers.  code * scale is exact in float16, so K and V enter the products exactly.  A
 // row of q is scaled by the power of two that brings its largest magnitude to 2^14..2^15
 // and is then exact in float16 when it is bf16 (8 bits, over 28 binades); a float32 q is
-// split into two float16 parts.  Weights are 2^15 times their value (so that float16 keeps
-// full precision over 29 binades below the largest) and rounded to float16 for bf16
-// outputs, u = 2^-11 against the output's own 2^-8, or split in two for float32 ones.
-// Maxima, sums and both accumulators are float32.
+// split into two float16 parts.  Weights are held as 2^11 2^(logit - reference), the reference at
+// most 2^4 below the running maximum (the sums and the output are rescaled only when the maximum
+// grows by more than that): they stay below float16's 2^16 and keep full precision over 25
+// binades.  They are rounded to float16 for bf16 outputs, u = 2^-11 against the output's own
+// 2^-8, or split in two for float32 ones.  Maxima, sums and both accumulators are float32.
 //
 // Fragments.  mma.m16n8k16 lets the summed index be permuted freely as long as both
 // operands agree, so a lane takes what lies together: of K the D / 4 consecutive channels
@@ -35,9 +36,16 @@
 //
 // What bounds it: the issue slots.  mma.sync keeps a scheduler for about 8 cycles, during which
 // little else issues (measured: 32 mma with 64 cvt and 64 multiplications take 2 cycles per mma
-// plus 1/4 per other instruction on an SM, whatever the number of warps), so a tile of 64 keys at
-// D = 128 costs 256 + 1000 / 4 cycles wide and 128 + 850 / 4 narrow, against 400 for its bytes at
-// the measured copy bandwidth.
+// plus 1/4 per other instruction on an SM, whether 8 or 16 warps run), so a tile of 64 keys at
+// D = 128 costs 256 + 970 / 4 = 498 cycles wide, and takes 540; its bytes take 400 at the measured
+// copy bandwidth.  Narrow it is 128 + 860 / 4, and the bytes bind.  Measured on the device: 48
+// ragged requests, 909 MB, 8 heads a KV head: 161 us, 83% of the copy bandwidth; 256 tokens of 2048
+// selected keys, 301 MB, 16 heads: 84 us, 53%.  About 7 us of a launch pass before the first tile
+// is worked on (start of the run, lookups, first copies).
+//
+// Tried and slower: a copying warp for four others (five warps a CTA limit registers to 168);
+// three CTAs an SM wide (168 registers, 15% more instructions); codes to float16 by shifts and masks (5.7
+// against 3.1 cycles per 8 codes and warp).
 #include <algorithm>
 #include <atomic>
 
