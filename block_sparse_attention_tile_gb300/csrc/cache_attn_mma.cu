@@ -278,6 +278,22 @@ struct Ahead {
 // kStream: where each warp's run begins and how long it is.  The tiles of a group of rows that
 // share their keys' number are counted once: a token's without lists, a (token, head)'s with.
 constexpr int kScanGroups = 8192;
+// The row that holds tile x, the tile of the row it is, and the row's tiles: the warp cuts the groups in 32 until one
+// is left.  One copy of it: a launch's first microseconds go into fetching its instructions.
+__device__ __noinline__ int3 find_tile(const int* sums, int groups, int mult, int x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = groups;  // the first group that ends behind x is in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) >> 5, at = lo + lane * step, end = min(at + step, lo + len);
+        const uint32_t behind = __ballot_sync(0xffffffffu, at < lo + len && sums[max(end, 1) - 1] * mult > x);
+        const int pick = lo + (__ffs(behind) - 1) * step;
+        len = min(step, lo + len - pick);
+        lo = pick;
+    }
+    const int before = lo ? sums[lo - 1] : 0, in = x - before * mult, n = sums[lo] - before;
+    const int whole = (unsigned)in / (unsigned)n;
+    return make_int3(lo * mult + whole, in - whole * n, n);
+}
 __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, int* sums, int warps, int id, Ahead& ahead,
                                            int& base, int& total, int& run_hi) {
     __shared__ int part[kWarps];
@@ -317,21 +333,9 @@ __device__ __forceinline__ void find_start(const CacheAttn& a, const Plan& p, in
         __syncthreads();
     }
     total = all * mult;  // below 2^31: checked by the host
-    // the row that holds tile x, and the tile of the row it is: the warp cuts the groups in 32 until one is left
     auto find = [&](int x, int& row, int& tile, int& n) {
-        int lo = 0, len = groups;  // the first group that ends behind x is in [lo, lo + len)
-        while (len > 1) {
-            const int step = (len + 31) >> 5, at = lo + lane * step, end = min(at + step, lo + len);
-            const uint32_t behind = __ballot_sync(0xffffffffu, at < lo + len && sums[max(end, 1) - 1] * mult > x);
-            const int pick = lo + (__ffs(behind) - 1) * step;
-            len = min(step, lo + len - pick);
-            lo = pick;
-        }
-        const int before = lo ? sums[lo - 1] : 0, in = x - before * mult;
-        n = sums[lo] - before;
-        const int whole = (unsigned)in / (unsigned)n;
-        row = lo * mult + whole;
-        tile = in - whole * n;
+        const int3 f = find_tile(sums, groups, mult, x);
+        row = f.x, tile = f.y, n = f.z;
     };
     base = 0;
     if (p.unit) {  // the unit's share begins and ends with the row that begins at or behind an equal cut
@@ -1080,11 +1084,13 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
     p.tile_strips = kTile;
     p.tile_log2 = 2;
     const long long strips = (max_keys + kStrip - 1) / kStrip, tiles = (strips + kTile - 1) / kTile;
-    if (rows * tiles <= kWarps * grid || (rows <= grid && strips <= 16)) {
-        // at most about a tile for every warp of the GPU: spread the strips over a cluster
+    // A row to a cluster, in one launch, while that leaves a warp five tiles at most and the CTAs fit at once.
+    // Measured, us, split against stream: 64 rows of 8, 16, 32, 64 tiles 10.4, 11.1, 13.2, 18.1 against 13.8, 14.8,
+    // 16.4, 21.6; 4 rows of 256 tiles (8 to a warp) 20.8 against 16.3.
+    int s = 1;
+    while (s < 8 && rows * s * 2 <= grid && strips > kWarps * s) s *= 2;
+    if (rows * s <= grid && tiles <= 5 * kWarps * s) {
         p.mode = kSplit;
-        int s = 1;
-        while (s < 8 && rows * s * 2 <= grid && strips > kWarps * s) s *= 2;
         p.splits = s;
         while (p.tile_strips > 1 && strips <= (long long)s * kWarps * (p.tile_strips / 2)) p.tile_strips /= 2, --p.tile_log2;
         z.grid = (int)(rows * s);

@@ -439,22 +439,27 @@ def test_attention_running_maximum_moves_per_row(lib, pl):
                     check_attend(out[pick], lse[pick], want_attend(d))
 
 
-# Batches that are cut in each of the ways the tensor-core kernel has (rows * tiles of 64 keys against its warps):
-# equal runs of tiles with a join behind them (ragged, full), whole rows to clusters (many rows with lists), whole
-# rows to warps (more rows than a start is searched for)
+# Batches that are cut in each of the ways the tensor-core kernel has: a row to a cluster (few rows), equal runs of
+# tiles with a join behind them (more rows than CTAs, or long ones), whole rows to clusters (many rows with lists),
+# whole rows to warps (more rows than a start is searched for)
+JOIN_8 = (120, 1, 1, 330, 32, 4, 128, 64, 0, 0, torch.bfloat16)
+JOIN_16 = (80, 1, 1, 430, 64, 4, 128, 16, 0, 0, torch.bfloat16)
+UNITS_8 = (150, 2, 2, 700, 32, 4, 128, 64, 5, 64, torch.bfloat16)
+UNITS_16 = (150, 2, 2, 700, 64, 4, 128, 32, 9, 32, torch.bfloat16)
 BATCHES = [
     # R, n, lo, hi, HQ, H, D, P, S, BS, dtype
+    JOIN_8, JOIN_16, (40, 2, 2, 300, 8, 4, 64, 32, 0, 0, torch.float32),
     (40, 1, 1, 830, 32, 4, 128, 64, 0, 0, torch.bfloat16),
     (40, 1, 1, 830, 64, 4, 128, 16, 0, 0, torch.bfloat16),
     (23, 2, 2, 900, 8, 4, 64, 32, 0, 0, torch.float32),
     (3, 1, 9000, 30000, 40, 1, 64, 128, 0, 0, torch.bfloat16),
     (2, 1, 20000, 60000, 3, 1, 128, 64, 0, 0, torch.float32),
-    (150, 2, 2, 700, 32, 4, 128, 64, 5, 64, torch.bfloat16),
-    (150, 2, 2, 700, 64, 4, 128, 32, 9, 32, torch.bfloat16),
+    UNITS_8, UNITS_16,
     (140, 3, 3, 600, 20, 4, 64, 16, 3, 128, torch.float32),
     (70, 30, 30, 200, 8, 4, 64, 16, 6, 16, torch.bfloat16),
     (70, 30, 30, 200, 36, 4, 64, 16, 6, 16, torch.float32),
     (180, 30, 30, 100, 4, 2, 64, 16, 0, 0, torch.bfloat16),
+    (180, 30, 30, 60, 4, 4, 64, 16, 3, 16, torch.bfloat16),
 ]
 
 
@@ -607,7 +612,7 @@ def test_attention_propagates_nan_and_infinity_that_a_row_sees(lib, pl):
 
 
 @pytest.mark.parametrize("stall", [0, 2])
-@pytest.mark.parametrize("case", [BATCHES[0], BATCHES[1], BATCHES[5], BATCHES[6], ATTEND_CASES[9], ATTEND_CASES[15]],
+@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_8, UNITS_16, ATTEND_CASES[9], ATTEND_CASES[15]],
                          ids=["join-8", "join-16", "units-8", "units-16", "split-lists", "split"])
 def test_attention_expired_wait_is_reported_and_recovers(lib, pl, case, stall):
     """A tile that is never copied: its wait runs out (after 1 ms under the switch), the kernel latches
@@ -718,7 +723,7 @@ def test_a_captured_step_replays_with_new_lengths(lib, pl):
         assert torch.equal(eager.cache, graph.cache) and torch.equal(eager.block_table, graph.block_table)
 
 
-@pytest.mark.parametrize("case", [BATCHES[0], BATCHES[1], BATCHES[6]], ids=["join-8", "join-16", "units"])
+@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_16], ids=["join-8", "join-16", "units"])
 def test_captured_batches_replay(lib, pl, case):
     """Large batches captured (the join behind its kernel, the clusters) and replayed over other positions, twice,
     beside a second graph of the same call: equal to eager calls."""
@@ -749,7 +754,7 @@ def test_captured_batches_replay(lib, pl, case):
 
 
 def test_calls_on_two_streams_do_not_disturb_each_other(lib, pl):
-    cases = [attend_case(30 + i, R, 1, 300, 800, 16, 2, 128, 64, 0, 0, torch.bfloat16) for i, R in ((0, 4), (1, 70))]
+    cases = [attend_case(30 + i, R, 1, 300, 800, 16, 2, 128, 64, 0, 0, torch.bfloat16) for i, R in ((0, 4), (1, 240))]
     want = [want_attend(c) for c in cases]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
