@@ -11,7 +11,8 @@
 //             m = max m_i,   l = sum l_i 2^(m_i - m),   U = sum U_i 2^(m_i - m),   O = U / l;
 //   units   many rows of about the same length: clusters of an SM's worth of CTAs share out the rows,
 //           whole, and the warps of a cluster its tiles; a cut row is joined inside its cluster, in one launch;
-//   rows    so many rows that whole ones balance: a run of rows each;
+//   rows    so many rows that whole ones balance: each warp takes the next row when it is done with one (from the
+//           stream's work counter; in a captured graph every warps-th row);
 //   split   so few tiles that one launch counts: a cluster of up to 8 CTAs per row, joined through
 //           shared and distributed shared memory.
 //
@@ -73,7 +74,8 @@ struct Plan {
     unsigned long long inv_H;  // ceil(2^32 / H): g / H = g * inv_H >> 32 for g * H below 2^32
     int unit;         // kStream: CTAs of a unit (their cluster), or 0
     int rows;
-    int warps;        // kStream: of the grid
+    int warps;        // of the grid
+    unsigned* work;   // kRows: (rows claimed behind the first ones, warps done), zero between launches, or null
     int stall;        // tests only: a tile of each warp that is never copied (-1: none), waits end after 1 ms
     float* part;      // kStream: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
     float2* ml;       // [warps][2][rows of U]
@@ -223,7 +225,8 @@ constexpr int kBegin = 1, kEnd = 2, kCarried = 4, kCut = 8;
 struct Ahead {
     bool have = false;
     int next_row = 0, first_tile = 0;  // the row after the current one; where the run begins in its first row
-    int left = 0;                      // tiles (kRows: rows) behind the current row's
+    int left = 0;                      // tiles behind the current row's (kRows: 1)
+    unsigned claim = 0;                // kRows, lane 0: the row claimed for later
     // the current row: tiles [lo, hi) of n are the warp's, the batch is [off, off + size), the tile held off + at
     int row = 0, lo = 0, hi = 0, n = 0, off = 0, size = 0, at = 0;
     bool opened = false;               // kStream: the row begins here
@@ -241,6 +244,10 @@ struct Ahead {
         while (off == hi) {
             if (left <= 0 || next_row >= p.rows) return;
             row = next_row++;
+            if (p.mode == kRows) {  // the claim made at the last row becomes the next one
+                next_row = p.work ? p.warps + (int)__shfl_sync(0xffffffffu, claim, 0) : row + p.warps;
+                if (p.work && lane == 0 && next_row < p.rows) claim = atomicAdd(p.work, 1u);
+            }
             const Where w = where(a, p, row);
             h = w.h;
             r = row_of(a, w.t, w.h, lane == 0);
@@ -253,7 +260,6 @@ struct Ahead {
                 asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
             if (p.mode == kRows) {
                 hi = n;
-                --left;
             } else {
                 hi = min(n, off + left);
                 left -= hi - off;
@@ -760,8 +766,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
             p.ml[(long long)id * 2 * S::kRows + lane] = make_float2(-INFINITY, 0.f);
         advance();
     } else if (p.mode == kRows) {
-        ahead.next_row = (int)((long long)p.rows * id / warps);
-        ahead.left = (int)((long long)p.rows * (id + 1) / warps) - ahead.next_row;
+        ahead.next_row = id;
+        ahead.left = 1;
+        if (p.work && lane == 0) ahead.claim = atomicAdd(p.work, 1u);
         advance();
     } else {
         ahead.next_row = blockIdx.x / p.splits;
@@ -890,6 +897,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     }
     if (!alive)  // bounded too: let the copies of the ring land before the memory is given up
         for (int i = 0; i < kStages; ++i) wait_slow(full + i * 8, 0, a.status, p.stall), wait_slow(full + i * 8, 1, a.status, p.stall);
+    if (p.mode == kRows && p.work && lane == 0) {
+        __threadfence();
+        if (atomicAdd(p.work + 1, 1u) == (unsigned)p.warps - 1) {  // nobody claims any more: zero for the next launch
+            p.work[0] = 0;
+            p.work[1] = 0;
+        }
+    }
     if (p.mode != kSplit) {
         if (!p.unit) return;
         // ---- the cut rows of the unit: the warp that began one adds the following warps' parts
@@ -1050,6 +1064,10 @@ __global__ void __launch_bounds__(1024) cache_attn_join_kernel(CacheAttn a, Plan
 // ---------------------------------------------------------------- host
 
 constexpr int kSms = 152;
+// From so many rows a warp on, lists' rows are taken whole, without a look at all of them first.  Measured, us, 4
+// requests' chunks of 16 blocks of 64, rows against units / stream: all lists full 127, 191, 291 against 117, 211,
+// 340 at 2.1, 4.1 and 6.7 rows a warp; 1 to 16 blocks a row 105, 143, 204 against 75, 130, 201.
+constexpr int kRowsPerWarp = 6;
 
 template <typename F>
 bool once_per_device(F f) {  // f(): whether it succeeded; called until it has, for each device
@@ -1097,7 +1115,8 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
         return z;
     }
     const long long groups = lists ? (long long)T * H : T;
-    p.mode = groups <= kScanGroups && rows * (tiles + 1) <= 0x7fffffffLL ? kStream : kRows;
+    const bool rows_balance = lists && rows >= (long long)kRowsPerWarp * grid * kWarps;
+    p.mode = groups <= kScanGroups && rows * (tiles + 1) <= 0x7fffffffLL && !rows_balance ? kStream : kRows;
     z.grid = grid;
     if (p.mode == kStream) {
         // Whole rows to units where that leaves none with much more than its share: lists' rows are about as long as
@@ -1124,6 +1143,7 @@ bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     Plan p = z.plan;
     p.warps = z.grid * kWarps;
     p.stall = test_stall_tile();
+    p.work = p.mode == kRows ? sched_counter(st) : nullptr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)z.grid);
     cfg.blockDim = dim3(S::kThreads);

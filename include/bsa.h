@@ -24,7 +24,8 @@
  *    that expired) are latched in a device status word; bsa_device_status()
  *    synchronises the stream, returns that status and clears it.
  *  - The tensor-core attention kernels (bsa_fwd_qouter, bsa_fwd_summary and
- *    bsa_fwd_qouter_tokens with bf16, D = 128) are persistent grids that take
+ *    bsa_fwd_qouter_tokens with bf16, D = 128, and bsa_fwd_cache_tokens with
+ *    block lists of many rows) are persistent grids that take
  *    their work items from a counter pair the library keeps per (device,
  *    stream) in static device memory (64 streams per device; further streams
  *    take a static schedule).  Launches on one stream run in order and each
@@ -548,6 +549,8 @@ bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T
  * int32 [T]; block_indices: [device] int32 [T, H, S], block_counts: [device]
  * int32 [T, H], or both NULL for every key.  block_size: a multiple of 16.
  * D a multiple of 16 up to 128.
+ * Deterministic: a row's sums run in an order fixed by the sizes and positions.
+ * D = 64 and 128 run on the tensor cores, other sizes on the CUDA cores.
  * workspace: [device] bsa_cache_attention_workspace bytes, 32-byte aligned, its
  * contents meaningless between calls; max_keys is the most keys that a row can
  * see: S * block_size with lists, else max_pages * page_size. */

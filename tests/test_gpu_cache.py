@@ -445,6 +445,7 @@ def test_attention_running_maximum_moves_per_row(lib, pl):
 JOIN_8 = (120, 1, 1, 330, 32, 4, 128, 64, 0, 0, torch.bfloat16)
 JOIN_16 = (80, 1, 1, 430, 64, 4, 128, 16, 0, 0, torch.bfloat16)
 UNITS_8 = (150, 2, 2, 700, 32, 4, 128, 64, 5, 64, torch.bfloat16)
+ROWS_8 = (70, 30, 30, 200, 8, 4, 64, 16, 6, 16, torch.bfloat16)
 UNITS_16 = (150, 2, 2, 700, 64, 4, 128, 32, 9, 32, torch.bfloat16)
 BATCHES = [
     # R, n, lo, hi, HQ, H, D, P, S, BS, dtype
@@ -456,7 +457,7 @@ BATCHES = [
     (2, 1, 20000, 60000, 3, 1, 128, 64, 0, 0, torch.float32),
     UNITS_8, UNITS_16,
     (140, 3, 3, 600, 20, 4, 64, 16, 3, 128, torch.float32),
-    (70, 30, 30, 200, 8, 4, 64, 16, 6, 16, torch.bfloat16),
+    ROWS_8,
     (70, 30, 30, 200, 36, 4, 64, 16, 6, 16, torch.float32),
     (180, 30, 30, 100, 4, 2, 64, 16, 0, 0, torch.bfloat16),
     (180, 30, 30, 60, 4, 4, 64, 16, 3, 16, torch.bfloat16),
@@ -612,8 +613,8 @@ def test_attention_propagates_nan_and_infinity_that_a_row_sees(lib, pl):
 
 
 @pytest.mark.parametrize("stall", [0, 2])
-@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_8, UNITS_16, ATTEND_CASES[9], ATTEND_CASES[15]],
-                         ids=["join-8", "join-16", "units-8", "units-16", "split-lists", "split"])
+@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_8, UNITS_16, ROWS_8, ATTEND_CASES[9], ATTEND_CASES[15]],
+                         ids=["join-8", "join-16", "units-8", "units-16", "rows-8", "split-lists", "split"])
 def test_attention_expired_wait_is_reported_and_recovers(lib, pl, case, stall):
     """A tile that is never copied: its wait runs out (after 1 ms under the switch), the kernel latches
     BSA_ERR_TIMEOUT and ends, also where other warps and the join look for its parts; the next call is as before."""
@@ -723,7 +724,7 @@ def test_a_captured_step_replays_with_new_lengths(lib, pl):
         assert torch.equal(eager.cache, graph.cache) and torch.equal(eager.block_table, graph.block_table)
 
 
-@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_16], ids=["join-8", "join-16", "units"])
+@pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_16, ROWS_8], ids=["join-8", "join-16", "units", "rows"])
 def test_captured_batches_replay(lib, pl, case):
     """Large batches captured (the join behind its kernel, the clusters) and replayed over other positions, twice,
     beside a second graph of the same call: equal to eager calls."""
@@ -754,7 +755,8 @@ def test_captured_batches_replay(lib, pl, case):
 
 
 def test_calls_on_two_streams_do_not_disturb_each_other(lib, pl):
-    cases = [attend_case(30 + i, R, 1, 300, 800, 16, 2, 128, 64, 0, 0, torch.bfloat16) for i, R in ((0, 4), (1, 240))]
+    cases = [attend_case(30 + i, R, 1, lo, hi, 16, 2, 128, 64, 0, 0, torch.bfloat16)
+             for i, R, lo, hi in ((0, 4, 300, 800), (1, 160, 20, 150))]
     want = [want_attend(c) for c in cases]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
