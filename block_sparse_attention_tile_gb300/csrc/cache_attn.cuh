@@ -84,7 +84,7 @@ __device__ __forceinline__ int strip_index(const CacheAttn& a, const Row& r, int
     return ((page * a.H + h) << (a.sh - 4)) + ((first & ((1 << a.sh) - 1)) >> 4);
 }
 
-// The tensor-core kernel (D = 64 or 128).
+// The tensor-core kernels (D = 64 or 128).
 size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_keys);
 bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
                                cudaStream_t st);

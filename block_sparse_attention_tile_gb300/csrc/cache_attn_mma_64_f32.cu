@@ -1,0 +1,12 @@
+// Attention over the 4-bit paged cache on the tensor cores (a14): D = 64, float32.
+#include "cache_attn_mma.cuh"
+
+namespace bsa {
+namespace cmma {
+
+bsa_status launch_64_f32(const CacheAttn& a, const Sizes& z, bool narrow, cudaStream_t st) {
+    return narrow ? launch<64, float, true>(a, z, st) : launch<64, float, false>(a, z, st);
+}
+
+}  // namespace cmma
+}  // namespace bsa
