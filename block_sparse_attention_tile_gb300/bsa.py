@@ -314,7 +314,9 @@ def bsa_permute_rows(src, dst, BH, N, D, n_prefix, perm, inverse=False, stream=N
 
 # The cache entry points check what the C side cannot see (types, layouts, sizes
 # behind the pointers, devices) and run on the device of their tensors, whichever
-# is current.
+# is current.  A call for a few tokens costs the host more than the GPU, so the
+# checks of a call are one expression, and only where it fails are its tensors
+# gone through one by one for the error to name the one that does not fit.
 
 def _device_of(t):
     dev = t.get_device()
@@ -348,13 +350,19 @@ def _rows(name, t, T, heads, D, dtype, dev):
     return t.data_ptr(), st[0] if T > 1 else heads * D
 
 
-def _run_on(dev, stream, fn, args):
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _on(dev, stream):
+    """The raw stream of a call on this device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _call(dev, fn, *args):
     if dev == torch._C._cuda_getDevice():
-        _check(fn(*args, raw))
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, raw))
+            rc = fn(*args)
+    if rc != BSA_OK:
+        _check(rc)
 
 
 def bsa_cache_bytes(n_pages, H, page_size, D):
@@ -369,14 +377,28 @@ def bsa_cache_tables_workspace(R):
 def bsa_cache_tables(old_lens, new_lens, R, page_size, block_table, max_pages, pool, n_pages, pool_count,
                      pool_count_out, query_start, token_req, token_pos, slots, max_tokens, workspace=None, stream=None):
     dev, i32 = _device_of(block_table), torch.int32
-    _run_on(dev, stream, _lib.bsa_cache_tables, (
-        _expect("old_lens", old_lens, i32, R, dev), _expect("new_lens", new_lens, i32, R, dev), R, page_size,
-        _expect("block_table", block_table, i32, R * max_pages, dev), max_pages,
-        _expect("pool", pool, i32, n_pages, dev), n_pages, _expect("pool_count", pool_count, i32, 1, dev),
-        _expect("pool_count_out", pool_count_out, i32, 1, dev), _expect("query_start", query_start, i32, R + 1, dev),
-        _expect("token_req", token_req, i32, max_tokens, dev), _expect("token_pos", token_pos, i32, max_tokens, dev),
-        _expect("slots", slots, torch.int64, max_tokens, dev), max_tokens,
-        *_workspace(workspace, dev)))
+    if not (old_lens.dtype is i32 and old_lens.get_device() == dev and old_lens.numel() >= R and old_lens.is_contiguous()
+            and new_lens.dtype is i32 and new_lens.get_device() == dev and new_lens.numel() >= R
+            and new_lens.is_contiguous() and block_table.dtype is i32 and block_table.numel() >= R * max_pages
+            and block_table.is_contiguous() and pool.dtype is i32 and pool.get_device() == dev
+            and pool.numel() >= n_pages and pool.is_contiguous() and pool_count.dtype is i32
+            and pool_count.get_device() == dev and pool_count.numel() >= 1 and pool_count_out.dtype is i32
+            and pool_count_out.get_device() == dev and pool_count_out.numel() >= 1 and query_start.dtype is i32
+            and query_start.get_device() == dev and query_start.numel() > R and query_start.is_contiguous()
+            and token_req.dtype is i32 and token_req.get_device() == dev and token_req.numel() >= max_tokens
+            and token_req.is_contiguous() and token_pos.dtype is i32 and token_pos.get_device() == dev
+            and token_pos.numel() >= max_tokens and token_pos.is_contiguous() and slots.dtype is torch.int64
+            and slots.get_device() == dev and slots.numel() >= max_tokens and slots.is_contiguous()):
+        for x in (("old_lens", old_lens, i32, R), ("new_lens", new_lens, i32, R),
+                  ("block_table", block_table, i32, R * max_pages), ("pool", pool, i32, n_pages),
+                  ("pool_count", pool_count, i32, 1), ("pool_count_out", pool_count_out, i32, 1),
+                  ("query_start", query_start, i32, R + 1), ("token_req", token_req, i32, max_tokens),
+                  ("token_pos", token_pos, i32, max_tokens), ("slots", slots, torch.int64, max_tokens)):
+            _expect(*x, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(dev, _lib.bsa_cache_tables, old_lens.data_ptr(), new_lens.data_ptr(), R, page_size, block_table.data_ptr(),
+          max_pages, pool.data_ptr(), n_pages, pool_count.data_ptr(), pool_count_out.data_ptr(), query_start.data_ptr(),
+          token_req.data_ptr(), token_pos.data_ptr(), slots.data_ptr(), max_tokens, ws, ws_bytes, _on(dev, stream))
 
 
 def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=None, v_scale=None, k_val=None,
@@ -384,11 +406,10 @@ def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=No
     dev, dt = _device_of(cache), k.dtype
     kp, ks = _rows("k", k, T, H, D, dt, dev)
     vp, vs = _rows("v", v, T, H, D, dt, dev)
-    _run_on(dev, stream, _lib.bsa_cache_append, (
-        kp, vp, _dtype(k), T, H, D, ks, vs, _expect("slots", slots, torch.int64, T, dev),
-        _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
-        _expect("k_scale", k_scale, torch.float32, H, dev), _expect("v_scale", v_scale, torch.float32, H, dev),
-        _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev)))
+    _call(dev, _lib.bsa_cache_append, kp, vp, _dtype(k), T, H, D, ks, vs, _expect("slots", slots, torch.int64, T, dev),
+          _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
+          _expect("k_scale", k_scale, torch.float32, H, dev), _expect("v_scale", v_scale, torch.float32, H, dev),
+          _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev), _on(dev, stream))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -401,13 +422,28 @@ def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table,
                          workspace=None, stream=None):
     dev, dt, i32, f32 = _device_of(cache), q.dtype, torch.int32, torch.float32
     qp, qs = _rows("q", q, T, HQ, D, dt, dev)
-    _run_on(dev, stream, _lib.bsa_fwd_cache_tokens, (
-        qp, _dtype(q), T, HQ, H, D, qs,
-        _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
-        _expect("block_table", block_table, i32, R * max_pages, dev), R, max_pages,
-        _expect("token_req", token_req, i32, T, dev), _expect("token_pos", token_pos, i32, T, dev),
-        _expect("k_scale", k_scale, f32, H, dev), _expect("v_scale", v_scale, f32, H, dev),
-        _expect("block_indices", block_indices, i32, T * H * S, dev),
-        _expect("block_counts", block_counts, i32, T * H, dev), S, block_size, scale,
-        _expect("out", out, dt, T * HQ * D, dev), _expect("lse", lse, f32, T * HQ, dev),
-        *_workspace(workspace, dev)))
+    nbytes = n_pages * H * page_size // 16 * 18 * D
+    if not (cache.dtype is torch.uint8 and cache.numel() >= nbytes and cache.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == dev and block_table.numel() >= R * max_pages
+            and block_table.is_contiguous() and token_req.dtype is i32 and token_req.get_device() == dev
+            and token_req.numel() >= T and token_req.is_contiguous() and token_pos.dtype is i32
+            and token_pos.get_device() == dev and token_pos.numel() >= T and token_pos.is_contiguous()
+            and out.dtype is dt and out.get_device() == dev and out.numel() >= T * HQ * D and out.is_contiguous()):
+        for x in (("cache", cache, torch.uint8, nbytes), ("block_table", block_table, i32, R * max_pages),
+                  ("token_req", token_req, i32, T), ("token_pos", token_pos, i32, T), ("out", out, dt, T * HQ * D)):
+            _expect(*x, dev)
+    ksp = vsp = ip = cp = lp = None
+    if k_scale is not None:
+        ksp = _expect("k_scale", k_scale, f32, H, dev)
+    if v_scale is not None:
+        vsp = _expect("v_scale", v_scale, f32, H, dev)
+    if block_indices is not None:
+        ip = _expect("block_indices", block_indices, i32, T * H * S, dev)
+    if block_counts is not None:
+        cp = _expect("block_counts", block_counts, i32, T * H, dev)
+    if lse is not None:
+        lp = _expect("lse", lse, f32, T * HQ, dev)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev)
+    _call(dev, _lib.bsa_fwd_cache_tokens, qp, _dtype(q), T, HQ, H, D, qs, cache.data_ptr(), n_pages, page_size,
+          block_table.data_ptr(), R, max_pages, token_req.data_ptr(), token_pos.data_ptr(), ksp, vsp, ip, cp, S,
+          block_size, scale, out.data_ptr(), lp, ws, ws_bytes, _on(dev, stream))

@@ -519,8 +519,8 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
 bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D, int64_t k_stride,
                             int64_t v_stride, const int64_t* slots, void* cache, int n_pages, int page_size,
                             const float* k_scale, const float* v_scale, void* k_val, void* v_val, void* stream) {
-    BSA_REQUIRE(k && v && slots && cache, "cache append: null pointer");
-    BSA_REQUIRE((k_val == nullptr) == (v_val == nullptr), "cache append: k_val and v_val come together");
+    BSA_REQUIRE(cache && (T == 0 || (k && v && slots)), "cache append: null pointer");
+    BSA_REQUIRE(T == 0 || (k_val == nullptr) == (v_val == nullptr), "cache append: k_val and v_val come together");
     BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "cache append: dtype");
     BSA_REQUIRE(T >= 0 && H > 0 && n_pages > 0, "cache append: sizes out of range (T=%d H=%d n_pages=%d)", T, H, n_pages);
     BSA_REQUIRE(page_size_ok(page_size), "cache append: page_size must be a power of two in 16..1024, got %d", page_size);

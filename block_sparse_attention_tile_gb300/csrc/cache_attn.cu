@@ -109,7 +109,7 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
                                 const float* k_scale, const float* v_scale, const int32_t* block_indices,
                                 const int32_t* block_counts, int S, int block_size, float scale, void* out, float* lse,
                                 void* workspace, size_t workspace_bytes, void* stream) {
-    BSA_REQUIRE(q && cache && block_table && token_req && token_pos && out, "cache attention: null pointer");
+    BSA_REQUIRE(cache && block_table && (T == 0 || (q && token_req && token_pos && out)), "cache attention: null pointer");
     BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "cache attention: dtype");
     BSA_REQUIRE(T >= 0 && H > 0 && HQ > 0 && HQ % H == 0 && n_pages > 0 && R > 0 && max_pages > 0,
                 "cache attention: sizes out of range (T=%d HQ=%d H=%d n_pages=%d R=%d max_pages=%d)", T, HQ, H, n_pages,
@@ -120,7 +120,7 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
     BSA_REQUIRE((long long)max_pages * page_size <= 0x7fffffffLL, "cache attention: max_pages * page_size must be below 2^31");
     BSA_REQUIRE(T <= 1 || q_stride >= (int64_t)HQ * D, "cache attention: a token's stride is below HQ * D");
     BSA_REQUIRE((((uintptr_t)cache | (uintptr_t)out) & 15) == 0, "cache attention: cache and out must be 16-byte aligned");
-    BSA_REQUIRE((block_indices == nullptr) == (block_counts == nullptr),
+    BSA_REQUIRE(T == 0 || (block_indices == nullptr) == (block_counts == nullptr),
                 "cache attention: block_indices and block_counts come together");
     BSA_REQUIRE(!block_indices || (S > 0 && block_size > 0 && (long long)S * block_size <= 0x7fffffffLL),
                 "cache attention: block lists need S and block_size");

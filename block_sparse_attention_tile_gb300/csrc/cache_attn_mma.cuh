@@ -40,9 +40,11 @@
 // plus 1/4 per other instruction on an SM, whether 8 or 16 warps run), so a tile of 64 keys at
 // D = 128 costs 256 + 970 / 4 = 498 cycles wide, and takes 540; its bytes take 400 at the measured
 // copy bandwidth.  Narrow it is 128 + 860 / 4, and the bytes bind.  Measured on the device: 48
-// ragged requests, 909 MB, 8 heads a KV head: 161 us, 83% of the copy bandwidth; 256 tokens of 2048
-// selected keys, 301 MB, 16 heads: 84 us, 53%.  About 7 us of a launch pass before the first tile
-// is worked on (start of the run, lookups, first copies).
+// ragged requests, 909 MB, 8 heads a KV head: 159 us, 85% of the copy bandwidth; 256 tokens of 2048
+// selected keys, 301 MB, 16 heads: 82 us, 54%.  About 7 us of a launch pass before the first tile
+// is worked on (start of the run, lookups, first copies), part of them for fetching instructions:
+// a kernel for each of the four ways instead of one with branches took 1 to 4 us less (31.2 -> 30.5 us
+// for one request of 131072 keys, 9.0 -> 8.5 us for 8 short ones).
 //
 // Tried and slower: a copying warp for four others (five warps a CTA limit registers to 168);
 // three CTAs an SM wide (168 registers, 15% more instructions); codes to float16 by shifts and masks (5.7
@@ -453,7 +455,8 @@ struct Part {
             const int e = (int)(__float_as_uint(top) >> 23);
             const int up = e == 0 || e == 255 ? 0 : min(126, 14 + 127 - e);
             const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), raw.ks);
-            rs[half] = fmaxf(fabsf(raw.ks) * __uint_as_float((uint32_t)(127 - up) << 23), 1.17549435e-38f);
+            const float size = fabsf(raw.ks) * __uint_as_float((uint32_t)(127 - up) << 23);
+            rs[half] = size < 1.17549435e-38f ? 1.17549435e-38f : size;  // a NaN stays one
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll

@@ -521,7 +521,9 @@ bsa_status bsa_cache_tables(const int32_t* old_lens, int32_t* new_lens, int R, i
  * positive, or NULL for 1.
  * k_val, v_val: [device] [T, H, D] of `dtype`, the values as stored (code * s * g,
  * rounded once to `dtype`), so that a prefill can attend to what later steps
- * will read; rows of skipped tokens are left as they were.  Both or neither. */
+ * will read; rows of skipped tokens are left as they were.  Both or neither;
+ * they must not overlap k, v or each other.  T = 0 does nothing (k, v and slots
+ * may be NULL). */
 bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D,
                             int64_t k_stride, int64_t v_stride, const int64_t* slots, void* cache,
                             int n_pages, int page_size, const float* k_scale, const float* v_scale,
@@ -549,6 +551,7 @@ bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T
  * int32 [T]; block_indices: [device] int32 [T, H, S], block_counts: [device]
  * int32 [T, H], or both NULL for every key.  block_size: a multiple of 16.
  * D a multiple of 16 up to 128.
+ * T = 0 does nothing (the token arrays may be NULL).
  * Deterministic: a row's sums run in an order fixed by the sizes and positions.
  * D = 64 and 128 run on the tensor cores, other sizes on the CUDA cores.
  * workspace: [device] bsa_cache_attention_workspace bytes, 32-byte aligned, its

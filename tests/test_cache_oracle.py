@@ -229,6 +229,13 @@ def test_an_empty_step_needs_no_launch(bsa):
     assert bsa._lib.bsa_fwd_cache_tokens(*_args(ATTEND, T=0)) == bsa.BSA_OK
 
 
+def test_an_empty_step_has_no_arrays(bsa):
+    # an empty tensor's pointer is null
+    assert bsa._lib.bsa_cache_append(*_args(APPEND, T=0, k=None, v=None, slots=None, v_val=16)) == bsa.BSA_OK
+    assert bsa._lib.bsa_fwd_cache_tokens(*_args(ATTEND, T=0, q=None, req=None, pos=None, out=None, cnt=None, ws=None,
+                                                ws_bytes=0)) == bsa.BSA_OK
+
+
 def test_sizes(bsa):
     assert bsa.bsa_cache_bytes(3, 4, 64, 128) == 3 * 4 * 4 * 18 * 128 == oracle.empty_cache(3, 4, 64, 128).nbytes
     assert bsa.bsa_cache_bytes(1 << 20, 8, 128, 128) == (1 << 20) * 8 * 8 * 2304  # past 32 bits
@@ -266,3 +273,13 @@ def test_pipeline_refuses_a_cache_of_other_sizes(bsa):
         pipeline.cache_append(rows, rows, torch.zeros(1, dtype=torch.int64), cache)
     with pytest.raises(ValueError, match="does not hold"):
         pipeline.cache_attention(rows, cache, cache, None, None)
+
+
+def test_token_cache_refuses_lengths_of_other_requests(bsa):
+    from block_sparse_attention_tile_gb300 import pipeline
+    c = pipeline.TokenCache(3, 4, 2, 1, 64, page_size=16, device="cpu")
+    for R in (2, 4):
+        with pytest.raises(ValueError, match="3 requests"):
+            c.step(torch.zeros(R, dtype=torch.int32), 8)
+    with pytest.raises(ValueError, match="another cache"):
+        pipeline.TokenCache(3, 4, 2, 1, 64, page_size=16, device="cpu", tables=c).step(c.lens, 8)

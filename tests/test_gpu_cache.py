@@ -612,6 +612,25 @@ def test_attention_propagates_nan_and_infinity_that_a_row_sees(lib, pl):
         assert o3[1, 3].isnan().all() and l3[1, 3].isnan() and torch.equal(o3[1, :3], out[1, :3])
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("HQ", [4, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_scale_that_is_no_number(lib, pl, D, HQ, dtype):
+    c = attend_case(5, 2, 1, 20, 90, HQ, 1, D, 16, 0, 0, dtype)
+    out, lse = attend(pl, c, scale=float("nan"))
+    assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("S", [0, 2])
+def test_a_step_without_tokens(lib, pl, S):
+    cache = pl.new_cache(2, 2, 16, 64)
+    rows = torch.zeros((0, 2, 64), device=DEV)
+    pl.cache_append(rows, rows, dev(np.zeros(0), torch.int64), cache, values=(rows, rows.clone()))
+    lists = (dev(np.zeros((0, 2, S))), dev(np.zeros((0, 2))), 16) if S else ()
+    out, lse = pl.cache_attention(rows, cache, dev(np.zeros((1, 2))), dev(np.zeros(0)), dev(np.zeros(0)), None, None, *lists)
+    assert out.shape == (0, 2, 64) and lse.shape == (0, 2)
+
+
 @pytest.mark.parametrize("stall", [0, 2])
 @pytest.mark.parametrize("case", [JOIN_8, JOIN_16, UNITS_8, UNITS_16, ROWS_8, ATTEND_CASES[9], ATTEND_CASES[15]],
                          ids=["join-8", "join-16", "units-8", "units-16", "rows-8", "split-lists", "split"])
