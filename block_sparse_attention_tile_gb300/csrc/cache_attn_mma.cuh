@@ -38,7 +38,7 @@
 // What bounds it: the issue slots.  mma.sync keeps a scheduler for about 8 cycles, during which
 // little else issues (measured: 32 mma with 64 cvt and 64 multiplications take 2 cycles per mma
 // plus 1/4 per other instruction on an SM, whether 8 or 16 warps run), so a tile of 64 keys at
-// D = 128 costs 256 + 970 / 4 = 498 cycles wide, and takes 540; its bytes take 400 at the measured
+// D = 128 costs 256 + 970 / 4 = 498 cycles wide, and takes about 620; its bytes take 400 at the measured
 // copy bandwidth.  Narrow it is 128 + 860 / 4, and the bytes bind.  Measured on the device: 48
 // ragged requests, 909 MB, 8 heads a KV head: 159 us, 85% of the copy bandwidth; 256 tokens of 2048
 // selected keys, 301 MB, 16 heads: 82 us, 54%.  About 7 us of a launch pass before the first tile

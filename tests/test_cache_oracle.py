@@ -152,6 +152,8 @@ def test_cache_attention_is_softmax_over_the_stored_rows():
             torch.tensor(q[t])[:, None], K[:m].transpose(0, 1).repeat_interleave(G, 0),
             V[:m].transpose(0, 1).repeat_interleave(G, 0))[:, 0]
         assert np.allclose(o[t], want.numpy(), rtol=0, atol=1e-12)
+        x = torch.einsum("hd,nhd->hn", torch.tensor(q[t]), K[:m].repeat_interleave(G, 1)) * D ** -0.5
+        assert np.allclose(lse[t], x.logsumexp(1).numpy(), rtol=0, atol=1e-12)
     # all blocks listed once in any order: the same; a block of later keys adds nothing; none: zero and -inf
     idx = np.array([[[2, 0, 1, 5]] * H] * 2)
     o2, l2 = oracle.cache_attention(q, cache, np.pad(table, ((0, 0), (0, 5))), [0, 0], pos, block_indices=idx,
