@@ -57,21 +57,21 @@ __global__ void __launch_bounds__(128) cache_attn_simt_kernel(CacheAttn a) {
             for (int j = 0; j < seen; ++j) top = fmaxf(top, Pm[tid][j]);
             const float base = top == -INFINITY ? 0.f : top;
             corr[tid] = exp2f(m[tid] - base);
-            float sum = l[tid] * corr[tid];
+            float sum = 0.f;  // of the strip first, so that a long row's sums take a sixteenth of the roundings
             for (int j = 0; j < kStrip; ++j) {
                 const float p = exp2f(Pm[tid][j] - base);
                 Pm[tid][j] = p;
                 sum += p;
             }
             m[tid] = top;
-            l[tid] = sum;
+            l[tid] = fmaf(l[tid], corr[tid], sum);
         }
         __syncthreads();
         if (tid < D)
             for (int r = 0; r < heads; ++r) {
-                float x = o[r] * corr[r];
+                float x = 0.f;
                 for (int j = 0; j < kStrip; ++j) x = fmaf(Pm[r][j], V[j][tid], x);
-                o[r] = x;
+                o[r] = fmaf(o[r], corr[r], x);
             }
     }
     __syncthreads();
