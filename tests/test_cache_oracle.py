@@ -285,3 +285,49 @@ def test_token_cache_refuses_lengths_of_other_requests(bsa):
             c.step(torch.zeros(R, dtype=torch.int32), 8)
     with pytest.raises(ValueError, match="another cache"):
         pipeline.TokenCache(3, 4, 2, 1, 64, page_size=16, device="cpu", tables=c).step(c.lens, 8)
+
+
+@pytest.mark.parametrize("lists,word", [
+    (dict(block_indices=(4, 8, 3)), "block_indices"), (dict(block_indices=(4, 2, 2, 3)), "block_indices"),
+    (dict(block_indices=(8, 3)), "block_indices"), (dict(block_indices=(3, 2, 3)), "block_indices"),
+    (dict(block_indices=(2, 4, 3)), "block_indices"),
+    (dict(block_counts=(4, 8)), "block_counts"), (dict(block_counts=(4, 2, 3)), "block_counts"),
+    (dict(block_counts=(8,)), "block_counts"), (dict(block_counts=(2, 4)), "block_counts"),
+])
+def test_attention_refuses_lists_of_other_heads(bsa, lists, word):
+    """Tensors with enough elements in another order: their rows would be read as other rows."""
+    from block_sparse_attention_tile_gb300 import pipeline
+    T, HQ, H, D = 4, 8, 2, 64
+    shapes = {"block_indices": (T, H, 3), "block_counts": (T, H), **lists}
+    a = {k: torch.zeros(s, dtype=torch.int32) for k, s in shapes.items()}
+    ints = torch.zeros(T, dtype=torch.int32)
+    with pytest.raises(ValueError, match=word):
+        pipeline.cache_attention(torch.zeros(T, HQ, D), pipeline.new_cache(2, H, 16, D, device="cpu"),
+                                 torch.zeros(1, 2, dtype=torch.int32), ints, ints, block_size=16, **a)
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 64), (3, 2, 64), (4, 64, 2), (512,)])
+def test_append_refuses_values_of_other_shapes(bsa, shape):
+    from block_sparse_attention_tile_gb300 import pipeline
+    T, H, D = 4, 2, 64
+    rows = torch.zeros(T, H, D)
+    for which in (0, 1):
+        values = [torch.zeros(T, H, D), torch.zeros(T, H, D)]
+        values[which] = torch.zeros(shape)
+        with pytest.raises(ValueError, match="values"):
+            pipeline.cache_append(rows, rows, torch.zeros(T, dtype=torch.int64),
+                                  pipeline.new_cache(2, H, 16, D, device="cpu"), values=tuple(values))
+
+
+def test_longer_buffers_of_the_right_rows_pass_the_shape_checks(bsa):
+    """Buffers for more tokens than the call's go on to the next check (here: no CUDA tensor)."""
+    from block_sparse_attention_tile_gb300 import pipeline
+    T, HQ, H, D = 4, 8, 2, 64
+    ints, cache = torch.zeros(9, dtype=torch.int32), pipeline.new_cache(2, H, 16, D, device="cpu")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pipeline.cache_attention(torch.zeros(T, HQ, D), cache, torch.zeros(1, 2, dtype=torch.int32), ints, ints,
+                                 torch.zeros(H), torch.zeros(H), torch.zeros(9, H, 3, dtype=torch.int32),
+                                 torch.zeros(9, H, dtype=torch.int32), 16)
+    rows, long = torch.zeros(T, H, D), torch.zeros(9, H, D)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pipeline.cache_append(rows, rows, torch.zeros(9, dtype=torch.int64), cache, values=(long, long))
