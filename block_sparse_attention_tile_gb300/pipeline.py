@@ -365,12 +365,19 @@ def _check_rows(name, t, T, *rest):
         raise ValueError("%s: a tensor %s is needed, got %s" % (name, [T, *rest], tuple(t.shape)))
 
 
+def _check_scales(k_scale, v_scale, H):
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and t.numel() != H:
+            raise ValueError("%s: a scale for each of %d KV heads is needed, got %s" % (name, H, tuple(t.shape)))
+
+
 def cache_append(k, v, slots, cache, k_scale=None, v_scale=None, values=None):
     """K and V rows [T, H, D] (token stride free) rounded to 4 bits into their slots of the cache.  ``values``: a
     pair of [T, H, D] tensors (or longer ones) that receive the rows as the cache holds them."""
     T, H, D = k.shape
     if cache.shape[1] != H or cache.shape[3] != 18 * D:
         raise ValueError("cache %s does not hold %d heads of %d channels" % (tuple(cache.shape), H, D))
+    _check_scales(k_scale, v_scale, H)
     kv, vv = (None, None) if values is None else values
     _check_rows("values", kv, T, H, D)
     _check_rows("values", vv, T, H, D)
@@ -387,6 +394,8 @@ def cache_attention(q, cache, block_table, token_req, token_pos, k_scale=None, v
     if width != 18 * D:
         raise ValueError("cache %s does not hold %d channels" % (tuple(cache.shape), D))
     R, max_pages = block_table.shape
+    if k_scale is not None or v_scale is not None:
+        _check_scales(k_scale, v_scale, H)
     S = 0
     if block_indices is not None:
         S = block_indices.shape[-1]

@@ -319,6 +319,19 @@ def test_append_refuses_values_of_other_shapes(bsa, shape):
                                   pipeline.new_cache(2, H, 16, D, device="cpu"), values=tuple(values))
 
 
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("shape", [(8,), (1,), (2, 64), (4, 2)])
+def test_scales_of_other_heads_are_refused(bsa, name, shape):
+    from block_sparse_attention_tile_gb300 import pipeline
+    T, HQ, H, D = 4, 8, 2, 64
+    cache, rows = pipeline.new_cache(2, H, 16, D, device="cpu"), torch.zeros(T, H, D)
+    ints, scale = torch.zeros(T, dtype=torch.int32), {name: torch.zeros(shape)}
+    with pytest.raises(ValueError, match=name):
+        pipeline.cache_attention(torch.zeros(T, HQ, D), cache, torch.zeros(1, 2, dtype=torch.int32), ints, ints, **scale)
+    with pytest.raises(ValueError, match=name):
+        pipeline.cache_append(rows, rows, torch.zeros(T, dtype=torch.int64), cache, **scale)
+
+
 def test_longer_buffers_of_the_right_rows_pass_the_shape_checks(bsa):
     """Buffers for more tokens than the call's go on to the next check (here: no CUDA tensor)."""
     from block_sparse_attention_tile_gb300 import pipeline
