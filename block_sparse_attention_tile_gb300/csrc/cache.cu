@@ -380,13 +380,14 @@ __device__ __forceinline__ uint2 quantise16(const Group<T>& g, float head_scale,
     const uint32_t sb = finite ? f32_to_e4m3(__fdiv_rn(top, kE2M1Max)) : 0x7fu;
     const uint32_t s16 = e4m3x2_to_f16x2(sb | sb << 8);  // (s, s)
     const float s = f16x2_to_f32(s16).x, r = s > 0.f ? __frcp_rn(s) : 0.f;  // a scale of zero stores zeros
-    // two at a time; adding -0 leaves a product as it is
-    const float2 inv2 = make_float2(inv, inv), r2 = make_float2(r, r), s2 = make_float2(-s, -s), none = make_float2(-0.f, -0.f);
+    // Two at a time; adding -0 leaves a product as it is.  From -y, with -r: of y = -0 the remainder q0 s + (-y) is +0
+    // and -r of it -0, so the quotient keeps its sign (y - q0 s would be +0, and +0 r + -0 is +0).
+    const float2 inv2 = make_float2(-inv, -inv), r2 = make_float2(-r, -r), s2 = make_float2(s, s), none = make_float2(-0.f, -0.f);
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 y = ptx::ffma2(make_float2(element<T>(g, 2 * i), element<T>(g, 2 * i + 1)), inv2, none);
-        const float2 q0 = ptx::ffma2(y, r2, none), q = ptx::ffma2(ptx::ffma2(q0, s2, y), r2, q0);
+        const float2 ny = ptx::ffma2(make_float2(element<T>(g, 2 * i), element<T>(g, 2 * i + 1)), inv2, none);
+        const float2 q0 = ptx::ffma2(ny, r2, none), q = ptx::ffma2(ptx::ffma2(q0, s2, ny), r2, q0);
         const uint32_t two = f32x2_to_e2m1x2(q.x, q.y);
         w[i >> 2] |= two << (8 * (i & 3));
         if constexpr (kValues) {

@@ -262,6 +262,29 @@ def test_append_borders_and_non_finite(lib, pl):
             assert np.array_equal(vals[which][t, 0].double().cpu().numpy(), want)
 
 
+def test_append_stores_the_sign_of_zero(lib, pl):
+    """Bytes of zeros with a sign: in a group of numbers, of zeros, and where x / g underflows (g = 4)."""
+    for dtype in (torch.float32, torch.bfloat16):
+        tiny = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133  # the smallest numbers
+        rows = torch.zeros((5, 1, 32), dtype=dtype)
+        rows[0] = torch.linspace(-3, 3, 32).to(dtype)
+        rows[0, 0, 1::2] = -0.0
+        rows[1, 0, ::3] = -0.0                       # groups of zeros only
+        rows[2, 0] = torch.tensor([-tiny, tiny]).repeat(16).to(dtype)
+        rows[2, 0, 0], rows[2, 0, 31] = 5.0, -5.0
+        rows[3, 0] = torch.tensor([-tiny, 0.0, tiny, -0.0]).repeat(8).to(dtype)
+        rows[4, 0, 20] = -448 * 6.0
+        rows[4, 0, 21:] = -0.0
+        for g in (1.0, 4.0):
+            scale, slots = np.full(1, g, np.float32), np.arange(5)
+            cache = torch.full((1, 1, 1, 18 * 32), 0xAA, dtype=torch.uint8, device=DEV)
+            d = rows.to(DEV)
+            pl.cache_append(d, -d, dev(slots, torch.int64), cache, dev(scale, torch.float32), dev(scale, torch.float32))
+            x = rows.double().numpy()
+            want = oracle_bytes(np.full((1, 1, 1, 18 * 32), 0xAA, np.uint8), slots, x, -x, scale, scale)
+            assert np.array_equal(cache.cpu().numpy(), want), (dtype, g)
+
+
 def test_append_reports_a_slot_outside_the_cache(lib, pl):
     x = torch.randn((3, 1, 16), device=DEV)
     cache = pl.new_cache(2, 1, 16, 16)
