@@ -76,6 +76,7 @@ _SIGS = {
     "bsa_cache_tables": (I, [P, P, I, I, P, I, P, I, P, P, P, P, P, P, I, P, SZ, P]),
     "bsa_cache_append": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P]),
     "bsa_cache_attention_workspace": (SZ, [I, I, I, I, I]),
+    "bsa_cache_attention_way": (I, [I, I, I, I, I, I, I]),
     "bsa_fwd_cache_tokens": (I, [P, I, I, I, I, I, I64, P, I, I, P, I, I, P, P, P, P, P, P, I, I, F, P, P, P, SZ, P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -415,6 +416,11 @@ def bsa_cache_append(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale=No
 @functools.lru_cache(maxsize=1024)
 def bsa_cache_attention_workspace(T, HQ, H, D, max_keys):
     return _lib.bsa_cache_attention_workspace(T, HQ, H, D, max_keys)
+
+
+def bsa_cache_attention_way(T, HQ, H, D, dtype, lists, max_keys):
+    return _lib.bsa_cache_attention_way(T, HQ, H, D, BSA_F32 if dtype is torch.float32 else BSA_BF16, 1 if lists else 0,
+                                        max_keys)
 
 
 def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table, R, max_pages, token_req, token_pos,

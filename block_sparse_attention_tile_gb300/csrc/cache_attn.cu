@@ -103,6 +103,11 @@ size_t bsa_cache_attention_workspace(int T, int HQ, int H, int D, int max_keys) 
     return mma_cache_attention_workspace(T, HQ, H, D, max_keys);
 }
 
+int bsa_cache_attention_way(int T, int HQ, int H, int D, bsa_dtype dtype, int lists, int max_keys) {
+    if (T < 1 || H < 1 || HQ < 1 || HQ % H || max_keys < 1 || D < 16 || D > 128 || D % 16) return -1;
+    return on_tensor_cores(D) ? mma_cache_attention_way(T, HQ, H, D, dtype == BSA_F32, lists != 0, max_keys) : 0;
+}
+
 bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, int H, int D, int64_t q_stride,
                                 const void* cache, int n_pages, int page_size, const int32_t* block_table, int R,
                                 int max_pages, const int32_t* token_req, const int32_t* token_pos,

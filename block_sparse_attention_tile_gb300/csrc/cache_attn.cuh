@@ -86,6 +86,7 @@ __device__ __forceinline__ int strip_index(const CacheAttn& a, const Row& r, int
 
 // The tensor-core kernels (D = 64 or 128).
 size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_keys);
+int mma_cache_attention_way(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys);
 bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
                                cudaStream_t st);
 

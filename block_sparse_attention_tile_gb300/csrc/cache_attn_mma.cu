@@ -71,6 +71,10 @@ size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_
     return most;
 }
 
+int mma_cache_attention_way(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys) {
+    return 1 + (int)cut(T, HQ, H, D, f32, lists, max_keys).mode;
+}
+
 bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long max_keys, void* workspace,
                                cudaStream_t st) {
     if ((long long)a.T * a.H * ((a.HQ / a.H + 15) / 16) > 0x7fffffffLL)

@@ -25,7 +25,8 @@ bool force_simt();
 
 // Tests of the bounded waits only: BSA_TEST_STALL_TILE = n makes the next
 // tensor-core token attention leave the K loads of each CTA's n-th tile
-// unissued and limit every wait to 1 ms, so the waits run out, the kernel
+// unissued, and the next tensor-core cache attention all copies of each warp's
+// n-th tile, and limits every wait to 1 ms, so the waits run out, the kernel
 // latches BSA_ERR_TIMEOUT and returns.  -1 (the default) when unset.
 int test_stall_tile();
 

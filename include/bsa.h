@@ -558,6 +558,10 @@ bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T
  * contents meaningless between calls; max_keys is the most keys that a row can
  * see: S * block_size with lists, else max_pages * page_size. */
 size_t bsa_cache_attention_workspace(int T, int HQ, int H, int D, int max_keys);
+/* Which kernel a call of these sizes takes (lists: whether it has block lists), for profiles and tests: 0 CUDA
+ * cores; tensor cores with 1 a row to a cluster of CTAs, 2 equal runs of tiles and a join, 3 whole rows to clusters,
+ * 4 whole rows to warps; -1 for sizes out of range. */
+int bsa_cache_attention_way(int T, int HQ, int H, int D, bsa_dtype dtype, int lists, int max_keys);
 bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, int H, int D, int64_t q_stride,
                                 const void* cache, int n_pages, int page_size, const int32_t* block_table,
                                 int R, int max_pages, const int32_t* token_req, const int32_t* token_pos,

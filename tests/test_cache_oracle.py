@@ -246,6 +246,18 @@ def test_sizes(bsa):
     assert bsa.bsa_cache_tables_workspace(2401) == (8 + 2 * 2402) * 4 and bsa.bsa_cache_tables_workspace(2400) == 0
 
 
+def test_way_of_sizes(bsa):
+    way = bsa.bsa_cache_attention_way
+    assert way(8, 8, 2, 96, torch.bfloat16, False, 600) == 0              # head sizes without a tensor-core kernel
+    assert way(1, 64, 4, 128, torch.bfloat16, True, 16 * 64) == 1         # few rows: a cluster each
+    assert way(48, 64, 8, 128, torch.bfloat16, False, 32768) == 2         # long rows: equal runs
+    assert way(256, 64, 4, 128, torch.bfloat16, True, 16 * 128) == 3      # many lists of one length
+    assert way(2048, 64, 4, 128, torch.float32, True, 16 * 64) == 4       # more than six rows a warp
+    for bad in (dict(T=0), dict(HQ=7), dict(H=0), dict(D=40), dict(D=144), dict(max_keys=0)):
+        a = {**dict(T=8, HQ=8, H=2, D=64, dtype=torch.float32, lists=True, max_keys=64), **bad}
+        assert way(*a.values()) == -1
+
+
 def test_binding_refuses_tensors_that_do_not_fit(bsa):
     cpu = torch.zeros(8, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA tensor"):

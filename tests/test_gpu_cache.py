@@ -834,3 +834,152 @@ def test_prefill_over_the_stored_values_agrees_with_decoding_them(lib, pl):
     a, b = out.float(), want[0].float()
     assert (a - b).abs().max() <= 2 * 2e-2 and (a - b).norm() / b.norm() <= 2 * 5e-3
     assert (lse - wl[0])[live].abs().max() <= 2e-3
+
+
+# ---------------------------------------------------------------- every kernel that the sizes choose
+
+WAYS = ("cuda cores", "split", "stream", "units", "rows")
+
+
+def way_of(lib, c):
+    """The kernel that this batch takes."""
+    T, HQ, D = c["q"].shape
+    H, P = c["cache"].shape[1], c["cache"].shape[2] * 16
+    most = c["table"].shape[1] * P if c["idx"] is None else c["idx"].shape[2] * c["BS"]
+    return WAYS[lib.bsa_cache_attention_way(T, HQ, H, D, c["q"].dtype, c["idx"] is not None, most)]
+
+
+def rows_of(c, pick):
+    """The batch's tokens of these numbers."""
+    return {**c, **{k: c[k][pick] for k in ("q", "req", "pos", "idx", "cnt") if c[k] is not None}}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["float32", "bfloat16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [3, 12])
+@pytest.mark.parametrize("way", WAYS[1:])
+def test_attention_every_kernel(lib, pl, way, G, D, dtype):
+    """Each of the tensor-core kernels (way x up to 8 or more heads x D x type) on ragged rows with padding tokens:
+    rows from across the batch against the oracle, all of them against the CUDA-core kernel (as in
+    test_attention_batches), and twice the same bits."""
+    R, n, lo, hi, P, S, BS = {"split": (3, 1, 300, 1300, 64, 0, 0), "stream": (130, 1, 1, 1300, 64, 0, 0),
+                              "units": (150, 2, 2, 900, 32, 9, 64), "rows": (4, 700, 700, 1500, 16, 5, 64)}[way]
+    c = attend_case(G + D, R, n, lo, hi, 4 * G, 4, D, P, S, BS, dtype)
+    assert way_of(lib, c) == way
+    T = R * n
+    rng = np.random.default_rng(T)
+    pad = rng.random(T) < (0.05 if T > 10 else 0)
+    c["req"] = np.where(pad, -1, c["req"])
+    out, lse = attend(pl, c)
+    again = attend(pl, c)
+    live = torch.as_tensor(~pad, device=DEV)
+    assert torch.equal(out[live], again[0][live]) and torch.equal(lse[live], again[1][live])
+    pick = np.unique(np.linspace(0, T - 1, 9).astype(int))
+    check_attend(out[pick], lse[pick], want_attend(rows_of(c, pick)))
+    set_force_simt(True)
+    o2, l2 = attend(pl, c)
+    both = live[:, None] & torch.isfinite(l2)
+    assert torch.equal(both, live[:, None] & torch.isfinite(lse))
+    a, b = out.float()[both], o2.float()[both]
+    u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -14
+    assert (a - b).norm() <= 2 * u * b.norm()
+    assert (lse - l2)[both].abs().max() <= 2.0 ** -14 * (1 + l2[both].abs().max())
+
+
+def growing_case(seed, T, n, G, H, D, S, dtype):
+    """T tokens of one request near its n-th key, whose K scales grow along the keys; with S, ascending lists of S
+    blocks of 128.  Heads are sharp by other amounts, so each moves its maximum at other keys."""
+    P, rng = 64, np.random.default_rng(seed)
+    c = attend_case(seed, 1, 1, n, n, G * H, H, D, P, 0, 0, dtype, scales=False)
+    p = np.arange(n)
+    grow = (0x20 + p * 0x30 // n).astype(np.uint8)  # 2^-3 .. 2^3
+    cols = 16 * D + (p % 16)[:, None] * (D // 16) + np.arange(D // 16)
+    for h in range(H):
+        c["cache"][c["table"][0, p // P][:, None], h, (p % P // 16)[:, None], cols] = grow[:, None]
+    q = rng.standard_normal((T, G * H, D)) * np.logspace(-1, 0.3, G * H)[:, None]
+    c["q"] = torch.tensor(q, dtype=dtype)
+    c["req"], c["pos"] = np.zeros(T, np.int64), n - 1 - rng.integers(0, 100, T)
+    if S:
+        pool = np.argsort(rng.random((T, H, n // 128)), axis=2)[:, :, :S]
+        c["idx"], c["cnt"], c["BS"] = np.sort(pool, axis=2), np.full((T, H), S), 128
+    return c
+
+
+# tokens, keys, KV heads, blocks of 128: rows of 23 tiles of 64 keys in runs of nine tiles a warp and more, whole rows
+# of 20 tiles shared by a cluster's warps, whole rows of 20 tiles a warp; a row of 19 tiles over four warps
+GROWING = {"split": (60, 1200, 4, 0), "stream": (700, 1500, 2, 0), "units": (300, 2000, 4, 10), "rows": (2800, 2000, 4, 10)}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["float32", "bfloat16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [5, 16])
+@pytest.mark.parametrize("way", WAYS[1:])
+def test_attention_maxima_move_through_long_runs(lib, pl, way, G, D, dtype):
+    """Each row's sum and output are rescaled by its own factor, many times in one warp's run of tiles."""
+    T, n, H, S = GROWING[way]
+    if way == "split" and G > 8:
+        T = 40  # two CTAs an SM
+    c = growing_case(G, T, n, G, H, D, S, dtype)
+    assert way_of(lib, c) == way
+    out, lse = attend(pl, c)
+    pick = np.unique(np.linspace(0, T - 1, 7).astype(int))
+    check_attend(out[pick], lse[pick], want_attend(rows_of(c, pick)))
+
+
+def on_device(c):
+    """The arguments of cache_attention for this batch."""
+    f = torch.float32
+    return (c["q"].to(DEV), dev(c["cache"], torch.uint8), dev(c["table"]), dev(c["req"]), dev(c["pos"]),
+            None if c["ks"] is None else dev(c["ks"], f), None if c["vs"] is None else dev(c["vs"], f),
+            None if c["idx"] is None else dev(c["idx"]), None if c["cnt"] is None else dev(c["cnt"]), c["BS"])
+
+
+ROWS_16 = (70, 30, 30, 200, 48, 4, 128, 16, 6, 16, torch.bfloat16)
+
+
+@pytest.mark.parametrize("pair", [(JOIN_8, JOIN_16), (UNITS_16, UNITS_8), (ROWS_8, ROWS_16), (JOIN_8, ROWS_8)],
+                         ids=["stream", "units", "rows", "stream-rows"])
+def test_two_streams_keep_parts_and_counters_apart(lib, pl, pair):
+    """Batches with parts in a workspace, a join launched early, or the stream's work counter, interleaved on two
+    streams: the bits of calls made one by one."""
+    assert {way_of(lib, attend_case(0, *x)) for x in pair} <= {"stream", "units", "rows"}
+    args = [on_device(attend_case(sum(x[:-1]), *x)) for x in pair]
+    want = []
+    for a in args:
+        want.append(pl.cache_attention(*a))
+        torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for i in range(8):
+        for s, a, to in zip(streams, args, got):
+            with torch.cuda.stream(s):
+                to.append(pl.cache_attention(*a))
+        if i == 3:  # the other way round, behind a call on the first stream
+            streams.reverse()
+            streams[0].wait_stream(streams[1])
+            streams[1].wait_stream(streams[0])
+    torch.cuda.synchronize()
+    for (o, l), to in zip(want, got):
+        assert all(torch.equal(o, out) and torch.equal(l, lse) for out, lse in to)
+
+
+@pytest.mark.parametrize("stall", [0, 2, 3])
+@pytest.mark.parametrize("G", [5, 16])
+@pytest.mark.parametrize("way", WAYS[1:])
+def test_attention_wait_that_expires_late_is_reported(lib, pl, way, G, stall):
+    """Runs of four tiles and more: a later tile of each warp is never copied, when parts have been written and rows
+    claimed already.  The expiry (1 ms under the switch) is reported, and the next call is as before."""
+    T, n, H, S = GROWING[way]
+    if way == "split" and G > 8:
+        T = 40
+    c = growing_case(G, T, n, G, H, 128, S, torch.bfloat16)
+    assert way_of(lib, c) == way
+    args = on_device(c)
+    want = pl.cache_attention(*args)
+    os.environ["BSA_TEST_STALL_TILE"] = str(stall)
+    try:
+        pl.cache_attention(*args)
+    finally:
+        os.environ.pop("BSA_TEST_STALL_TILE")
+    assert lib.bsa_device_status() == lib.BSA_ERR_TIMEOUT
+    out, lse = pl.cache_attention(*args)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
