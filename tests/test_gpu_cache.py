@@ -983,3 +983,60 @@ def test_attention_wait_that_expires_late_is_reported(lib, pl, way, G, stall):
     assert lib.bsa_device_status() == lib.BSA_ERR_TIMEOUT
     out, lse = pl.cache_attention(*args)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+@pytest.mark.parametrize("D", [80, 128])
+def test_pages_past_32_bits_of_bytes(lib, pl, D):
+    """Pages on both sides of the cache's 2^31st and 2^32nd byte hold what the same pages of a small cache hold."""
+    H, P, G = 4, 64, 4
+    page = H * (P // 16) * 18 * D
+    n_pages = 2 ** 32 // page + 3
+    ids = sorted({0, 2 ** 31 // page - 1, 2 ** 31 // page, 2 ** 31 // page + 1, 2 ** 32 // page - 1, 2 ** 32 // page, n_pages - 1})
+    n = len(ids) * P - 5
+    x = torch.randn((n, H * (G + 2), D), device=DEV).bfloat16()
+    got = []
+    for pages, ids_of in ((n_pages, ids), (len(ids), list(range(len(ids))))):
+        cache = torch.full((pages, H, P // 16, 18 * D), 0xFF, dtype=torch.uint8, device=DEV)
+        p = torch.arange(n, device=DEV)
+        table = dev([ids_of])
+        pl.cache_append(x[:, H * G:H * G + H], x[:, H * G + H:], table[0].long()[p // P] * P + p % P, cache)
+        req, pos = dev(np.zeros(9)), dev(np.linspace(0, n - 1, 9).astype(int))
+        out = pl.cache_attention(x[:9, :H * G], cache, table, req, pos)
+        got.append((cache[dev(ids_of).long()], *out))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][1].isfinite().all()
+
+
+def test_rows_past_32_bits_of_elements(lib, pl):
+    """Queries, outputs and appended rows past the 2^31st element: the last tokens as in a call of their own."""
+    T, H, G, D, P = 2 ** 31 // (64 * 128) + 70, 4, 16, 128, 64
+    q = torch.zeros((T, H * G, D), dtype=torch.bfloat16, device=DEV)
+    q[-80:] = torch.randn((80, H * G, D), device=DEV)
+    cache, table, n = pl.new_cache(3, H, P, D), dev([[2, 0, 1]]), 3 * P
+    x, p = torch.randn((n, 2 * H, D), device=DEV).bfloat16(), torch.arange(n, device=DEV)
+    pl.cache_append(x[:, :H], x[:, H:], table[0].long()[p // P] * P + p % P, cache)
+    req, pos = torch.zeros(T, dtype=torch.int32, device=DEV), torch.arange(T, device=DEV).remainder(n).int()
+    idx = torch.arange(T * H, device=DEV).remainder(12).int().view(T, H, 1)
+    cnt = torch.ones((T, H), dtype=torch.int32, device=DEV)
+    whole = pl.cache_attention(q, cache, table, req, pos, None, None, idx, cnt, 16)
+    last = pl.cache_attention(q[-80:], cache, table, req[-80:], pos[-80:], None, None, idx[-80:], cnt[-80:], 16)
+    empty = torch.isneginf(last[1])
+    assert torch.equal(empty, torch.isneginf(whole[1][-80:])) and not empty.all()
+    # one row to a warp or to a cluster: other orders of the same sums, so bf16 outputs are a rounding each apart
+    a, b = whole[0][-80:].float(), last[0].float()
+    assert (a - b).norm() <= 2 * 2.0 ** -8 * b.norm()
+    assert (whole[1][-80:] - last[1])[~empty].abs().max() <= 2.0 ** -14 * (1 + last[1][~empty].abs().max())
+    del q, whole, last
+    H = 32
+    T = 2 ** 31 // (2 * H * D) + 70
+    rows = torch.zeros((T, 2 * H, D), dtype=torch.bfloat16, device=DEV)
+    rows[-80:] = torch.randn((80, 2 * H, D), device=DEV)
+    slots = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    slots[-80:] = torch.arange(80, device=DEV).flip(0) + 11
+    vals = tuple(torch.zeros((T, H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    a, b = pl.new_cache(2, H, P, D), pl.new_cache(2, H, P, D)
+    pl.cache_append(rows[:, :H], rows[:, H:], slots, a, values=vals)
+    some = tuple(torch.zeros((80, H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pl.cache_append(rows[-80:, :H], rows[-80:, H:], slots[-80:], b, values=some)
+    assert torch.equal(a, b) and a.any() and all(torch.equal(x[-80:], y) and not x[:-80].any() for x, y in zip(vals, some))
