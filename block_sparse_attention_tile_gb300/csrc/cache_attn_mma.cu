@@ -54,6 +54,7 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
         z.ml = slots * sizeof(float2);
         z.begun = z.mode == kUnits ? 0 : (size_t)rows * sizeof(int2);
     }
+    if (!f32 && tiles > kAside) z.aside = (size_t)grid * kWarps * (narrow ? 8 : 16) * D * sizeof(float);
     return z;
 }
 
@@ -66,7 +67,7 @@ size_t mma_cache_attention_workspace(int T, int HQ, int H, int D, long long max_
     size_t most = 0;  // of both types, with and without lists: a workspace is asked for by sizes alone
     for (int k = 0; k < 4; ++k) {
         const Sizes z = cut(T, HQ, H, D, k & 1, k >> 1, max_keys);
-        most = std::max(most, z.part + z.ml + z.begun);
+        most = std::max(most, z.aside + z.part + z.ml + z.begun);
     }
     return most;
 }
@@ -81,9 +82,10 @@ bsa_status mma_cache_attention(const CacheAttn& a, bsa_dtype dtype, long long ma
         return fail(BSA_ERR_UNSUPPORTED, "cache attention: too many (token, head) rows");
     Sizes z = cut(a.T, a.HQ, a.H, a.D, dtype == BSA_F32, a.blocks != nullptr, max_keys);
     char* ws = static_cast<char*>(workspace);
-    z.plan.part = reinterpret_cast<float*>(ws);
-    z.plan.ml = reinterpret_cast<float2*>(ws + z.part);
-    z.plan.begun = reinterpret_cast<int2*>(ws + z.part + z.ml);
+    z.plan.aside = z.aside ? reinterpret_cast<float*>(ws) : nullptr;  // first: it needs the workspace's alignment
+    z.plan.part = reinterpret_cast<float*>(ws + z.aside);
+    z.plan.ml = reinterpret_cast<float2*>(ws + z.aside + z.part);
+    z.plan.begun = reinterpret_cast<int2*>(ws + z.aside + z.part + z.ml);
     const bool narrow = a.HQ / a.H <= 8;
     if (dtype == BSA_F32) return a.D == 128 ? launch_128_f32(a, z, narrow, st) : launch_64_f32(a, z, narrow, st);
     return a.D == 128 ? launch_128_bf16(a, z, narrow, st) : launch_64_bf16(a, z, narrow, st);

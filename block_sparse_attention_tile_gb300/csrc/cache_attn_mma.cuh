@@ -65,6 +65,13 @@ constexpr int kTile = 4;     // strips of a tile, at most
 constexpr uint64_t kWaitNs = 500ull * 1000 * 1000;
 constexpr float kWeightLog2 = 11.f;  // weights are held 2^11 times, relative to a reference
 constexpr float kSlack = 4.f;        // that the running maximum may pass by 2^4 before it is moved
+// The tensor cores cut sums off rather than round them, each time by up to a step of the running sum, so a run of n
+// keys brings values of one sign out short by about 6e-9 n: 8e-4 of them at 131072 keys, 3e-3 at half a million.  bf16
+// outputs therefore put their sums aside every so many tiles, where they are added up rounded to nearest (float32 ones
+// add every strip so): 5e-5 short at most, an eightieth of the output's own rounding.  Measured, us, without, with 256,
+// 128 and 64 tiles: 300 requests of 32768 keys, 16 heads on each of 4, 1161, 1166, 1171, 1176; 8 on 8, 1708, 1735,
+// 1742, 1753.
+constexpr int kAside = 128;
 
 enum Mode { kSplit, kStream, kUnits, kRows };
 
@@ -83,6 +90,7 @@ struct Plan {
     float* part;      // kStream, kUnits: [warps][2][rows of U][D], slot 0 a row carried on, slot 1 a row begun
     float2* ml;       // [warps][2][rows of U]
     int2* begun;      // [rows] the warp that began a cut row and in how many parts it is (0: whole)
+    float* aside;     // [warps][rows of U][D] sums of runs longer than kAside tiles, or null: no row has as many
 };
 
 // ---------------------------------------------------------------- pieces
@@ -232,6 +240,7 @@ __device__ __forceinline__ int tiles_of(const Row& r, const Plan& p) {
 
 // Flags of a tile.
 constexpr int kBegin = 1, kEnd = 2, kCarried = 4, kCut = 8;
+constexpr int kPut = 16, kHeld = 32;  // the row's sums are put aside behind this tile; they were behind an earlier one
 
 // The tiles of a warp, looked up eight at a time (lane 4 i + j: strip j of the batch's tile i), a
 // batch ahead of the first copy that needs it.
@@ -289,9 +298,13 @@ struct Ahead {
             if (first >= 0) page = a.table[(long long)r.req * a.max_pages + (first >> a.sh)];
         }
     }
+    template <bool kPuts>
     __device__ __forceinline__ int flags() const {
         const int t = off + at;
-        return (t == lo ? kBegin : 0) | (t == hi - 1 ? kEnd : 0) | (lo > 0 ? kCarried : 0) | (lo > 0 || hi < n ? kCut : 0);
+        int f = (t == lo ? kBegin : 0) | (t == hi - 1 ? kEnd : 0) | (lo > 0 ? kCarried : 0) | (lo > 0 || hi < n ? kCut : 0);
+        if constexpr (kPuts)
+            if (t - lo >= kAside - 1) f |= ((t - lo) % kAside == kAside - 1 && t < hi - 1 ? kPut : 0) | (t - lo >= kAside ? kHeld : 0);
+        return f;
     }
 };
 
@@ -730,6 +743,34 @@ struct Part {
         if constexpr (kNarrow) return u[i / 2][(i & 1) * 2 + r];
         else return u[i % kCh][2 * r + i / kCh];
     }
+
+    // Sums of a long run beside U: at `at` (the warp's, kept lane by lane in runs of eight 256 floats apart) relative
+    // to references `was`, -inf while there are none.  U += those.
+    __device__ __forceinline__ void add_aside(const float* at, const float* was, int lane) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float f = was[r] == -INFINITY ? 0.f : ptx::ex2(was[r] - m[r]);
+#pragma unroll
+            for (int i = 0; i < kRun; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(at + r * (S::kRows * D / 2) + i / 8 * 256 + lane * 8 + i % 8);
+                ref(r, i) = fmaf(x.x, f, ref(r, i)), ref(r, i + 1) = fmaf(x.y, f, ref(r, i + 1));
+                ref(r, i + 2) = fmaf(x.z, f, ref(r, i + 2)), ref(r, i + 3) = fmaf(x.w, f, ref(r, i + 3));
+            }
+        }
+    }
+    __device__ __forceinline__ void put_aside(float* at, float* was, int lane) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            was[r] = m[r];
+#pragma unroll
+            for (int i = 0; i < kRun; i += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = ref(r, i + k), ref(r, i + k) = 0.f;
+                ptx::st_global_v8(at + r * (S::kRows * D / 2) + i * 32 + lane * 8, reinterpret_cast<const uint32_t*>(v));
+            }
+        }
+    }
 };
 
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -750,7 +791,8 @@ __device__ __forceinline__ void write_out(const CacheAttn& a, const Where& w, in
 
 // ---------------------------------------------------------------- the kernel
 
-template <int D, typename T, bool kNarrow, Mode M>
+// kPuts: rows may have more tiles than kAside, and bf16 outputs.
+template <int D, typename T, bool kNarrow, Mode M, bool kPuts>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) cache_attn_mma_kernel(CacheAttn a, Plan p) {
     using S = Shape<D, T, kNarrow>;
     using P = Part<D, T, kNarrow>;
@@ -818,7 +860,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
         int* mt = meta + stage * 8;
         if (mine) mt[lane & 3] = first;
         if (lane == 0) {
-            mt[4] = ahead.row, mt[5] = ahead.r.pos, mt[6] = ahead.flags();
+            mt[4] = ahead.row, mt[5] = ahead.r.pos, mt[6] = ahead.flags<kPuts>();
             ptx::mbar_arrive_expect_tx(full + stage * 8, __popc(live) * S::kStripB);
         }
         __syncwarp();
@@ -858,6 +900,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
     auto unit_part = [&](int of, int r, int ln) {
         return p.part + (long long)of * 2 * S::kRows * D + r * (S::kRows * D / 2) + ln * 8;
     };
+    float was[2];
+    auto aside = [&] { return p.aside + (long long)id * S::kRows * D; };
     bool alive = true;
     {
         typename P::Raw raw;  // the first row's queries while its first tiles are looked up
@@ -895,9 +939,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, T, kNarrow>::kBlocks) ca
         }
         __syncwarp();
         if (++stage == kStages) stage = 0, parity ^= 1;
-        if (M != kSplit && (tag.z & kEnd)) {
+        if (M != kSplit && (tag.z & (kEnd | kPut))) {
+            if (kPuts && (tag.z & kHeld)) part.add_aside(aside(), was, lane);
             part.totals(sum);
-            if (M == kRows || !(tag.z & kCut)) {
+            if (kPuts && (tag.z & kPut)) {
+                part.put_aside(aside(), was, lane);
+            } else if (M == kRows || !(tag.z & kCut)) {
                 finish(tag.x);
             } else if (M == kStream || (tag.z & kCarried)) {
 #pragma unroll
@@ -1102,13 +1149,13 @@ struct Sizes {
     Mode mode;
     Plan plan;
     int grid;
-    size_t part, ml, begun;  // workspace bytes
+    size_t part, ml, begun, aside;  // workspace bytes
 };
 
-template <int D, typename T, bool kNarrow, Mode M>
+template <int D, typename T, bool kNarrow, Mode M, bool kPuts>
 static bsa_status launch_mode(const CacheAttn& a, const Plan& p, int grid, cudaStream_t st) {
     using S = Shape<D, T, kNarrow>;
-    auto kern = cache_attn_mma_kernel<D, T, kNarrow, M>;
+    auto kern = cache_attn_mma_kernel<D, T, kNarrow, M, kPuts>;
     if (!once_per_device([&] {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) == cudaSuccess;
         }))
@@ -1147,12 +1194,17 @@ static bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     p.warps = z.grid * kWarps;
     p.stall = test_stall_tile();
     p.work = z.mode == kRows ? sched_counter(st) : nullptr;
+    // A split row's warp has five tiles at most.  Rows that are short by their sizes have a kernel of their own: what
+    // the other one holds for long ones costs 279 us instead of 274 (2048 tokens of 16 blocks of 64).
+    constexpr bool kPuts = Shape<D, T, kNarrow>::kTerms == 1;
     switch (z.mode) {
-        case kSplit: return launch_mode<D, T, kNarrow, kSplit>(a, p, z.grid, st);
-        case kStream: return launch_mode<D, T, kNarrow, kStream>(a, p, z.grid, st);
-        case kUnits: return launch_mode<D, T, kNarrow, kUnits>(a, p, z.grid, st);
-        default: return launch_mode<D, T, kNarrow, kRows>(a, p, z.grid, st);
+        case kSplit: return launch_mode<D, T, kNarrow, kSplit, false>(a, p, z.grid, st);
+        case kStream: return launch_mode<D, T, kNarrow, kStream, kPuts>(a, p, z.grid, st);
+        case kUnits: return launch_mode<D, T, kNarrow, kUnits, kPuts>(a, p, z.grid, st);
+        default: break;
     }
+    if (p.aside) return launch_mode<D, T, kNarrow, kRows, kPuts>(a, p, z.grid, st);
+    return launch_mode<D, T, kNarrow, kRows, false>(a, p, z.grid, st);
 }
 
 // One translation unit each (they compile side by side).

@@ -926,6 +926,30 @@ def test_attention_maxima_move_through_long_runs(lib, pl, way, G, D, dtype):
     check_attend(out[pick], lse[pick], want_attend(rows_of(c, pick)))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [8, 16])
+@pytest.mark.parametrize("way,T", [("stream", 2000), ("units", 1216), ("rows", 8200)])
+def test_attention_long_runs_do_not_shrink(lib, pl, way, T, G, D):
+    """Rows of 2^19 keys, each in one warp's run, over values of one sign (2048 tokens, paged in again and again): the
+    mean relative difference between bf16 and float32 outputs of the same queries.  A weight's rounding to float16 is
+    at most 2^-11, taken as if all went one way; the outputs' own roundings (at most 2^-8, uniform, T G rows taken as
+    one each) average to 2^-8 / sqrt(3 T G), five times that; float32 outputs are within 2^-14."""
+    c = attend_case(G, 1, 1, 2048, 2048, G, 1, D, 1024, 0, 0, torch.bfloat16, scales=False)
+    c["cache"][..., 8 * D:16 * D] &= 0x77
+    c["table"] = np.tile(c["table"], (1, 256))
+    n = c["table"].shape[1] * 1024
+    c["q"] = torch.randn((T, G, D)).bfloat16()
+    c["req"], c["pos"] = np.zeros(T, np.int64), np.full(T, n - 1)
+    if way != "stream":
+        c["idx"], c["cnt"], c["BS"] = np.tile(np.array([3, 0, 7, 1, 2, 6, 4, 5]), (T, 1, 1)), np.full((T, 1), 8), n // 8
+    assert way_of(lib, c) == way
+    a = attend(pl, c)
+    b = attend(pl, {**c, "q": c["q"].float()})
+    short = ((a[0].double() - b[0].double()) / b[0].double()).mean().item()
+    assert b[0].min() > 0 and abs(short) <= 2.0 ** -11 + 5 * 2.0 ** -8 / (3 * T * G) ** 0.5 + 2.0 ** -14, short
+    assert (a[1] - b[1]).abs().max() <= 2.0 ** -14 * (1 + b[1].abs().max())
+
+
 def on_device(c):
     """The arguments of cache_attention for this batch."""
     f = torch.float32
