@@ -361,7 +361,7 @@ def cache_tables(old_lens, new_lens, page_size, block_table, pool, pool_count, m
 
 def _check_rows(name, t, T, *rest):
     """A tensor [T or more, *rest]: others may have as many elements, and would be read as other rows."""
-    if t is not None and t.shape != (T, *rest) and (t.shape[1:] != rest or t.shape[0] < T):
+    if t is not None and (t.shape[1:] != rest or t.shape[0] < T):
         raise ValueError("%s: a tensor %s is needed, got %s" % (name, [T, *rest], tuple(t.shape)))
 
 
@@ -377,10 +377,12 @@ def cache_append(k, v, slots, cache, k_scale=None, v_scale=None, values=None):
     T, H, D = k.shape
     if cache.shape[1] != H or cache.shape[3] != 18 * D:
         raise ValueError("cache %s does not hold %d heads of %d channels" % (tuple(cache.shape), H, D))
-    _check_scales(k_scale, v_scale, H)
+    if (k_scale is not None and k_scale.numel() != H) or (v_scale is not None and v_scale.numel() != H):
+        _check_scales(k_scale, v_scale, H)
     kv, vv = (None, None) if values is None else values
-    _check_rows("values", kv, T, H, D)
-    _check_rows("values", vv, T, H, D)
+    if values is not None and (kv is None or vv is None or kv.shape != k.shape or vv.shape != k.shape):
+        _check_rows("values", kv, T, H, D)
+        _check_rows("values", vv, T, H, D)
     bsa.bsa_cache_append(k, v, T, H, D, slots, cache, cache.shape[0], cache.shape[2] * 16, k_scale, v_scale, kv, vv)
 
 
@@ -394,13 +396,14 @@ def cache_attention(q, cache, block_table, token_req, token_pos, k_scale=None, v
     if width != 18 * D:
         raise ValueError("cache %s does not hold %d channels" % (tuple(cache.shape), D))
     R, max_pages = block_table.shape
-    if k_scale is not None or v_scale is not None:
+    if (k_scale is not None and k_scale.numel() != H) or (v_scale is not None and v_scale.numel() != H):
         _check_scales(k_scale, v_scale, H)
     S = 0
     if block_indices is not None:
         S = block_indices.shape[-1]
-        _check_rows("block_indices", block_indices, T, H, S)
-        _check_rows("block_counts", block_counts, T, H)
+        if block_indices.shape != (T, H, S) or block_counts is None or block_counts.shape != (T, H):
+            _check_rows("block_indices", block_indices, T, H, S)
+            _check_rows("block_counts", block_counts, T, H)
     max_keys = S * block_size if S else max_pages * strips * 16
     # (sizes one by one: as a tuple they take torch 1.6 us longer to parse, of the call's 20)
     out = torch.empty(T, HQ, D, dtype=q.dtype, device=q.device)
