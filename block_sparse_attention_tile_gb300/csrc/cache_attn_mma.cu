@@ -6,9 +6,11 @@ namespace cmma {
 namespace {
 
 constexpr int kSms = 152;
-// From so many rows a warp on, lists' rows are taken whole, without a look at all of them first.  Measured, us, 4
-// requests' chunks of 16 blocks of 64, rows against units / stream: all lists full 127, 191, 291 against 117, 211,
-// 340 at 2.1, 4.1 and 6.7 rows a warp; 1 to 16 blocks a row 105, 143, 204 against 75, 130, 201.
+// From so many rows a warp on, lists' rows are taken whole, without a look at all of them first: whatever their lengths
+// they then cost little more than equal shares.  Measured, us, 4 requests' chunks, 16 heads on each of 4, rows against
+// units, at 2.0, 3.9 and 6.1 rows a warp: 16 blocks of 64, all lists full, 81, 159, 256 against 90, 187, 313; 1 to 16
+// blocks a row 78, 145, 195 against 69, 122, 182; 1 to 16 blocks of 128 144, 272, 364 against 104, 192, 292 (full 153,
+// 301, 487 against 161, 317, 497).
 constexpr int kRowsPerWarp = 6;
 
 // How the work is cut, from the sizes that the host knows.
@@ -45,10 +47,15 @@ Sizes cut(int T, int HQ, int H, int D, bool f32, bool lists, long long max_keys)
     z.grid = grid;
     if (z.mode == kStream) {
         // Whole rows to units where that leaves none with much more than its share: lists' rows are about as long as
-        // one another.  A unit is what an SM holds: larger clusters do not tile the GPU (76 clusters of four CTAs ran
-        // in two rounds: 143 us for 256 tokens of 2048 selected keys, against 99 with the join).
+        // one another.  A unit is the two CTAs that an SM holds: larger clusters do not tile the GPU (76 clusters of
+        // four ran in two rounds: 143 us for 256 tokens of 2048 selected keys, against 99 with the join), and neither
+        // do the three of bf16's up to 8 heads.  Measured, us, units against stream.  16 heads, lists of 16 blocks of
+        // 128, the units' largest share 0, 4, 9, 14, 19, 27 and 43% over the mean: 51, 82, 128, 43, 61, 43, 42 against
+        // 55, 90, 138, 45, 62, 43, 39; float32 of 8 heads, 1 to 9% over: 97, 87, 138 against 109, 94, 145; every key of
+        // 12000 rows of 64 to 1024 keys (79 a unit): 388 against 436, float32 of 8 heads 357 against 399.  bf16 of 8
+        // heads with clusters of three: 91, 139 and 318 against 72, 111 and 288.
         const long long most = (rows + kSms - 1) / kSms;
-        if (most * kSms * 100 <= rows * 108 && (lists || most >= 64)) z.mode = kUnits, p.unit = grid / kSms;
+        if (grid == 2 * kSms && most * kSms * 100 <= rows * 108 && (lists || most >= 64)) z.mode = kUnits, p.unit = 2;
         const size_t slots = (size_t)grid * kWarps * 2 * (narrow ? 8 : 16);
         z.part = slots * D * sizeof(float);
         z.ml = slots * sizeof(float2);

@@ -9,7 +9,7 @@
 //           end (so a batch of ragged lengths is balanced to a tile); a row that is cut leaves
 //           parts (m, l, U) in the workspace, and a second kernel joins them:
 //             m = max m_i,   l = sum l_i 2^(m_i - m),   U = sum U_i 2^(m_i - m),   O = U / l;
-//   units   many rows of about the same length: clusters of an SM's worth of CTAs share out the rows,
+//   units   many rows of about the same length, two CTAs an SM: clusters of these two share out the rows,
 //           whole, and the warps of a cluster its tiles; a cut row is joined inside its cluster, in one launch;
 //   rows    so many rows that whole ones balance: each warp takes the next row when it is done with one (from the
 //           stream's work counter; in a captured graph every warps-th row);
@@ -1200,10 +1200,12 @@ static bsa_status launch(const CacheAttn& a, const Sizes& z, cudaStream_t st) {
     switch (z.mode) {
         case kSplit: return launch_mode<D, T, kNarrow, kSplit, false>(a, p, z.grid, st);
         case kStream: return launch_mode<D, T, kNarrow, kStream, kPuts>(a, p, z.grid, st);
-        case kUnits: return launch_mode<D, T, kNarrow, kUnits, kPuts>(a, p, z.grid, st);
+        case kUnits:
+            if constexpr (Shape<D, T, kNarrow>::kBlocks == 2) return launch_mode<D, T, kNarrow, kUnits, kPuts>(a, p, z.grid, st);
+            break;  // never asked for
         default: break;
     }
-    if (p.aside) return launch_mode<D, T, kNarrow, kRows, kPuts>(a, p, z.grid, st);
+    if (kPuts && p.aside) return launch_mode<D, T, kNarrow, kRows, kPuts>(a, p, z.grid, st);
     return launch_mode<D, T, kNarrow, kRows, false>(a, p, z.grid, st);
 }
 

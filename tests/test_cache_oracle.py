@@ -252,6 +252,9 @@ def test_way_of_sizes(bsa):
     assert way(1, 64, 4, 128, torch.bfloat16, True, 16 * 64) == 1         # few rows: a cluster each
     assert way(48, 64, 8, 128, torch.bfloat16, False, 32768) == 2         # long rows: equal runs
     assert way(256, 64, 4, 128, torch.bfloat16, True, 16 * 128) == 3      # many lists of one length
+    assert way(256, 32, 4, 128, torch.float32, True, 16 * 128) == 3
+    assert way(256, 32, 4, 128, torch.bfloat16, True, 16 * 128) == 2      # three CTAs an SM: clusters of them do not fit
+    assert way(3000, 32, 4, 128, torch.bfloat16, False, 1024) == 2
     assert way(2048, 64, 4, 128, torch.float32, True, 16 * 64) == 4       # more than six rows a warp
     for bad in (dict(T=0), dict(HQ=7), dict(H=0), dict(D=40), dict(D=144), dict(max_keys=0)):
         a = {**dict(T=8, HQ=8, H=2, D=64, dtype=torch.float32, lists=True, max_keys=64), **bad}

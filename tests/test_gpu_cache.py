@@ -849,6 +849,11 @@ def way_of(lib, c):
     return WAYS[lib.bsa_cache_attention_way(T, HQ, H, D, c["q"].dtype, c["idx"] is not None, most)]
 
 
+def asked(way, G, dtype):
+    """Up to 8 heads in bfloat16 have no units: such batches are cut as a stream."""
+    return "stream" if way == "units" and G <= 8 and dtype == torch.bfloat16 else way
+
+
 def rows_of(c, pick):
     """The batch's tokens of these numbers."""
     return {**c, **{k: c[k][pick] for k in ("q", "req", "pos", "idx", "cnt") if c[k] is not None}}
@@ -865,7 +870,7 @@ def test_attention_every_kernel(lib, pl, way, G, D, dtype):
     R, n, lo, hi, P, S, BS = {"split": (3, 1, 300, 1300, 64, 0, 0), "stream": (130, 1, 1, 1300, 64, 0, 0),
                               "units": (150, 2, 2, 900, 32, 9, 64), "rows": (4, 700, 700, 1500, 16, 5, 64)}[way]
     c = attend_case(G + D, R, n, lo, hi, 4 * G, 4, D, P, S, BS, dtype)
-    assert way_of(lib, c) == way
+    assert way_of(lib, c) == asked(way, G, dtype)
     T = R * n
     rng = np.random.default_rng(T)
     pad = rng.random(T) < (0.05 if T > 10 else 0)
@@ -920,7 +925,7 @@ def test_attention_maxima_move_through_long_runs(lib, pl, way, G, D, dtype):
     if way == "split" and G > 8:
         T = 40  # two CTAs an SM
     c = growing_case(G, T, n, G, H, D, S, dtype)
-    assert way_of(lib, c) == way
+    assert way_of(lib, c) == asked(way, G, dtype)
     out, lse = attend(pl, c)
     pick = np.unique(np.linspace(0, T - 1, 7).astype(int))
     check_attend(out[pick], lse[pick], want_attend(rows_of(c, pick)))
@@ -942,7 +947,7 @@ def test_attention_long_runs_do_not_shrink(lib, pl, way, T, G, D):
     c["req"], c["pos"] = np.zeros(T, np.int64), np.full(T, n - 1)
     if way != "stream":
         c["idx"], c["cnt"], c["BS"] = np.tile(np.array([3, 0, 7, 1, 2, 6, 4, 5]), (T, 1, 1)), np.full((T, 1), 8), n // 8
-    assert way_of(lib, c) == way
+    assert way_of(lib, c) == asked(way, G, torch.bfloat16)
     a = attend(pl, c)
     b = attend(pl, {**c, "q": c["q"].float()})
     short = ((a[0].double() - b[0].double()) / b[0].double()).mean().item()
@@ -996,7 +1001,7 @@ def test_attention_wait_that_expires_late_is_reported(lib, pl, way, G, stall):
     if way == "split" and G > 8:
         T = 40
     c = growing_case(G, T, n, G, H, 128, S, torch.bfloat16)
-    assert way_of(lib, c) == way
+    assert way_of(lib, c) == asked(way, G, torch.bfloat16)
     args = on_device(c)
     want = pl.cache_attention(*args)
     os.environ["BSA_TEST_STALL_TILE"] = str(stall)
