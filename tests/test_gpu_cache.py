@@ -963,6 +963,30 @@ def on_device(c):
             None if c["idx"] is None else dev(c["idx"]), None if c["cnt"] is None else dev(c["cnt"]), c["BS"])
 
 
+def test_captured_long_runs_replay(lib, pl):
+    """Runs of more than 128 tiles, whose sums are put aside in the workspace, captured in two graphs and replayed over
+    other positions: the bits of eager calls, and rows within tolerance of the oracle."""
+    c = growing_case(3, 400, 20000, 5, 2, 128, 0, torch.bfloat16)
+    assert way_of(lib, c) == "stream"  # 800 rows of 311 tiles or more on 1824 warps
+    args = on_device(c)
+    pl.cache_attention(*args)
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            got.append(pl.cache_attention(*args))
+    for shift in (0, 5000, 3):
+        args[4].copy_(dev(c["pos"] - shift))
+        want = pl.cache_attention(*args)
+        for g, (out, lse) in zip(graphs, got):
+            out.zero_(), lse.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    pick = np.array([0, 399])
+    check_attend(want[0][pick], want[1][pick], want_attend(rows_of({**c, "pos": c["pos"] - 3}, pick)))
+
+
 ROWS_16 = (70, 30, 30, 200, 48, 4, 128, 16, 6, 16, torch.bfloat16)
 
 
