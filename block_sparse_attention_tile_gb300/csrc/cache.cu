@@ -17,7 +17,7 @@ namespace bsa {
 // waiting for any write of the call, and no two threads touch the same word.
 //
 // Nothing here computes; a small call is bound by the launch and the scan's
-// latency (64 requests of one token: 4.6 us on the device), a large one by its two
+// latency (64 requests of one token: 4.8 us on the device), a large one by its two
 // launches and the dependent lookups of each page (1024 mixed requests, 786432 token
 // rows, 12.8 MB: 12 us, of which the bytes are 2).
 
@@ -42,7 +42,10 @@ struct Sums {
 };
 
 constexpr int kScanThreads = 1024;
-constexpr int kOneCtaTokens = 4096;  // up to here one CTA does all: 4 tokens a thread cost less than a second launch
+// Up to here one CTA does all: 4 tokens a thread cost less than a second launch.  The pages given back count nothing
+// here, since the host does not know them: many long requests that end at once take longer in one CTA (64 of 512 pages
+// 23 us, in a grid 6; 1024 of 128 pages 115 against 15).
+constexpr int kOneCtaTokens = 4096;
 constexpr int kOneCtaRequests = 1024;
 inline bool one_cta(int R, int max_tokens) { return R <= kOneCtaRequests && max_tokens <= kOneCtaTokens; }
 
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(256) cache_place_kernel(Tables a, int sh, cons
 //
 // Per element: 2 bytes read and 9/16 written (and 2 for the values), and about 20 instructions with the
 // values: at 16.8M elements a tensor (32768 tokens, 153 MB) 28 us, 80% of the copy bandwidth, with the issue
-// slots 70% busy.
+// slots 63% busy.  Without the values 19.4 us for 86 MB (66%), where the instructions bind; float32 30 us without (76%)
+// and 46 with them (93%).
 
 // Sixteen elements as they lie in memory.
 template <typename T> struct Group { uint32_t w[4 * sizeof(T)]; };

@@ -23,7 +23,9 @@
 // most 2^4 below the running maximum (the sums and the output are rescaled only when the maximum
 // grows by more than that): they stay below float16's 2^16 and keep full precision over 25
 // binades.  They are rounded to float16 for bf16 outputs, u = 2^-11 against the output's own
-// 2^-8, or split in two for float32 ones.  Maxima, sums and both accumulators are float32.
+// 2^-8 (a second product for the rest would cost what float32 outputs pay: 64 us for 24 requests of 8192
+// keys, against 40), or split in two for float32 ones.  The rows' sums take them unrounded, since the LSE is
+// float32 from them.  Maxima, sums and both accumulators are float32.
 //
 // Fragments.  mma.m16n8k16 lets the summed index be permuted freely as long as both
 // operands agree, so a lane takes what lies together: of K the D / 4 consecutive channels
@@ -35,13 +37,15 @@
 // 8-column one (transposed in registers by movmatrix), which halves the products and the output's
 // registers.
 //
-// What bounds it: the issue slots.  mma.sync keeps a scheduler for about 8 cycles, during which
+// What bounds it.  mma.sync keeps a scheduler for about 8 cycles, during which
 // little else issues (measured: 32 mma with 64 cvt and 64 multiplications take 2 cycles per mma
 // plus 1/4 per other instruction on an SM, whether 8 or 16 warps run), so a tile of 64 keys at
-// D = 128 costs 256 + 970 / 4 = 498 cycles wide, and takes about 620; its bytes take 400 at the measured
-// copy bandwidth.  Narrow it is 128 + 860 / 4, and the bytes bind.  Measured on the device: 48
-// ragged requests, 909 MB, 8 heads a KV head: 159 us, 85% of the copy bandwidth; 256 tokens of 2048
-// selected keys, 301 MB, 16 heads: 82 us, 54%.  About 7 us of a launch pass before the first tile
+// D = 128 costs 256 + 970 / 4 = 498 cycles wide; its bytes take 400 at the measured copy bandwidth.  It
+// takes about 620: a scheduler has two warps, and both mostly wait for results of their own (profiled:
+// 42 to 47% of the issue slots used, 0.5 to 0.6 warps ready a cycle, 1.2 cycles an instruction waiting for the one
+// before it, 0.5 for the tensor pipe, 0.2 to 0.4 for memory).  Narrow it is 128 + 860 / 4, and the bytes bind.
+// Measured on the device: 48 ragged requests, 909 MB, 8 heads a KV head: 161 us, 84% of the copy bandwidth; 256
+// tokens of 2048 selected keys, 301 MB, 16 heads: 82 us, 54%.  About 7 us of a launch pass before the first tile
 // is worked on (start of the run, lookups, first copies), part of them for fetching instructions:
 // a kernel for each of the four ways instead of one with branches took 1 to 4 us less (31.2 -> 30.5 us
 // for one request of 131072 keys, 9.0 -> 8.5 us for 8 short ones).
