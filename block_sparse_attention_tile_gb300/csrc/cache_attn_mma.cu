@@ -6,8 +6,8 @@ namespace cmma {
 namespace {
 
 constexpr int kSms = 152;
-// From so many rows a warp on, lists' rows are taken whole, without a look at all of them first: whatever their lengths
-// they then cost little more than equal shares.  Measured, us, 4 requests' chunks, 16 heads on each of 4, rows against
+// From so many rows a warp on, lists' rows are taken whole, without a look at all of them first: full lists then gain
+// up to a fifth, and only long ragged ones lose as much.  Measured, us, 4 requests' chunks, 16 heads on each of 4, rows against
 // units, at 2.0, 3.9 and 6.1 rows a warp: 16 blocks of 64, all lists full, 81, 159, 256 against 90, 187, 313; 1 to 16
 // blocks a row 78, 145, 195 against 69, 122, 182; 1 to 16 blocks of 128 144, 272, 364 against 104, 192, 292 (full 153,
 // 301, 487 against 161, 317, 497).
