@@ -78,6 +78,11 @@ _SIGS = {
     "bsa_cache_attention_workspace": (SZ, [I, I, I, I, I]),
     "bsa_cache_attention_way": (I, [I, I, I, I, I, I, I]),
     "bsa_fwd_cache_tokens": (I, [P, I, I, I, I, I, I64, P, I, I, P, I, I, P, P, P, P, P, P, I, I, F, P, P, P, SZ, P]),
+    "bsa_rotary_table": (I, [P, I, I, P, P, I, F, P, P, P]),
+    "bsa_rotate": (I, [I, I, I, I, I, I, I, P, P, I64, P, I, P, P, P, I, P, P, P, F, P]),
+    "bsa_cache_append_rotated": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P, P, I, I, P, I, I64, P, P]),
+    "bsa_cross_workspace": (SZ, [I, I, I, I, I, I, I, I, I]),
+    "bsa_fwd_cross": (I, [P, P, P, I, I, I, I, I, I, I, P, P, P, P, F, P, P, P, SZ, P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -453,3 +458,88 @@ def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table,
     _call(dev, _lib.bsa_fwd_cache_tokens, qp, _dtype(q), T, HQ, H, D, qs, cache.data_ptr(), n_pages, page_size,
           block_table.data_ptr(), R, max_pages, token_req.data_ptr(), token_pos.data_ptr(), ksp, vsp, ip, cp, S,
           block_size, scale, out.data_ptr(), lp, ws, ws_bytes, _on(dev, stream))
+
+
+# ---------------------------------------------------------------- rotary positions, cross attention
+
+def _heads(name, t, shape, dtype, dev):
+    """Data pointer and batch, token and head stride of rows [B, T, heads, D] whose channels are adjacent."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError("%s: a %s tensor %s on cuda:%d is needed, got %s %s on %s"
+                         % (name, dtype, list(shape), dev, t.dtype, tuple(t.shape), t.device))
+    st = t.stride()
+    if st[3] != 1 and shape[3] > 1:
+        raise ValueError("%s: a row's channels must be adjacent, got strides %s" % (name, st))
+    return t.data_ptr(), st[:3]
+
+
+def bsa_rotary_table(positions, T, axes, turns, axis, P, factor, cos_out, sin_out, stream=None):
+    dev, f32 = _device_of(turns), torch.float32
+    _call(dev, _lib.bsa_rotary_table, _expect("positions", positions, torch.int32, T * axes, dev), T, axes,
+          _expect("turns", turns, torch.int64, P, dev), _expect("axis", axis, torch.int32, P, dev), P, factor,
+          _expect("cos_out", cos_out, f32, T * P, dev), _expect("sin_out", sin_out, f32, T * P, dev), _on(dev, stream))
+
+
+def bsa_rotate(q, k, B, T, HQ, H, D, P, cos_table, sin_table, table_batch_stride, q_out, k_out, interleaved=False,
+               transpose=False, q_weight=None, k_weight=None, eps=1e-6, stream=None):
+    """q, k and their outputs are [B, T, heads, D] views of any batch, token and head strides."""
+    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
+    qp, qs = _heads("q", q, (B, T, HQ, D), dt, dev)
+    qo, qos = _heads("q_out", q_out, (B, T, HQ, D), dt, dev)
+    kp = ko = None
+    ks = kos = (0, 0, 0)
+    if k is not None:
+        kp, ks = _heads("k", k, (B, T, H, D), dt, dev)
+        ko, kos = _heads("k_out", k_out, (B, T, H, D), dt, dev)
+    rows = T * P + (B - 1) * table_batch_stride if B and T else 0
+    _call(dev, _lib.bsa_rotate, _dtype(q), B, T, D, P, 1 if interleaved else 0, 1 if transpose else 0,
+          _expect("cos_table", cos_table, f32, rows, dev), _expect("sin_table", sin_table, f32, rows, dev),
+          table_batch_stride, qp, HQ, _expect("q_weight", q_weight, f32, D, dev), qo, kp, H if k is not None else 0,
+          _expect("k_weight", k_weight, f32, D, dev), ko, (I64 * 12)(*qs, *qos, *ks, *kos), eps, _on(dev, stream))
+
+
+def bsa_cache_append_rotated(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale, v_scale, k_val, v_val, cos_table,
+                             sin_table, P, interleaved=False, q=None, HQ=0, q_out=None, stream=None):
+    dev, dt, f32 = _device_of(cache), k.dtype, torch.float32
+    kp, ks = _rows("k", k, T, H, D, dt, dev)
+    vp, vs = _rows("v", v, T, H, D, dt, dev)
+    qp, qs = (None, 0) if q is None else _rows("q", q, T, HQ, D, dt, dev)
+    _call(dev, _lib.bsa_cache_append_rotated, kp, vp, _dtype(k), T, H, D, ks, vs,
+          _expect("slots", slots, torch.int64, T, dev),
+          _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
+          _expect("k_scale", k_scale, f32, H, dev), _expect("v_scale", v_scale, f32, H, dev),
+          _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev),
+          _expect("cos_table", cos_table, f32, T * P, dev), _expect("sin_table", sin_table, f32, T * P, dev), P,
+          1 if interleaved else 0, qp, HQ, qs, _expect("q_out", q_out, dt, T * HQ * D, dev), _on(dev, stream))
+
+
+@functools.lru_cache(maxsize=1024)
+def bsa_cross_workspace(dtype, B, N, M, HQ, H, D, packed_queries, packed_keys):
+    return _lib.bsa_cross_workspace(BSA_F32 if dtype is torch.float32 else BSA_BF16, B, N, M, HQ, H, D,
+                                    1 if packed_queries else 0, 1 if packed_keys else 0)
+
+
+def bsa_fwd_cross(q, k, v, B, N, M, HQ, H, D, query_start, key_start, key_lens, scale, out, lse=None, workspace=None,
+                  stream=None):
+    """q and out are [B, N, HQ, D] views ([1, N, HQ, D] with query_start), k and v [B, M, H, D] ([1, M, H, D] with
+    key_start), lse [B, N, HQ] ([1, N, HQ])."""
+    dev, dt, i32 = _device_of(q), q.dtype, torch.int32
+    qb, kb = 1 if query_start is not None else B, 1 if key_start is not None else B
+    qp, qs = _heads("q", q, (qb, N, HQ, D), dt, dev)
+    kp, ks = _heads("k", k, (kb, M, H, D), dt, dev)
+    vp, vs = _heads("v", v, (kb, M, H, D), dt, dev)
+    op, os_ = _heads("out", out, (qb, N, HQ, D), dt, dev)
+    lp, ls = None, (0, 0, 0)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (qb, N, HQ):
+            raise ValueError("lse: a float32 tensor %s on cuda:%d is needed, got %s %s on %s"
+                             % ([qb, N, HQ], dev, lse.dtype, tuple(lse.shape), lse.device))
+        lp, ls = lse.data_ptr(), lse.stride()
+    if key_start is not None and key_lens is not None:
+        raise ValueError("key_start and key_lens exclude each other")
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev)
+    _call(dev, _lib.bsa_fwd_cross, qp, kp, vp, _dtype(q), B, N, M, HQ, H, D, (I64 * 15)(*qs, *ks, *vs, *os_, *ls),
+          None if query_start is None else _expect("query_start", query_start, i32, B + 1, dev),
+          None if key_start is None else _expect("key_start", key_start, i32, B + 1, dev),
+          None if key_lens is None else _expect("key_lens", key_lens, i32, B, dev), scale, op, lp, ws, ws_bytes,
+          _on(dev, stream))

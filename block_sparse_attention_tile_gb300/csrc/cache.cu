@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "cache.cuh"
+#include "rotary.cuh"
 #include "tc_ptx.cuh"
 
 namespace bsa {
@@ -439,6 +440,192 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
     }
 }
 
+// ---------------------------------------------------------------- a17 rotated append
+//
+// The append with the keys rotated on the way, and the step's queries rotated by the blocks behind kv_blocks.  A
+// thread takes one group as above; its key channels' partners are the group P channels away (half layout, read
+// too) or the group itself (interleaved).  The rotation is rounded to float32 and quantised from there: keys are
+// not rounded to bf16 on the way.
+struct Rotated {
+    const float* cos;
+    const float* sin;
+    int P;
+    bool interleaved, wide, q_wide;  // groups' and units' wide loads
+    const void* q;
+    long long q_stride;
+    int HQ;
+    void* q_out;
+    unsigned kv_blocks;
+    int splits;
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Group<float> rotated_key(const T* row, int g, const float* cs, const float* sn, const Rotated& a) {
+    Group<float> y;
+    const Group<T> x = load16<T, kVec>(row + g * 16);
+    const int first = g * 16, R = 2 * a.P;
+    if (first >= R) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y.w[i] = __float_as_uint(element<T>(x, i));
+    } else if (a.wide && a.interleaved) {
+        float c[8], s[8];
+        load8(cs + g * 8, c);
+        load8(sn + g * 8, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float p = element<T>(x, 2 * i), r = element<T>(x, 2 * i + 1);
+            rotate_pair(p, r, c[i], s[i]);
+            y.w[2 * i] = __float_as_uint(p);
+            y.w[2 * i + 1] = __float_as_uint(r);
+        }
+    } else if (a.wide) {
+        const bool low = first < a.P;
+        const int at = low ? first : first - a.P;
+        const Group<T> o = load16<T, kVec>(row + (low ? first + a.P : at));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float c[8], s[8];
+            load8(cs + at + 8 * h, c);
+            load8(sn + at + 8 * h, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = 8 * h + j;
+                const float own = __fmul_rn(element<T>(x, i), c[j]), other = __fmul_rn(element<T>(o, i), s[j]);
+                y.w[i] = __float_as_uint(low ? __fsub_rn(own, other) : __fadd_rn(own, other));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int ch = first + i;
+            float v = element<T>(x, i);
+            if (ch < R) {
+                const bool low = a.interleaved ? !(ch & 1) : ch < a.P;
+                const int p = a.interleaved ? ch >> 1 : low ? ch : ch - a.P;
+                const float o = to_f32(row[a.interleaved ? ch ^ 1 : low ? ch + a.P : ch - a.P]);
+                v = low ? __fsub_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, sn[p])) : __fadd_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, sn[p]));
+            }
+            y.w[i] = __float_as_uint(v);
+        }
+    }
+    return y;
+}
+
+template <typename T, bool kVec, bool kValues>
+__global__ void __launch_bounds__(256) cache_append_rotated_kernel(
+    const T* __restrict__ k, const T* __restrict__ v, long long k_stride, long long v_stride, unsigned items, int H,
+    int D, const int64_t* __restrict__ slots, uint8_t* __restrict__ cache, long long n_slots, int sh,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, T* __restrict__ k_val, T* __restrict__ v_val,
+    int T_, const Rotated a, int* status) {
+    if (blockIdx.x >= a.kv_blocks) {
+        const int lane = threadIdx.x & 31, lanes = D <= 32 ? 2 : D <= 64 ? 4 : 8, u = lane % lanes;
+        const bool live = 16 * u < D, turn = 8 * u < a.P;
+        const long long n = (long long)T_ * a.splits;
+        for (long long i = (long long)(blockIdx.x - a.kv_blocks) * 8 + (threadIdx.x >> 5); i < n;
+             i += (long long)(gridDim.x - a.kv_blocks) * 8) {
+            const long long t = i / a.splits;
+            const int part = (int)(i - t * a.splits);
+            const long long slot = slots[t];
+            if (slot < 0 || slot >= n_slots) continue;  // whole warps; the keys' side latches
+            const int h0 = (int)((long long)a.HQ * part / a.splits), h1 = (int)((long long)a.HQ * (part + 1) / a.splits);
+            const T* x = (const T*)a.q + t * a.q_stride;
+            T* y = (T*)a.q_out + t * a.HQ * D;
+            const float *cs = a.cos + t * a.P, *sn = a.sin + t * a.P;
+            if (a.q_wide) {
+                float c[8], s[8];
+                int c0, c1;
+                unit_runs(u, a.P, a.interleaved, c0, c1);
+                if (turn) {
+                    load8(cs + 8 * u, c);
+                    load8(sn + 8 * u, s);
+                }
+                for (int h = h0 + lane / lanes; h < h1; h += 32 / lanes) {
+                    if (!live) break;
+                    float z[16];
+                    load8(x + h * D + c0, z);
+                    load8(x + h * D + c1, z + 8);
+                    if (turn) rotate_unit(z, c, s, a.interleaved);
+                    store8(y + h * D + c0, z);
+                    store8(y + h * D + c1, z + 8);
+                }
+            } else {
+                for (int e = h0 * D + lane; e < h1 * D; e += 32) {
+                    const int ch = e % D;
+                    float z = to_f32(x[e]);
+                    if (ch < 2 * a.P) {
+                        const bool low = a.interleaved ? !(ch & 1) : ch < a.P;
+                        const int p = a.interleaved ? ch >> 1 : low ? ch : ch - a.P;
+                        const float o = to_f32(x[e - ch + (a.interleaved ? ch ^ 1 : low ? ch + a.P : ch - a.P)]);
+                        z = low ? __fsub_rn(__fmul_rn(z, cs[p]), __fmul_rn(o, sn[p]))
+                                : __fadd_rn(__fmul_rn(z, cs[p]), __fmul_rn(o, sn[p]));
+                    }
+                    y[e] = from_f32<T>(z);
+                }
+            }
+        }
+        return;
+    }
+    const unsigned ng = D / 16;
+    for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < items; i += a.kv_blocks * blockDim.x) {
+        const unsigned row = i / ng, t = row / (unsigned)H;
+        const int g = (int)(i - row * ng), h = (int)(row - t * H);
+        const long long slot = slots[t];
+        if (slot < 0 || slot >= n_slots) {
+            if (slot != -1) raise_status(status, BSA_ERR_INDEX);
+            continue;
+        }
+        const Group<float> kx = rotated_key<T, kVec>(k + t * k_stride + h * D, g, a.cos + (long long)t * a.P,
+                                                     a.sin + (long long)t * a.P, a);
+        const Group<T> vx = load16<T, kVec>(v + t * v_stride + h * D + g * 16);
+        const float ks = k_scale ? k_scale[h] : 1.f, vs = v_scale ? v_scale[h] : 1.f;
+        const long long page = slot >> sh, at = (long long)i * 16;
+        const int in = (int)(slot & ((1 << sh) - 1)), j = in & 15;
+        uint8_t* strip = cache + (((page * H + h) << (sh - 4)) + (in >> 4)) * strip_bytes(D);
+        float x[16];
+        uint32_t byte;
+        *reinterpret_cast<uint2*>(strip + j * (D / 2) + g * 8) = quantise16<float, kValues>(kx, ks, &byte, x);
+        strip[16 * D + j * ng + g] = (uint8_t)byte;
+        if (kValues) store16<T, kVec>(k_val + at, x);
+        *reinterpret_cast<uint2*>(strip + 8 * D + (g * 16 + j) * 8) = quantise16<T, kValues>(vx, vs, &byte, x);
+        strip[17 * D + g * 16 + j] = (uint8_t)byte;
+        if (kValues) store16<T, kVec>(v_val + at, x);
+    }
+}
+
+template <typename T>
+static bsa_status launch_append_rotated(const void* k, const void* v, long long ks, long long vs, int T_, int H, int D,
+                                        const int64_t* slots, uint8_t* cache, long long n_slots, int sh,
+                                        const float* k_scale, const float* v_scale, void* k_val, void* v_val, Rotated a,
+                                        cudaStream_t st) {
+    const long long items = (long long)T_ * H * (D / 16);
+    if (items > (1LL << 31)) return fail(BSA_ERR_UNSUPPORTED, "rotated append: too many rows (T=%d H=%d D=%d)", T_, H, D);
+    a.kv_blocks = (unsigned)std::min<long long>((items + 255) / 256, 1 << 20);
+    const uintptr_t in = (uintptr_t)k | (uintptr_t)v | (uintptr_t)(ks * (long long)sizeof(T)) |
+                         (uintptr_t)(vs * (long long)sizeof(T)), out = (uintptr_t)k_val | (uintptr_t)v_val;
+    const uintptr_t table = (uintptr_t)a.cos | (uintptr_t)a.sin;
+    const bool vec = (in & 15) == 0 && (out & 31) == 0;
+    a.wide = (table & 15) == 0 && (a.interleaved ? a.P % 8 == 0 : a.P % 16 == 0);
+    a.q_wide = (table & 15) == 0 && a.P % 8 == 0 &&
+               (((uintptr_t)a.q | (uintptr_t)a.q_out | (uintptr_t)(a.q_stride * (long long)sizeof(T))) & 15) == 0;
+    unsigned q_blocks = 0;
+    if (a.q) {
+        const int lanes = D <= 32 ? 2 : D <= 64 ? 4 : 8;
+        a.splits = (int)std::max<long long>(1, std::min<long long>((a.HQ * lanes + 31) / 32, 152 * 32 / T_));
+        q_blocks = (unsigned)std::min<long long>(((long long)T_ * a.splits + 7) / 8, 152 * 64);
+    }
+#define BSA_APPEND(V, W)                                                                                            \
+    cache_append_rotated_kernel<T, V, W><<<a.kv_blocks + q_blocks, 256, 0, st>>>(                                   \
+        (const T*)k, (const T*)v, ks, vs, items, H, D, slots, cache, n_slots, sh, k_scale, v_scale, (T*)k_val,      \
+        (T*)v_val, T_, a, status_word())
+    if (vec) {
+        if (k_val) BSA_APPEND(true, true); else BSA_APPEND(true, false);
+    } else {
+        if (k_val) BSA_APPEND(false, true); else BSA_APPEND(false, false);
+    }
+#undef BSA_APPEND
+    return check_launch("cache_append_rotated_kernel");
+}
+
 template <typename T>
 static bsa_status launch_append(const void* k, const void* v, long long ks, long long vs, int T_, int H, int D,
                                 const int64_t* slots, uint8_t* cache, long long n_slots, int sh, const float* k_scale,
@@ -542,6 +729,45 @@ bsa_status bsa_cache_append(const void* k, const void* v, bsa_dtype dtype, int T
                                       v_scale, k_val, v_val, st)
                : launch_append<__nv_bfloat16>(k, v, k_stride, v_stride, T, H, D, slots, (uint8_t*)cache, n_slots, sh,
                                               k_scale, v_scale, k_val, v_val, st);
+}
+
+bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D,
+                                    int64_t k_stride, int64_t v_stride, const int64_t* slots, void* cache, int n_pages,
+                                    int page_size, const float* k_scale, const float* v_scale, void* k_val,
+                                    void* v_val, const float* cos_table, const float* sin_table, int P,
+                                    int interleaved, const void* q, int HQ, int64_t q_stride, void* q_out,
+                                    void* stream) {
+    BSA_REQUIRE(cache && (T == 0 || (k && v && slots && cos_table && sin_table)), "rotated append: null pointer");
+    BSA_REQUIRE(T == 0 || (k_val == nullptr) == (v_val == nullptr), "rotated append: k_val and v_val come together");
+    BSA_REQUIRE(T == 0 || (q == nullptr) == (q_out == nullptr), "rotated append: q and q_out come together");
+    BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "rotated append: dtype");
+    BSA_REQUIRE(T >= 0 && H > 0 && n_pages > 0, "rotated append: sizes out of range (T=%d H=%d n_pages=%d)", T, H, n_pages);
+    BSA_REQUIRE(page_size_ok(page_size), "rotated append: page_size must be a power of two in 16..1024, got %d", page_size);
+    BSA_REQUIRE(D >= 16 && D <= 128 && D % 16 == 0, "rotated append: D must be a multiple of 16 up to 128, got %d", D);
+    BSA_REQUIRE(P >= 1 && 2 * P <= D, "rotated append: 1 <= P <= D / 2 is needed, got P=%d", P);
+    BSA_REQUIRE(H <= (1 << 20) && (T <= 1 || (k_stride >= (int64_t)H * D && v_stride >= (int64_t)H * D)),
+                "rotated append: a token's stride is below H * D");
+    BSA_REQUIRE(!q || (HQ >= 1 && HQ <= (1 << 20) && (T <= 1 || q_stride >= (int64_t)HQ * D)),
+                "rotated append: HQ out of range, or a query token's stride below HQ * D");
+    BSA_REQUIRE(((uintptr_t)cache & 15) == 0, "rotated append: the cache must be 16-byte aligned");
+    if (T == 0) return BSA_OK;
+    const long long n_slots = (long long)n_pages * page_size;
+    const int sh = log2i(page_size);
+    cudaStream_t st = as_stream(stream);
+    Rotated a{};
+    a.cos = cos_table;
+    a.sin = sin_table;
+    a.P = P;
+    a.interleaved = interleaved != 0;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.HQ = HQ;
+    a.q_out = q_out;
+    return dtype == BSA_F32
+               ? launch_append_rotated<float>(k, v, k_stride, v_stride, T, H, D, slots, (uint8_t*)cache, n_slots, sh,
+                                              k_scale, v_scale, k_val, v_val, a, st)
+               : launch_append_rotated<__nv_bfloat16>(k, v, k_stride, v_stride, T, H, D, slots, (uint8_t*)cache,
+                                                      n_slots, sh, k_scale, v_scale, k_val, v_val, a, st);
 }
 
 }  // extern "C"

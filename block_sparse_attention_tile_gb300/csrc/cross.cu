@@ -1,0 +1,278 @@
+// a18 cross attention on the CUDA cores (float32, and sizes that the tensor-core kernels do not take), the join of
+// the keys' parts, and the entry points.
+//
+// "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.5: the log2-domain recurrence of the online softmax; a row with
+// no key outputs zero.
+#include <algorithm>
+#include <climits>
+#include <math_constants.h>
+
+#include "cross.cuh"
+
+namespace bsa {
+
+// ---------------------------------------------------------------- CUDA cores
+//
+// A block holds 64 rows against 64 keys at a time: 16 x 16 threads, 4 rows x 4 keys of the logits and 4 rows x D / 16
+// channels of the output each, both products from shared memory in float32.
+constexpr int kSimtRows = 64, kSimtKeys = 64;
+
+static size_t simt_smem(int D4) { return sizeof(float) * ((size_t)kSimtRows * (D4 + 4) + 2 * kSimtKeys * (D4 + 4) + kSimtRows * (kSimtKeys + 4)); }
+
+template <typename T, int kC>  // kC: groups of 64 channels
+__global__ void __launch_bounds__(256) cross_simt_kernel(const Cross a) {
+    extern __shared__ __align__(16) float smem[];
+    const int Dp = (a.D + 3) & ~3, ld = Dp + 4;
+    float *Qs = smem, *Ks = Qs + kSimtRows * ld, *Vs = Ks + kSimtKeys * ld, *Ps = Vs + kSimtKeys * ld;
+    constexpr int kPd = kSimtKeys + 4;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int h = blockIdx.y, part = blockIdx.z;
+    int b, row0, q0, n, k0, m;
+    tile_of<kSimtRows>(a, blockIdx.x, b, row0);
+    if (b < 0) return;
+    queries_of(a, b, q0, n);
+    keys_of(a, b, k0, m);
+    const long long rows = (long long)n * a.G;
+    const int nr = (int)min((long long)kSimtRows, rows - row0);
+    const long long qbat = a.query_start ? 0 : b, kbat = a.key_start ? 0 : b;
+    const T* q = (const T*)a.q + qbat * a.qb + (long long)h * a.G * a.qh;
+    const T* k = (const T*)a.k + kbat * a.kb + (long long)h * a.kh + k0 * a.kt;
+    const T* v = (const T*)a.v + kbat * a.vb + (long long)h * a.vh + k0 * a.vt;
+    const float scale = a.scale * kLog2e;
+    for (int i = threadIdx.x; i < kSimtRows * Dp; i += 256) {
+        const int r = i / Dp, d = i - r * Dp;
+        float x = 0.f;
+        if (r < nr && d < a.D) x = to_f32(q[(long long)(q0 + (row0 + r) / a.G) * a.qt + (row0 + r) % a.G * a.qh + d]);
+        Qs[r * ld + d] = x * scale;
+    }
+    float mx[4], l[4], acc[4][kC][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        mx[r] = -CUDART_INF_F;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[r][c][e] = 0.f;
+    }
+    const int nt = (m + kSimtKeys - 1) / kSimtKeys;
+    const int t1 = (int)((long long)nt * (part + 1) / a.parts);
+    for (int t = (int)((long long)nt * part / a.parts); t < t1; ++t) {
+        const int first = t * kSimtKeys, nk = min(kSimtKeys, m - first);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kSimtKeys * Dp; i += 256) {
+            const int r = i / Dp, d = i - r * Dp;
+            const bool on = r < nk && d < a.D;
+            Ks[r * ld + d] = on ? to_f32(k[(first + r) * a.kt + d]) : 0.f;
+            Vs[r * ld + d] = on ? to_f32(v[(first + r) * a.vt + d]) : 0.f;
+        }
+        __syncthreads();
+        float s[4][4] = {};
+        for (int d = 0; d < Dp; d += 4) {
+            float4 qv[4], kv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4*>(Qs + (4 * ty + r) * ld + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * ld + d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[r][j] = fmaf(qv[r].x, kv[j].x, fmaf(qv[r].y, kv[j].y, fmaf(qv[r].z, kv[j].z, fmaf(qv[r].w, kv[j].w, s[r][j]))));
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (tx + 16 * j >= nk) s[r][j] = -CUDART_INF_F;
+                top = fmaxf(top, s[r][j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float now = fmaxf(mx[r], top), ref = now == -CUDART_INF_F ? 0.f : now, alpha = exp2f(mx[r] - ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[r][j] - ref);
+                Ps[(4 * ty + r) * kPd + tx + 16 * j] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            mx[r] = now;
+            l[r] = l[r] * alpha + sum;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][c][e] *= alpha;
+        }
+        __syncwarp();  // a row's weights are written and read by one warp
+        for (int j = 0; j < nk; ++j) {
+            float p[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[r] = Ps[(4 * ty + r) * kPd + j];
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                if (4 * tx + 64 * c >= Dp) continue;
+                const float4 x = *reinterpret_cast<const float4*>(Vs + j * ld + 4 * tx + 64 * c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[r][c][0] = fmaf(p[r], x.x, acc[r][c][0]);
+                    acc[r][c][1] = fmaf(p[r], x.y, acc[r][c][1]);
+                    acc[r][c][2] = fmaf(p[r], x.z, acc[r][c][2]);
+                    acc[r][c][3] = fmaf(p[r], x.w, acc[r][c][3]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (4 * ty + r >= nr) break;
+        const int tok = q0 + (row0 + 4 * ty + r) / a.G, hq = h * a.G + (row0 + 4 * ty + r) % a.G;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], lse = l[r] == 0.f ? -CUDART_INF_F : (mx[r] + log2f(l[r])) * kLn2;
+        if (a.parts > 1) {
+            const long long total = a.query_start ? a.N : (long long)a.B * a.N;
+            const long long at = (part * total + (a.query_start ? 0 : (long long)b * a.N) + tok) * a.HQ + hq;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * tx + 64 * c + e < a.D) a.part_out[at * a.D + 4 * tx + 64 * c + e] = acc[r][c][e] * inv;
+            if (tx == 0) a.part_lse[at] = lse;
+        } else {
+            T* o = (T*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * tx + 64 * c + e < a.D) o[4 * tx + 64 * c + e] = from_f32<T>(acc[r][c][e] * inv);
+            if (tx == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- join
+//
+// A warp a row: out = sum_p exp(lse_p - L) out_p, L = log sum_p exp(lse_p), in the order of the parts.
+template <typename T>
+__global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
+    const int lane = threadIdx.x & 31, h = blockIdx.y;
+    int b, row0, q0, n;
+    tile_of<kSimtRows>(a, blockIdx.x, b, row0);
+    if (b < 0) return;
+    queries_of(a, b, q0, n);
+    const long long total = a.query_start ? a.N : (long long)a.B * a.N, rows = (long long)n * a.G;
+    const long long step = total * a.HQ, qbat = a.query_start ? 0 : b;
+    for (long long r = row0 + (threadIdx.x >> 5); r < min(rows, (long long)row0 + kSimtRows); r += 8) {
+        const int tok = q0 + (int)(r / a.G), hq = h * a.G + (int)(r % a.G);
+        const long long i = ((a.query_start ? 0 : (long long)b * a.N) + tok) * a.HQ + hq;
+        float top = -CUDART_INF_F;
+        for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.part_lse[p * step + i]);
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        float sum = 0.f, acc[4] = {};
+        for (int p = 0; p < a.parts; ++p) {
+            const long long at = p * step + i;
+            const float w = exp2f((a.part_lse[at] - ref) * kLog2e);
+            sum += w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (lane + 32 * c < a.D) acc[c] = fmaf(w, a.part_out[at * a.D + lane + 32 * c], acc[c]);
+        }
+        T* o = (T*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (lane + 32 * c < a.D) o[lane + 32 * c] = from_f32<T>(acc[c] * inv);
+        if (lane == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct CrossPlan {
+    int parts;
+    long long tiles;
+};
+
+static CrossPlan cross_plan(int B, int N, int M, int HQ, int H, bool packed_q, bool packed_k) {
+    CrossPlan p;
+    p.tiles = row_tiles(B, N, HQ / H, packed_q, kSimtRows);
+    const long long blocks = std::max<long long>(1, p.tiles * H);
+    const long long keys = packed_k ? (M + B - 1) / std::max(B, 1) : M;
+    p.parts = (int)std::max<long long>(1, std::min<long long>({2 * 152 / blocks, (keys + 127) / 128, 64}));
+    return p;
+}
+
+static bool cross_sizes_ok(int B, int N, int M, int HQ, int H, int D) {
+    return B >= 0 && N >= 0 && M >= 0 && HQ >= 1 && H >= 1 && HQ <= 65535 && HQ % H == 0 && D >= 1 && D <= 128 &&
+           (long long)B * std::max(N, 1) <= INT_MAX && (long long)N * (HQ / H) * (long long)std::max(B, 1) <= INT_MAX / 2;
+}
+
+static size_t part_bytes(const CrossPlan& p, int B, int N, int HQ, int D, bool packed_q) {
+    return p.parts <= 1 ? 0 : sizeof(float) * (size_t)p.parts * (packed_q ? N : (size_t)B * N) * HQ * (D + 1);
+}
+
+template <typename T>
+static bsa_status launch_cross_simt(const Cross& a, cudaStream_t st) {
+    const size_t smem = simt_smem((a.D + 3) & ~3);
+    const dim3 grid((unsigned)a.tiles, a.H, a.parts);
+    auto fn = a.D <= 64 ? cross_simt_kernel<T, 1> : cross_simt_kernel<T, 2>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(BSA_ERR_CUDA, "cross attention attribute: %s", cudaGetErrorString(e));
+    fn<<<grid, 256, smem, st>>>(a);
+    return check_launch("cross_simt_kernel");
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" {
+
+size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
+                           int packed_keys) {
+    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D) || B == 0 || N == 0) return 0;
+    return part_bytes(cross_plan(B, N, M, HQ, H, packed_queries != 0, packed_keys != 0), B, N, HQ, D, packed_queries != 0);
+}
+
+bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype dtype, int B, int N, int M, int HQ,
+                         int H, int D, const int64_t* strides, const int32_t* query_start, const int32_t* key_start,
+                         const int32_t* key_lens, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "cross attention: dtype");
+    BSA_REQUIRE(cross_sizes_ok(B, N, M, HQ, H, D), "cross attention: sizes out of range (B=%d N=%d M=%d HQ=%d H=%d D=%d)",
+                B, N, M, HQ, H, D);
+    BSA_REQUIRE(strides, "cross attention: null strides");
+    BSA_REQUIRE(!(key_start && key_lens), "cross attention: key_start and key_lens exclude each other");
+    BSA_REQUIRE(scale >= 0.f && scale <= 3.0e38f, "cross attention: the scale must be finite and not negative");
+    if (B == 0 || N == 0) return BSA_OK;
+    BSA_REQUIRE(q && out && (M == 0 || (k && v)), "cross attention: null pointer");
+    const CrossPlan p = cross_plan(B, N, M, HQ, H, query_start != nullptr, key_start != nullptr);
+    const size_t need = part_bytes(p, B, N, HQ, D, query_start != nullptr);
+    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 15) == 0),
+                "cross attention: a 16-byte aligned workspace of %zu bytes is needed", need);
+    Cross a{};
+    a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
+    long long* to[15] = {&a.qb, &a.qt, &a.qh, &a.kb, &a.kt, &a.kh, &a.vb, &a.vt, &a.vh, &a.ob, &a.ot, &a.oh, &a.lb, &a.lt, &a.lh};
+    for (int i = 0; i < 15; ++i) *to[i] = strides[i];
+    a.query_start = query_start, a.key_start = key_start, a.key_lens = key_lens;
+    a.B = B, a.N = N, a.M = M, a.HQ = HQ, a.H = H, a.D = D, a.G = HQ / H;
+    a.scale = scale;
+    a.parts = p.parts;
+    a.tiles = (int)p.tiles;
+    a.status = status_word();
+    const long long rows = (query_start ? (long long)N : (long long)B * N) * HQ;
+    a.part_out = need ? static_cast<float*>(workspace) : nullptr;
+    a.part_lse = need ? a.part_out + (size_t)p.parts * rows * D : nullptr;
+    cudaStream_t st = as_stream(stream);
+    bsa_status rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
+    if (rc != BSA_OK || p.parts == 1) return rc;
+    const dim3 grid((unsigned)p.tiles, H);
+    if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 256, 0, st>>>(a);
+    else cross_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    return check_launch("cross_join_kernel");
+}
+
+}  // extern "C"

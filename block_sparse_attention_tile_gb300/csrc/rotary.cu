@@ -1,0 +1,233 @@
+// a15 rotary table, a16 rotation of q and k.
+//
+// "The token path": queries and keys reach the attention after the projections, a norm over each head and
+// the rotation by their positions; these two kernels are that step, from the projection's layout to the one
+// that the attention reads.
+#include <algorithm>
+
+#include "rotary.cuh"
+
+namespace bsa {
+
+// ---------------------------------------------------------------- a15 table
+//
+// A frequency is held as turns a position in units of 2^-64, so the angle's fraction of a turn is the low 64
+// bits of an integer product: exact for any position, where a float32 product would have lost the angle of
+// position 2^24 altogether.  The upper 32 bits are cut into quadrant and remainder, and only the
+// remainder, an eighth of a turn at most, becomes a float.
+__device__ __forceinline__ void cos_sin(uint64_t turn, float factor, float& c, float& s) {
+    const uint32_t t = (uint32_t)((turn + 0x80000000ull) >> 32);  // 2^-32 turns
+    const uint32_t quad = (t + (1u << 29)) >> 30;
+    const float x = (float)(int32_t)(t - (quad << 30)) * 0x1p-31f;  // half turns, |x| <= 1/4
+    float sn, cs;
+    sincospif(x, &sn, &cs);
+    const float a = quad & 1 ? sn : cs, b = quad & 1 ? cs : sn;
+    c = ((quad + 1) & 2 ? -a : a) * factor;
+    s = (quad & 2 ? -b : b) * factor;
+}
+
+template <int V>
+__global__ void __launch_bounds__(256) rotary_table_kernel(const int32_t* __restrict__ positions, int axes,
+                                                           const int64_t* __restrict__ turns,
+                                                           const int32_t* __restrict__ axis, int P, float factor,
+                                                           float* __restrict__ cos_out, float* __restrict__ sin_out,
+                                                           long long items, int* status) {
+    const int per = P / V;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
+        const long long t = i / per;
+        const int p = (int)(i - t * per) * V;
+        float c[V], s[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            int a = axis ? axis[p + j] : 0;
+            if ((unsigned)a >= (unsigned)axes) {
+                raise_status(status, BSA_ERR_INDEX);
+                a = 0;
+            }
+            cos_sin((uint64_t)turns[p + j] * (uint64_t)(int64_t)positions[t * axes + a], factor, c[j], s[j]);
+        }
+        const long long at = t * P + p;
+        if constexpr (V == 4) {
+            *reinterpret_cast<float4*>(cos_out + at) = make_float4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<float4*>(sin_out + at) = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+            cos_out[at] = c[0];
+            sin_out[at] = s[0];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- a16 rotate
+
+struct Rotate {
+    RowSet set[2];
+    const float* cos;
+    const float* sin;
+    long long table_batch;
+    int T, D, P, splits;
+    long long items;  // B * T * splits
+    float eps;
+    bool interleaved, transpose;
+};
+
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(256) rotate_kernel(const Rotate a) {
+    const int lane = threadIdx.x & 31, u = lane % kLanes;
+    const bool live = 16 * u < a.D, turn = 8 * u < a.P;
+    int c0, c1;
+    unit_runs(u, a.P, a.interleaved, c0, c1);
+    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < a.items; i += (long long)gridDim.x * 8) {
+        const long long tok = i / a.splits;
+        const int part = (int)(i - tok * a.splits);
+        const long long b = tok / a.T, t = tok - b * a.T;
+        float c[8], s[8];
+        if (turn) {
+            const long long at = b * a.table_batch + t * a.P + 8 * u;
+            load8(a.cos + at, c);
+            load8(a.sin + at, s);
+            if (a.transpose) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = -s[j];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const RowSet& r = a.set[n];
+            const int h0 = (int)((long long)r.heads * part / a.splits), h1 = (int)((long long)r.heads * (part + 1) / a.splits);
+            rotate_heads<T, kLanes>(r, (const T*)r.x + b * r.xb + t * r.xt, (T*)r.y + b * r.yb + t * r.yt, h0, h1, lane,
+                                    a.D, live, turn, c0, c1, c, s, a.interleaved, a.eps);
+        }
+    }
+}
+
+// Any D up to 256, any number of pairs, any strides: a warp a row, a channel a lane at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) rotate_any_kernel(const Rotate a, long long rows) {
+    const int lane = threadIdx.x & 31, heads = a.set[0].heads + a.set[1].heads;
+    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * 8) {
+        const long long tok = i / heads, b = tok / a.T, t = tok - b * a.T;
+        int h = (int)(i - tok * heads);
+        const int n = h >= a.set[0].heads;
+        if (n) h -= a.set[0].heads;
+        const RowSet& r = a.set[n];
+        const T* x = (const T*)r.x + b * r.xb + t * r.xt + h * r.xh;
+        T* y = (T*)r.y + b * r.yb + t * r.yt + h * r.yh;
+        const float *cs = a.cos + b * a.table_batch + t * a.P, *sn = a.sin + b * a.table_batch + t * a.P;
+        float norm = 1.f, out[8];
+        if (r.weight) {
+            float ss = 0.f;
+            for (int c = lane; c < a.D; c += 32) ss = fmaf(to_f32(x[c]), to_f32(x[c]), ss);
+            norm = rsqrtf(warp_sum(ss) / a.D + a.eps);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = lane + 32 * j;
+            if (c >= a.D) break;
+            const auto at = [&](int ch) { return r.weight ? to_f32(x[ch]) * (norm * r.weight[ch]) : to_f32(x[ch]); };
+            float v = at(c);
+            if (c < 2 * a.P) {
+                const bool first = a.interleaved ? !(c & 1) : c < a.P;
+                const int p = a.interleaved ? c >> 1 : first ? c : c - a.P;
+                const float o = at(a.interleaved ? c ^ 1 : first ? c + a.P : c - a.P), s = a.transpose ? -sn[p] : sn[p];
+                v = first ? __fsub_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, s)) : __fadd_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, s));
+            }
+            out[j] = v;
+        }
+        __syncwarp();  // y may be x
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (lane + 32 * j < a.D) y[lane + 32 * j] = from_f32<T>(out[j]);
+    }
+}
+
+template <typename T>
+static bsa_status launch_rotate(Rotate& a, long long tokens, bool wide, cudaStream_t st) {
+    const int heads = a.set[0].heads + a.set[1].heads;
+    const auto blocks = [](long long warps) { return (unsigned)std::min<long long>((warps + 7) / 8, 152 * 64); };
+    if (!wide) {
+        rotate_any_kernel<T><<<blocks(tokens * heads), 256, 0, st>>>(a, tokens * heads);
+        return check_launch("rotate_any_kernel");
+    }
+    const int lanes = a.D <= 32 ? 2 : a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
+    const int steps = (heads * lanes + 31) / 32;  // of a whole token
+    a.splits = (int)std::max<long long>(1, std::min<long long>(steps, 152 * 32 / std::max<long long>(tokens, 1)));
+    a.items = tokens * a.splits;
+    const unsigned grid = blocks(a.items);
+    if (lanes == 2) rotate_kernel<T, 2><<<grid, 256, 0, st>>>(a);
+    else if (lanes == 4) rotate_kernel<T, 4><<<grid, 256, 0, st>>>(a);
+    else if (lanes == 8) rotate_kernel<T, 8><<<grid, 256, 0, st>>>(a);
+    else rotate_kernel<T, 16><<<grid, 256, 0, st>>>(a);
+    return check_launch("rotate_kernel");
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" {
+
+bsa_status bsa_rotary_table(const int32_t* positions, int T, int axes, const int64_t* turns, const int32_t* axis,
+                            int P, float factor, float* cos_out, float* sin_out, void* stream) {
+    BSA_REQUIRE(T >= 0 && axes >= 1 && axes <= 8 && P >= 1 && P <= 128,
+                "rotary table: sizes out of range (T=%d axes=%d P=%d)", T, axes, P);
+    BSA_REQUIRE(turns && (T == 0 || (positions && cos_out && sin_out)), "rotary table: null pointer");
+    BSA_REQUIRE(axes == 1 || axis, "rotary table: several axes need an axis for each frequency");
+    if (T == 0) return BSA_OK;
+    const bool wide = P % 4 == 0 && (((uintptr_t)cos_out | (uintptr_t)sin_out) & 15) == 0;
+    const long long items = (long long)T * P / (wide ? 4 : 1);
+    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 152 * 64);
+    cudaStream_t st = as_stream(stream);
+    if (wide)
+        rotary_table_kernel<4><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, items,
+                                                     status_word());
+    else
+        rotary_table_kernel<1><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, items,
+                                                     status_word());
+    return check_launch("rotary_table_kernel");
+}
+
+bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleaved, int transpose,
+                      const float* cos_table, const float* sin_table, int64_t table_batch_stride, const void* q, int HQ,
+                      const float* q_weight, void* q_out, const void* k, int H, const float* k_weight, void* k_out,
+                      const int64_t* strides, float eps, void* stream) {
+    BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "rotate: dtype");
+    BSA_REQUIRE(B >= 0 && T >= 0 && D >= 2 && D <= 256 && P >= 1 && 2 * P <= D && HQ >= 1 && HQ <= (1 << 20) && H >= 0 &&
+                    H <= (1 << 20),
+                "rotate: sizes out of range (B=%d T=%d D=%d P=%d HQ=%d H=%d)", B, T, D, P, HQ, H);
+    BSA_REQUIRE(strides, "rotate: null strides");
+    if (B == 0 || T == 0) return BSA_OK;
+    BSA_REQUIRE(cos_table && sin_table && q && q_out && (H == 0 || (k && k_out)), "rotate: null pointer");
+    BSA_REQUIRE(!transpose || (!q_weight && !k_weight), "rotate: the transposed rotation takes no norm");
+    BSA_REQUIRE(!(q_weight || k_weight) || (eps >= 0.f && eps <= 1.f), "rotate: eps must lie in [0, 1]");
+    Rotate a{};
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const float* weight[2] = {q_weight, k_weight};
+    const int heads[2] = {HQ, H};
+    const int size = dtype == BSA_F32 ? 4 : 2;
+    bool wide = D % 16 == 0 && P % 8 == 0 && (((uintptr_t)cos_table | (uintptr_t)sin_table) & 15) == 0 &&
+                table_batch_stride % 4 == 0;
+    for (int n = 0; n < 2; ++n) {
+        const int64_t* s = strides + 6 * n;
+        a.set[n] = RowSet{in[n], out[n], weight[n], s[0], s[1], s[2], s[3], s[4], s[5], heads[n]};
+        if (!heads[n]) continue;
+        uintptr_t any = (uintptr_t)in[n] | (uintptr_t)out[n] | (uintptr_t)weight[n];
+        for (int j = 0; j < 6; ++j) any |= (uintptr_t)(s[j] * size);
+        wide = wide && (any & 15) == 0;
+    }
+    a.cos = cos_table;
+    a.sin = sin_table;
+    a.table_batch = table_batch_stride;
+    a.T = T;
+    a.D = D;
+    a.P = P;
+    a.eps = eps;
+    a.interleaved = interleaved != 0;
+    a.transpose = transpose != 0;
+    cudaStream_t st = as_stream(stream);
+    const long long tokens = (long long)B * T;
+    return dtype == BSA_F32 ? launch_rotate<float>(a, tokens, wide, st)
+                            : launch_rotate<__nv_bfloat16>(a, tokens, wide, st);
+}
+
+}  // extern "C"

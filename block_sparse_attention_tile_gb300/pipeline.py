@@ -6,6 +6,7 @@ stages in order on the current stream.  No arithmetic of the method happens
 in Python.
 """
 
+import math
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
@@ -416,6 +417,170 @@ def cache_attention(q, cache, block_table, token_req, token_pos, k_scale=None, v
     return out, lse
 
 
+class Rotary(NamedTuple):
+    """Frequencies of a rotation: turns int64 [P] in 2^-64 turns a position, the axis
+    of each (int32 [P], None with one axis) and the factor of cos and sin."""
+    turns: torch.Tensor
+    axis: Optional[torch.Tensor]
+    factor: float
+
+    def table(self, positions, out=None):
+        return rotary_table(positions, self.turns, self.axis, self.factor, out)
+
+
+def rotary_frequencies(channels, base=10000.0, sections=None, scaling=None, stretch=1.0, trained=0, ramp=(1.0, 32.0),
+                       device="cuda"):
+    """Frequencies of ``channels`` rotated channels: base^(-i / P) for pair i of P.  ``sections``: channels of each
+    axis (they sum to ``channels``), every axis with a ladder of its own.  For contexts ``stretch`` times the
+    ``trained`` positions, ``scaling`` is
+      "linear"  every frequency / stretch
+      "base"    base * stretch^(d / (d - 2)) over the axis's d channels: the highest frequency stays, the lowest is
+                divided by stretch
+      "parts"   frequencies of fewer than ramp[0] turns in ``trained`` positions / stretch, those of more than ramp[1]
+                as they are, linear between the two; cos and sin times 0.1 ln(stretch) + 1."""
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError("no scaling %r" % (scaling,))
+    sections = [channels] if sections is None else list(sections)
+    if sum(sections) != channels or any(d < 2 or d % 2 for d in sections):
+        raise ValueError("sections %s: even numbers that sum to %d are needed" % (sections, channels))
+    if not stretch >= 1.0 or (scaling == "parts" and not (trained > 0 and ramp[1] > ramp[0])):
+        raise ValueError("stretch must be at least 1, and scaling by parts needs trained positions and a rising ramp")
+    turns, axis = [], []
+    for a, d in enumerate(sections):
+        own = base * stretch ** (d / (d - 2)) if scaling == "base" and d > 2 else base
+        for i in range(d // 2):
+            f = own ** (-2 * i / d) / (2 * math.pi)  # turns a position
+            if scaling == "linear":
+                f /= stretch
+            elif scaling == "parts":
+                kept = min(1.0, max(0.0, (f * trained - ramp[0]) / (ramp[1] - ramp[0])))
+                f = f * kept + f / stretch * (1.0 - kept)
+            t = round(f * 2.0 ** 64) % (1 << 64)
+            turns.append(t - (1 << 64) if t >> 63 else t)
+            axis.append(a)
+    return Rotary(torch.tensor(turns, dtype=torch.int64, device=device),
+                  torch.tensor(axis, dtype=torch.int32, device=device) if len(sections) > 1 else None,
+                  0.1 * math.log(stretch) + 1.0 if scaling == "parts" else 1.0)
+
+
+def rotary_table(positions, turns, axis=None, factor=1.0, out=None):
+    """(cos, sin) float32 [T, P] of positions int32 [T] or [T, axes] and the frequencies of ``Rotary``."""
+    T, axes = positions.shape[0], positions.shape[1] if positions.dim() == 2 else 1
+    P = turns.shape[0]
+    if axis is not None and axis.shape != turns.shape:
+        raise ValueError("axis: one for each of %d frequencies is needed, got %s" % (P, tuple(axis.shape)))
+    if out is None:
+        both = torch.empty(2, T, P, dtype=torch.float32, device=turns.device)
+        out = (both[0], both[1])
+    elif out[0].shape != (T, P) or out[1].shape != (T, P):
+        raise ValueError("out: two tensors [%d, %d] are needed" % (T, P))
+    bsa.bsa_rotary_table(positions, T, axes, turns, axis, P, factor, out[0], out[1])
+    return out
+
+
+def rotate(q, k, cos, sin, interleaved=False, q_weight=None, k_weight=None, eps=1e-6, heads_first=False,
+           transpose=False, out=None):
+    """q [B, T, HQ, D] and k [B, T, H, D] (or both without B; k may be None) rotated by cos and sin [T, P] ([B, T, P]:
+    of each sequence), after an RMS norm over each head's channels where there is a weight [D].  Any strides with
+    adjacent channels.  Returns (q, k) as new tensors of the same layout, or heads first ([B, H, T, D], what the
+    block-sparse stages read).  ``transpose``: the transposed rotation, which is the gradient's and takes a rotation
+    back.  ``out``: the two tensors to write instead of new ones, q and k themselves among them."""
+    flat = q.dim() == 3
+    if flat:
+        q, k = q[None], None if k is None else k[None]
+    B, T, HQ, D = q.shape
+    H, P = 0 if k is None else k.shape[2], cos.shape[-1]
+    if sin.shape != cos.shape or cos.shape not in ((T, P), (B, T, P)):
+        raise ValueError("tables [%d, P] or [%d, %d, P] are needed, got %s and %s"
+                         % (T, B, T, tuple(cos.shape), tuple(sin.shape)))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.shape != (D,):
+            raise ValueError("%s: [%d] is needed, got %s" % (name, D, tuple(w.shape)))
+    made = []
+    for n, x in enumerate((q, k)):
+        if x is None:
+            made.append((None, None))
+            continue
+        shape = (B, x.shape[2], T, D) if heads_first else (B, T, x.shape[2], D)
+        if out is None:
+            y = torch.empty(shape, dtype=q.dtype, device=q.device)
+        else:
+            y = out[n][None] if flat else out[n]
+            if y.shape != shape:
+                raise ValueError("out: %s is needed, got %s" % (list(shape[1:] if flat else shape), tuple(out[n].shape)))
+        made.append((y, y.transpose(1, 2) if heads_first else y))
+    bsa.bsa_rotate(q, k, B, T, HQ, H, D, P, cos, sin, T * P if cos.dim() == 3 else 0, made[0][1], made[1][1],
+                   interleaved, transpose, q_weight, k_weight, eps)
+    if out is not None:
+        return out
+    return tuple(y[0] if flat and y is not None else y for y, _ in made)
+
+
+def cache_append_rotated(k, v, slots, cache, cos, sin, k_scale=None, v_scale=None, interleaved=False, values=None,
+                         q=None, q_out=None):
+    """``cache_append`` with K rotated on the way by cos and sin [T, P], and the queries q [T, HQ, D] rotated in the
+    same launch into ``q_out`` (a new tensor if None), which is returned."""
+    T, H, D = k.shape
+    if cache.shape[1] != H or cache.shape[3] != 18 * D:
+        raise ValueError("cache %s does not hold %d heads of %d channels" % (tuple(cache.shape), H, D))
+    P = cos.shape[-1]
+    if cos.shape != (T, P) or sin.shape != (T, P):
+        raise ValueError("tables [%d, P] are needed, got %s and %s" % (T, tuple(cos.shape), tuple(sin.shape)))
+    _check_scales(k_scale, v_scale, H)
+    kv, vv = (None, None) if values is None else values
+    if values is not None:
+        _check_rows("values", kv, T, H, D)
+        _check_rows("values", vv, T, H, D)
+    HQ = 0
+    if q is not None:
+        HQ = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(T, HQ, D, dtype=q.dtype, device=q.device)
+        else:
+            _check_rows("q_out", q_out, T, HQ, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    bsa.bsa_cache_append_rotated(k, v, T, H, D, slots, cache, cache.shape[0], cache.shape[2] * 16, k_scale, v_scale, kv,
+                                 vv, cos, sin, P, interleaved, q, HQ, q_out)
+    return q_out
+
+
+def cross_attention(q, k, v, key_lens=None, query_start=None, key_start=None, scale=None, need_lse=True, out=None,
+                    lse=None):
+    """Queries over an encoder's states.  Padded: q [B, N, HQ, D], k and v [B, M, H, D], the first key_lens[b]
+    (int32 [B], None: all) states of sequence b count.  Packed: q [N, HQ, D] with query_start, k and v [M, H, D] with
+    key_start (int32 [B + 1] each; either alone or both).  Any strides with adjacent channels.  Returns
+    (out as q, lse [B, N, HQ] or [N, HQ], or None).  ``out``, ``lse``: tensors to write instead of new ones; rows of
+    no sequence are left as they were."""
+    packed_q, packed_k = query_start is not None, key_start is not None
+    if q.dim() != (3 if packed_q else 4) or k.dim() != (3 if packed_k else 4) or v.shape != k.shape:
+        raise ValueError("q %s, k %s, v %s: packed rows have three dimensions, padded ones four"
+                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    if out is None:
+        out = torch.empty_like(q)
+    if packed_q:
+        B = query_start.shape[0] - 1
+        N, HQ, D = q.shape
+    else:
+        B, N, HQ, D = q.shape
+    M, H = k.shape[-3], k.shape[-2]
+    if (packed_k and key_start.shape[0] - 1 != B) or (key_lens is not None and key_lens.shape != (B,)):
+        raise ValueError("the states of %d sequences are needed" % B)
+    if need_lse and lse is None:
+        if packed_q:
+            lse = torch.empty(N, HQ, dtype=torch.float32, device=q.device)
+        elif q.stride(2) > q.stride(1):  # heads first, as q
+            lse = torch.empty(B, HQ, N, dtype=torch.float32, device=q.device).transpose(1, 2)
+        else:
+            lse = torch.empty(B, N, HQ, dtype=torch.float32, device=q.device)
+    nbytes = bsa.bsa_cross_workspace(q.dtype, B, N, M, HQ, H, D, packed_q, packed_k)
+    ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
+    bsa.bsa_fwd_cross(q[None] if packed_q else q, k[None] if packed_k else k, v[None] if packed_k else v, B, N, M, HQ, H,
+                      D, query_start, key_start, key_lens, D ** -0.5 if scale is None else scale,
+                      out[None] if packed_q else out, lse if lse is None or not packed_q else lse[None], ws)
+    return out, lse
+
+
 class TokenCache:
     """One layer's paged 4-bit cache with its tables, for R requests.
 
@@ -458,8 +623,16 @@ class TokenCache:
         self.lens.copy_(held)
         return out
 
-    def append(self, k, v, step, values=None):
-        cache_append(k, v, step.slots, self.cache, self.k_scale, self.v_scale, values)
+    def append(self, k, v, step, values=None, rotary=None, interleaved=False, q=None):
+        """The step's K and V into the cache.  ``rotary``: the step's (cos, sin) tables (``rotary_table`` of
+        step.token_pos); K is then rotated on the way, and ``q`` [max_tokens, HQ, D], where given, is returned
+        rotated."""
+        if rotary is None:
+            if q is not None:
+                raise ValueError("queries are rotated by the rotary tables of the step")
+            return cache_append(k, v, step.slots, self.cache, self.k_scale, self.v_scale, values)
+        return cache_append_rotated(k, v, step.slots, self.cache, rotary[0], rotary[1], self.k_scale, self.v_scale,
+                                    interleaved, values, q)
 
     def attend(self, q, step, block_indices=None, block_counts=None, block_size=0, scale=None, need_lse=True):
         return cache_attention(q, self.cache, self.block_table, step.token_req, step.token_pos, self.k_scale,

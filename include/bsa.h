@@ -7,7 +7,8 @@
  * plus the caller-routed GQA variant (NSA selected branch), the KV-outer
  * order (reverse index, partial pass, log-sum-exp combine), the
  * exact-plus-summary variant, and token-by-token use of the GQA variant over a
- * paged cache held in 4 bits.
+ * paged cache held in 4 bits; and what stands between a model's projections and
+ * these: rotary positions, and attention to an encoder's states.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -573,6 +574,90 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
                                 const float* k_scale, const float* v_scale, const int32_t* block_indices,
                                 const int32_t* block_counts, int S, int block_size, float scale, void* out,
                                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ a15 ---
+ * Rotary table: cos and sin of the angles by which the pairs of channels of
+ * each token turn.  Pair i of token t turns by 2 pi times the fraction of
+ *   positions[t, axis[i]] * turns[i] / 2^64,
+ * turns being the frequency in units of 2^-64 turns a position (a frequency of f
+ * radians is round(f / 2 pi * 2^64)): the product is exact, so a position of any size, negative ones
+ * too, keeps its angle.  cos_out, sin_out [T, P] = factor * cos, factor * sin (factor: 1, or the
+ * attention factor of a stretched context).
+ * positions: [device] int32 [T, axes] (axes <= 8: one for text, t / y / x for a
+ * video); turns: [device] int64 [P]; axis: [device] int32 [P], or NULL with one
+ * axis (an axis outside [0, axes) latches BSA_ERR_INDEX and is read as 0);
+ * P <= 128.  cos_out, sin_out: [device] float [T, P].  T = 0 does nothing.
+ * Every row is written, those of padding tokens (position -1) too. */
+bsa_status bsa_rotary_table(const int32_t* positions, int T, int axes, const int64_t* turns,
+                            const int32_t* axis, int P, float factor, float* cos_out,
+                            float* sin_out, void* stream);
+
+/* ------------------------------------------------------------------ a16 ---
+ * Rotates queries and keys ([Spark] and [VSA] take them "after QK-norm and
+ * RoPE").  For each row x of D channels: with a weight w, x = x * w /
+ * sqrt(mean(x^2) + eps) (float32); then pair i, channels (i, i + P), or with
+ * interleaved != 0 (2i, 2i + 1), becomes
+ *   (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))),  c, s = table[t][i]
+ * and channels from 2 P on stay; the result is rounded once to `dtype`.
+ * transpose != 0 takes -s: the transposed rotation, which is the gradient's, and undoes a
+ * rotation (of factor 1); it takes no weight.
+ * q: [device] HQ heads of B * T tokens, k: [device] H heads (H = 0: none);
+ * strides: [host] int64 [2][6], for q and k each the batch, token and head stride
+ * of the input and of the output in elements (channels are adjacent), so that slices of a fused
+ * projection are read in place and either layout (BTHD, BHSD) is written.
+ * q_out may be q with the same strides, k_out likewise; otherwise outputs must not overlap
+ * anything.  q_weight, k_weight: [device] float [D] or NULL.  cos_table, sin_table:
+ * [device] float rows of P, token t of batch b at b * table_batch_stride + t * P
+ * (a stride of 0: one table for the batch).  2 <= D <= 256, 2 P <= D.
+ * Wide loads where D is a multiple of 16, P of 8, and all addresses and strides of 16
+ * bytes; a channel at a time otherwise. */
+bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleaved, int transpose,
+                      const float* cos_table, const float* sin_table, int64_t table_batch_stride,
+                      const void* q, int HQ, const float* q_weight, void* q_out, const void* k, int H,
+                      const float* k_weight, void* k_out, const int64_t* strides, float eps,
+                      void* stream);
+
+/* ------------------------------------------------------------------ a17 ---
+ * bsa_cache_append with the keys rotated on the way (as bsa_rotate without a
+ * weight, in float32 and not rounded to `dtype` before they are quantised) and,
+ * in the same launch, the tokens' queries rotated into q_out.  The first fourteen
+ * arguments are bsa_cache_append's; cos_table, sin_table: [device] float [T, P],
+ * 2 P <= D; q: [device] [T, HQ, D] of `dtype`, tokens q_stride elements apart, or NULL;
+ * q_out: [device] [T, HQ, D] contiguous, which must not overlap q.  Queries of
+ * skipped tokens (slot -1 or outside the cache) are left as they were.  k_val holds the rotated keys as
+ * stored. */
+bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtype, int T, int H, int D,
+                                    int64_t k_stride, int64_t v_stride, const int64_t* slots, void* cache,
+                                    int n_pages, int page_size, const float* k_scale,
+                                    const float* v_scale, void* k_val, void* v_val,
+                                    const float* cos_table, const float* sin_table, int P,
+                                    int interleaved, const void* q, int HQ, int64_t q_stride,
+                                    void* q_out, void* stream);
+
+/* ------------------------------------------------------------------ a18 ---
+ * Cross attention: queries over an encoder's states of another length (a
+ * caption's for a video, a request's for its tokens).  Query head hq reads KV head
+ * hq / (HQ / H); softmax(scale * q k^T) v over all states of the row's sequence.
+ * Queries: B sequences of N tokens, or, with query_start [B + 1], packed rows: N rows in
+ * all, sequence b's from query_start[b] to query_start[b + 1] (bsa_cache_tables'
+ * query_start fits); rows outside are left as they were.
+ * States: B sequences of M of which the first key_lens[b] count (NULL: all), or,
+ * with key_start [B + 1], packed: M rows in all.  What lies in rows that do not count, NaN
+ * included, is not seen.  A sequence without states gives rows of 0 and LSE -inf.
+ * Starts must ascend within [0, N] / [0, M]: a sequence that breaks this latches
+ * BSA_ERR_INDEX and counts as empty; a length outside [0, M] is clamped and latched.
+ * strides: [host] int64 [5][3]: batch, token and head stride of q, k, v, out and
+ * lse in elements (channels are adjacent; a batch stride is not used where the rows are packed; strides of 0
+ * broadcast k and v).  lse: [device] float or NULL.  1 <= D <= 128, scale >= 0.
+ * query_start, key_start, key_lens: [device] int32.
+ * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
+ * between calls.  Deterministic. */
+size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
+                           int packed_keys);
+bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype dtype, int B, int N, int M,
+                         int HQ, int H, int D, const int64_t* strides, const int32_t* query_start,
+                         const int32_t* key_start, const int32_t* key_lens, float scale, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

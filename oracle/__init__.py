@@ -17,7 +17,8 @@ float64 restatement of the definitions given on four pages:
   hierarchical partition).
 
 ``cache.py`` restates the paged 4-bit cache (tables, rounding and storage, the
-NSA selected branch over it) from the definitions in ``include/bsa.h``.
+NSA selected branch over it) and ``positions.py`` rotary positions and cross
+attention from the definitions in ``include/bsa.h``.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 ``--impl reference`` legs of ``bench.py`` may import this package.  The CUDA
@@ -53,3 +54,4 @@ from .reblock import (  # noqa: F401
 from .cache import (  # noqa: F401
     e4m3_value, quantise_group, code_value, empty_cache, store, load, cache_tables, cache_attention,
 )
+from .positions import rotary_table, rms_norm, rotate, rotate_f32, cross_attention  # noqa: F401
