@@ -81,6 +81,7 @@ _SIGS = {
     "bsa_rotary_table": (I, [P, I, I, P, P, I, F, P, P, P]),
     "bsa_rotate": (I, [I, I, I, I, I, I, I, P, P, I64, P, I, P, P, P, I, P, P, P, F, P]),
     "bsa_cache_append_rotated": (I, [P, P, I, I, I, I, I64, I64, P, P, I, I, P, P, P, P, P, P, I, I, P, I, I64, P, P]),
+    "bsa_cross_way": (I, [I, I, I, I, I, I, I, I, I]),
     "bsa_cross_workspace": (SZ, [I, I, I, I, I, I, I, I, I]),
     "bsa_fwd_cross": (I, [P, P, P, I, I, I, I, I, I, I, P, P, P, P, F, P, P, P, SZ, P]),
 }
@@ -517,6 +518,11 @@ def bsa_cache_append_rotated(k, v, T, H, D, slots, cache, n_pages, page_size, k_
 def bsa_cross_workspace(dtype, B, N, M, HQ, H, D, packed_queries, packed_keys):
     return _lib.bsa_cross_workspace(BSA_F32 if dtype is torch.float32 else BSA_BF16, B, N, M, HQ, H, D,
                                     1 if packed_queries else 0, 1 if packed_keys else 0)
+
+
+def bsa_cross_way(dtype, B, N, M, HQ, H, D, packed_queries=False, packed_keys=False):
+    return _lib.bsa_cross_way(BSA_F32 if dtype is torch.float32 else BSA_BF16, B, N, M, HQ, H, D,
+                              1 if packed_queries else 0, 1 if packed_keys else 0)
 
 
 def bsa_fwd_cross(q, k, v, B, N, M, HQ, H, D, query_start, key_start, key_lens, scale, out, lse=None, workspace=None,

@@ -192,16 +192,24 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
 // ---------------------------------------------------------------- host side
 
 struct CrossPlan {
-    int parts;
-    long long tiles;
+    int way;    // 0 CUDA cores, 1 tensor cores
+    int parts;  // of the keys
 };
 
-static CrossPlan cross_plan(int B, int N, int M, int HQ, int H, bool packed_q, bool packed_k) {
-    CrossPlan p;
-    p.tiles = row_tiles(B, N, HQ / H, packed_q, kSimtRows);
-    const long long blocks = std::max<long long>(1, p.tiles * H);
-    const long long keys = packed_k ? (M + B - 1) / std::max(B, 1) : M;
-    p.parts = (int)std::max<long long>(1, std::min<long long>({2 * 152 / blocks, (keys + 127) / 128, 64}));
+static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
+    CrossPlan p{};
+    const int G = HQ / H, Gt = cross_tc_heads(G);
+    const long long rows = (packed_q ? (N + B - 1) / B : (long long)N) * G;  // of a sequence and KV head, on average
+    const long long keys = packed_k ? (M + B - 1) / B : M;
+    long long items;
+    if (cross_tc_sizes(dtype, D) && rows >= 32) {
+        p.way = 1;
+        items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
+        p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
+    } else {
+        items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
+        p.parts = (int)std::max<long long>(1, std::min<long long>({2 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
+    }
     return p;
 }
 
@@ -234,7 +242,13 @@ extern "C" {
 size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
                            int packed_keys) {
     if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D) || B == 0 || N == 0) return 0;
-    return part_bytes(cross_plan(B, N, M, HQ, H, packed_queries != 0, packed_keys != 0), B, N, HQ, D, packed_queries != 0);
+    return part_bytes(cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0), B, N, HQ, D,
+                      packed_queries != 0);
+}
+
+int bsa_cross_way(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries, int packed_keys) {
+    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D) || B == 0 || N == 0) return -1;
+    return cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0).way;
 }
 
 bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype dtype, int B, int N, int M, int HQ,
@@ -249,10 +263,10 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     BSA_REQUIRE(scale >= 0.f && scale <= 3.0e38f, "cross attention: the scale must be finite and not negative");
     if (B == 0 || N == 0) return BSA_OK;
     BSA_REQUIRE(q && out && (M == 0 || (k && v)), "cross attention: null pointer");
-    const CrossPlan p = cross_plan(B, N, M, HQ, H, query_start != nullptr, key_start != nullptr);
+    const CrossPlan p = cross_plan(dtype, B, N, M, HQ, H, D, query_start != nullptr, key_start != nullptr);
     const size_t need = part_bytes(p, B, N, HQ, D, query_start != nullptr);
-    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 15) == 0),
-                "cross attention: a 16-byte aligned workspace of %zu bytes is needed", need);
+    BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && ((uintptr_t)workspace & 31) == 0),
+                "cross attention: a 32-byte aligned workspace of %zu bytes is needed", need);
     Cross a{};
     a.q = q, a.k = k, a.v = v, a.out = out, a.lse = lse;
     long long* to[15] = {&a.qb, &a.qt, &a.qh, &a.kb, &a.kt, &a.kh, &a.vb, &a.vt, &a.vh, &a.ob, &a.ot, &a.oh, &a.lb, &a.lt, &a.lh};
@@ -261,15 +275,19 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     a.B = B, a.N = N, a.M = M, a.HQ = HQ, a.H = H, a.D = D, a.G = HQ / H;
     a.scale = scale;
     a.parts = p.parts;
-    a.tiles = (int)p.tiles;
+    a.tiles = (int)row_tiles(B, N, a.G, query_start != nullptr, kSimtRows);
     a.status = status_word();
     const long long rows = (query_start ? (long long)N : (long long)B * N) * HQ;
     a.part_out = need ? static_cast<float*>(workspace) : nullptr;
     a.part_lse = need ? a.part_out + (size_t)p.parts * rows * D : nullptr;
     cudaStream_t st = as_stream(stream);
-    bsa_status rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
+    bsa_status rc = BSA_OK;
+    bool handled = false;
+    if (p.way == 1) rc = cross_tc(a, st, &handled);
+    if (!handled && rc == BSA_OK)
+        rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
     if (rc != BSA_OK || p.parts == 1) return rc;
-    const dim3 grid((unsigned)p.tiles, H);
+    const dim3 grid((unsigned)a.tiles, H);
     if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 256, 0, st>>>(a);
     else cross_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
     return check_launch("cross_join_kernel");

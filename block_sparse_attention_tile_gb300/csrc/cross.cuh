@@ -102,4 +102,8 @@ inline long long row_tiles(int B, int N, int G, bool packed, int kRows) {
     return packed ? rows / kRows + B : B * ((rows + kRows - 1) / kRows);
 }
 
+int cross_tc_heads(int G);
+bool cross_tc_sizes(bsa_dtype dtype, int D);
+bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled);
+
 }  // namespace bsa

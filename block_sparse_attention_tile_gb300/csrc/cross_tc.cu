@@ -1,0 +1,632 @@
+// a18 cross attention on the tensor cores: bf16, head dims up to 128 that are multiples of 8, float32 accumulation
+// in TMEM.
+//
+// "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.3, §6.5 for the online softmax in the log2 domain.
+//
+// A persistent grid, one CTA per SM, 12 warps.  An item is 256 query rows (two tiles of 128: tokens x up to 64 of
+// the heads that share a KV head) against a part of one sequence's keys; both tiles read the same K and V tiles, so
+// that a key is brought from L2 once for 256 rows.  TMEM: S of the two tiles [0, 256), O behind it.
+//   warp 3      scheduler: the next item's sequence, rows and key tiles into one of two headers
+//   warps 0, 2  producers: Q and the K ring, the V ring, by 4-D TMA boxes straight from the strided tensors (channels
+//               past D and rows past the tensor are filled with zeros).  V rows behind the sequence's last key are
+//               set to zero in shared memory: a weight of 0 times a NaN there would be NaN.
+//   warp 1      MMA issuer: per key tile j and row tile w, P_w V_j and then S_w of tile j + 1, so that one tile's
+//               softmax runs while the tensor cores work for the other.
+//   warps 4-7, 8-11  softmax of row tile 0 and 1, one row a thread: running maximum (O is rescaled only when it grows
+//               by more than 2^8) and sum, the weights back to TMEM as bf16, at the item's end the output.
+// Every wait is bounded (2 s): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "cross.cuh"
+#include "tc_ptx.cuh"
+
+namespace bsa {
+namespace cross {
+
+constexpr int kBM = 128, kBN = 128;      // rows of a tile, keys of a tile
+constexpr int kRows = 2 * kBM;           // rows of an item
+constexpr int kThreads = 384;
+constexpr int kKStages = 3, kVStages = 2, kStages = kKStages + kVStages;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kRegsLow = 64, kRegsHigh = 216, kRegsLaunch = 168;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split exceeds the launch");
+constexpr uint32_t kHalf = kBN * 64 * 2;  // 128 rows x 64 channels
+
+constexpr int BAR_QFULL = 0, BAR_QFREE = 2, BAR_FULL = 4, BAR_EMPTY = BAR_FULL + kStages, BAR_SF = BAR_EMPTY + kStages,
+              BAR_PF = BAR_SF + 2, BAR_OF = BAR_PF + 2, BAR_OFREE = BAR_OF + 2, BAR_TFULL = BAR_OFREE + 2,
+              BAR_TFREE = BAR_TFULL + 2, BAR_RAW = BAR_TFREE + 2, BAR_DRAIN = BAR_RAW + 1, NBAR = BAR_DRAIN + 1;
+constexpr int kTabUsers = 3 + 8;
+
+template <int HD> struct Smem {
+    static constexpr uint32_t kTile = kBN * HD * 2;
+    static constexpr uint32_t kRing = 2 * kTile;                       // Q first
+    static constexpr uint32_t kHdr = kRing + kStages * kTile;          // Item[2]
+    static constexpr uint32_t kBar = kHdr + 2 * 48;
+    static constexpr uint32_t kMisc = kBar + 8 * NBAR;
+    static constexpr uint32_t kBytes = kMisc + 32 + 1024;
+};
+static_assert(Smem<128>::kBytes <= 227 * 1024, "shared memory budget");
+
+struct Params {
+    Cross a;            // G: the heads side by side in a row tile
+    int groups, per_kv; // groups of G query heads; of them per KV head
+    int qbm, kbm, vbm, khm, vhm;  // multipliers of the TMA coordinates (0: broadcast dimension)
+    float scale_log2;
+    int items;
+    unsigned* sched;
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    while (true) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            raise_status(status, BSA_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// Keeps the descriptors built from x out of registers: hoisted out of the loops, they are more than the issuer has.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+    asm volatile("mov.b32 %0, %0;" : "+r"(x));
+    return x;
+}
+
+// An item as the header holds it.
+struct Item {
+    int b, group, row, rows;     // row: the item's first of the sequence; rows <= 256 of it
+    int key, keys, t0, t1;       // the sequence's keys; key tiles [t0, t1) of them
+    int part, pad[3];
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const Params prm) {
+    using L = Smem<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (base - raw);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+    auto bar = [&](int i) { return base + L::kBar + 8u * (uint32_t)i; };
+    auto hdr = [&](int b) { return reinterpret_cast<Item*>(sm + L::kHdr) + b; };
+    int* const status = prm.a.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(BAR_QFULL + i), 1);
+            ptx::mbar_init(bar(BAR_QFREE + i), 1);
+            ptx::mbar_init(bar(BAR_SF + i), 1);
+            ptx::mbar_init(bar(BAR_PF + i), kBM);
+            ptx::mbar_init(bar(BAR_OF + i), 1);
+            ptx::mbar_init(bar(BAR_OFREE + i), kBM);
+            ptx::mbar_init(bar(BAR_TFULL + i), 1);
+            ptx::mbar_init(bar(BAR_TFREE + i), kTabUsers);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(bar(BAR_FULL + i), 1);
+            ptx::mbar_init(bar(BAR_EMPTY + i), 1);
+        }
+        ptx::mbar_init(bar(BAR_RAW), 1);
+        ptx::mbar_init(bar(BAR_DRAIN), 1);
+        ptx::fence_mbar_init();
+        misc[1] = 0;
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(base + L::kMisc, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    // Every role walks the same items: item it uses header it & 1.  Row tile w takes part in an item (is "live") when
+    // the item has key tiles and more than 128 w rows; barriers of a row tile count its live items.
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+      if (warp == 3) {
+        int next = blockIdx.x;
+        for (int it = 0;; ++it) {
+            Item x{};
+            x.b = -1;
+            while (true) {
+                int t;
+                if (prm.sched) {
+                    unsigned tk = 0;
+                    if (lane == 0) tk = atomicAdd(prm.sched, 1u);
+                    t = (int)__shfl_sync(0xffffffffu, tk, 0);
+                } else {
+                    t = next;
+                    next += gridDim.x;
+                }
+                if (t < 0 || t >= prm.items) break;
+                const int part = t % prm.a.parts, u = t / prm.a.parts;
+                x.part = part;
+                x.group = u / prm.a.tiles;
+                int row0, q0, n;
+                tile_of<kRows>(prm.a, u % prm.a.tiles, x.b, row0);
+                if (x.b < 0) continue;  // behind the last sequence's tiles
+                queries_of(prm.a, x.b, q0, n);
+                keys_of(prm.a, x.b, x.key, x.keys);
+                x.row = row0;
+                x.rows = min((long long)kRows, (long long)n * prm.a.G - row0);
+                const int nt = (x.keys + kBN - 1) / kBN;
+                x.t0 = (int)((long long)nt * part / prm.a.parts);
+                x.t1 = (int)((long long)nt * (part + 1) / prm.a.parts);
+                break;
+            }
+            if (it >= 2 && !warp_wait(bar(BAR_TFREE + (it & 1)), (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status)) break;
+            if (lane == 0) {
+                *hdr(it & 1) = x;
+                ptx::mbar_arrive(bar(BAR_TFULL + (it & 1)));
+            }
+            if (x.b < 0) break;
+        }
+      } else if (warp == 0) {
+        // ------------------------------------------------------------ Q and K
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        int cnt = 0, ql[2] = {0, 0};
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            const Item x = *hdr(it & 1);
+            if (x.b < 0) break;
+            if (x.t1 > x.t0) {
+                int q0 = prm.a.query_start ? prm.a.query_start[x.b] : 0;
+                q0 += x.row / prm.a.G;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!ok || x.rows <= w * kBM) break;
+                    if (ql[w] > 0) ok = warp_wait(bar(BAR_QFREE + w), (uint32_t)(ql[w] - 1) & 1u, abort_flag, status);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(bar(BAR_QFULL + w), L::kTile);
+#pragma unroll
+                        for (int c = 0; c < HD / 64; ++c)
+                            tma_load_4d(base + w * L::kTile + c * kHalf, &tm_q, 64 * c, x.group * prm.a.G,
+                                        q0 + w * (kBM / prm.a.G), x.b * prm.qbm, bar(BAR_QFULL + w));
+                    }
+                    ++ql[w];
+                }
+                const int h = x.group / prm.per_kv * prm.khm;
+                for (int j = x.t0; j < x.t1 && ok; ++j) {
+                    const int st = cnt % kKStages;
+                    ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / kKStages) & 1u) ^ 1u, abort_flag, status);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(bar(BAR_FULL + st), L::kTile);
+#pragma unroll
+                        for (int c = 0; c < HD / 64; ++c)
+                            tma_load_4d(base + L::kRing + st * L::kTile + c * kHalf, &tm_k, 64 * c, h, x.key + j * kBN,
+                                        x.b * prm.kbm, bar(BAR_FULL + st));
+                    }
+                    ++cnt;
+                }
+                if (!ok) break;
+            }
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+        }
+        if (*abort_flag) {  // wait (bounded) for this warp's copies in flight
+            const uint64_t t0 = ptx::globaltimer();
+            auto drain = [&](int b, uint32_t ph) {
+                while (!ptx::mbar_try_wait(bar(b), ph) && ptx::globaltimer() - t0 < kWaitNs) {}
+            };
+            for (int c = max(0, cnt - kKStages); c < cnt; ++c) drain(BAR_FULL + c % kKStages, (uint32_t)(c / kKStages) & 1u);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (ql[w]) drain(BAR_QFULL + w, (uint32_t)(ql[w] - 1) & 1u);
+        }
+      } else if (warp == 2) {
+        // ------------------------------------------------------------ V
+        ptx::prefetch_tmap(&tm_v);
+        int cnt = 0, patched = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+            const Item x = *hdr(it & 1);
+            if (x.b < 0) break;
+            const int h = x.group / prm.per_kv * prm.vhm;
+            for (int j = x.t0; j < x.t1; ++j) {
+                const int st = kKStages + cnt % kVStages, nv = x.keys - j * kBN;
+                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / kVStages) & 1u) ^ 1u, abort_flag, status);
+                if (!ok) break;
+                const uint32_t dst = base + L::kRing + st * L::kTile, full = bar(nv < kBN ? BAR_RAW : BAR_FULL + st);
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_4d(dst + c * kHalf, &tm_v, 64 * c, h, x.key + j * kBN, x.b * prm.vbm, full);
+                }
+                ++cnt;
+                if (nv < kBN) {
+                    ok = warp_wait(full, (uint32_t)patched & 1u, abort_flag, status);
+                    ++patched;
+                    if (!ok) break;
+                    for (int c = 0; c < HD / 64; ++c)
+                        for (int i = nv * 8 + lane; i < kBN * 8; i += 32)
+                            *reinterpret_cast<uint4*>(sm + (dst - base) + c * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(BAR_FULL + st));
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+        }
+        if (*abort_flag) {
+            const uint64_t t0 = ptx::globaltimer();
+            for (int c = max(0, cnt - kVStages); c < cnt; ++c)
+                while (!ptx::mbar_try_wait(bar(BAR_FULL + kKStages + c % kVStages), (uint32_t)(c / kVStages) & 1u) &&
+                       ptx::globaltimer() - t0 < kWaitNs) {
+                }
+            if (patched)
+                while (!ptx::mbar_try_wait(bar(BAR_RAW), (uint32_t)(patched - 1) & 1u) && ptx::globaltimer() - t0 < kWaitNs) {}
+        }
+      } else if (lane == 0) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t idS = ptx::idesc_bf16(kBM, kBN, false), idO = ptx::idesc_bf16(kBM, HD, true);
+        int kc = 0, vc = 0;                // K and V tiles consumed
+        int live[2] = {0, 0}, up[2] = {0, 0};  // live items, P tiles consumed
+        bool ok = true;
+        auto wait = [&](int b, uint32_t ph) { return wait_bar(bar(b), ph & 1u, abort_flag, status); };
+        auto issue_s = [&](int w, int st) {
+            const uint64_t dq = ptx::smem_desc(here(base + w * L::kTile), 16, 1024);
+            const uint64_t dk = ptx::smem_desc(here(base + L::kRing + st * L::kTile), 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                ptx::mma_ss(tmem + (uint32_t)w * 128, dq + off, dk + off, idS, kk > 0);
+            }
+            ptx::mma_commit(bar(BAR_SF + w));
+        };
+        for (int it = 0; ok; ++it) {
+            if (!wait(BAR_TFULL + (it & 1), (uint32_t)(it >> 1))) break;
+            const Item x = *hdr(it & 1);
+            if (x.b < 0) break;
+            const int n = x.t1 - x.t0, nw = x.rows > kBM ? 2 : 1;
+            if (n > 0) {
+                // S of the first key tile
+                int st = kc % kKStages;
+                ok = wait(BAR_FULL + st, (uint32_t)(kc / kKStages));
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!ok || w >= nw) break;
+                    ok = wait(BAR_QFULL + w, (uint32_t)live[w]);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    issue_s(w, st);
+                    if (n == 1) ptx::mma_commit(bar(BAR_QFREE + w));
+                }
+                if (!ok) break;
+                ptx::mma_commit(bar(BAR_EMPTY + st));
+                ++kc;
+                for (int j = 0; j < n && ok; ++j) {
+                    const int vst = kKStages + vc % kVStages, kst = kc % kKStages;
+                    const bool more = j + 1 < n;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok || w >= nw) break;
+                        if (j == 0 && live[w] > 0) ok = wait(BAR_OFREE + w, (uint32_t)(live[w] - 1));
+                        ok = ok && wait(BAR_PF + w, (uint32_t)up[w]) &&
+                             (w > 0 || (wait(BAR_FULL + vst, (uint32_t)(vc / kVStages)) &&
+                                        (!more || wait(BAR_FULL + kst, (uint32_t)(kc / kKStages)))));
+                        if (!ok) break;
+                        ++up[w];
+                        ptx::tc_fence_after();
+                        const uint64_t dv = ptx::smem_desc(here(base + L::kRing + vst * L::kTile), kHalf, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < kBN / 16; ++kk)
+                            ptx::mma_ts(tmem + 256 + (uint32_t)w * HD, tmem + (uint32_t)w * 128 + kk * 8,
+                                        dv + (uint32_t)(kk * 2048 >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + vst));
+                        if (more) {
+                            issue_s(w, kst);
+                            if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + kst));
+                            if (j + 2 == n) ptx::mma_commit(bar(BAR_QFREE + w));
+                        } else {
+                            ptx::mma_commit(bar(BAR_OF + w));
+                        }
+                    }
+                    ++vc;
+                    if (more) ++kc;
+                }
+                if (!ok) break;
+                ++live[0];
+                live[1] += nw - 1;
+            }
+            ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+        }
+        // nothing that this thread issued may still run when TMEM is freed
+        ptx::mma_commit(bar(BAR_DRAIN));
+        const uint64_t t0 = ptx::globaltimer();
+        while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::globaltimer() - t0 < kWaitNs) {}
+      }
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+      // -------------------------------------------------------------- softmax and output
+      const int w = (warp - 4) >> 2, row = threadIdx.x & 127;
+      const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t tO = tmem + lane_off + 256 + HD * w, tS = tmem + lane_off + (uint32_t)w * 128;
+      const Cross& a = prm.a;
+      int su = 0, live = 0;  // S tiles, live items
+      uint32_t r[16];
+      float x[kBN];
+      for (int it = 0;; ++it) {
+        if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
+        const Item* hd = hdr(it & 1);
+        if (hd->b < 0) break;
+        if (hd->rows <= w * kBM) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+            continue;
+        }
+        const int n = hd->t1 - hd->t0;
+        int left = hd->keys - hd->t0 * kBN;  // keys from the current tile on
+        float m_ref = -CUDART_INF_F, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j, left -= kBN) {
+            const int nv = left;
+            ok = warp_wait(bar(BAR_SF + w), (uint32_t)su & 1u, abort_flag, status);
+            if (!ok) break;
+            ++su;
+            ptx::tc_fence_after();
+            {
+                uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+                ptx::tmem_ld32(tS + 0, xr + 0);
+                ptx::tmem_ld32(tS + 32, xr + 32);
+                ptx::tmem_ld32(tS + 64, xr + 64);
+                ptx::tmem_ld32(tS + 96, xr + 96);
+                ptx::tmem_wait_ld();
+            }
+            if (nv < kBN) {
+#pragma unroll
+                for (int c = 0; c < kBN; ++c) x[c] = c < nv ? x[c] : -CUDART_INF_F;
+            }
+            float mxp[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mxp[u] = -CUDART_INF_F;
+#pragma unroll
+            for (int c = 0; c < kBN; c += 16)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) mxp[u] = ptx::fmax3(mxp[u], x[c + u], x[c + 8 + u]);
+            // maxima of raw Q.K: scale once (scale > 0 keeps the order)
+            const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * prm.scale_log2;
+            const float m_new = fmaxf(m_ref, mx);
+            const bool need = m_new > m_ref + kRescaleThreshold;
+            if (__any_sync(0xffffffffu, need)) {
+                const float alpha = need ? ptx::ex2(m_ref - m_new) : 1.f;
+                if (need) m_ref = m_new;
+                l *= alpha;
+                if (j > 0) {
+                    // S_j was issued after the last product added to O: O is complete here
+#pragma unroll
+                    for (int c = 0; c < HD / 16; ++c) {
+                        ptx::tmem_ld16(tO + c * 16, r);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                        ptx::tmem_st16(tO + c * 16, r);
+                    }
+                    ptx::tmem_wait_st();
+                }
+            }
+            const bool some = m_ref != -CUDART_INF_F;
+            const float sc = some ? prm.scale_log2 : 1.f, ref = some ? m_ref : 0.f;
+            const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
+            float2 acc[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[u] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                for (int c = h * 32; c < h * 32 + 32; c += 2) {
+                    const float2 z = ptx::ffma2(make_float2(x[c], x[c + 1]), sc2, nm2);
+                    x[c] = ptx::ex2(z.x);
+                    x[c + 1] = ptx::ex2(z.y);
+                    acc[(c >> 1) & 3] = ptx::fadd2(acc[(c >> 1) & 3], make_float2(x[c], x[c + 1]));
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = ptx::pack_bf16x2(x[h * 32 + 2 * e], x[h * 32 + 2 * e + 1]);
+                ptx::tmem_st16(tS + h * 16, r);
+            }
+            l += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(BAR_PF + w));
+        }
+        if (!ok) break;
+        if (n > 0) {
+            if (!warp_wait(bar(BAR_OF + w), (uint32_t)live & 1u, abort_flag, status)) break;
+            ++live;
+            ptx::tc_fence_after();
+        }
+        const Item m = *hd;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+        const int at = w * kBM + row;
+        const bool write = at < m.rows;
+        const int rr = m.row + (write ? at : 0), t = rr / a.G, hq = m.group * a.G + (rr - t * a.G);
+        const long long tok = (a.query_start ? a.query_start[m.b] : 0) + t, qbat = a.query_start ? 0 : m.b;
+        const float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
+        __nv_bfloat16* o = (__nv_bfloat16*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
+        long long pr = 0;  // row of the part's results
+        if (a.parts > 1) pr = ((long long)m.part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) {
+            if (n > 0) {
+                ptx::tmem_ld16(tO + c * 16, r);
+                ptx::tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = 0u;
+            }
+            if (c == HD / 16 - 1 && n > 0) {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(BAR_OFREE + w));
+            }
+            if (write) {
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]) * inv;
+                if (a.parts > 1) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (16 * c + 8 * h < a.D)
+                            ptx::st_global_v8(a.part_out + pr * a.D + 16 * c + 8 * h, reinterpret_cast<uint32_t*>(v) + 8 * h);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (16 * c + 8 * h < a.D)
+                            *reinterpret_cast<uint4*>(o + 16 * c + 8 * h) =
+                                make_uint4(ptx::pack_bf16x2(v[8 * h], v[8 * h + 1]), ptx::pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
+                                           ptx::pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), ptx::pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
+                }
+            }
+        }
+        if (write && a.parts > 1) a.part_lse[pr] = lse;
+        else if (write && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
+      }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && prm.sched) {
+        __threadfence();
+        if (atomicAdd(prm.sched + 1, 1u) == gridDim.x - 1) {
+            atomicExch(prm.sched, 0u);
+            atomicExch(prm.sched + 1, 0u);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// 4-D map (channel, head, token, batch) over a strided tensor, box {64, heads, tokens, 1}.  A dimension of one entry or
+// of stride 0 (a broadcast) becomes one entry at coordinate 0, which the caller's multiplier says.
+static bool make_map(CUtensorMap* m, const void* ptr, int D, int heads, long long tokens, int batch, long long sh,
+                     long long st, long long sb, int box_heads, int box_tokens, int* head_mul, int* batch_mul) {
+    auto fn = encode_fn();
+    if (!fn || ((uintptr_t)ptr & 15)) return false;
+    *head_mul = heads > 1 && sh != 0;
+    *batch_mul = batch > 1 && sb != 0;
+    if (tokens > 1 && st == 0) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(*head_mul ? heads : 1), (cuuint64_t)tokens,
+                                (cuuint64_t)(*batch_mul ? batch : 1)};
+    const long long s[3] = {*head_mul ? 2 * sh : 16, tokens > 1 ? 2 * st : 16, *batch_mul ? 2 * sb : 16};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        if (s[i] <= 0 || s[i] % 16 || s[i] >= (1LL << 40)) return false;
+        strides[i] = (cuuint64_t)s[i];
+    }
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD>
+static bsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& prm,
+                         cudaStream_t st, bool* handled) {
+    static int fits = 0;  // 0 unknown, 1 fits, -1 does not: setmaxnreg.inc would wait for registers
+    if (!fits) {
+        cudaFuncAttributes a;
+        fits = (cudaFuncGetAttributes(&a, cross_tc_kernel<HD>) == cudaSuccess &&
+                a.numRegs * kThreads >= 128 * kRegsLow + 256 * kRegsHigh) ? 1 : -1;
+    }
+    if (fits < 0) return BSA_OK;
+    *handled = true;
+    cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Smem<HD>::kBytes);
+    if (e != cudaSuccess) return fail(BSA_ERR_CUDA, "cross attention attribute: %s", cudaGetErrorString(e));
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return fail(BSA_ERR_CUDA, "cross attention: device query failed");
+    cross_tc_kernel<HD><<<std::min(prm.items, sms), kThreads, Smem<HD>::kBytes, st>>>(mq, mk, mv, prm);
+    return check_launch("cross_tc_kernel");
+}
+
+}  // namespace cross
+
+// The heads of a KV head that lie side by side in a row tile: the largest power of two that divides G, up to 64.
+int cross_tc_heads(int G) {
+    int g = G & -G;
+    return g > 64 ? 64 : g;
+}
+
+// Whether the sizes suit the tensor-core kernel (strides and addresses are looked at at the launch).
+bool cross_tc_sizes(bsa_dtype dtype, int D) { return dtype == BSA_BF16 && D % 8 == 0 && !force_simt(); }
+
+bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled) {
+    using namespace cross;
+    *handled = false;
+    Params prm{};
+    prm.a = a;
+    prm.a.G = cross_tc_heads(a.G);
+    prm.per_kv = a.G / prm.a.G;
+    prm.groups = a.HQ / prm.a.G;
+    const bool pq = a.query_start != nullptr, pk = a.key_start != nullptr;
+    const long long tiles = row_tiles(a.B, a.N, prm.a.G, pq, kRows), items = tiles * prm.groups * a.parts;
+    if (items > INT_MAX / 2) return BSA_OK;
+    if (((uintptr_t)a.out & 15) || ((2 * a.ot) & 15) || ((2 * a.oh) & 15) || ((2 * a.ob) & 15)) return BSA_OK;
+    prm.a.tiles = (int)tiles;
+    prm.items = (int)items;
+    CUtensorMap mq, mk, mv;
+    int qhm;
+    if (a.M == 0) return BSA_OK;  // no state at all: nothing to map
+    if (!make_map(&mq, a.q, a.D, a.HQ, a.N, pq ? 1 : a.B, a.qh, a.qt, a.qb, prm.a.G, kBM / prm.a.G, &qhm, &prm.qbm) ||
+        !make_map(&mk, a.k, a.D, a.H, a.M, pk ? 1 : a.B, a.kh, a.kt, a.kb, 1, kBN, &prm.khm, &prm.kbm) ||
+        !make_map(&mv, a.v, a.D, a.H, a.M, pk ? 1 : a.B, a.vh, a.vt, a.vb, 1, kBN, &prm.vhm, &prm.vbm))
+        return BSA_OK;
+    if (a.HQ > 1 && !qhm) return BSA_OK;      // queries shared by the heads
+    // a scale of 0 would turn a masked -inf into NaN: the smallest normal scale gives the same weights
+    prm.scale_log2 = std::max(a.scale * kLog2e, 1.2e-38f);
+    prm.sched = sched_counter(st);
+    return a.D <= 64 ? launch<64>(mq, mk, mv, prm, st, handled) : launch<128>(mq, mk, mv, prm, st, handled);
+}
+
+}  // namespace bsa
