@@ -3,17 +3,18 @@
 //
 // "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.3, §6.5 for the online softmax in the log2 domain.
 //
-// A persistent grid, one CTA per SM, 12 warps.  An item is 256 query rows (two tiles of 128: tokens x up to 64 of
+// A persistent grid, one CTA per SM, 16 warps.  An item is 256 query rows (two tiles of 128: tokens x up to 64 of
 // the heads that share a KV head) against a part of one sequence's keys; both tiles read the same K and V tiles, so
 // that a key is brought from L2 once for 256 rows.  TMEM: S of the two tiles [0, 256), O behind it.
-//   warp 3      scheduler: the next item's sequence, rows and key tiles into one of two headers
+//   warp 3      scheduler: the next item's sequence, rows and key tiles into one of two headers, their queries on their way to L2
 //   warps 0, 2  producers: Q and the K ring, the V ring, by 4-D TMA boxes straight from the strided tensors (channels
 //               past D and rows past the tensor are filled with zeros).  V rows behind the sequence's last key are
 //               set to zero in shared memory: a weight of 0 times a NaN there would be NaN.
 //   warp 1      MMA issuer: per key tile j and row tile w, P_w V_j and then S_w of tile j + 1, so that one tile's
 //               softmax runs while the tensor cores work for the other.
 //   warps 4-7, 8-11  softmax of row tile 0 and 1, one row a thread: running maximum (O is rescaled only when it grows
-//               by more than 2^8) and sum, the weights back to TMEM as bf16, at the item's end the output.
+//               by more than 2^8) and sum, the weights back to TMEM as bf16.
+//   warps 12-15 output: O times 1 / sum to global memory while the softmax is at the next item.
 // Every wait is bounded (2 s): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -30,24 +31,29 @@ namespace cross {
 
 constexpr int kBM = 128, kBN = 128;      // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kBM;           // rows of an item
-constexpr int kThreads = 384;
-constexpr int kKStages = 3, kVStages = 2, kStages = kKStages + kVStages;
+constexpr int kThreads = 512;
+constexpr int kMaxStages = 6;            // K and V tiles in flight, at most
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kRegsLow = 64, kRegsHigh = 216, kRegsLaunch = 168;
-static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "register split exceeds the launch");
+constexpr int kRegsLow = 64, kRegsHigh = 176, kRegsOut = 96, kRegsLaunch = 128;  // setmaxnreg (x 128 / 256 / 128 threads)
+static_assert(128 * kRegsLow + 256 * kRegsHigh + 128 * kRegsOut <= kThreads * kRegsLaunch, "register split exceeds the launch");
 constexpr uint32_t kHalf = kBN * 64 * 2;  // 128 rows x 64 channels
 
-constexpr int BAR_QFULL = 0, BAR_QFREE = 2, BAR_FULL = 4, BAR_EMPTY = BAR_FULL + kStages, BAR_SF = BAR_EMPTY + kStages,
+constexpr int kHeaders = 2;  // items known at once (with 4 a CTA holds more of a short batch's items than its share)
+constexpr int BAR_QFULL = 0, BAR_QFREE = 2, BAR_FULL = 4, BAR_EMPTY = BAR_FULL + kMaxStages, BAR_SF = BAR_EMPTY + kMaxStages,
               BAR_PF = BAR_SF + 2, BAR_OF = BAR_PF + 2, BAR_OFREE = BAR_OF + 2, BAR_TFULL = BAR_OFREE + 2,
-              BAR_TFREE = BAR_TFULL + 2, BAR_RAW = BAR_TFREE + 2, BAR_DRAIN = BAR_RAW + 1, NBAR = BAR_DRAIN + 1;
-constexpr int kTabUsers = 3 + 8;
+              BAR_TFREE = BAR_TFULL + kHeaders, BAR_XF = BAR_TFREE + kHeaders, BAR_RAW = BAR_XF + 2,
+              BAR_DRAIN = BAR_RAW + 1, NBAR = BAR_DRAIN + 1;
+constexpr int kTabUsers = 3 + 8 + 4;
 
 template <int HD> struct Smem {
+    static constexpr int kK = HD == 128 ? 2 : 3, kV = kK;              // stages of the K and V rings
     static constexpr uint32_t kTile = kBN * HD * 2;
     static constexpr uint32_t kRing = 2 * kTile;                       // Q first
-    static constexpr uint32_t kHdr = kRing + kStages * kTile;          // Item[2]
-    static constexpr uint32_t kBar = kHdr + 2 * 48;
+    static constexpr uint32_t kOut = kRing + (kK + kV) * kTile;        // a row tile of the output, for whole-line stores
+    static constexpr uint32_t kHdr = kOut + kTile;                     // Item[kHeaders]
+    static constexpr uint32_t kInv = kHdr + kHeaders * 48;             // float[2][128]: 1 / sum of a row
+    static constexpr uint32_t kBar = kInv + 4 * kRows;
     static constexpr uint32_t kMisc = kBar + 8 * NBAR;
     static constexpr uint32_t kBytes = kMisc + 32 + 1024;
 };
@@ -87,18 +93,60 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Keeps the descriptors built from x out of registers: hoisted out of the loops, they are more than the issuer has.
-__device__ __forceinline__ uint32_t here(uint32_t x) {
-    asm volatile("mov.b32 %0, %0;" : "+r"(x));
-    return x;
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
+// 32 columns of this thread's TMEM lane, and the largest of them as floats.
+__device__ __forceinline__ void ld32_max(uint32_t taddr, uint32_t* r, float& top) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+        : "r"(taddr)
+        : "memory");
+}
+
+// A shared-memory matrix descriptor (128-byte swizzle, stride 1024) from its address in units of 16 bytes.
+__device__ __forceinline__ uint64_t desc(uint32_t addr16, uint32_t lbo_bytes) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | (lbo_bytes >> 4) << 16), "r"((1024u >> 4) | 1u << 14 | 2u << 29));
+    return d;
+}
+
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // An item as the header holds it.
 struct Item {
     int b, group, row, rows;     // row: the item's first of the sequence; rows <= 256 of it
     int key, keys, t0, t1;       // the sequence's keys; key tiles [t0, t1) of them
-    int part, pad[3];
+    int part, q0, shift, pad;    // q0: the sequence's first query; shift: log2 G
 };
+
+// Where row `at` of an item lies: batch, token, query head, and its row in the part's results.
+struct RowAt {
+    long long batch, tok, part;
+    int hq;
+};
+__device__ __forceinline__ RowAt row_at(const Cross& a, const Item& x, int at) {
+    const int r = x.row + at, t = r >> x.shift;  // G is a power of two
+    RowAt p;
+    p.hq = x.group * a.G + (r & (a.G - 1));
+    p.batch = a.query_start ? 0 : x.b;
+    p.tok = x.q0 + t;
+    p.part = a.parts > 1 ? ((long long)x.part * (a.query_start ? a.N : (long long)a.B * a.N) + p.batch * a.N + p.tok) * a.HQ + p.hq : 0;
+    return p;
+}
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -112,6 +160,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     auto bar = [&](int i) { return base + L::kBar + 8u * (uint32_t)i; };
+    float* inv = reinterpret_cast<float*>(sm + L::kInv);
     auto hdr = [&](int b) { return reinterpret_cast<Item*>(sm + L::kHdr) + b; };
     int* const status = prm.a.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -124,10 +173,13 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             ptx::mbar_init(bar(BAR_PF + i), kBM);
             ptx::mbar_init(bar(BAR_OF + i), 1);
             ptx::mbar_init(bar(BAR_OFREE + i), kBM);
+            ptx::mbar_init(bar(BAR_XF + i), kBM);
+        }
+        for (int i = 0; i < kHeaders; ++i) {
             ptx::mbar_init(bar(BAR_TFULL + i), 1);
             ptx::mbar_init(bar(BAR_TFREE + i), kTabUsers);
         }
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < L::kK + L::kV; ++i) {
             ptx::mbar_init(bar(BAR_FULL + i), 1);
             ptx::mbar_init(bar(BAR_EMPTY + i), 1);
         }
@@ -145,7 +197,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     ptx::tc_fence_after();
     const uint32_t tmem = misc[0];
 
-    // Every role walks the same items: item it uses header it & 1.  Row tile w takes part in an item (is "live") when
+    // Every role walks the same items: item it uses header it % kHeaders.  Row tile w takes part in an item (is "live") when
     // the item has key tiles and more than 128 w rows; barriers of a row tile count its live items.
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -173,6 +225,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (x.b < 0) continue;  // behind the last sequence's tiles
                 queries_of(prm.a, x.b, q0, n);
                 keys_of(prm.a, x.b, x.key, x.keys);
+                x.q0 = q0;
+                x.shift = __ffs(prm.a.G) - 1;
                 x.row = row0;
                 x.rows = min((long long)kRows, (long long)n * prm.a.G - row0);
                 const int nt = (x.keys + kBN - 1) / kBN;
@@ -180,10 +234,14 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 x.t1 = (int)((long long)nt * (part + 1) / prm.a.parts);
                 break;
             }
-            if (it >= 2 && !warp_wait(bar(BAR_TFREE + (it & 1)), (uint32_t)((it - 2) >> 1) & 1u, abort_flag, status)) break;
+            // the item's queries on their way to L2 meanwhile: their buffers are free only just before they are needed
+            if (x.b >= 0 && x.t1 > x.t0 && lane < 2 * (HD / 64) && (lane & 1) * kBM < x.rows)
+                tma_prefetch_4d(&tm_q, 64 * (lane >> 1), x.group * prm.a.G, x.q0 + x.row / prm.a.G + (lane & 1) * (kBM / prm.a.G),
+                                x.b * prm.qbm);
+            if (it >= kHeaders && !warp_wait(bar(BAR_TFREE + it % kHeaders), (uint32_t)(it / kHeaders - 1) & 1u, abort_flag, status)) break;
             if (lane == 0) {
-                *hdr(it & 1) = x;
-                ptx::mbar_arrive(bar(BAR_TFULL + (it & 1)));
+                *hdr(it % kHeaders) = x;
+                ptx::mbar_arrive(bar(BAR_TFULL + it % kHeaders));
             }
             if (x.b < 0) break;
         }
@@ -194,16 +252,27 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int cnt = 0, ql[2] = {0, 0};
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
-            const Item x = *hdr(it & 1);
+            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+            const Item x = *hdr(it % kHeaders);
             if (x.b < 0) break;
-            if (x.t1 > x.t0) {
-                int q0 = prm.a.query_start ? prm.a.query_start[x.b] : 0;
-                q0 += x.row / prm.a.G;
+            const int q0 = x.q0 + x.row / prm.a.G, h = x.group / prm.per_kv * prm.khm;
+            // in the order in which they are needed and their buffers become free: K_0, Q_0, K_1, Q_1, K_2 ...
+            for (int j = x.t0; j < x.t1 && ok; ++j) {
+                const int st = cnt % L::kK;
+                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kK) & 1u) ^ 1u, abort_flag, status);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(BAR_FULL + st), L::kTile);
+#pragma unroll
+                    for (int c = 0; c < HD / 64; ++c)
+                        tma_load_4d(base + L::kRing + st * L::kTile + c * kHalf, &tm_k, 64 * c, h, x.key + j * kBN,
+                                    x.b * prm.kbm, bar(BAR_FULL + st));
+                }
+                ++cnt;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    if (!ok || x.rows <= w * kBM) break;
-                    if (ql[w] > 0) ok = warp_wait(bar(BAR_QFREE + w), (uint32_t)(ql[w] - 1) & 1u, abort_flag, status);
+                    if (x.rows <= w * kBM || (j != x.t0 + w && !(w == 1 && x.t1 - x.t0 == 1))) continue;
+                    if (ql[w] > 0) ok = ok && warp_wait(bar(BAR_QFREE + w), (uint32_t)(ql[w] - 1) & 1u, abort_flag, status);
                     if (!ok) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(BAR_QFULL + w), L::kTile);
@@ -214,30 +283,16 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                     ++ql[w];
                 }
-                const int h = x.group / prm.per_kv * prm.khm;
-                for (int j = x.t0; j < x.t1 && ok; ++j) {
-                    const int st = cnt % kKStages;
-                    ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / kKStages) & 1u) ^ 1u, abort_flag, status);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(bar(BAR_FULL + st), L::kTile);
-#pragma unroll
-                        for (int c = 0; c < HD / 64; ++c)
-                            tma_load_4d(base + L::kRing + st * L::kTile + c * kHalf, &tm_k, 64 * c, h, x.key + j * kBN,
-                                        x.b * prm.kbm, bar(BAR_FULL + st));
-                    }
-                    ++cnt;
-                }
-                if (!ok) break;
             }
-            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+            if (!ok) break;
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
         }
         if (*abort_flag) {  // wait (bounded) for this warp's copies in flight
             const uint64_t t0 = ptx::globaltimer();
             auto drain = [&](int b, uint32_t ph) {
                 while (!ptx::mbar_try_wait(bar(b), ph) && ptx::globaltimer() - t0 < kWaitNs) {}
             };
-            for (int c = max(0, cnt - kKStages); c < cnt; ++c) drain(BAR_FULL + c % kKStages, (uint32_t)(c / kKStages) & 1u);
+            for (int c = max(0, cnt - L::kK); c < cnt; ++c) drain(BAR_FULL + c % L::kK, (uint32_t)(c / L::kK) & 1u);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
                 if (ql[w]) drain(BAR_QFULL + w, (uint32_t)(ql[w] - 1) & 1u);
@@ -248,13 +303,13 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int cnt = 0, patched = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
-            const Item x = *hdr(it & 1);
+            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+            const Item x = *hdr(it % kHeaders);
             if (x.b < 0) break;
             const int h = x.group / prm.per_kv * prm.vhm;
             for (int j = x.t0; j < x.t1; ++j) {
-                const int st = kKStages + cnt % kVStages, nv = x.keys - j * kBN;
-                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / kVStages) & 1u) ^ 1u, abort_flag, status);
+                const int st = L::kK + cnt % L::kV, nv = x.keys - j * kBN;
+                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kV) & 1u) ^ 1u, abort_flag, status);
                 if (!ok) break;
                 const uint32_t dst = base + L::kRing + st * L::kTile, full = bar(nv < kBN ? BAR_RAW : BAR_FULL + st);
                 if (lane == 0) {
@@ -277,97 +332,139 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             if (!ok) break;
-            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
         }
         if (*abort_flag) {
             const uint64_t t0 = ptx::globaltimer();
-            for (int c = max(0, cnt - kVStages); c < cnt; ++c)
-                while (!ptx::mbar_try_wait(bar(BAR_FULL + kKStages + c % kVStages), (uint32_t)(c / kVStages) & 1u) &&
+            for (int c = max(0, cnt - L::kV); c < cnt; ++c)
+                while (!ptx::mbar_try_wait(bar(BAR_FULL + L::kK + c % L::kV), (uint32_t)(c / L::kV) & 1u) &&
                        ptx::globaltimer() - t0 < kWaitNs) {
                 }
             if (patched)
                 while (!ptx::mbar_try_wait(bar(BAR_RAW), (uint32_t)(patched - 1) & 1u) && ptx::globaltimer() - t0 < kWaitNs) {}
         }
-      } else if (lane == 0) {
+      } else if (elect()) {
         // ------------------------------------------------------------ MMA issuer
+        // One elected lane, which the compiler knows to be alone: a product then takes some 60 cycles to issue, of the
+        // 64 that it runs (95 from `if (lane == 0)`; and with the whole warp in the loop every wait costs 100 more).
+        // After the last weights of row tile 0 the next item's first S of it goes ahead of row tile 1's last product,
+        // if its queries have come.
         constexpr uint32_t idS = ptx::idesc_bf16(kBM, kBN, false), idO = ptx::idesc_bf16(kBM, HD, true);
+        const uint32_t tm = tmem;
         int kc = 0, vc = 0;                // K and V tiles consumed
-        int live[2] = {0, 0}, up[2] = {0, 0};  // live items, P tiles consumed
+        int live0 = 0, live1 = 0, up0 = 0, up1 = 0;  // live items and P tiles consumed of the two row tiles
         bool ok = true;
         auto wait = [&](int b, uint32_t ph) { return wait_bar(bar(b), ph & 1u, abort_flag, status); };
+        const uint32_t lo = (base >> 4) & 0x3FFF;  // descriptors differ in their address alone, in units of 16 bytes
         auto issue_s = [&](int w, int st) {
-            const uint64_t dq = ptx::smem_desc(here(base + w * L::kTile), 16, 1024);
-            const uint64_t dk = ptx::smem_desc(here(base + L::kRing + st * L::kTile), 16, 1024);
+            const uint32_t dq = lo + (uint32_t)w * (L::kTile >> 4), dk = lo + (L::kRing >> 4) + (uint32_t)st * (L::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                ptx::mma_ss(tmem + (uint32_t)w * 128, dq + off, dk + off, idS, kk > 0);
+                ptx::mma_ss(tm + (uint32_t)w * 128, desc(dq + off, 16), desc(dk + off, 16), idS, kk > 0);
             }
             ptx::mma_commit(bar(BAR_SF + w));
         };
+        auto test = [&](int b, uint32_t ph) { return ptx::mbar_test_wait(bar(b), ph & 1u); };
+        constexpr int kMaxSpins = 1 << 16;
+        int spins = 0;
+        int n = 0, nw = 0, early = 0;  // key tiles and row tiles of the item; its first S that are issued already
+        auto open = [&](int it) {      // reads the published header of item it: whether there is one
+            const Item* x = hdr(it % kHeaders);
+            const int b = x->b;
+            n = x->t1 - x->t0;
+            nw = x->rows > kBM ? 2 : 1;
+            return b >= 0;
+        };
+        // S of the item's first key tile for row tile w
+        auto first_s = [&](int w) {
+            const int kst = kc % L::kK;
+            ptx::tc_fence_after();
+            {
+                issue_s(w, kst);
+                if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + kst));
+                if (n == 1) ptx::mma_commit(bar(BAR_QFREE + w));
+            }
+            kc += w == nw - 1;
+        };
+        ok = wait(BAR_TFULL, 0) && open(0);
         for (int it = 0; ok; ++it) {
-            if (!wait(BAR_TFULL + (it & 1), (uint32_t)(it >> 1))) break;
-            const Item x = *hdr(it & 1);
-            if (x.b < 0) break;
-            const int n = x.t1 - x.t0, nw = x.rows > kBM ? 2 : 1;
-            if (n > 0) {
-                // S of the first key tile
-                int st = kc % kKStages;
-                ok = wait(BAR_FULL + st, (uint32_t)(kc / kKStages));
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (!ok || w >= nw) break;
-                    ok = wait(BAR_QFULL + w, (uint32_t)live[w]);
+            for (int w = early; w < nw && n > 0 && ok; ++w) {
+                ok = wait(BAR_QFULL + w, (uint32_t)(w ? live1 : live0)) && (w || wait(BAR_FULL + kc % L::kK, (uint32_t)(kc / L::kK)));
+                if (ok) first_s(w);
+            }
+            early = 0;
+            bool some = n > 0, opened = false, next = false;
+#pragma unroll 1
+            for (int j = 0; j < n && ok; ++j) {
+                const int vst = L::kK + vc % L::kV, kst = kc % L::kK;
+                const bool more = j + 1 < n;
+                const int last = nw - 1;
+#pragma unroll 1
+                for (int w = 0; w <= last; ++w) {
+                    if (w == 0) ok = wait(BAR_FULL + vst, (uint32_t)(vc / L::kV)) && (!more || wait(BAR_FULL + kst, (uint32_t)(kc / L::kK)));
+                    if (j == 0 && (w ? live1 : live0) > 0) ok = ok && wait(BAR_OFREE + w, (uint32_t)((w ? live1 : live0) - 1));
+                    if (w == 1 && !more) {
+                        // while the last weights of row tile 1 are awaited: the next item's first S of row tile 0
+                        const int n_ = n, nw_ = nw;
+                        while (ok && !test(BAR_PF + 1, (uint32_t)up1)) {
+                            if (!opened && test(BAR_TFULL + (it + 1) % kHeaders, (uint32_t)((it + 1) / kHeaders))) {
+                                opened = true;
+                                next = open(it + 1);
+                            }
+                            if (!opened || !next || n == 0) break;
+                            if (test(BAR_QFULL, (uint32_t)(live0 + 1)) && test(BAR_FULL + kc % L::kK, (uint32_t)(kc / L::kK))) {
+                                first_s(0);
+                                early = 1;
+                                break;
+                            }
+                            if (*abort_flag) ok = false;
+                            if (++spins > kMaxSpins) break;  // the waits behind are bounded by time
+                        }
+                        spins = 0;
+                        if (!early) opened = false;  // read again below
+                        n = n_;
+                        nw = nw_;
+                    }
+                    ok = ok && wait(BAR_PF + w, (uint32_t)(w ? up1++ : up0++));
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    issue_s(w, st);
-                    if (n == 1) ptx::mma_commit(bar(BAR_QFREE + w));
-                }
-                if (!ok) break;
-                ptx::mma_commit(bar(BAR_EMPTY + st));
-                ++kc;
-                for (int j = 0; j < n && ok; ++j) {
-                    const int vst = kKStages + vc % kVStages, kst = kc % kKStages;
-                    const bool more = j + 1 < n;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (!ok || w >= nw) break;
-                        if (j == 0 && live[w] > 0) ok = wait(BAR_OFREE + w, (uint32_t)(live[w] - 1));
-                        ok = ok && wait(BAR_PF + w, (uint32_t)up[w]) &&
-                             (w > 0 || (wait(BAR_FULL + vst, (uint32_t)(vc / kVStages)) &&
-                                        (!more || wait(BAR_FULL + kst, (uint32_t)(kc / kKStages)))));
-                        if (!ok) break;
-                        ++up[w];
-                        ptx::tc_fence_after();
-                        const uint64_t dv = ptx::smem_desc(here(base + L::kRing + vst * L::kTile), kHalf, 1024);
+                    {
+                        const uint32_t dv = lo + (L::kRing >> 4) + (uint32_t)vst * (L::kTile >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            ptx::mma_ts(tmem + 256 + (uint32_t)w * HD, tmem + (uint32_t)w * 128 + kk * 8,
-                                        dv + (uint32_t)(kk * 2048 >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
-                        if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + vst));
+                            ptx::mma_ts(tm + 256 + (uint32_t)w * HD, tm + (uint32_t)w * 128 + kk * 8,
+                                        desc(dv + (kk * 2048 >> 4), kHalf), idO, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (w == last) ptx::mma_commit(bar(BAR_EMPTY + vst));
                         if (more) {
                             issue_s(w, kst);
-                            if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + kst));
+                            if (w == last) ptx::mma_commit(bar(BAR_EMPTY + kst));
                             if (j + 2 == n) ptx::mma_commit(bar(BAR_QFREE + w));
                         } else {
                             ptx::mma_commit(bar(BAR_OF + w));
                         }
                     }
-                    ++vc;
-                    if (more) ++kc;
-                }
+                        }
                 if (!ok) break;
-                ++live[0];
-                live[1] += nw - 1;
+                ++vc;
+                kc += more;
             }
-            ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+            if (!ok) break;
+            if (some) {
+                ++live0;
+                live1 += nw - 1;
+            }
+            ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
+            ok = wait(BAR_TFULL + (it + 1) % kHeaders, (uint32_t)((it + 1) / kHeaders)) && open(it + 1);
         }
-        // nothing that this thread issued may still run when TMEM is freed
-        ptx::mma_commit(bar(BAR_DRAIN));
-        const uint64_t t0 = ptx::globaltimer();
-        while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::globaltimer() - t0 < kWaitNs) {}
+        // nothing that this warp issued may still run when TMEM is freed
+        {
+            ptx::mma_commit(bar(BAR_DRAIN));
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::globaltimer() - t0 < kWaitNs) {}
+        }
       }
-    } else {
+    } else if (warp < 12) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
       // -------------------------------------------------------------- softmax and output
       const int w = (warp - 4) >> 2, row = threadIdx.x & 127;
@@ -378,12 +475,12 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       uint32_t r[16];
       float x[kBN];
       for (int it = 0;; ++it) {
-        if (!warp_wait(bar(BAR_TFULL + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag, status)) break;
-        const Item* hd = hdr(it & 1);
+        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+        const Item* hd = hdr(it % kHeaders);
         if (hd->b < 0) break;
         if (hd->rows <= w * kBM) {
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
+            if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
             continue;
         }
         const int n = hd->t1 - hd->t0;
@@ -396,28 +493,27 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             ++su;
             ptx::tc_fence_after();
+            // maxima of raw Q.K come with the load: scale once (scale > 0 keeps the order)
+            float mx;
             {
                 uint32_t* xr = reinterpret_cast<uint32_t*>(x);
-                ptx::tmem_ld32(tS + 0, xr + 0);
-                ptx::tmem_ld32(tS + 32, xr + 32);
-                ptx::tmem_ld32(tS + 64, xr + 64);
-                ptx::tmem_ld32(tS + 96, xr + 96);
+                float top[4];
+                ld32_max(tS + 0, xr + 0, top[0]);
+                ld32_max(tS + 32, xr + 32, top[1]);
+                ld32_max(tS + 64, xr + 64, top[2]);
+                ld32_max(tS + 96, xr + 96, top[3]);
                 ptx::tmem_wait_ld();
+                mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             }
             if (nv < kBN) {
+                mx = -CUDART_INF_F;
 #pragma unroll
-                for (int c = 0; c < kBN; ++c) x[c] = c < nv ? x[c] : -CUDART_INF_F;
+                for (int c = 0; c < kBN; ++c) {
+                    x[c] = c < nv ? x[c] : -CUDART_INF_F;
+                    mx = fmaxf(mx, x[c]);
+                }
             }
-            float mxp[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) mxp[u] = -CUDART_INF_F;
-#pragma unroll
-            for (int c = 0; c < kBN; c += 16)
-#pragma unroll
-                for (int u = 0; u < 8; ++u) mxp[u] = ptx::fmax3(mxp[u], x[c + u], x[c + 8 + u]);
-            // maxima of raw Q.K: scale once (scale > 0 keeps the order)
-            const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
-                                   fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]))) * prm.scale_log2;
+            mx *= prm.scale_log2;
             const float m_new = fmaxf(m_ref, mx);
             const bool need = m_new > m_ref + kRescaleThreshold;
             if (__any_sync(0xffffffffu, need)) {
@@ -463,55 +559,96 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         if (!ok) break;
         if (n > 0) {
-            if (!warp_wait(bar(BAR_OF + w), (uint32_t)live & 1u, abort_flag, status)) break;
+            // the output is another warpgroup's: it gets 1 / sum, once it has read the last item's
+            if (live > 0 && !warp_wait(bar(BAR_OFREE + w), (uint32_t)(live - 1) & 1u, abort_flag, status)) break;
             ++live;
-            ptx::tc_fence_after();
+            inv[w * kBM + row] = l == 0.f ? 0.f : 1.f / l;
+            ptx::mbar_arrive(bar(BAR_XF + w));
         }
-        const Item m = *hd;
+        if ((a.parts > 1 || a.lse) && w * kBM + row < hd->rows) {
+            const RowAt p = row_at(a, *hd, w * kBM + row);
+            const float lse = l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
+            if (a.parts > 1) a.part_lse[p.part] = lse;
+            else a.lse[p.batch * a.lb + p.tok * a.lt + p.hq * a.lh] = lse;
+        }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + (it & 1)));
-        const int at = w * kBM + row;
-        const bool write = at < m.rows;
-        const int rr = m.row + (write ? at : 0), t = rr / a.G, hq = m.group * a.G + (rr - t * a.G);
-        const long long tok = (a.query_start ? a.query_start[m.b] : 0) + t, qbat = a.query_start ? 0 : m.b;
-        const float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
-        __nv_bfloat16* o = (__nv_bfloat16*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
-        long long pr = 0;  // row of the part's results
-        if (a.parts > 1) pr = ((long long)m.part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
+      }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+      // -------------------------------------------------------------- output
+      const int row = threadIdx.x & 127;
+      const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+      const Cross& a = prm.a;
+      constexpr int kChunks = HD / 8;  // of 16 bytes, in a row
+      uint4* stage = reinterpret_cast<uint4*>(sm + L::kOut);
+      const auto pack = [](const uint32_t* v) { return ptx::pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+      int live[2] = {0, 0};
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+        const Item& hd = *hdr(it % kHeaders);
+        if (hd.b < 0) break;
+        const bool some = hd.t1 > hd.t0;
 #pragma unroll
-        for (int c = 0; c < HD / 16; ++c) {
-            if (n > 0) {
-                ptx::tmem_ld16(tO + c * 16, r);
-                ptx::tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = 0u;
+        for (int w = 0; w < 2; ++w) {
+            if (!ok || hd.rows <= w * kBM) break;
+            const int at = w * kBM + row;
+            float scale = 0.f;
+            if (some) {
+                ok = warp_wait(bar(BAR_XF + w), (uint32_t)live[w] & 1u, abort_flag, status) &&
+                     warp_wait(bar(BAR_OF + w), (uint32_t)live[w] & 1u, abort_flag, status);
+                if (!ok) break;
+                ++live[w];
+                ptx::tc_fence_after();
+                scale = inv[at];
             }
-            if (c == HD / 16 - 1 && n > 0) {
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(bar(BAR_OFREE + w));
-            }
-            if (write) {
-                float v[16];
+            const uint32_t tO = tmem + lane_off + 256 + HD * w;
+            float* po = a.parts > 1 && at < hd.rows ? a.part_out + row_at(a, hd, at).part * a.D : nullptr;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]) * inv;
-                if (a.parts > 1) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (16 * c + 8 * h < a.D)
-                            ptx::st_global_v8(a.part_out + pr * a.D + 16 * c + 8 * h, reinterpret_cast<uint32_t*>(v) + 8 * h);
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t r[32];
+                if (some) {
+                    ptx::tmem_ld32(tO + c * 32, r);
+                    ptx::tmem_wait_ld();
+                    if (c == HD / 32 - 1) {
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(bar(BAR_OFREE + w));
+                    }
                 } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (16 * c + 8 * h < a.D)
-                            *reinterpret_cast<uint4*>(o + 16 * c + 8 * h) =
-                                make_uint4(ptx::pack_bf16x2(v[8 * h], v[8 * h + 1]), ptx::pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
-                                           ptx::pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), ptx::pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
+                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * scale);
+                if (a.parts > 1) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        if (po && 32 * c + 8 * h < a.D) ptx::st_global_v8(po + 32 * c + 8 * h, r + 8 * h);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        stage[row * kChunks + ((4 * c + h) ^ (row & 7))] =
+                            make_uint4(pack(r + 8 * h), pack(r + 8 * h + 2), pack(r + 8 * h + 4), pack(r + 8 * h + 6));
                 }
             }
+            if (a.parts > 1) continue;
+            // a warp's own 32 rows, a whole row to adjacent lanes
+            __syncwarp();
+            const int ch = lane % kChunks, x0 = (warp & 3) * 32 + lane / kChunks, r0 = hd.row + w * kBM + x0;
+            const int live_rows = 8 * ch < a.D ? hd.rows - w * kBM : 0, shift = hd.shift, low = a.G - 1;
+            __nv_bfloat16* o = (__nv_bfloat16*)a.out + (a.query_start ? 0 : hd.b) * a.ob + hd.q0 * a.ot + (long long)hd.group * a.G * a.oh + 8 * ch;
+#pragma unroll 8
+            for (int i = 0; i < kChunks; ++i) {
+                const int d = i * (32 / kChunks), x = x0 + d;
+                if (x < live_rows)
+                    *reinterpret_cast<uint4*>(o + ((r0 + d) >> shift) * a.ot + ((r0 + d) & low) * a.oh) = stage[x * kChunks + (ch ^ (x & 7))];
+            }
+            __syncwarp();
         }
-        if (write && a.parts > 1) a.part_lse[pr] = lse;
-        else if (write && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
       }
     }
 
@@ -575,7 +712,7 @@ static bsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     if (!fits) {
         cudaFuncAttributes a;
         fits = (cudaFuncGetAttributes(&a, cross_tc_kernel<HD>) == cudaSuccess &&
-                a.numRegs * kThreads >= 128 * kRegsLow + 256 * kRegsHigh) ? 1 : -1;
+                a.numRegs * kThreads >= 128 * kRegsLow + 256 * kRegsHigh + 128 * kRegsOut) ? 1 : -1;
     }
     if (fits < 0) return BSA_OK;
     *handled = true;
