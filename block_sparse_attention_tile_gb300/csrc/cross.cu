@@ -192,9 +192,12 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
 // ---------------------------------------------------------------- host side
 
 struct CrossPlan {
-    int way;    // 0 CUDA cores, 1 tensor cores
-    int parts;  // of the keys
+    int way;      // 0 CUDA cores, 1 tensor cores, 2 tensor cores with 16 rows a tile
+    int parts;    // of the keys, in the workspace
+    int cluster;  // way 2: blocks that join their keys in a cluster; each part is cut into so many
 };
+
+constexpr int kFewRows = 31;  // of a sequence and KV head
 
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
     CrossPlan p{};
@@ -202,7 +205,14 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
     const long long rows = (packed_q ? (N + B - 1) / B : (long long)N) * G;  // of a sequence and KV head, on average
     const long long keys = packed_k ? (M + B - 1) / B : M;
     long long items;
-    if (cross_tc_sizes(dtype, D) && rows >= 32) {
+    p.cluster = 1;
+    if (cross_tc_sizes(dtype, D) && rows <= kFewRows) {
+        p.way = 2;
+        items = row_tiles(B, N, G, packed_q, 16) * H;
+        const long long want = std::max<long long>(1, std::min<long long>((keys + 63) / 64, (8 * 152 + items - 1) / std::max(items, 1LL)));
+        while (p.cluster < 8 && p.cluster < want) p.cluster *= 2;
+        p.parts = (int)std::min<long long>((want + p.cluster - 1) / p.cluster, 16);
+    } else if (cross_tc_sizes(dtype, D)) {
         p.way = 1;
         items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
         p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
@@ -284,6 +294,11 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     bsa_status rc = BSA_OK;
     bool handled = false;
     if (p.way == 1) rc = cross_tc(a, st, &handled);
+    if (p.way == 2) {
+        Cross r = a;
+        r.parts = p.parts * p.cluster;
+        rc = cross_rows(r, p.cluster, st, &handled);
+    }
     if (!handled && rc == BSA_OK)
         rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
     if (rc != BSA_OK || p.parts == 1) return rc;

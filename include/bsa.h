@@ -652,8 +652,9 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * query_start, key_start, key_lens: [device] int32.
  * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
  * between calls.  Deterministic. */
-/* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores (addresses and
- * strides that are no multiples of 16 bytes take 0 all the same); -1 for sizes out of range. */
+/* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
+ * tiles of 16 rows (addresses and strides that are no multiples of 16 bytes take 0 all the same); -1 for sizes out of
+ * range. */
 int bsa_cross_way(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries, int packed_keys);
 size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
                            int packed_keys);
