@@ -463,40 +463,64 @@ def bsa_fwd_cache_tokens(q, T, HQ, H, D, cache, n_pages, page_size, block_table,
 
 # ---------------------------------------------------------------- rotary positions, cross attention
 
-def _heads(name, t, shape, dtype, dev):
-    """Data pointer and batch, token and head stride of rows [B, T, heads, D] whose channels are adjacent."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        raise ValueError("%s: a %s tensor %s on cuda:%d is needed, got %s %s on %s"
-                         % (name, dtype, list(shape), dev, t.dtype, tuple(t.shape), t.device))
-    st = t.stride()
-    if st[3] != 1 and shape[3] > 1:
-        raise ValueError("%s: a row's channels must be adjacent, got strides %s" % (name, st))
-    return t.data_ptr(), st[:3]
+def _heads(name, t, B, T, heads, D, dtype, dev, first=False):
+    """Data pointer and batch, token and head stride of rows [B, T, heads, D] (``first``: [B, heads, T, D]; without B
+    where that is 1) whose channels are adjacent."""
+    if t.dtype is dtype and t.get_device() == dev:
+        shape, st = t.shape, t.stride()
+        if shape == ((B, heads, T, D) if first else (B, T, heads, D)):
+            if st[3] == 1 or D == 1:
+                return (t.data_ptr(), st[0], st[2], st[1]) if first else (t.data_ptr(), st[0], st[1], st[2])
+        elif B == 1 and shape == ((heads, T, D) if first else (T, heads, D)):
+            if st[2] == 1 or D == 1:
+                return (t.data_ptr(), 0, st[1], st[0]) if first else (t.data_ptr(), 0, st[0], st[1])
+        else:
+            st = None
+        if st is not None:
+            raise ValueError("%s: a row's channels must be adjacent, got strides %s" % (name, st))
+    raise ValueError("%s: a %s tensor %s on cuda:%d is needed, got %s %s on %s"
+                     % (name, dtype, [B, heads, T, D] if first else [B, T, heads, D], dev, t.dtype, tuple(t.shape), t.device))
+
+
+@functools.lru_cache(maxsize=4096)
+def _int64s(*values):
+    """A host array of strides."""
+    return (I64 * len(values))(*values)
 
 
 def bsa_rotary_table(positions, T, axes, turns, axis, P, factor, cos_out, sin_out, stream=None):
-    dev, f32 = _device_of(turns), torch.float32
-    _call(dev, _lib.bsa_rotary_table, _expect("positions", positions, torch.int32, T * axes, dev), T, axes,
-          _expect("turns", turns, torch.int64, P, dev), _expect("axis", axis, torch.int32, P, dev), P, factor,
-          _expect("cos_out", cos_out, f32, T * P, dev), _expect("sin_out", sin_out, f32, T * P, dev), _on(dev, stream))
+    dev, f32, i32 = _device_of(turns), torch.float32, torch.int32
+    if not (turns.dtype is torch.int64 and turns.numel() >= P and turns.is_contiguous() and positions.dtype is i32
+            and positions.get_device() == dev and positions.numel() >= T * axes and positions.is_contiguous()
+            and cos_out.dtype is f32 and cos_out.get_device() == dev and cos_out.numel() >= T * P
+            and cos_out.is_contiguous() and sin_out.dtype is f32 and sin_out.get_device() == dev
+            and sin_out.numel() >= T * P and sin_out.is_contiguous()):
+        for x in (("positions", positions, i32, T * axes), ("turns", turns, torch.int64, P),
+                  ("cos_out", cos_out, f32, T * P), ("sin_out", sin_out, f32, T * P)):
+            _expect(*x, dev)
+    _call(dev, _lib.bsa_rotary_table, positions.data_ptr(), T, axes, turns.data_ptr(),
+          None if axis is None else _expect("axis", axis, i32, P, dev), P, factor, cos_out.data_ptr(),
+          sin_out.data_ptr(), _on(dev, stream))
 
 
 def bsa_rotate(q, k, B, T, HQ, H, D, P, cos_table, sin_table, table_batch_stride, q_out, k_out, interleaved=False,
-               transpose=False, q_weight=None, k_weight=None, eps=1e-6, stream=None):
-    """q, k and their outputs are [B, T, heads, D] views of any batch, token and head strides."""
+               transpose=False, q_weight=None, k_weight=None, eps=1e-6, heads_first=False, stream=None):
+    """q and k are [B, T, heads, D] (or without B where that is 1) of any batch, token and head strides, their outputs
+    the same or, with ``heads_first``, [B, heads, T, D]."""
     dev, dt, f32 = _device_of(q), q.dtype, torch.float32
-    qp, qs = _heads("q", q, (B, T, HQ, D), dt, dev)
-    qo, qos = _heads("q_out", q_out, (B, T, HQ, D), dt, dev)
+    qp, q0, q1, q2 = _heads("q", q, B, T, HQ, D, dt, dev)
+    qo, q3, q4, q5 = _heads("q_out", q_out, B, T, HQ, D, dt, dev, heads_first)
     kp = ko = None
-    ks = kos = (0, 0, 0)
+    k0 = k1 = k2 = k3 = k4 = k5 = 0
     if k is not None:
-        kp, ks = _heads("k", k, (B, T, H, D), dt, dev)
-        ko, kos = _heads("k_out", k_out, (B, T, H, D), dt, dev)
+        kp, k0, k1, k2 = _heads("k", k, B, T, H, D, dt, dev)
+        ko, k3, k4, k5 = _heads("k_out", k_out, B, T, H, D, dt, dev, heads_first)
     rows = T * P + (B - 1) * table_batch_stride if B and T else 0
     _call(dev, _lib.bsa_rotate, _dtype(q), B, T, D, P, 1 if interleaved else 0, 1 if transpose else 0,
           _expect("cos_table", cos_table, f32, rows, dev), _expect("sin_table", sin_table, f32, rows, dev),
-          table_batch_stride, qp, HQ, _expect("q_weight", q_weight, f32, D, dev), qo, kp, H if k is not None else 0,
-          _expect("k_weight", k_weight, f32, D, dev), ko, (I64 * 12)(*qs, *qos, *ks, *kos), eps, _on(dev, stream))
+          table_batch_stride, qp, HQ, None if q_weight is None else _expect("q_weight", q_weight, f32, D, dev), qo, kp,
+          H if k is not None else 0, None if k_weight is None else _expect("k_weight", k_weight, f32, D, dev), ko,
+          _int64s(q0, q1, q2, q3, q4, q5, k0, k1, k2, k3, k4, k5), eps, _on(dev, stream))
 
 
 def bsa_cache_append_rotated(k, v, T, H, D, slots, cache, n_pages, page_size, k_scale, v_scale, k_val, v_val, cos_table,
@@ -504,14 +528,31 @@ def bsa_cache_append_rotated(k, v, T, H, D, slots, cache, n_pages, page_size, k_
     dev, dt, f32 = _device_of(cache), k.dtype, torch.float32
     kp, ks = _rows("k", k, T, H, D, dt, dev)
     vp, vs = _rows("v", v, T, H, D, dt, dev)
-    qp, qs = (None, 0) if q is None else _rows("q", q, T, HQ, D, dt, dev)
-    _call(dev, _lib.bsa_cache_append_rotated, kp, vp, _dtype(k), T, H, D, ks, vs,
-          _expect("slots", slots, torch.int64, T, dev),
-          _expect("cache", cache, torch.uint8, n_pages * H * page_size // 16 * 18 * D, dev), n_pages, page_size,
-          _expect("k_scale", k_scale, f32, H, dev), _expect("v_scale", v_scale, f32, H, dev),
-          _expect("k_val", k_val, dt, T * H * D, dev), _expect("v_val", v_val, dt, T * H * D, dev),
-          _expect("cos_table", cos_table, f32, T * P, dev), _expect("sin_table", sin_table, f32, T * P, dev), P,
-          1 if interleaved else 0, qp, HQ, qs, _expect("q_out", q_out, dt, T * HQ * D, dev), _on(dev, stream))
+    nbytes = n_pages * H * page_size // 16 * 18 * D
+    if not (slots.dtype is torch.int64 and slots.get_device() == dev and slots.numel() >= T and slots.is_contiguous()
+            and cache.dtype is torch.uint8 and cache.numel() >= nbytes and cache.is_contiguous()
+            and cos_table.dtype is f32 and cos_table.get_device() == dev and cos_table.numel() >= T * P
+            and cos_table.is_contiguous() and sin_table.dtype is f32 and sin_table.get_device() == dev
+            and sin_table.numel() >= T * P and sin_table.is_contiguous()):
+        for x in (("slots", slots, torch.int64, T), ("cache", cache, torch.uint8, nbytes),
+                  ("cos_table", cos_table, f32, T * P), ("sin_table", sin_table, f32, T * P)):
+            _expect(*x, dev)
+    qp = qo = ksp = vsp = kvp = vvp = None
+    qs = 0
+    if q is not None:
+        qp, qs = _rows("q", q, T, HQ, D, dt, dev)
+        qo = _expect("q_out", q_out, dt, T * HQ * D, dev)
+    if k_scale is not None:
+        ksp = _expect("k_scale", k_scale, f32, H, dev)
+    if v_scale is not None:
+        vsp = _expect("v_scale", v_scale, f32, H, dev)
+    if k_val is not None:
+        kvp = _expect("k_val", k_val, dt, T * H * D, dev)
+    if v_val is not None:
+        vvp = _expect("v_val", v_val, dt, T * H * D, dev)
+    _call(dev, _lib.bsa_cache_append_rotated, kp, vp, _dtype(k), T, H, D, ks, vs, slots.data_ptr(), cache.data_ptr(),
+          n_pages, page_size, ksp, vsp, kvp, vvp, cos_table.data_ptr(), sin_table.data_ptr(), P, 1 if interleaved else 0,
+          qp, HQ, qs, qo, _on(dev, stream))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -527,25 +568,32 @@ def bsa_cross_way(dtype, B, N, M, HQ, H, D, packed_queries=False, packed_keys=Fa
 
 def bsa_fwd_cross(q, k, v, B, N, M, HQ, H, D, query_start, key_start, key_lens, scale, out, lse=None, workspace=None,
                   stream=None):
-    """q and out are [B, N, HQ, D] views ([1, N, HQ, D] with query_start), k and v [B, M, H, D] ([1, M, H, D] with
-    key_start), lse [B, N, HQ] ([1, N, HQ])."""
+    """q and out are [B, N, HQ, D] ([N, HQ, D] with query_start), k and v [B, M, H, D] ([M, H, D] with key_start), lse
+    [B, N, HQ] ([N, HQ]), of any strides."""
     dev, dt, i32 = _device_of(q), q.dtype, torch.int32
     qb, kb = 1 if query_start is not None else B, 1 if key_start is not None else B
-    qp, qs = _heads("q", q, (qb, N, HQ, D), dt, dev)
-    kp, ks = _heads("k", k, (kb, M, H, D), dt, dev)
-    vp, vs = _heads("v", v, (kb, M, H, D), dt, dev)
-    op, os_ = _heads("out", out, (qb, N, HQ, D), dt, dev)
-    lp, ls = None, (0, 0, 0)
+    qp, q0, q1, q2 = _heads("q", q, qb, N, HQ, D, dt, dev)
+    kp, k0, k1, k2 = _heads("k", k, kb, M, H, D, dt, dev)
+    vp, v0, v1, v2 = _heads("v", v, kb, M, H, D, dt, dev)
+    op, o0, o1, o2 = _heads("out", out, qb, N, HQ, D, dt, dev)
+    lp = qsp = ksp = klp = None
+    l0 = l1 = l2 = 0
     if lse is not None:
-        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (qb, N, HQ):
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or \
+                (lse.shape != (qb, N, HQ) and (qb != 1 or lse.shape != (N, HQ))):
             raise ValueError("lse: a float32 tensor %s on cuda:%d is needed, got %s %s on %s"
                              % ([qb, N, HQ], dev, lse.dtype, tuple(lse.shape), lse.device))
-        lp, ls = lse.data_ptr(), lse.stride()
-    if key_start is not None and key_lens is not None:
-        raise ValueError("key_start and key_lens exclude each other")
+        lp, st = lse.data_ptr(), lse.stride()
+        l0, l1, l2 = st if len(st) == 3 else (0, *st)
+    if query_start is not None:
+        qsp = _expect("query_start", query_start, i32, B + 1, dev)
+    if key_start is not None:
+        ksp = _expect("key_start", key_start, i32, B + 1, dev)
+    if key_lens is not None:
+        klp = _expect("key_lens", key_lens, i32, B, dev)
+        if ksp is not None:
+            raise ValueError("key_start and key_lens exclude each other")
     ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace, dev)
-    _call(dev, _lib.bsa_fwd_cross, qp, kp, vp, _dtype(q), B, N, M, HQ, H, D, (I64 * 15)(*qs, *ks, *vs, *os_, *ls),
-          None if query_start is None else _expect("query_start", query_start, i32, B + 1, dev),
-          None if key_start is None else _expect("key_start", key_start, i32, B + 1, dev),
-          None if key_lens is None else _expect("key_lens", key_lens, i32, B, dev), scale, op, lp, ws, ws_bytes,
+    _call(dev, _lib.bsa_fwd_cross, qp, kp, vp, _dtype(q), B, N, M, HQ, H, D,
+          _int64s(q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2, l0, l1, l2), qsp, ksp, klp, scale, op, lp, ws, ws_bytes,
           _on(dev, stream))

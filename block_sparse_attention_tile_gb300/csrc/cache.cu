@@ -446,6 +446,39 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
 // thread takes one group as above; its key channels' partners are the group P channels away (half layout, read
 // too) or the group itself (interleaved).  The rotation is rounded to float32 and quantised from there: keys are
 // not rounded to bf16 on the way.
+// Eight channels at 16-byte aligned p.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
+                                              ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Queries go by units of 16 channels, two runs of 8 (half layout: 8u .. and P + 8u ..): first channels of the runs.
+__device__ __forceinline__ void unit_runs(int u, int P, bool interleaved, int& c0, int& c1) {
+    if (!interleaved && 8 * u < P) c0 = 8 * u, c1 = P + 8 * u;
+    else c0 = interleaved ? 16 * u : 2 * P + 16 * (u - P / 8), c1 = c0 + 8;
+}
+
+// Turns a unit's 16 channels (x[0..7] the first run, x[8..15] the second).
+__device__ __forceinline__ void rotate_unit(float* x, const float* c, const float* s, bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate_pair(x[i], x[8 + i], c[i], s[i]);
+    }
+}
+
 struct Rotated {
     const float* cos;
     const float* sin;

@@ -209,7 +209,7 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
     if (cross_tc_sizes(dtype, D) && rows <= kFewRows) {
         p.way = 2;
         items = row_tiles(B, N, G, packed_q, 16) * H;
-        const long long want = std::max<long long>(1, std::min<long long>((keys + 63) / 64, (8 * 152 + items - 1) / std::max(items, 1LL)));
+        const long long want = std::max<long long>(1, std::min<long long>((keys + 63) / 64, ((keys <= 1024 ? 2 : 8) * 152 + items - 1) / std::max(items, 1LL)));
         while (p.cluster < 8 && p.cluster < want) p.cluster *= 2;
         p.parts = (int)std::min<long long>((want + p.cluster - 1) / p.cluster, 16);
     } else if (cross_tc_sizes(dtype, D)) {

@@ -14,16 +14,28 @@ namespace bsa {
 // A frequency is held as turns a position in units of 2^-64, so the angle's fraction of a turn is the low 64
 // bits of an integer product: exact for any position, where a float32 product would have lost the angle of
 // position 2^24 altogether.  The upper 32 bits are cut into quadrant and remainder, and only the
-// remainder, an eighth of a turn at most, becomes a float.
+// remainder, an eighth of a turn at most, becomes a float.  Its sine and cosine are the first five and six terms of
+// their series: what is left out is below 2e-9 of the one and 4e-11 of the other.
+// A thread keeps the frequencies of four neighbouring pairs (one, where P is odd to four) and walks the tokens.  The writes
+// bound it, 8 bytes a pair.
 __device__ __forceinline__ void cos_sin(uint64_t turn, float factor, float& c, float& s) {
     const uint32_t t = (uint32_t)((turn + 0x80000000ull) >> 32);  // 2^-32 turns
     const uint32_t quad = (t + (1u << 29)) >> 30;
     const float x = (float)(int32_t)(t - (quad << 30)) * 0x1p-31f;  // half turns, |x| <= 1/4
-    float sn, cs;
-    sincospif(x, &sn, &cs);
+    constexpr double kPi = 3.14159265358979323846, kPi2 = kPi * kPi;
+    const float y = x * x;
+    float sn = fmaf(y, (float)(kPi * kPi2 * kPi2 * kPi2 * kPi2 / 362880), (float)(-kPi * kPi2 * kPi2 * kPi2 / 5040));
+    sn = fmaf(sn, y, (float)(kPi * kPi2 * kPi2 / 120));
+    sn = fmaf(sn, y, (float)(-kPi * kPi2 / 6));
+    sn = fmaf(sn * y, x, x * (float)kPi);
+    float cs = fmaf(y, (float)(-kPi2 * kPi2 * kPi2 * kPi2 * kPi2 / 3628800), (float)(kPi2 * kPi2 * kPi2 * kPi2 / 40320));
+    cs = fmaf(cs, y, (float)(-kPi2 * kPi2 * kPi2 / 720));
+    cs = fmaf(cs, y, (float)(kPi2 * kPi2 / 24));
+    cs = fmaf(cs, y, (float)(-kPi2 / 2));
+    cs = fmaf(cs, y, 1.f);
     const float a = quad & 1 ? sn : cs, b = quad & 1 ? cs : sn;
-    c = ((quad + 1) & 2 ? -a : a) * factor;
-    s = (quad & 2 ? -b : b) * factor;
+    c = a * ((quad + 1) & 2 ? -factor : factor);
+    s = b * (quad & 2 ? -factor : factor);
 }
 
 template <int V>
@@ -31,21 +43,25 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const int32_t* __rest
                                                            const int64_t* __restrict__ turns,
                                                            const int32_t* __restrict__ axis, int P, float factor,
                                                            float* __restrict__ cos_out, float* __restrict__ sin_out,
-                                                           long long items, int* status) {
-    const int per = P / V;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
-        const long long t = i / per;
-        const int p = (int)(i - t * per) * V;
+                                                           int T, int* status) {
+    const int per = P / V, tokens = 256 / per;  // threads a token, tokens a block
+    const int p = (int)(threadIdx.x % per) * V;
+    uint64_t f[V];
+    int ax[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        f[j] = (uint64_t)turns[p + j];
+        ax[j] = axis ? axis[p + j] : 0;
+        if ((unsigned)ax[j] >= (unsigned)axes) {
+            raise_status(status, BSA_ERR_INDEX);
+            ax[j] = 0;
+        }
+    }
+    if ((int)threadIdx.x >= tokens * per) return;
+    for (long long t = (long long)blockIdx.x * tokens + threadIdx.x / per; t < T; t += (long long)gridDim.x * tokens) {
         float c[V], s[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            int a = axis ? axis[p + j] : 0;
-            if ((unsigned)a >= (unsigned)axes) {
-                raise_status(status, BSA_ERR_INDEX);
-                a = 0;
-            }
-            cos_sin((uint64_t)turns[p + j] * (uint64_t)(int64_t)positions[t * axes + a], factor, c[j], s[j]);
-        }
+        for (int j = 0; j < V; ++j) cos_sin(f[j] * (uint64_t)(int64_t)positions[t * axes + ax[j]], factor, c[j], s[j]);
         const long long at = t * P + p;
         if constexpr (V == 4) {
             *reinterpret_cast<float4*>(cos_out + at) = make_float4(c[0], c[1], c[2], c[3]);
@@ -70,34 +86,37 @@ struct Rotate {
     bool interleaved, transpose;
 };
 
-template <typename T, int kLanes>
-__global__ void __launch_bounds__(256) rotate_kernel(const Rotate a) {
-    const int lane = threadIdx.x & 31, u = lane % kLanes;
-    const bool live = 16 * u < a.D, turn = 8 * u < a.P;
-    int c0, c1;
-    unit_runs(u, a.P, a.interleaved, c0, c1);
+// Blocks y = 0 take q, y = 1 k: apart, a warp has fewer registers to hold.
+template <typename T, int kLanes, bool kNorm, bool kInterleaved>
+__global__ void __launch_bounds__(256, 4) rotate_kernel(const Rotate a) {
+    const int u = (threadIdx.x & 31) % kLanes;
+    const RowSet& r = a.set[blockIdx.y];
     for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < a.items; i += (long long)gridDim.x * 8) {
-        const long long tok = i / a.splits;
+        const long long tok = a.splits > 1 ? i / a.splits : i, b = tok < a.T ? 0 : tok / a.T, t = tok - b * a.T;
         const int part = (int)(i - tok * a.splits);
-        const long long b = tok / a.T, t = tok - b * a.T;
-        float c[8], s[8];
-        if (turn) {
-            const long long at = b * a.table_batch + t * a.P + 8 * u;
-            load8(a.cos + at, c);
-            load8(a.sin + at, s);
-            if (a.transpose) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = -s[j];
-            }
+        float c[4], s[4];
+        if (4 * u < a.P) {
+            const long long at = b * a.table_batch + t * a.P + 4 * u;
+            const float4 x = *reinterpret_cast<const float4*>(a.cos + at), y = *reinterpret_cast<const float4*>(a.sin + at);
+            const float f = a.transpose ? -1.f : 1.f;
+            c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+            s[0] = f * y.x, s[1] = f * y.y, s[2] = f * y.z, s[3] = f * y.w;
         }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const RowSet& r = a.set[n];
-            const int h0 = (int)((long long)r.heads * part / a.splits), h1 = (int)((long long)r.heads * (part + 1) / a.splits);
-            rotate_heads<T, kLanes>(r, (const T*)r.x + b * r.xb + t * r.xt, (T*)r.y + b * r.yb + t * r.yt, h0, h1, lane,
-                                    a.D, live, turn, c0, c1, c, s, a.interleaved, a.eps);
-        }
+        const int h0 = (int)((long long)r.heads * part / a.splits), h1 = (int)((long long)r.heads * (part + 1) / a.splits);
+        const T* x = (const T*)r.x + b * r.xb + t * r.xt;
+        T* y = (T*)r.y + b * r.yb + t * r.yt;
+        if (kNorm && r.weight) rotate_heads<T, kLanes, true, kInterleaved>(r.weight, x, y, r.xh, r.yh, h0, h1, a.D, a.P, c, s, a.eps);
+        else rotate_heads<T, kLanes, false, kInterleaved>(nullptr, x, y, r.xh, r.yh, h0, h1, a.D, a.P, c, s, 0.f);
     }
+}
+
+template <typename T, int kLanes>
+static void start_rotate(const Rotate& a, dim3 grid, cudaStream_t st) {
+    const bool norm = a.set[0].weight || a.set[1].weight;
+    if (norm && a.interleaved) rotate_kernel<T, kLanes, true, true><<<grid, 256, 0, st>>>(a);
+    else if (norm) rotate_kernel<T, kLanes, true, false><<<grid, 256, 0, st>>>(a);
+    else if (a.interleaved) rotate_kernel<T, kLanes, false, true><<<grid, 256, 0, st>>>(a);
+    else rotate_kernel<T, kLanes, false, false><<<grid, 256, 0, st>>>(a);
 }
 
 // Any D up to 256, any number of pairs, any strides: a warp a row, a channel a lane at a time.
@@ -148,15 +167,15 @@ static bsa_status launch_rotate(Rotate& a, long long tokens, bool wide, cudaStre
         rotate_any_kernel<T><<<blocks(tokens * heads), 256, 0, st>>>(a, tokens * heads);
         return check_launch("rotate_any_kernel");
     }
-    const int lanes = a.D <= 32 ? 2 : a.D <= 64 ? 4 : a.D <= 128 ? 8 : 16;
-    const int steps = (heads * lanes + 31) / 32;  // of a whole token
+    const int lanes = row_lanes(a.D), steps = (std::max(a.set[0].heads, a.set[1].heads) * lanes + 31) / 32;  // of a token
+    // a share of the heads to a warp where there are few tokens
     a.splits = (int)std::max<long long>(1, std::min<long long>(steps, 152 * 32 / std::max<long long>(tokens, 1)));
     a.items = tokens * a.splits;
-    const unsigned grid = blocks(a.items);
-    if (lanes == 2) rotate_kernel<T, 2><<<grid, 256, 0, st>>>(a);
-    else if (lanes == 4) rotate_kernel<T, 4><<<grid, 256, 0, st>>>(a);
-    else if (lanes == 8) rotate_kernel<T, 8><<<grid, 256, 0, st>>>(a);
-    else rotate_kernel<T, 16><<<grid, 256, 0, st>>>(a);
+    const dim3 grid(blocks(a.items), a.set[1].heads ? 2 : 1);
+    if (lanes == 4) start_rotate<T, 4>(a, grid, st);
+    else if (lanes == 8) start_rotate<T, 8>(a, grid, st);
+    else if (lanes == 16) start_rotate<T, 16>(a, grid, st);
+    else start_rotate<T, 32>(a, grid, st);
     return check_launch("rotate_kernel");
 }
 
@@ -174,14 +193,14 @@ bsa_status bsa_rotary_table(const int32_t* positions, int T, int axes, const int
     BSA_REQUIRE(axes == 1 || axis, "rotary table: several axes need an axis for each frequency");
     if (T == 0) return BSA_OK;
     const bool wide = P % 4 == 0 && (((uintptr_t)cos_out | (uintptr_t)sin_out) & 15) == 0;
-    const long long items = (long long)T * P / (wide ? 4 : 1);
-    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 152 * 64);
+    const int tokens = 256 / (wide ? P / 4 : P);
+    const unsigned grid = (unsigned)std::min<long long>(((long long)T + tokens - 1) / tokens, 152 * 16);
     cudaStream_t st = as_stream(stream);
     if (wide)
-        rotary_table_kernel<4><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, items,
+        rotary_table_kernel<4><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, T,
                                                      status_word());
     else
-        rotary_table_kernel<1><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, items,
+        rotary_table_kernel<1><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, T,
                                                      status_word());
     return check_launch("rotary_table_kernel");
 }
@@ -205,15 +224,16 @@ bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleav
     const float* weight[2] = {q_weight, k_weight};
     const int heads[2] = {HQ, H};
     const int size = dtype == BSA_F32 ? 4 : 2;
-    bool wide = D % 16 == 0 && P % 8 == 0 && (((uintptr_t)cos_table | (uintptr_t)sin_table) & 15) == 0 &&
+    const uintptr_t run = 4 * size - 1;  // runs of four channels
+    bool wide = D % 8 == 0 && P % 4 == 0 && (((uintptr_t)cos_table | (uintptr_t)sin_table) & 15) == 0 &&
                 table_batch_stride % 4 == 0;
     for (int n = 0; n < 2; ++n) {
         const int64_t* s = strides + 6 * n;
         a.set[n] = RowSet{in[n], out[n], weight[n], s[0], s[1], s[2], s[3], s[4], s[5], heads[n]};
         if (!heads[n]) continue;
-        uintptr_t any = (uintptr_t)in[n] | (uintptr_t)out[n] | (uintptr_t)weight[n];
+        uintptr_t any = (uintptr_t)in[n] | (uintptr_t)out[n];
         for (int j = 0; j < 6; ++j) any |= (uintptr_t)(s[j] * size);
-        wide = wide && (any & 15) == 0;
+        wide = wide && (any & run) == 0 && ((uintptr_t)weight[n] & 15) == 0;
     }
     a.cos = cos_table;
     a.sin = sin_table;

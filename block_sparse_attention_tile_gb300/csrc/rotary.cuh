@@ -5,10 +5,10 @@
 // Products and sums are rounded one by one, not fused: the result is then the same in whatever order a program
 // computes it, and with it the 4-bit codes that the cache append makes of it.
 //
-// A row of D channels is cut into units of 16: two runs of 8 channels that a lane reads with wide loads and
-// whose pairs lie inside the unit.  Half layout: pair i is (i, i + P), unit u < P / 8 holds channels 8u .. and
-// P + 8u ..; the rest of the row, 16 at a time, is copied.  Interleaved layout: pair i is (2i, 2i + 1), unit u
-// holds channels 16u .. 16u + 15.  In both, unit u turns by the table's entries 8u .. 8u + 7.
+// A row of D channels is cut into units of 8: two runs of 4 channels that a lane reads at once and whose pairs lie
+// inside the unit.  Half layout: pair i is (i, i + P), unit u < P / 4 holds channels 4u .. and P + 4u ..; the rest of
+// the row, 8 at a time, is copied.  Interleaved layout: pair i is (2i, 2i + 1), unit u holds channels 8u .. 8u + 7.
+// In both, unit u turns by the table's entries 4u .. 4u + 3.
 #pragma once
 
 #include "common.cuh"
@@ -22,42 +22,35 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
     a = x;
 }
 
-// Eight channels at 16-byte aligned p.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Four channels as they lie in memory (8- or 16-byte aligned), and as floats.
+template <typename T> struct Run4;
+template <> struct Run4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void floats(float* x) const {
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+};
+template <> struct Run4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void floats(float* x) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+};
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
 }
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+// Eight table entries at 16-byte aligned p.
 __device__ __forceinline__ void load8(const float* p, float* x) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
-                                              ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-}
 
-// First channels of a unit's two runs.
-__device__ __forceinline__ void unit_runs(int u, int P, bool interleaved, int& c0, int& c1) {
-    if (!interleaved && 8 * u < P) c0 = 8 * u, c1 = P + 8 * u;
-    else c0 = interleaved ? 16 * u : 2 * P + 16 * (u - P / 8), c1 = c0 + 8;
-}
-
-// Turns a unit's 16 channels (x[0..7] the first run, x[8..15] the second).
-__device__ __forceinline__ void rotate_unit(float* x, const float* c, const float* s, bool interleaved) {
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rotate_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rotate_pair(x[i], x[8 + i], c[i], s[i]);
-    }
-}
+// Lanes that share a row of D channels: a power of two, 8 channels each.
+__host__ __device__ constexpr int row_lanes(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
 // Rows of `heads` heads to rotate, x into y (which may be x).
 struct RowSet {
@@ -68,43 +61,66 @@ struct RowSet {
     int heads;
 };
 
-// A warp takes one token (or a share of its heads): the lane's table entries stay in registers over the heads.
-template <typename T, int kLanes>
-__device__ __forceinline__ void rotate_heads(const RowSet& r, const T* x0, T* y0, int h0, int h1, int lane, int D,
-                                             bool live, bool turn, int c0, int c1, const float* c, const float* s,
-                                             bool interleaved, float eps) {
-    constexpr int kRows = 32 / kLanes;
-    float w[16];
-    if (r.weight && live) {
-        load8(r.weight + c0, w);
-        load8(r.weight + c1, w + 8);
-    }
-#pragma unroll 2
-    for (int h = h0 + lane / kLanes; h < h1 + lane / kLanes; h += kRows) {  // whole warps: shuffles below
-        const bool on = live && h < h1;
-        float x[16];
-        if (on) {
-            load8(x0 + h * r.xh + c0, x);
-            load8(x0 + h * r.xh + c1, x + 8);
-        }
-        if (r.weight) {
-            float ss = 0.f;
-            if (on) {
+// One token's heads [h0, h1) by a warp, 32 / kLanes rows a step; the lane's table entries stay in registers over them.
+// The rows of kBatch steps are read before the first of them is written (y may be x: the compiler cannot move a read
+// over a write).  What bounds it is the read and the write of every row once, so it is made for many bytes on their
+// way at 64 registers: units of 8 channels, weights from L1.  (115200 tokens of 24 + 24 heads of 128 channels with a
+// norm: units of 16 channels took 561 to 1000 us, by registers or spills; rows copied ahead into shared memory with
+// 8 warps an SM 982.)
+template <typename T, int kLanes, bool kNorm, bool kInterleaved>
+__device__ __forceinline__ void rotate_heads(const float* weight, const T* x, T* y, long long xh, long long yh, int h0,
+                                             int h1, int D, int P, const float* c, const float* s, float eps) {
+    constexpr int kRows = 32 / kLanes, kBatch = sizeof(T) == 2 ? 3 : 2;
+    const int lane = threadIdx.x & 31, u = lane % kLanes, own = lane / kLanes;
+    const bool live = 8 * u < D, turn = 4 * u < P;
+    const int c0 = kInterleaved ? 8 * u : turn ? 4 * u : 2 * P + 8 * (u - P / 4), c1 = !kInterleaved && turn ? P + 4 * u : c0 + 4;
+    x += (h0 + own) * xh + c0;
+    y += (h0 + own) * yh + c0;
+    const int d = c1 - c0;
+    for (int h = h0; h < h1; h += kRows * kBatch) {
+        Run4<T> a[kBatch], b[kBatch];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+        for (int i = 0; i < kBatch; ++i) {
+            if (live && h + i * kRows + own < h1) {
+                a[i].load(x);
+                b[i].load(x + d);
             }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float n = rsqrtf(ss / D + eps);
-            if (on) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= n * w[i];
-            }
+            x += kRows * xh;
         }
-        if (on) {
-            if (turn) rotate_unit(x, c, s, interleaved);
-            store8(y0 + h * r.yh + c0, x);
-            store8(y0 + h * r.yh + c1, x + 8);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (h + i * kRows >= h1) break;  // whole warps: shuffles below
+            const bool on = live && h + i * kRows + own < h1;
+            float z[8];
+            a[i].floats(z);
+            b[i].floats(z + 4);
+            if (kNorm) {
+                float ss = 0.f;
+                if (on) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(z[e], z[e], ss);
+                }
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float n = rsqrtf(__fdividef(ss, (float)D) + eps);
+                if (on) {
+                    const float4 w0 = *reinterpret_cast<const float4*>(weight + c0), w1 = *reinterpret_cast<const float4*>(weight + c1);
+                    z[0] *= n * w0.x, z[1] *= n * w0.y, z[2] *= n * w0.z, z[3] *= n * w0.w;
+                    z[4] *= n * w1.x, z[5] *= n * w1.y, z[6] *= n * w1.z, z[7] *= n * w1.w;
+                }
+            }
+            if (on) {
+                if (turn) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (kInterleaved) rotate_pair(z[2 * e], z[2 * e + 1], c[e], s[e]);
+                        else rotate_pair(z[e], z[4 + e], c[e], s[e]);
+                    }
+                }
+                store4(y, z);
+                store4(y + d, z + 4);
+            }
+            y += kRows * yh;
         }
     }
 }

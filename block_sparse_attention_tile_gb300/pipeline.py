@@ -470,8 +470,8 @@ def rotary_table(positions, turns, axis=None, factor=1.0, out=None):
     if axis is not None and axis.shape != turns.shape:
         raise ValueError("axis: one for each of %d frequencies is needed, got %s" % (P, tuple(axis.shape)))
     if out is None:
-        both = torch.empty(2, T, P, dtype=torch.float32, device=turns.device)
-        out = (both[0], both[1])
+        dev = turns.device
+        out = (torch.empty(T, P, dtype=torch.float32, device=dev), torch.empty(T, P, dtype=torch.float32, device=dev))
     elif out[0].shape != (T, P) or out[1].shape != (T, P):
         raise ValueError("out: two tensors [%d, %d] are needed" % (T, P))
     bsa.bsa_rotary_table(positions, T, axes, turns, axis, P, factor, out[0], out[1])
@@ -485,35 +485,25 @@ def rotate(q, k, cos, sin, interleaved=False, q_weight=None, k_weight=None, eps=
     adjacent channels.  Returns (q, k) as new tensors of the same layout, or heads first ([B, H, T, D], what the
     block-sparse stages read).  ``transpose``: the transposed rotation, which is the gradient's and takes a rotation
     back.  ``out``: the two tensors to write instead of new ones, q and k themselves among them."""
-    flat = q.dim() == 3
-    if flat:
-        q, k = q[None], None if k is None else k[None]
-    B, T, HQ, D = q.shape
-    H, P = 0 if k is None else k.shape[2], cos.shape[-1]
-    if sin.shape != cos.shape or cos.shape not in ((T, P), (B, T, P)):
+    shape, flat = q.shape, q.dim() == 3
+    B, T, HQ, D = (1, *shape) if flat else shape
+    H, P = 0 if k is None else k.shape[-2], cos.shape[-1]
+    if sin.shape != cos.shape or (cos.shape != (T, P) and cos.shape != (B, T, P)):
         raise ValueError("tables [%d, P] or [%d, %d, P] are needed, got %s and %s"
                          % (T, B, T, tuple(cos.shape), tuple(sin.shape)))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and w.shape != (D,):
-            raise ValueError("%s: [%d] is needed, got %s" % (name, D, tuple(w.shape)))
-    made = []
-    for n, x in enumerate((q, k)):
-        if x is None:
-            made.append((None, None))
-            continue
-        shape = (B, x.shape[2], T, D) if heads_first else (B, T, x.shape[2], D)
-        if out is None:
-            y = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if (q_weight is not None and q_weight.shape != (D,)) or (k_weight is not None and k_weight.shape != (D,)):
+        raise ValueError("q_weight, k_weight: [%d] is needed" % D)
+    if out is None:
+        dt, dev = q.dtype, q.device
+        if heads_first:
+            out = (torch.empty(*shape[:-3], HQ, T, D, dtype=dt, device=dev),
+                   None if k is None else torch.empty(*shape[:-3], H, T, D, dtype=dt, device=dev))
         else:
-            y = out[n][None] if flat else out[n]
-            if y.shape != shape:
-                raise ValueError("out: %s is needed, got %s" % (list(shape[1:] if flat else shape), tuple(out[n].shape)))
-        made.append((y, y.transpose(1, 2) if heads_first else y))
-    bsa.bsa_rotate(q, k, B, T, HQ, H, D, P, cos, sin, T * P if cos.dim() == 3 else 0, made[0][1], made[1][1],
-                   interleaved, transpose, q_weight, k_weight, eps)
-    if out is not None:
-        return out
-    return tuple(y[0] if flat and y is not None else y for y, _ in made)
+            out = (torch.empty(*shape, dtype=dt, device=dev),
+                   None if k is None else torch.empty(*shape[:-2], H, D, dtype=dt, device=dev))
+    bsa.bsa_rotate(q, k, B, T, HQ, H, D, P, cos, sin, T * P if cos.dim() == 3 else 0, out[0], out[1], interleaved,
+                   transpose, q_weight, k_weight, eps, heads_first)
+    return out
 
 
 def cache_append_rotated(k, v, slots, cache, cos, sin, k_scale=None, v_scale=None, interleaved=False, values=None,
@@ -526,9 +516,10 @@ def cache_append_rotated(k, v, slots, cache, cos, sin, k_scale=None, v_scale=Non
     P = cos.shape[-1]
     if cos.shape != (T, P) or sin.shape != (T, P):
         raise ValueError("tables [%d, P] are needed, got %s and %s" % (T, tuple(cos.shape), tuple(sin.shape)))
-    _check_scales(k_scale, v_scale, H)
+    if (k_scale is not None and k_scale.numel() != H) or (v_scale is not None and v_scale.numel() != H):
+        _check_scales(k_scale, v_scale, H)
     kv, vv = (None, None) if values is None else values
-    if values is not None:
+    if values is not None and (kv is None or vv is None or kv.shape != k.shape or vv.shape != k.shape):
         _check_rows("values", kv, T, H, D)
         _check_rows("values", vv, T, H, D)
     HQ = 0
@@ -536,7 +527,7 @@ def cache_append_rotated(k, v, slots, cache, cos, sin, k_scale=None, v_scale=Non
         HQ = q.shape[1]
         if q_out is None:
             q_out = torch.empty(T, HQ, D, dtype=q.dtype, device=q.device)
-        else:
+        elif q_out.shape != q.shape:
             _check_rows("q_out", q_out, T, HQ, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -552,20 +543,20 @@ def cross_attention(q, k, v, key_lens=None, query_start=None, key_start=None, sc
     key_start (int32 [B + 1] each; either alone or both).  Any strides with adjacent channels.  Returns
     (out as q, lse [B, N, HQ] or [N, HQ], or None).  ``out``, ``lse``: tensors to write instead of new ones; rows of
     no sequence are left as they were."""
-    packed_q, packed_k = query_start is not None, key_start is not None
-    if q.dim() != (3 if packed_q else 4) or k.dim() != (3 if packed_k else 4) or v.shape != k.shape:
+    packed_q, packed_k, qshape, kshape = query_start is not None, key_start is not None, q.shape, k.shape
+    if len(qshape) != (3 if packed_q else 4) or len(kshape) != (3 if packed_k else 4) or v.shape != kshape:
         raise ValueError("q %s, k %s, v %s: packed rows have three dimensions, padded ones four"
-                         % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
-    if out is None:
-        out = torch.empty_like(q)
+                         % (tuple(qshape), tuple(kshape), tuple(v.shape)))
     if packed_q:
         B = query_start.shape[0] - 1
-        N, HQ, D = q.shape
+        N, HQ, D = qshape
     else:
-        B, N, HQ, D = q.shape
-    M, H = k.shape[-3], k.shape[-2]
+        B, N, HQ, D = qshape
+    M, H = kshape[-3], kshape[-2]
     if (packed_k and key_start.shape[0] - 1 != B) or (key_lens is not None and key_lens.shape != (B,)):
         raise ValueError("the states of %d sequences are needed" % B)
+    if out is None:
+        out = torch.empty_like(q)
     if need_lse and lse is None:
         if packed_q:
             lse = torch.empty(N, HQ, dtype=torch.float32, device=q.device)
@@ -575,9 +566,8 @@ def cross_attention(q, k, v, key_lens=None, query_start=None, key_start=None, sc
             lse = torch.empty(B, N, HQ, dtype=torch.float32, device=q.device)
     nbytes = bsa.bsa_cross_workspace(q.dtype, B, N, M, HQ, H, D, packed_q, packed_k)
     ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
-    bsa.bsa_fwd_cross(q[None] if packed_q else q, k[None] if packed_k else k, v[None] if packed_k else v, B, N, M, HQ, H,
-                      D, query_start, key_start, key_lens, D ** -0.5 if scale is None else scale,
-                      out[None] if packed_q else out, lse if lse is None or not packed_q else lse[None], ws)
+    bsa.bsa_fwd_cross(q, k, v, B, N, M, HQ, H, D, query_start, key_start, key_lens,
+                      D ** -0.5 if scale is None else scale, out, lse, ws)
     return out, lse
 
 
