@@ -1,5 +1,5 @@
-// a18 cross attention on the CUDA cores (float32, and sizes that the tensor-core kernels do not take), the join of
-// the keys' parts, and the entry points.
+// a18 cross attention on the CUDA cores (sizes, strides and addresses that the tensor-core kernels do not take), the join
+// of the keys' parts, and the entry points.
 //
 // "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.5: the log2-domain recurrence of the online softmax; a row with
 // no key outputs zero.
@@ -192,11 +192,12 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
 // ---------------------------------------------------------------- host side
 
 struct CrossPlan {
-    int way;      // 0 CUDA cores, 1 tensor cores, 2 tensor cores with 16 rows a tile
+    int way;      // 0 CUDA cores, 1 tensor cores, 2 tensor cores with 16 rows a tile, 3 tensor cores, float32
     int parts;    // of the keys, in the workspace
     int cluster;  // way 2: blocks that join their keys in a cluster; each part is cut into so many
 };
 
+constexpr int kWant = 8, kLeast = 128;
 constexpr int kFewRows = 31;  // of a sequence and KV head
 
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
@@ -217,8 +218,9 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
         items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
         p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
     } else {
+        p.way = dtype == BSA_F32 && !force_simt() ? 3 : 0;
         items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
-        p.parts = (int)std::max<long long>(1, std::min<long long>({2 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
+        p.parts = (int)std::max<long long>(1, std::min<long long>({kWant * 152 / std::max(items, 1LL), (keys + kLeast - 1) / kLeast, 64}));
     }
     return p;
 }
@@ -299,6 +301,7 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
         r.parts = p.parts * p.cluster;
         rc = cross_rows(r, p.cluster, st, &handled);
     }
+    if (p.way == 3) rc = cross_f32(a, st), handled = true;
     if (!handled && rc == BSA_OK)
         rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
     if (rc != BSA_OK || p.parts == 1) return rc;

@@ -653,8 +653,8 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
  * between calls.  Deterministic. */
 /* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
- * tiles of 16 rows (addresses and strides that are no multiples of 16 bytes take 0 all the same); -1 for sizes out of
- * range. */
+ * tiles of 16 rows, 3 tensor cores in float32 (1 and 2: addresses and strides that are no multiples of 16 bytes take 0
+ * all the same); -1 for sizes out of range. */
 int bsa_cross_way(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries, int packed_keys);
 size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
                            int packed_keys);
