@@ -194,11 +194,12 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
 struct CrossPlan {
     int way;      // 0 CUDA cores, 1 tensor cores, 2 tensor cores with 16 rows a tile, 3 tensor cores, float32
     int parts;    // of the keys, in the workspace
-    int cluster;  // way 2: blocks that join their keys in a cluster; each part is cut into so many
+    int cluster;  // way 2: blocks that join their keys in a cluster
+    int runs;     // way 2, long rows: equal runs of all keys instead
 };
 
 constexpr int kWant = 8, kLeast = 128;
-constexpr int kFewRows = 31;  // of a sequence and KV head
+constexpr int kLongRow = 1024;  // keys
 
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
     CrossPlan p{};
@@ -207,12 +208,15 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
     const long long keys = packed_k ? (M + B - 1) / B : M;
     long long items;
     p.cluster = 1;
-    if (cross_tc_sizes(dtype, D) && rows <= kFewRows) {
+    if (cross_tc_sizes(dtype, D) && rows <= (keys > kLongRow ? 16 : 31)) {
         p.way = 2;
         items = row_tiles(B, N, G, packed_q, 16) * H;
-        const long long want = std::max<long long>(1, std::min<long long>((keys + 63) / 64, ((keys <= 1024 ? 2 : 8) * 152 + items - 1) / std::max(items, 1LL)));
+        const long long want = std::min<long long>((keys + 63) / 64, (2 * 152 + items - 1) / std::max(items, 1LL));
         while (p.cluster < 8 && p.cluster < want) p.cluster *= 2;
-        p.parts = (int)std::min<long long>((want + p.cluster - 1) / p.cluster, 16);
+        p.parts = 1;
+        // runs of four 64-key chunks or more
+        if (keys > kLongRow && items < 4 * 152)
+            p.runs = (int)std::min<long long>((D <= 64 ? 3 : 2) * 152, std::max<long long>(1, items * keys / 256));
     } else if (cross_tc_sizes(dtype, D)) {
         p.way = 1;
         items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
@@ -231,6 +235,7 @@ static bool cross_sizes_ok(int B, int N, int M, int HQ, int H, int D) {
 }
 
 static size_t part_bytes(const CrossPlan& p, int B, int N, int HQ, int D, bool packed_q) {
+    if (p.runs) return cross_runs_bytes(p.runs, D);
     return p.parts <= 1 ? 0 : sizeof(float) * (size_t)p.parts * (packed_q ? N : (size_t)B * N) * HQ * (D + 1);
 }
 
@@ -291,20 +296,20 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     a.status = status_word();
     const long long rows = (query_start ? (long long)N : (long long)B * N) * HQ;
     a.part_out = need ? static_cast<float*>(workspace) : nullptr;
-    a.part_lse = need ? a.part_out + (size_t)p.parts * rows * D : nullptr;
+    a.part_lse = need ? a.part_out + (p.runs ? (size_t)2 * p.runs * 16 : (size_t)p.parts * rows) * D : nullptr;
     cudaStream_t st = as_stream(stream);
     bsa_status rc = BSA_OK;
     bool handled = false;
     if (p.way == 1) rc = cross_tc(a, st, &handled);
     if (p.way == 2) {
         Cross r = a;
-        r.parts = p.parts * p.cluster;
-        rc = cross_rows(r, p.cluster, st, &handled);
+        r.parts = p.cluster;
+        rc = cross_rows(r, p.runs, st, &handled);
     }
     if (p.way == 3) rc = cross_f32(a, st), handled = true;
     if (!handled && rc == BSA_OK)
         rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
-    if (rc != BSA_OK || p.parts == 1) return rc;
+    if (rc != BSA_OK || p.parts == 1) return rc;  // runs join by themselves
     const dim3 grid((unsigned)a.tiles, H);
     if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 256, 0, st>>>(a);
     else cross_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);

@@ -106,6 +106,7 @@ int cross_tc_heads(int G);
 bool cross_tc_sizes(bsa_dtype dtype, int D);
 bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled);
 bsa_status cross_f32(const Cross& a, cudaStream_t st);
-bsa_status cross_rows(Cross a, int cluster, cudaStream_t st, bool* handled);
+size_t cross_runs_bytes(int runs, int D);
+bsa_status cross_rows(const Cross& a, int runs, cudaStream_t st, bool* handled);
 
 }  // namespace bsa

@@ -9,8 +9,8 @@
 // way; of V it reads 16 bytes at channels 8 g of the four keys 2c, 2c + 1, 2c + 8, 2c + 9 whose weights it holds, so
 // that channel 8 g + j is column g of product j.  The next 16 keys' reads go out as soon as a register is consumed:
 // 8 KB a warp are on their way, 64 KB an SM.
-// The four warps of a block, and the blocks of a cluster (up to 8, by shared memory of each other), join their parts
-// of the keys; with more parts than that the second kernel does.
+// The four warps of a block join their parts of the keys in shared memory.  Short rows: a cluster of up to 8 blocks an
+// item, which read each other's shared memory (one launch).  Long ones: equal runs and a join.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -25,6 +25,7 @@ namespace cross {
 namespace cg = cooperative_groups;
 
 constexpr int kRowTile = 16, kStep = 16, kWarps = 4;
+constexpr int kChunk = kStep * kWarps;
 constexpr float kGrow = 8.f;  // log2 units: the running maximum is raised, and O rescaled, only when it grows by more
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -36,20 +37,13 @@ __device__ __forceinline__ uint4 read16(const __nv_bfloat16* p, bool on) {
     return on ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
 
+// Key tiles [t0, t1) of 16 keys of sequence b and KV head h against the rows from row0: every warp's part of the
+// output, the maxima and the sums into shared memory (so: [kWarps][16][HD], sm: [kWarps][16] maxima, then sums).
 template <int HD>  // 64 or 128: channels, padded with zeros
-__global__ void __launch_bounds__(32 * kWarps, 2) cross_rows_kernel(const Cross a) {
+__device__ __forceinline__ void walk_keys(const Cross& a, int b, int h, int row0, int rows, int q0, int k0, int m, int t0, int t1,
+                                          float* so, float* sm) {
     constexpr int kC = HD / 32, kV = HD / 64;  // 16-byte runs of K and of V a lane reads of a key
-    extern __shared__ __align__(16) float rows_smem[];
-    float* so = rows_smem;                                    // [kWarps][16][HD]
-    float* sm = so + kWarps * kRowTile * HD;                  // [kWarps][16] maxima, then sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int h = blockIdx.y, part = blockIdx.z;
-    int b, row0, q0, n, k0, m;
-    tile_of<kRowTile>(a, blockIdx.x, b, row0);
-    if (b < 0) return;  // the whole cluster
-    queries_of(a, b, q0, n);
-    keys_of(a, b, k0, m);
-    const int rows = (int)min((long long)kRowTile, (long long)n * a.G - row0);
     const long long qbat = a.query_start ? 0 : b, kbat = a.key_start ? 0 : b;
     const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + qbat * a.qb + (long long)h * a.G * a.qh;
     const __nv_bfloat16* k = (const __nv_bfloat16*)a.k + kbat * a.kb + (long long)h * a.kh + k0 * a.kt;
@@ -66,9 +60,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) cross_rows_kernel(const Cross 
             qa[2 * i][s] = x.x, qa[2 * i][2 + s] = x.y, qa[2 * i + 1][s] = x.z, qa[2 * i + 1][2 + s] = x.w;
         }
 
-    const int nt = (m + kStep - 1) / kStep;
-    const int t1 = (int)((long long)nt * (part + 1) / a.parts);
-    int t = (int)((long long)nt * part / a.parts) + warp;
+    int t = t0 + warp;
     uint4 kx[2][kC], vx[4][kV];
     auto read_k = [&](int step) {
 #pragma unroll
@@ -179,11 +171,60 @@ __global__ void __launch_bounds__(32 * kWarps, 2) cross_rows_kernel(const Cross 
             sm[(kWarps + warp) * kRowTile + g + 8 * r] = l[r];
         }
     }
+}
+
+// Where row r of an item goes: the output, or (to a part's results) float32 and its log-sum-exp.  Four channels a thread.
+__device__ __forceinline__ void write_row(const Cross& a, int b, int h, int rr, int q0, int ch, const float* y, float lse,
+                                          long long part_row) {
+    const long long qbat = a.query_start ? 0 : b;
+    const int tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
+    if (part_row >= 0) {
+        if (ch < a.D) *reinterpret_cast<float4*>(a.part_out + part_row * a.D + ch) = make_float4(y[0], y[1], y[2], y[3]);
+        if (ch == 0) a.part_lse[part_row] = lse;
+    } else {
+        if (ch < a.D)
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh + ch) =
+                make_uint2(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]));
+        if (ch == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
+    }
+}
+
+// One row of one block's warps, added to (top's scale) sum and y.
+template <int HD>
+__device__ __forceinline__ void add_warps(const float* so, const float* sm, int r, int ch, float base, float& sum, float* y) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float f = ptx::ex2(sm[w * kRowTile + r] - base);
+        sum = fmaf(sm[(kWarps + w) * kRowTile + r], f, sum);
+        const float4 z = *reinterpret_cast<const float4*>(so + (w * kRowTile + r) * HD + ch);
+        y[0] = fmaf(z.x, f, y[0]), y[1] = fmaf(z.y, f, y[1]), y[2] = fmaf(z.z, f, y[2]), y[3] = fmaf(z.w, f, y[3]);
+    }
+}
+__device__ __forceinline__ void normalise(float top, float sum, float* y, float& lse) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    lse = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] *= inv;
+}
+
+// One item a cluster: its blocks take parts of the keys and finish a share of the rows each.
+template <int HD>
+__global__ void __launch_bounds__(32 * kWarps, 2) cross_rows_kernel(const Cross a) {
+    extern __shared__ __align__(16) float rows_smem[];
+    float *so = rows_smem, *sm = so + kWarps * kRowTile * HD;
+    const int h = blockIdx.y, part = blockIdx.z;
+    int b, row0, q0, n, k0, m;
+    tile_of<kRowTile>(a, blockIdx.x, b, row0);
+    if (b < 0) return;  // the whole cluster
+    queries_of(a, b, q0, n);
+    keys_of(a, b, k0, m);
+    const int rows = (int)min((long long)kRowTile, (long long)n * a.G - row0), nt = (m + kStep - 1) / kStep;
+    walk_keys<HD>(a, b, h, row0, rows, q0, k0, m, (int)((long long)nt * part / a.parts),
+                  (int)((long long)nt * (part + 1) / a.parts), so, sm);
     auto cluster = cg::this_cluster();
     const int peers = cluster.num_blocks(), rank = cluster.block_rank();
     if (peers > 1) cluster.sync();
     else __syncthreads();
-    // every block of the cluster finishes its share of the rows, four channels a thread
     const int per = (kRowTile + peers - 1) / peers;
     constexpr int kQuads = HD / 4;
     for (int i = threadIdx.x; i < per * kQuads; i += 32 * kWarps) {
@@ -196,35 +237,146 @@ __global__ void __launch_bounds__(32 * kWarps, 2) cross_rows_kernel(const Cross 
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ps[w * kRowTile + r]);
         }
         const float base = top == -CUDART_INF_F ? 0.f : top;
-        float sum = 0.f, y[4] = {};
-        for (int x = 0; x < peers; ++x) {
-            const float* ps = peers > 1 ? cluster.map_shared_rank(sm, x) : sm;
-            const float* po = peers > 1 ? cluster.map_shared_rank(so, x) : so;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ptx::ex2(ps[w * kRowTile + r] - base);
-                sum = fmaf(ps[(kWarps + w) * kRowTile + r], f, sum);
-                const float4 z = *reinterpret_cast<const float4*>(po + (w * kRowTile + r) * HD + ch);
-                y[0] = fmaf(z.x, f, y[0]), y[1] = fmaf(z.y, f, y[1]), y[2] = fmaf(z.z, f, y[2]), y[3] = fmaf(z.w, f, y[3]);
-            }
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum, lse = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] *= inv;
-        const int rr = row0 + r, tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
-        if (peers < a.parts) {
-            const long long total = a.query_start ? a.N : (long long)a.B * a.N;
-            const long long at = ((long long)(part / peers) * total + qbat * a.N + tok) * a.HQ + hq;
-            if (ch < a.D) *reinterpret_cast<float4*>(a.part_out + at * a.D + ch) = make_float4(y[0], y[1], y[2], y[3]);
-            if (ch == 0) a.part_lse[at] = lse;
-        } else {
-            if (ch < a.D)
-                *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh + ch) =
-                    make_uint2(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]));
-            if (ch == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
-        }
+        float sum = 0.f, y[4] = {}, lse;
+        for (int x = 0; x < peers; ++x)
+            add_warps<HD>(peers > 1 ? cluster.map_shared_rank(so, x) : so, peers > 1 ? cluster.map_shared_rank(sm, x) : sm, r,
+                          ch, base, sum, y);
+        normalise(top, sum, y, lse);
+        write_row(a, b, h, row0 + r, q0, ch, y, lse, -1);
     }
     if (peers > 1) cluster.sync();  // no block leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------- long rows: equal runs
+//
+// Every block takes an equal run of all items' 64-key chunks, in order of sequence, KV head, row tile and key, so that
+// ragged lengths balance themselves.  An item that lies in one run is finished there; of one that is cut every run
+// leaves its part in one of its two slots (0: the run's first segment, 1: its last), and the join finds them again from
+// the same counts.
+__device__ __forceinline__ long long chunks_of(const Cross& a, int b, int& tiles, int& per) {
+    int q0, n, k0, m;
+    queries_of(a, b, q0, n);
+    keys_of(a, b, k0, m);
+    tiles = (int)(((long long)n * a.G + kRowTile - 1) / kRowTile);
+    per = max(1, (m + kChunk - 1) / kChunk);  // a sequence without keys is written too
+    return (long long)tiles * per * a.H;
+}
+// The sequence that holds chunk `at` and the chunks before that sequence, or the chunks of all for at < 0; by a warp.
+__device__ __forceinline__ long long find_chunk(const Cross& a, long long at, int& b) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    b = -1;
+    for (int base = 0; base < a.B; base += 32) {
+        int tiles, per;
+        long long sum = base + lane < a.B ? chunks_of(a, base + lane, tiles, per) : 0;
+        const long long own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && before + sum > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            b = base + l;
+            return before + __shfl_sync(0xffffffffu, sum - own, l);
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return before;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kWarps, 2) cross_runs_kernel(const Cross a) {
+    extern __shared__ __align__(16) float rows_smem[];
+    float *so = rows_smem, *sm = so + kWarps * kRowTile * HD;
+    int b;
+    const long long all = find_chunk(a, -1, b);
+    const long long runs = min((long long)gridDim.x, all);  // none is empty
+    if (blockIdx.x >= runs) return;
+    long long at = all * blockIdx.x / runs;
+    const long long end = all * (blockIdx.x + 1) / runs, begin = at;
+    long long before = find_chunk(a, at, b);
+    while (at < end) {
+        int tiles, per, q0, n, k0, m;
+        const long long size = chunks_of(a, b, tiles, per);
+        if (at >= before + size) {  // the next sequence
+            before += size;
+            ++b;
+            continue;
+        }
+        queries_of(a, b, q0, n);
+        keys_of(a, b, k0, m);
+        const long long in = at - before, item = in / per;
+        const int chunk = (int)(in - item * per), h = (int)(item / tiles), row0 = (int)(item - (long long)h * tiles) * kRowTile;
+        const int take = (int)min((long long)(per - chunk), end - at);
+        const int rows = (int)min((long long)kRowTile, (long long)n * a.G - row0), nt = (m + kStep - 1) / kStep;
+        walk_keys<HD>(a, b, h, row0, rows, q0, k0, m, chunk * (kChunk / kStep), min(nt, (chunk + take) * (kChunk / kStep)), so, sm);
+        __syncthreads();
+        const long long slot = take == per ? -1 : 2 * (long long)blockIdx.x + (at != begin);
+        constexpr int kQuads = HD / 4;
+        for (int i = threadIdx.x; i < kRowTile * kQuads; i += 32 * kWarps) {
+            const int r = i / kQuads, ch = i % kQuads * 4;
+            if (r >= rows) break;
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kRowTile + r]);
+            float sum = 0.f, y[4] = {}, lse;
+            add_warps<HD>(so, sm, r, ch, top == -CUDART_INF_F ? 0.f : top, sum, y);
+            normalise(top, sum, y, lse);
+            write_row(a, b, h, row0 + r, q0, ch, y, lse, slot < 0 ? -1 : slot * kRowTile + r);
+        }
+        __syncthreads();
+        at += take;
+    }
+}
+
+// Four rows of an item a block: the parts that runs left of it, in order.
+template <int HD>
+__global__ void __launch_bounds__(4 * HD / 4) cross_runs_join_kernel(const Cross a, int blocks) {
+    const int h = blockIdx.y, lane = threadIdx.x & 31;
+    int b, row0, q0, n, none;
+    const long long all = find_chunk(a, -1, none), runs = min((long long)blocks, all);
+    tile_of<kRowTile>(a, blockIdx.x, b, row0);
+    if (b < 0) return;
+    queries_of(a, b, q0, n);
+    int tiles, per;
+    chunks_of(a, b, tiles, per);
+    long long before = 0;  // chunks of the sequences before b
+    for (int base = 0; base < b; base += 32) {
+        int x, y;
+        long long sum = base + lane < b ? chunks_of(a, base + lane, x, y) : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        before += sum;
+    }
+    const long long first = before + ((long long)h * tiles + row0 / kRowTile) * per, last = first + per - 1;
+    // run i holds the chunks [all i / runs, all (i + 1) / runs)
+    const int i0 = (int)(((first + 1) * runs - 1) / all), i1 = (int)(((last + 1) * runs - 1) / all);
+    if (i0 == i1) return;  // finished by its run
+    const int r = blockIdx.z * 4 + threadIdx.x / (HD / 4), ch = threadIdx.x % (HD / 4) * 4;
+    if (r >= min((long long)kRowTile, (long long)n * a.G - row0)) return;
+    // rows of the parts: the first run's last slot unless it begins with this item, the others' first
+    const long long lead = (2LL * i0 + (all * i0 / runs != first)) * kRowTile + r, next = (2LL * i0 + 2) * kRowTile + r;
+    const int parts = i1 - i0 + 1;
+    auto row_of = [&](int x) { return x == 0 ? lead : next + (long long)(x - 1) * 2 * kRowTile; };
+    float top = -CUDART_INF_F;
+#pragma unroll 8
+    for (int x = 0; x < parts; ++x) top = fmaxf(top, a.part_lse[row_of(x)]);
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    float sum = 0.f, y[4] = {};
+#pragma unroll 8
+    for (int x = 0; x < parts; ++x) {
+        const long long row = row_of(x);
+        const float w = exp2f((a.part_lse[row] - base) * kLog2e);
+        const float4 z = ch < a.D ? *reinterpret_cast<const float4*>(a.part_out + row * a.D + ch) : make_float4(0.f, 0.f, 0.f, 0.f);
+        sum += w;
+        y[0] = fmaf(w, z.x, y[0]), y[1] = fmaf(w, z.y, y[1]), y[2] = fmaf(w, z.z, y[2]), y[3] = fmaf(w, z.w, y[3]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] *= inv;
+    write_row(a, b, h, row0 + r, q0, ch, y, sum == 0.f ? -CUDART_INF_F : top + log2f(sum) * kLn2, -1);
 }
 
 template <int HD>
@@ -245,17 +397,30 @@ static bsa_status launch_rows(const Cross& a, int tiles, int cluster, cudaStream
     return check_launch("cross_rows_kernel");
 }
 
+template <int HD>
+static bsa_status launch_runs(const Cross& a, int tiles, int runs, cudaStream_t st) {
+    constexpr int kSmem = sizeof(float) * (kWarps * kRowTile * HD + 2 * kWarps * kRowTile);
+    cross_runs_kernel<HD><<<runs, 32 * kWarps, kSmem, st>>>(a);
+    bsa_status rc = check_launch("cross_runs_kernel");
+    if (rc != BSA_OK) return rc;
+    cross_runs_join_kernel<HD><<<dim3(tiles, a.H, kRowTile / 4), HD, 0, st>>>(a, runs);
+    return check_launch("cross_runs_join_kernel");
+}
+
 }  // namespace cross
 
-// parts: of the keys, a multiple of `cluster`; the join then has parts / cluster of them.
-bsa_status cross_rows(Cross a, int cluster, cudaStream_t st, bool* handled) {
+size_t cross_runs_bytes(int runs, int D) { return sizeof(float) * (size_t)2 * runs * cross::kRowTile * (D + 1); }
+
+// runs > 0: equal runs of all keys, and a join; otherwise one cluster of a.parts blocks an item.
+bsa_status cross_rows(const Cross& a, int runs, cudaStream_t st, bool* handled) {
     *handled = false;
     const long long tiles = row_tiles(a.B, a.N, a.G, a.query_start != nullptr, cross::kRowTile);
     uintptr_t any = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.out;
     for (long long s : {a.qb, a.qt, a.qh, a.kb, a.kt, a.kh, a.vb, a.vt, a.vh, a.ob, a.ot, a.oh}) any |= (uintptr_t)(2 * s);
     if ((any & 15) || a.M == 0 || a.H > 65535 || tiles > 0x7fffffffLL) return BSA_OK;
     *handled = true;
-    return a.D <= 64 ? cross::launch_rows<64>(a, (int)tiles, cluster, st) : cross::launch_rows<128>(a, (int)tiles, cluster, st);
+    if (runs) return a.D <= 64 ? cross::launch_runs<64>(a, (int)tiles, runs, st) : cross::launch_runs<128>(a, (int)tiles, runs, st);
+    return a.D <= 64 ? cross::launch_rows<64>(a, (int)tiles, a.parts, st) : cross::launch_rows<128>(a, (int)tiles, a.parts, st);
 }
 
 }  // namespace bsa

@@ -6,7 +6,7 @@
 // A persistent grid, one CTA per SM, 16 warps.  An item is 256 query rows (two tiles of 128: tokens x up to 64 of
 // the heads that share a KV head) against a part of one sequence's keys; both tiles read the same K and V tiles, so
 // that a key is brought from L2 once for 256 rows.  TMEM: S of the two tiles [0, 256), O behind it.
-//   warp 3      scheduler: the next item's sequence, rows and key tiles into one of two headers, their queries on their way to L2
+//   warp 3      scheduler: the next item's sequence, rows and key tiles into one of two headers
 //   warps 0, 2  producers: Q and the K ring, the V ring, by 4-D TMA boxes straight from the strided tensors (channels
 //               past D and rows past the tensor are filled with zeros).  V rows behind the sequence's last key are
 //               set to zero in shared memory: a weight of 0 times a NaN there would be NaN.
@@ -66,23 +66,25 @@ struct Params {
     float scale_log2;
     int items;
     unsigned* sched;
+    uint64_t wait_ns;   // of a bounded wait
+    int stall;          // tests only: this K tile of each CTA is not loaded, or -1
 };
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& prm) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
     while (true) {
         if (ptx::mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (ptx::globaltimer() - t0 > kWaitNs) {
+        if (ptx::globaltimer() - t0 > prm.wait_ns) {
             *abort_flag = 1;
-            raise_status(status, BSA_ERR_TIMEOUT);
+            raise_status(prm.a.status, BSA_ERR_TIMEOUT);
             return false;
         }
     }
 }
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Params& prm) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, prm));
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
@@ -91,12 +93,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-                 : "memory");
 }
 
 // 32 columns of this thread's TMEM lane, and the largest of them as floats.
@@ -162,7 +158,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     auto bar = [&](int i) { return base + L::kBar + 8u * (uint32_t)i; };
     float* inv = reinterpret_cast<float*>(sm + L::kInv);
     auto hdr = [&](int b) { return reinterpret_cast<Item*>(sm + L::kHdr) + b; };
-    int* const status = prm.a.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -208,10 +203,10 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             x.b = -1;
             while (true) {
                 int t;
-                if (prm.sched) {
+                if (prm.sched && next != (int)blockIdx.x) {  // the first item needs no ticket
                     unsigned tk = 0;
                     if (lane == 0) tk = atomicAdd(prm.sched, 1u);
-                    t = (int)__shfl_sync(0xffffffffu, tk, 0);
+                    t = (int)(gridDim.x + __shfl_sync(0xffffffffu, tk, 0));
                 } else {
                     t = next;
                     next += gridDim.x;
@@ -234,11 +229,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 x.t1 = (int)((long long)nt * (part + 1) / prm.a.parts);
                 break;
             }
-            // the item's queries on their way to L2 meanwhile: their buffers are free only just before they are needed
-            if (x.b >= 0 && x.t1 > x.t0 && lane < 2 * (HD / 64) && (lane & 1) * kBM < x.rows)
-                tma_prefetch_4d(&tm_q, 64 * (lane >> 1), x.group * prm.a.G, x.q0 + x.row / prm.a.G + (lane & 1) * (kBM / prm.a.G),
-                                x.b * prm.qbm);
-            if (it >= kHeaders && !warp_wait(bar(BAR_TFREE + it % kHeaders), (uint32_t)(it / kHeaders - 1) & 1u, abort_flag, status)) break;
+            if (it >= kHeaders && !warp_wait(bar(BAR_TFREE + it % kHeaders), (uint32_t)(it / kHeaders - 1) & 1u, abort_flag, prm)) break;
             if (lane == 0) {
                 *hdr(it % kHeaders) = x;
                 ptx::mbar_arrive(bar(BAR_TFULL + it % kHeaders));
@@ -252,16 +243,16 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int cnt = 0, ql[2] = {0, 0};
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
             const Item x = *hdr(it % kHeaders);
             if (x.b < 0) break;
             const int q0 = x.q0 + x.row / prm.a.G, h = x.group / prm.per_kv * prm.khm;
             // in the order in which they are needed and their buffers become free: K_0, Q_0, K_1, Q_1, K_2 ...
             for (int j = x.t0; j < x.t1 && ok; ++j) {
                 const int st = cnt % L::kK;
-                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kK) & 1u) ^ 1u, abort_flag, status);
+                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kK) & 1u) ^ 1u, abort_flag, prm);
                 if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && cnt != prm.stall) {
                     ptx::mbar_arrive_expect_tx(bar(BAR_FULL + st), L::kTile);
 #pragma unroll
                     for (int c = 0; c < HD / 64; ++c)
@@ -272,7 +263,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (x.rows <= w * kBM || (j != x.t0 + w && !(w == 1 && x.t1 - x.t0 == 1))) continue;
-                    if (ql[w] > 0) ok = ok && warp_wait(bar(BAR_QFREE + w), (uint32_t)(ql[w] - 1) & 1u, abort_flag, status);
+                    if (ql[w] > 0) ok = ok && warp_wait(bar(BAR_QFREE + w), (uint32_t)(ql[w] - 1) & 1u, abort_flag, prm);
                     if (!ok) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(BAR_QFULL + w), L::kTile);
@@ -290,7 +281,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (*abort_flag) {  // wait (bounded) for this warp's copies in flight
             const uint64_t t0 = ptx::globaltimer();
             auto drain = [&](int b, uint32_t ph) {
-                while (!ptx::mbar_try_wait(bar(b), ph) && ptx::globaltimer() - t0 < kWaitNs) {}
+                while (!ptx::mbar_try_wait(bar(b), ph) && ptx::globaltimer() - t0 < prm.wait_ns) {}
             };
             for (int c = max(0, cnt - L::kK); c < cnt; ++c) drain(BAR_FULL + c % L::kK, (uint32_t)(c / L::kK) & 1u);
 #pragma unroll
@@ -303,13 +294,13 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int cnt = 0, patched = 0;
         bool ok = true;
         for (int it = 0; ok; ++it) {
-            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+            if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
             const Item x = *hdr(it % kHeaders);
             if (x.b < 0) break;
             const int h = x.group / prm.per_kv * prm.vhm;
             for (int j = x.t0; j < x.t1; ++j) {
                 const int st = L::kK + cnt % L::kV, nv = x.keys - j * kBN;
-                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kV) & 1u) ^ 1u, abort_flag, status);
+                ok = warp_wait(bar(BAR_EMPTY + st), ((uint32_t)(cnt / L::kV) & 1u) ^ 1u, abort_flag, prm);
                 if (!ok) break;
                 const uint32_t dst = base + L::kRing + st * L::kTile, full = bar(nv < kBN ? BAR_RAW : BAR_FULL + st);
                 if (lane == 0) {
@@ -320,7 +311,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 ++cnt;
                 if (nv < kBN) {
-                    ok = warp_wait(full, (uint32_t)patched & 1u, abort_flag, status);
+                    ok = warp_wait(full, (uint32_t)patched & 1u, abort_flag, prm);
                     ++patched;
                     if (!ok) break;
                     for (int c = 0; c < HD / 64; ++c)
@@ -338,23 +329,23 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const uint64_t t0 = ptx::globaltimer();
             for (int c = max(0, cnt - L::kV); c < cnt; ++c)
                 while (!ptx::mbar_try_wait(bar(BAR_FULL + L::kK + c % L::kV), (uint32_t)(c / L::kV) & 1u) &&
-                       ptx::globaltimer() - t0 < kWaitNs) {
+                       ptx::globaltimer() - t0 < prm.wait_ns) {
                 }
             if (patched)
-                while (!ptx::mbar_try_wait(bar(BAR_RAW), (uint32_t)(patched - 1) & 1u) && ptx::globaltimer() - t0 < kWaitNs) {}
+                while (!ptx::mbar_try_wait(bar(BAR_RAW), (uint32_t)(patched - 1) & 1u) && ptx::globaltimer() - t0 < prm.wait_ns) {}
         }
       } else if (elect()) {
         // ------------------------------------------------------------ MMA issuer
         // One elected lane, which the compiler knows to be alone: a product then takes some 60 cycles to issue, of the
         // 64 that it runs (95 from `if (lane == 0)`; and with the whole warp in the loop every wait costs 100 more).
-        // After the last weights of row tile 0 the next item's first S of it goes ahead of row tile 1's last product,
-        // if its queries have come.
+        // What it walks is kept short, because most of it is fetched anew for each item: sending the next item's first S
+        // ahead of row tile 1's last product, and its queries to L2 ahead of that, cost more (611 us) than they gave (590).
         constexpr uint32_t idS = ptx::idesc_bf16(kBM, kBN, false), idO = ptx::idesc_bf16(kBM, HD, true);
         const uint32_t tm = tmem;
         int kc = 0, vc = 0;                // K and V tiles consumed
         int live0 = 0, live1 = 0, up0 = 0, up1 = 0;  // live items and P tiles consumed of the two row tiles
         bool ok = true;
-        auto wait = [&](int b, uint32_t ph) { return wait_bar(bar(b), ph & 1u, abort_flag, status); };
+        auto wait = [&](int b, uint32_t ph) { return wait_bar(bar(b), ph & 1u, abort_flag, prm); };
         const uint32_t lo = (base >> 4) & 0x3FFF;  // descriptors differ in their address alone, in units of 16 bytes
         auto issue_s = [&](int w, int st) {
             const uint32_t dq = lo + (uint32_t)w * (L::kTile >> 4), dk = lo + (L::kRing >> 4) + (uint32_t)st * (L::kTile >> 4);
@@ -365,10 +356,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             ptx::mma_commit(bar(BAR_SF + w));
         };
-        auto test = [&](int b, uint32_t ph) { return ptx::mbar_test_wait(bar(b), ph & 1u); };
-        constexpr int kMaxSpins = 1 << 16;
-        int spins = 0;
-        int n = 0, nw = 0, early = 0;  // key tiles and row tiles of the item; its first S that are issued already
+        int n = 0, nw = 0;  // key tiles and row tiles of the item
         auto open = [&](int it) {      // reads the published header of item it: whether there is one
             const Item* x = hdr(it % kHeaders);
             const int b = x->b;
@@ -389,12 +377,11 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         };
         ok = wait(BAR_TFULL, 0) && open(0);
         for (int it = 0; ok; ++it) {
-            for (int w = early; w < nw && n > 0 && ok; ++w) {
+            for (int w = 0; w < nw && n > 0 && ok; ++w) {
                 ok = wait(BAR_QFULL + w, (uint32_t)(w ? live1 : live0)) && (w || wait(BAR_FULL + kc % L::kK, (uint32_t)(kc / L::kK)));
                 if (ok) first_s(w);
             }
-            early = 0;
-            bool some = n > 0, opened = false, next = false;
+            const bool some = n > 0;
 #pragma unroll 1
             for (int j = 0; j < n && ok; ++j) {
                 const int vst = L::kK + vc % L::kV, kst = kc % L::kK;
@@ -404,28 +391,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 for (int w = 0; w <= last; ++w) {
                     if (w == 0) ok = wait(BAR_FULL + vst, (uint32_t)(vc / L::kV)) && (!more || wait(BAR_FULL + kst, (uint32_t)(kc / L::kK)));
                     if (j == 0 && (w ? live1 : live0) > 0) ok = ok && wait(BAR_OFREE + w, (uint32_t)((w ? live1 : live0) - 1));
-                    if (w == 1 && !more) {
-                        // while the last weights of row tile 1 are awaited: the next item's first S of row tile 0
-                        const int n_ = n, nw_ = nw;
-                        while (ok && !test(BAR_PF + 1, (uint32_t)up1)) {
-                            if (!opened && test(BAR_TFULL + (it + 1) % kHeaders, (uint32_t)((it + 1) / kHeaders))) {
-                                opened = true;
-                                next = open(it + 1);
-                            }
-                            if (!opened || !next || n == 0) break;
-                            if (test(BAR_QFULL, (uint32_t)(live0 + 1)) && test(BAR_FULL + kc % L::kK, (uint32_t)(kc / L::kK))) {
-                                first_s(0);
-                                early = 1;
-                                break;
-                            }
-                            if (*abort_flag) ok = false;
-                            if (++spins > kMaxSpins) break;  // the waits behind are bounded by time
-                        }
-                        spins = 0;
-                        if (!early) opened = false;  // read again below
-                        n = n_;
-                        nw = nw_;
-                    }
                     ok = ok && wait(BAR_PF + w, (uint32_t)(w ? up1++ : up0++));
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -461,7 +426,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         {
             ptx::mma_commit(bar(BAR_DRAIN));
             const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::globaltimer() - t0 < kWaitNs) {}
+            while (!ptx::mbar_try_wait(bar(BAR_DRAIN), 0) && ptx::globaltimer() - t0 < prm.wait_ns) {}
         }
       }
     } else if (warp < 12) {
@@ -475,7 +440,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       uint32_t r[16];
       float x[kBN];
       for (int it = 0;; ++it) {
-        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
         const Item* hd = hdr(it % kHeaders);
         if (hd->b < 0) break;
         if (hd->rows <= w * kBM) {
@@ -489,7 +454,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         bool ok = true;
         for (int j = 0; j < n; ++j, left -= kBN) {
             const int nv = left;
-            ok = warp_wait(bar(BAR_SF + w), (uint32_t)su & 1u, abort_flag, status);
+            ok = warp_wait(bar(BAR_SF + w), (uint32_t)su & 1u, abort_flag, prm);
             if (!ok) break;
             ++su;
             ptx::tc_fence_after();
@@ -560,7 +525,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (!ok) break;
         if (n > 0) {
             // the output is another warpgroup's: it gets 1 / sum, once it has read the last item's
-            if (live > 0 && !warp_wait(bar(BAR_OFREE + w), (uint32_t)(live - 1) & 1u, abort_flag, status)) break;
+            if (live > 0 && !warp_wait(bar(BAR_OFREE + w), (uint32_t)(live - 1) & 1u, abort_flag, prm)) break;
             ++live;
             inv[w * kBM + row] = l == 0.f ? 0.f : 1.f / l;
             ptx::mbar_arrive(bar(BAR_XF + w));
@@ -586,7 +551,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       int live[2] = {0, 0};
       bool ok = true;
       for (int it = 0; ok; ++it) {
-        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, status)) break;
+        if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
         const Item& hd = *hdr(it % kHeaders);
         if (hd.b < 0) break;
         const bool some = hd.t1 > hd.t0;
@@ -596,8 +561,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int at = w * kBM + row;
             float scale = 0.f;
             if (some) {
-                ok = warp_wait(bar(BAR_XF + w), (uint32_t)live[w] & 1u, abort_flag, status) &&
-                     warp_wait(bar(BAR_OF + w), (uint32_t)live[w] & 1u, abort_flag, status);
+                ok = warp_wait(bar(BAR_XF + w), (uint32_t)live[w] & 1u, abort_flag, prm) &&
+                     warp_wait(bar(BAR_OF + w), (uint32_t)live[w] & 1u, abort_flag, prm);
                 if (!ok) break;
                 ++live[w];
                 ptx::tc_fence_after();
@@ -763,6 +728,8 @@ bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled) {
     // a scale of 0 would turn a masked -inf into NaN: the smallest normal scale gives the same weights
     prm.scale_log2 = std::max(a.scale * kLog2e, 1.2e-38f);
     prm.sched = sched_counter(st);
+    prm.stall = test_stall_tile();
+    prm.wait_ns = prm.stall >= 0 ? 1000000ull : kWaitNs;
     return a.D <= 64 ? launch<64>(mq, mk, mv, prm, st, handled) : launch<128>(mq, mk, mv, prm, st, handled);
 }
 

@@ -15,6 +15,7 @@ Tolerances, from the arithmetic (u = half a step relative to the value: 2^-24 fl
   add n 2^-24, each of the parts and rescalings 2^-23 (at most n / 16 of them); the output's rounding 2^-8 or 2^-24 |o|."""
 
 import math
+import os
 
 import numpy as np
 import pytest
@@ -370,6 +371,35 @@ def test_cross_does_not_see_rows_that_do_not_count(pl, dtype, N, HQ, H, D):
     assert bool(torch.isnan(out[N:2 * N]).all())
 
 
+@pytest.mark.parametrize("HQ,H,D", [(8, 2, 128), (3, 3, 64), (4, 1, 96)])
+@pytest.mark.parametrize("n,m", [([1, 1, 1, 1], [9000, 0, 1, 4097]), ([2, 0, 1, 3, 1], [1500, 7000, 64, 63, 2000]), ([1], [20000]),
+                                 ([1] * 40, [1100 + 37 * i for i in range(40)]), ([1, 0], [3, 5000])])
+def test_cross_long_rows_in_equal_runs(pl, HQ, H, D, n, m):
+    """Ragged rows cut at 64-key borders into one run a block: whole, cut once, cut many times, without keys."""
+    starts = lambda x: torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV)  # noqa: E731
+    T, M, pad = sum(n), sum(m), 3
+    assert pl.bsa.bsa_cross_way(BF16, len(n), T + pad, M, HQ, H, D, True, True) == (2 if -(-(T + pad) // len(n)) * HQ // H <= 16 else 1)
+    q = rand(1, T + pad, HQ, D, dtype=BF16, scale=2.0)
+    k, v = rand(2, M, H, D, dtype=BF16), rand(3, M, H, D, dtype=BF16)
+    qs, ks = starts(n), starts(m)
+    out = torch.full((T + pad, HQ, D), 7.0, dtype=BF16, device=DEV)
+    lse = torch.full((T + pad, HQ), 7.0, device=DEV)
+    pl.cross_attention(q, k, v, query_start=qs, key_start=ks, out=out, lse=lse)
+    for b in range(len(n)):
+        r, c = slice(int(qs[b]), int(qs[b + 1])), slice(int(ks[b]), int(ks[b + 1]))
+        check_rows(out[r], lse[r], q[r], k[c], v[c], D ** -0.5, BF16)
+    assert bool((out[T:] == 7.0).all()) and bool((lse[T:] == 7.0).all())
+    # padded, NaN behind the lengths
+    most = max(m)
+    kp, vp = (torch.full((len(m), most, H, D), float("nan"), dtype=BF16, device=DEV) for _ in range(2))
+    for b in range(len(m)):
+        kp[b, :m[b]], vp[b, :m[b]] = k[ks[b]:ks[b + 1]], v[ks[b]:ks[b + 1]]
+    o2, l2 = pl.cross_attention(q[:T], kp, vp, query_start=qs, key_lens=torch.tensor(m, dtype=torch.int32, device=DEV))
+    for b in range(len(n)):
+        r, c = slice(int(qs[b]), int(qs[b + 1])), slice(int(ks[b]), int(ks[b + 1]))
+        check_rows(o2[r], l2[r], q[r], k[c], v[c], D ** -0.5, BF16)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 56])
 def test_cross_layouts(pl, dtype, D):
@@ -431,6 +461,44 @@ def test_cross_bad_starts_and_lengths_are_latched(pl, lib):
     out = pl.cross_attention(qp, kp, vp, key_lens=i32(16, 17, -5))[0]
     assert lib.bsa_device_status() == lib.BSA_ERR_INDEX
     assert torch.equal(out[:2], want[:2]) and not out[2].any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("stall", [0, 1, 4])
+def test_cross_expired_wait_is_reported_and_recovers(pl, lib, D, stall):
+    """A key tile that is never copied: the waits run out (after 1 ms under the switch), the kernel latches
+    BSA_ERR_TIMEOUT and ends; the next call is as before."""
+    B, N, M, H = 2, 1500, 700, 16
+    q, k, v = rand(1, B, N, H, D, dtype=BF16), rand(2, B, M, H, D, dtype=BF16), rand(3, B, M, H, D, dtype=BF16)
+    want, wl = pl.cross_attention(q, k, v)
+    os.environ["BSA_TEST_STALL_TILE"] = str(stall)
+    try:
+        pl.cross_attention(q, k, v)
+    finally:
+        os.environ.pop("BSA_TEST_STALL_TILE")
+    assert lib.bsa_device_status() == lib.BSA_ERR_TIMEOUT
+    out, lse = pl.cross_attention(q, k, v)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,M,HQ,H,D", [(2, 40, 300, 4, 2, 64), (1, 300, 130, 2, 2, 128), (3, 1, 2000, 8, 2, 128), (2, 1, 500, 4, 4, 40)])
+def test_cross_cuda_core_kernel_agrees(pl, lib, dtype, B, N, M, HQ, H, D):
+    """The kernels that the switch takes out of play, and the one that remains."""
+    q, k, v = rand(1, B, N, HQ, D, dtype=dtype), rand(2, B, M, H, D, dtype=dtype), rand(3, B, M, H, D, dtype=dtype)
+    kl = torch.tensor([M - 7 * b for b in range(B)], dtype=torch.int32, device=DEV)
+    out, lse = pl.cross_attention(q, k, v, key_lens=kl)
+    lib.bsa_cross_workspace.cache_clear()  # the plan goes by the switch
+    set_force_simt(True)
+    try:
+        assert lib.bsa_cross_way(dtype, B, N, M, HQ, H, D) == 0
+        out2, lse2 = pl.cross_attention(q, k, v, key_lens=kl)
+    finally:
+        set_force_simt(False)
+        lib.bsa_cross_workspace.cache_clear()
+    for o, z in ((out, lse), (out2, lse2)):
+        for b in range(B):
+            check_rows(o[b], z[b], q[b], k[b, :M - 7 * b], v[b, :M - 7 * b], D ** -0.5, dtype)
 
 
 @pytest.mark.parametrize("N,M", [(1, 3000), (300, 700)])
