@@ -155,38 +155,53 @@ __global__ void __launch_bounds__(256) cross_simt_kernel(const Cross a) {
 
 // ---------------------------------------------------------------- join
 //
-// A warp a row: out = sum_p exp(lse_p - L) out_p, L = log sum_p exp(lse_p), in the order of the parts.
+// A warp a row, four channels a lane: out = sum_p exp(lse_p - L) out_p, L = log sum_p exp(lse_p), in the order of the
+// parts.  (With eight rows a warp one after the other it took longer than what it joins.)
+constexpr int kJoinRows = 8;  // a block
+
 template <typename T>
-__global__ void __launch_bounds__(256) cross_join_kernel(const Cross a) {
+__global__ void __launch_bounds__(32 * kJoinRows) cross_join_kernel(const Cross a) {
     const int lane = threadIdx.x & 31, h = blockIdx.y;
     int b, row0, q0, n;
-    tile_of<kSimtRows>(a, blockIdx.x, b, row0);
+    tile_of<kJoinRows>(a, blockIdx.x, b, row0);
     if (b < 0) return;
     queries_of(a, b, q0, n);
-    const long long total = a.query_start ? a.N : (long long)a.B * a.N, rows = (long long)n * a.G;
-    const long long step = total * a.HQ, qbat = a.query_start ? 0 : b;
-    for (long long r = row0 + (threadIdx.x >> 5); r < min(rows, (long long)row0 + kSimtRows); r += 8) {
-        const int tok = q0 + (int)(r / a.G), hq = h * a.G + (int)(r % a.G);
-        const long long i = ((a.query_start ? 0 : (long long)b * a.N) + tok) * a.HQ + hq;
-        float top = -CUDART_INF_F;
-        for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.part_lse[p * step + i]);
-        const float ref = top == -CUDART_INF_F ? 0.f : top;
-        float sum = 0.f, acc[4] = {};
-        for (int p = 0; p < a.parts; ++p) {
-            const long long at = p * step + i;
-            const float w = exp2f((a.part_lse[at] - ref) * kLog2e);
-            sum += w;
+    const long long r = row0 + (threadIdx.x >> 5);
+    if (r >= (long long)n * a.G) return;
+    const int tok = q0 + (int)(r / a.G), hq = h * a.G + (int)(r % a.G), ch = 4 * lane;
+    const long long total = a.query_start ? a.N : (long long)a.B * a.N, step = total * a.HQ, qbat = a.query_start ? 0 : b;
+    const long long i = (qbat * a.N + tok) * a.HQ + hq;
+    const bool wide = a.D % 4 == 0;
+    float top = -CUDART_INF_F;
+#pragma unroll 8
+    for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.part_lse[p * step + i]);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float sum = 0.f, y[4] = {};
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p) {
+        const float* x = a.part_out + (p * step + i) * a.D + ch;
+        float z[4] = {};
+        if (wide) {
+            if (ch < a.D) {
+                const float4 v = *reinterpret_cast<const float4*>(x);
+                z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+            }
+        } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (lane + 32 * c < a.D) acc[c] = fmaf(w, a.part_out[at * a.D + lane + 32 * c], acc[c]);
+            for (int e = 0; e < 4; ++e)
+                if (ch + e < a.D) z[e] = x[e];
         }
-        T* o = (T*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float w = exp2f((a.part_lse[p * step + i] - ref) * kLog2e);
+        sum += w;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (lane + 32 * c < a.D) o[lane + 32 * c] = from_f32<T>(acc[c] * inv);
-        if (lane == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum) * kLn2;
+        for (int e = 0; e < 4; ++e) y[e] = fmaf(w, z[e], y[e]);
     }
+    T* o = (T*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh + ch;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (ch + e < a.D) o[e] = from_f32<T>(y[e] * inv);
+    if (lane == 0 && a.lse) a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum) * kLn2;
 }
 
 // ---------------------------------------------------------------- host side
@@ -310,9 +325,9 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     if (!handled && rc == BSA_OK)
         rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
     if (rc != BSA_OK || p.parts == 1) return rc;  // runs join by themselves
-    const dim3 grid((unsigned)a.tiles, H);
-    if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 256, 0, st>>>(a);
-    else cross_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    const dim3 grid((unsigned)row_tiles(B, N, a.G, query_start != nullptr, kJoinRows), H);
+    if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 32 * kJoinRows, 0, st>>>(a);
+    else cross_join_kernel<__nv_bfloat16><<<grid, 32 * kJoinRows, 0, st>>>(a);
     return check_launch("cross_join_kernel");
 }
 

@@ -347,7 +347,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         bool ok = true;
         auto wait = [&](int b, uint32_t ph) { return wait_bar(bar(b), ph & 1u, abort_flag, prm); };
         const uint32_t lo = (base >> 4) & 0x3FFF;  // descriptors differ in their address alone, in units of 16 bytes
-        auto issue_s = [&](int w, int st) {
+        auto issue_s = [&](int w, int st) {  // S of row tile w
             const uint32_t dq = lo + (uint32_t)w * (L::kTile >> 4), dk = lo + (L::kRing >> 4) + (uint32_t)st * (L::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
@@ -356,71 +356,51 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             ptx::mma_commit(bar(BAR_SF + w));
         };
-        int n = 0, nw = 0;  // key tiles and row tiles of the item
-        auto open = [&](int it) {      // reads the published header of item it: whether there is one
-            const Item* x = hdr(it % kHeaders);
-            const int b = x->b;
-            n = x->t1 - x->t0;
-            nw = x->rows > kBM ? 2 : 1;
-            return b >= 0;
+        auto issue_pv = [&](int w, int st, bool add) {
+            const uint32_t dv = lo + (L::kRing >> 4) + (uint32_t)st * (L::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+                ptx::mma_ts(tm + 256 + (uint32_t)w * HD, tm + (uint32_t)w * 128 + kk * 8, desc(dv + (kk * 2048 >> 4), kHalf),
+                            idO, (add || kk > 0) ? 1u : 0u);
         };
-        // S of the item's first key tile for row tile w
-        auto first_s = [&](int w) {
-            const int kst = kc % L::kK;
-            ptx::tc_fence_after();
-            {
-                issue_s(w, kst);
-                if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + kst));
-                if (n == 1) ptx::mma_commit(bar(BAR_QFREE + w));
-            }
-            kc += w == nw - 1;
-        };
-        ok = wait(BAR_TFULL, 0) && open(0);
         for (int it = 0; ok; ++it) {
-            for (int w = 0; w < nw && n > 0 && ok; ++w) {
-                ok = wait(BAR_QFULL + w, (uint32_t)(w ? live1 : live0)) && (w || wait(BAR_FULL + kc % L::kK, (uint32_t)(kc / L::kK)));
-                if (ok) first_s(w);
-            }
-            const bool some = n > 0;
+            if (!wait(BAR_TFULL + it % kHeaders, (uint32_t)(it / kHeaders))) break;
+            const Item* x = hdr(it % kHeaders);
+            if (x->b < 0) break;
+            const int n = x->t1 - x->t0, nw = x->rows > kBM ? 2 : 1;
+            // step -1: S of the first key tile; step j: P V of tile j, then S of tile j + 1
 #pragma unroll 1
-            for (int j = 0; j < n && ok; ++j) {
+            for (int j = -1; j < n && n > 0; ++j) {
                 const int vst = L::kK + vc % L::kV, kst = kc % L::kK;
                 const bool more = j + 1 < n;
-                const int last = nw - 1;
 #pragma unroll 1
-                for (int w = 0; w <= last; ++w) {
-                    if (w == 0) ok = wait(BAR_FULL + vst, (uint32_t)(vc / L::kV)) && (!more || wait(BAR_FULL + kst, (uint32_t)(kc / L::kK)));
+                for (int w = 0; w < nw; ++w) {
+                    if (j < 0) ok = wait(BAR_QFULL + w, (uint32_t)(w ? live1 : live0));
+                    if (w == 0) ok = ok && (j < 0 || wait(BAR_FULL + vst, (uint32_t)(vc / L::kV))) &&
+                                     (!more || wait(BAR_FULL + kst, (uint32_t)(kc / L::kK)));
                     if (j == 0 && (w ? live1 : live0) > 0) ok = ok && wait(BAR_OFREE + w, (uint32_t)((w ? live1 : live0) - 1));
-                    ok = ok && wait(BAR_PF + w, (uint32_t)(w ? up1++ : up0++));
+                    if (j >= 0) ok = ok && wait(BAR_PF + w, (uint32_t)(w ? up1++ : up0++));
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    {
-                        const uint32_t dv = lo + (L::kRing >> 4) + (uint32_t)vst * (L::kTile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < kBN / 16; ++kk)
-                            ptx::mma_ts(tm + 256 + (uint32_t)w * HD, tm + (uint32_t)w * 128 + kk * 8,
-                                        desc(dv + (kk * 2048 >> 4), kHalf), idO, (j > 0 || kk > 0) ? 1u : 0u);
-                        if (w == last) ptx::mma_commit(bar(BAR_EMPTY + vst));
-                        if (more) {
-                            issue_s(w, kst);
-                            if (w == last) ptx::mma_commit(bar(BAR_EMPTY + kst));
-                            if (j + 2 == n) ptx::mma_commit(bar(BAR_QFREE + w));
-                        } else {
-                            ptx::mma_commit(bar(BAR_OF + w));
-                        }
+                    if (j >= 0) {
+                        issue_pv(w, vst, j > 0);
+                        if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + vst));
+                        if (!more) ptx::mma_commit(bar(BAR_OF + w));
                     }
-                        }
+                    if (more) {
+                        issue_s(w, kst);
+                        if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + kst));
+                        if (j + 2 == n) ptx::mma_commit(bar(BAR_QFREE + w));
+                    }
+                }
                 if (!ok) break;
-                ++vc;
+                vc += j >= 0;
                 kc += more;
             }
             if (!ok) break;
-            if (some) {
-                ++live0;
-                live1 += nw - 1;
-            }
+            live0 += n > 0;
+            live1 += n > 0 && nw == 2;
             ptx::mbar_arrive(bar(BAR_TFREE + it % kHeaders));
-            ok = wait(BAR_TFULL + (it + 1) % kHeaders, (uint32_t)((it + 1) / kHeaders)) && open(it + 1);
         }
         // nothing that this warp issued may still run when TMEM is freed
         {
@@ -530,8 +510,9 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             inv[w * kBM + row] = l == 0.f ? 0.f : 1.f / l;
             ptx::mbar_arrive(bar(BAR_XF + w));
         }
-        if ((a.parts > 1 || a.lse) && w * kBM + row < hd->rows) {
-            const RowAt p = row_at(a, *hd, w * kBM + row);
+        const int at = w * kBM + row;
+        if ((a.parts > 1 || a.lse) && at < hd->rows) {
+            const RowAt p = row_at(a, *hd, at);
             const float lse = l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
             if (a.parts > 1) a.part_lse[p.part] = lse;
             else a.lse[p.batch * a.lb + p.tok * a.lt + p.hq * a.lh] = lse;
@@ -554,11 +535,11 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
         const Item& hd = *hdr(it % kHeaders);
         if (hd.b < 0) break;
-        const bool some = hd.t1 > hd.t0;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             if (!ok || hd.rows <= w * kBM) break;
             const int at = w * kBM + row;
+            const bool some = hd.t1 > hd.t0;
             float scale = 0.f;
             if (some) {
                 ok = warp_wait(bar(BAR_XF + w), (uint32_t)live[w] & 1u, abort_flag, prm) &&

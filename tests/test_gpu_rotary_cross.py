@@ -400,6 +400,29 @@ def test_cross_long_rows_in_equal_runs(pl, HQ, H, D, n, m):
         check_rows(o2[r], l2[r], q[r], k[c], v[c], D ** -0.5, BF16)
 
 
+@pytest.mark.parametrize("HQ,H,D", [(8, 2, 128), (3, 3, 64), (12, 1, 96)])
+@pytest.mark.parametrize("n,m", [([40, 33, 17, 64], [1200, 0, 100, 1285]), ([128, 1, 0, 30, 90], [128, 129, 900, 257, 1500]),
+                                 ([20], [9000]), ([31] * 9, [512 + 131 * i for i in range(9)]), ([250, 3, 5, 7], [700, 3, 2000, 640])])
+def test_cross_few_tokens_over_long_states(pl, HQ, H, D, n, m):
+    """Half-filled row tiles over parts of the keys: none, one, two, many key tiles, masked last ones."""
+    starts = lambda x: torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV)  # noqa: E731
+    T, M = sum(n), sum(m)
+    assert pl.bsa.bsa_cross_way(BF16, len(n), T, M, HQ, H, D, True, True) == 1
+    q = rand(1, T, HQ, D, dtype=BF16, scale=2.0)
+    k, v = rand(2, M, H, D, dtype=BF16), rand(3, M, H, D, dtype=BF16)
+    qs, ks = starts(n), starts(m)
+    out, lse = pl.cross_attention(q, k, v, query_start=qs, key_start=ks)
+    most = max(m)
+    kp, vp = (torch.full((len(m), most, H, D), float("nan"), dtype=BF16, device=DEV) for _ in range(2))
+    for b in range(len(m)):
+        kp[b, :m[b]], vp[b, :m[b]] = k[ks[b]:ks[b + 1]], v[ks[b]:ks[b + 1]]
+    o2, l2 = pl.cross_attention(q, kp, vp, query_start=qs, key_lens=torch.tensor(m, dtype=torch.int32, device=DEV))
+    for o, z in ((out, lse), (o2, l2)):
+        for b in range(len(n)):
+            r, c = slice(int(qs[b]), int(qs[b + 1])), slice(int(ks[b]), int(ks[b + 1]))
+            check_rows(o[r], z[r], q[r], k[c], v[c], D ** -0.5, BF16)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("D", [64, 128, 56])
 def test_cross_layouts(pl, dtype, D):
