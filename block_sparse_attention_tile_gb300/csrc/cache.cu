@@ -773,6 +773,7 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
     BSA_REQUIRE(cache && (T == 0 || (k && v && slots && cos_table && sin_table)), "rotated append: null pointer");
     BSA_REQUIRE(T == 0 || (k_val == nullptr) == (v_val == nullptr), "rotated append: k_val and v_val come together");
     BSA_REQUIRE(T == 0 || (q == nullptr) == (q_out == nullptr), "rotated append: q and q_out come together");
+    BSA_REQUIRE(!q || q != q_out, "rotated append: q_out must not be q");
     BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "rotated append: dtype");
     BSA_REQUIRE(T >= 0 && H > 0 && n_pages > 0, "rotated append: sizes out of range (T=%d H=%d n_pages=%d)", T, H, n_pages);
     BSA_REQUIRE(page_size_ok(page_size), "rotated append: page_size must be a power of two in 16..1024, got %d", page_size);

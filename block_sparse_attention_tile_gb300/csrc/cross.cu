@@ -244,9 +244,10 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
     return p;
 }
 
-static bool cross_sizes_ok(int B, int N, int M, int HQ, int H, int D) {
-    return B >= 0 && N >= 0 && M >= 0 && HQ >= 1 && H >= 1 && HQ <= 65535 && HQ % H == 0 && D >= 1 && D <= 128 &&
-           (long long)B * std::max(N, 1) <= INT_MAX && (long long)N * (HQ / H) * (long long)std::max(B, 1) <= INT_MAX / 2;
+static bool cross_sizes_ok(int B, int N, int M, int HQ, int H, int D, bool packed_q) {
+    if (B < 0 || N < 0 || M < 0 || HQ < 1 || H < 1 || HQ > 65535 || HQ % H || D < 1 || D > 128) return false;
+    const long long rows = (packed_q ? 1LL : std::max(B, 1)) * (long long)N;  // and with the heads of a KV head
+    return rows <= INT_MAX && rows * (HQ / H) <= INT_MAX / 2 && B <= INT_MAX / 2;
 }
 
 static size_t part_bytes(const CrossPlan& p, int B, int N, int HQ, int D, bool packed_q) {
@@ -273,13 +274,13 @@ extern "C" {
 
 size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries,
                            int packed_keys) {
-    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D) || B == 0 || N == 0) return 0;
+    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D, packed_queries != 0) || B == 0 || N == 0) return 0;
     return part_bytes(cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0), B, N, HQ, D,
                       packed_queries != 0);
 }
 
 int bsa_cross_way(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries, int packed_keys) {
-    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D) || B == 0 || N == 0) return -1;
+    if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D, packed_queries != 0) || B == 0 || N == 0) return -1;
     return cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0).way;
 }
 
@@ -288,7 +289,7 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
                          const int32_t* key_lens, float scale, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, void* stream) {
     BSA_REQUIRE(dtype == BSA_F32 || dtype == BSA_BF16, "cross attention: dtype");
-    BSA_REQUIRE(cross_sizes_ok(B, N, M, HQ, H, D), "cross attention: sizes out of range (B=%d N=%d M=%d HQ=%d H=%d D=%d)",
+    BSA_REQUIRE(cross_sizes_ok(B, N, M, HQ, H, D, query_start != nullptr), "cross attention: sizes out of range (B=%d N=%d M=%d HQ=%d H=%d D=%d)",
                 B, N, M, HQ, H, D);
     BSA_REQUIRE(strides, "cross attention: null strides");
     BSA_REQUIRE(!(key_start && key_lens), "cross attention: key_start and key_lens exclude each other");

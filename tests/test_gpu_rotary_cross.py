@@ -299,7 +299,7 @@ def check_rows(o, lse, q, k, v, scale, dtype):
 SHAPES = [  # B, N, M, HQ, H, D
     (1, 1, 1, 1, 1, 64), (2, 1, 7, 8, 1, 128), (3, 5, 130, 4, 2, 64), (1, 129, 128, 2, 2, 128), (2, 257, 300, 3, 1, 64),
     (1, 300, 1000, 16, 1, 128), (2, 40, 77, 24, 8, 80), (1, 3, 4000, 4, 1, 128), (1, 17, 65, 5, 5, 40), (2, 9, 33, 6, 2, 7),
-    (1, 64, 512, 48, 3, 96), (1, 600, 129, 4, 4, 16), (4, 16, 2050, 16, 8, 64), (1, 2, 1, 128, 1, 128), (2, 70, 10, 2, 1, 1)]
+    (1, 64, 512, 48, 3, 96), (1, 40, 300, 2, 2, 8), (2, 1, 90, 3, 1, 8), (1, 600, 129, 4, 4, 16), (4, 16, 2050, 16, 8, 64), (1, 2, 1, 128, 1, 128), (2, 70, 10, 2, 1, 1)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -465,6 +465,43 @@ def test_cross_extreme_logits(pl, N):
         out, lse = pl.cross_attention(q, k, v, scale=0.0)
         check_rows(out[0], lse[0], q[0], k[0], v[0], 0.0, dtype)
         assert np.allclose(f64(lse), math.log(M), atol=1e-5)
+
+
+@pytest.mark.parametrize("N,M", [(1, 131072), (200, 131072), (3, 1 << 20), (2000, 65536)])
+def test_cross_long_sums_of_one_sign(pl, N, M):
+    """Values of 1 over equal keys: sums of products of one sign, which the tensor cores round towards zero, stay within
+    an output's rounding of 1."""
+    H, D = 2, 128
+    q, k = rand(1, 1, N, H, D, dtype=BF16), rand(2, 1, M, H, D, dtype=BF16, scale=0.05)
+    out, lse = pl.cross_attention(q, k, torch.ones_like(k))
+    assert float((out.float() - 1).abs().max()) <= 2.0 ** -8
+    want = torch.logsumexp((q[0, :1, 0].double() @ k[0, :, 0].double().T) * D ** -0.5, 1)
+    assert float((lse[0, :1, 0].double() - want).abs().max()) <= 2.0 ** -18 * math.log(M) + M * 2.0 ** -24 / 16
+
+
+@pytest.mark.parametrize("dtype,N,M", [(BF16, 1, 300), (BF16, 150, 300), (F32, 3, 100), (BF16, 1, 2000)])
+def test_cross_offsets_past_32_bits(pl, dtype, N, M):
+    """Sequences more than 2^32 bytes apart in one buffer, in every argument."""
+    B, H, D = 2, 2, 64
+    far = (1 << 31) + 64
+    big = torch.empty(far + 4 * max(N, M) * H * D, dtype=dtype, device=DEV)
+    at = [0]
+
+    def place(x):
+        y = big.as_strided(x.shape, (far, *x.stride()[1:]), at[0])
+        at[0] += x[0].numel()
+        return y.copy_(x)
+    q, k, v = (rand(i, B, n, H, D, dtype=dtype) for i, n in ((1, N), (2, M), (3, M)))
+    want, wl = pl.cross_attention(q, k, v)
+    out = place(torch.zeros_like(q))
+    got, lse = pl.cross_attention(place(q), place(k), place(v), out=out)
+    assert torch.equal(got, want) and torch.equal(lse, wl)
+    cos, sin = tables(1, N, D // 2)
+    rot = pl.rotate(q, k[:, :N], cos, sin)
+    at[0] = 0
+    a, b = place(q), place(k[:, :N].contiguous())
+    pl.rotate(a, b, cos, sin, out=(a, b))
+    assert torch.equal(a, rot[0]) and torch.equal(b, rot[1])
 
 
 def test_cross_bad_starts_and_lengths_are_latched(pl, lib):

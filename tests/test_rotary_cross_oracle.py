@@ -166,12 +166,12 @@ def test_arguments_are_refused(bsa):
         assert rotate(**kw) == bad and word in bsa.bsa_last_error(), kw
     assert rotate(T=0, q=None) == bsa.BSA_OK and rotate(B=0, q=None) == bsa.BSA_OK
 
-    def append(T=4, D=64, P=32, q=16, q_out=16, HQ=4, q_stride=256, cos=16, page=16, k_val=16, v_val=16):
+    def append(T=4, D=64, P=32, q=16, q_out=32, HQ=4, q_stride=256, cos=16, page=16, k_val=16, v_val=16):
         return lib.bsa_cache_append_rotated(16, 16, 1, T, 2, D, 128, 128, 16, 16, 4, page, None, None, k_val, v_val, cos,
                                             16, P, 0, q, HQ, q_stride, q_out, None)
     for kw, word in ((dict(P=33), "P=33"), (dict(cos=None), "null"), (dict(q_out=None), "come together"),
                      (dict(q_stride=255), "stride"), (dict(HQ=0), "HQ"), (dict(D=72), "D must"), (dict(page=24), "page"),
-                     (dict(v_val=None), "come together")):
+                     (dict(v_val=None), "come together"), (dict(q_out=16), "must not be q")):
         assert append(**kw) == bad and word in bsa.bsa_last_error(), kw
     assert append(T=0) == bsa.BSA_OK
 
@@ -185,3 +185,6 @@ def test_arguments_are_refused(bsa):
     assert cross(N=0) == bsa.BSA_OK and cross(B=0) == bsa.BSA_OK
     assert bsa.bsa_cross_workspace(torch.bfloat16, 2, 4, 100000, 4, 2, 64, False, False) > 0
     assert bsa.bsa_cross_workspace(torch.bfloat16, 2, 4, 8, 3, 2, 64, False, False) == 0
+    # 2^30 padded rows with their heads are too many, the same tokens packed are not
+    assert bsa.bsa_cross_way(torch.bfloat16, 4096, 65536, 64, 64, 4, 128) == -1
+    assert bsa.bsa_cross_way(torch.bfloat16, 4096, 65536, 1 << 20, 64, 4, 128, True, True) >= 0
