@@ -109,6 +109,19 @@ __device__ __forceinline__ void ld32_max(uint32_t taddr, uint32_t* r, float& top
         : "memory");
 }
 
+// Columns from `first` on of this thread's row of S become -inf, in TMEM: rare, and a few instructions of the softmax's
+// straight code where a select for each of a row's 128 registers would be as long as the rest of it.
+__device__ __forceinline__ void hide_columns(uint32_t tS, int first) {
+    uint32_t none[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) none[e] = 0xff800000u;
+#pragma unroll 1
+    for (; first & 15; ++first) asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(tS + first), "r"(none[0]) : "memory");
+#pragma unroll 1
+    for (; first < kBN; first += 16) ptx::tmem_st16(tS + first, none);
+    ptx::tmem_wait_st();
+}
+
 // A shared-memory matrix descriptor (128-byte swizzle, stride 1024) from its address in units of 16 bytes.
 __device__ __forceinline__ uint64_t desc(uint32_t addr16, uint32_t lbo_bytes) {
     uint64_t d;
@@ -438,6 +451,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             ++su;
             ptx::tc_fence_after();
+            if (nv < kBN) hide_columns(tS, nv);
             // maxima of raw Q.K come with the load: scale once (scale > 0 keeps the order)
             float mx;
             {
@@ -450,14 +464,6 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 ptx::tmem_wait_ld();
                 mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             }
-            if (nv < kBN) {
-                mx = -CUDART_INF_F;
-#pragma unroll
-                for (int c = 0; c < kBN; ++c) {
-                    x[c] = c < nv ? x[c] : -CUDART_INF_F;
-                    mx = fmaxf(mx, x[c]);
-                }
-            }
             mx *= prm.scale_log2;
             const float m_new = fmaxf(m_ref, mx);
             const bool need = m_new > m_ref + kRescaleThreshold;
@@ -467,7 +473,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 l *= alpha;
                 if (j > 0) {
                     // S_j was issued after the last product added to O: O is complete here
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < HD / 16; ++c) {
                         ptx::tmem_ld16(tO + c * 16, r);
                         ptx::tmem_wait_ld();
@@ -551,7 +557,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             const uint32_t tO = tmem + lane_off + 256 + HD * w;
             float* po = a.parts > 1 && at < hd.rows ? a.part_out + row_at(a, hd, at).part * a.D : nullptr;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
                 uint32_t r[32];
                 if (some) {

@@ -12,14 +12,15 @@ namespace bsa {
 // ---------------------------------------------------------------- a15 table
 //
 // A frequency is held as turns a position in units of 2^-64, so the angle's fraction of a turn is the low 64
-// bits of an integer product: exact for any position, where a float32 product would have lost the angle of
+// bits of an integer product, of which the upper 32 are kept: exact to 2^-32 turns for any position, where a float32 product would have lost the angle of
 // position 2^24 altogether.  The upper 32 bits are cut into quadrant and remainder, and only the
 // remainder, an eighth of a turn at most, becomes a float.  Its sine and cosine are the first five and six terms of
 // their series: what is left out is below 2e-9 of the one and 4e-11 of the other.
 // A thread keeps the frequencies of four neighbouring pairs (one, where P is odd to four) and walks the tokens.  The writes
 // bound it, 8 bytes a pair.
-__device__ __forceinline__ void cos_sin(uint64_t turn, float factor, float& c, float& s) {
-    const uint32_t t = (uint32_t)((turn + 0x80000000ull) >> 32);  // 2^-32 turns
+__device__ __forceinline__ void cos_sin(uint32_t high, uint32_t low, int32_t pos, float factor, float& c, float& s) {
+    // 2^-32 turns: the product's upper half, of an unsigned and a signed factor
+    const uint32_t t = high * (uint32_t)pos + __umulhi(low, (uint32_t)pos) - (pos < 0 ? low : 0u);
     const uint32_t quad = (t + (1u << 29)) >> 30;
     const float x = (float)(int32_t)(t - (quad << 30)) * 0x1p-31f;  // half turns, |x| <= 1/4
     constexpr double kPi = 3.14159265358979323846, kPi2 = kPi * kPi;
@@ -34,8 +35,9 @@ __device__ __forceinline__ void cos_sin(uint64_t turn, float factor, float& c, f
     cs = fmaf(cs, y, (float)(-kPi2 / 2));
     cs = fmaf(cs, y, 1.f);
     const float a = quad & 1 ? sn : cs, b = quad & 1 ? cs : sn;
-    c = a * ((quad + 1) & 2 ? -factor : factor);
-    s = b * (quad & 2 ? -factor : factor);
+    // minus signs: of the cosine in quadrants 1 and 2, of the sine in 2 and 3
+    c = __uint_as_float(__float_as_uint(a * factor) ^ (quad + 1) >> 1 << 31);
+    s = __uint_as_float(__float_as_uint(b * factor) ^ quad >> 1 << 31);
 }
 
 template <int V>
@@ -46,29 +48,34 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const int32_t* __rest
                                                            int T, int* status) {
     const int per = P / V, tokens = 256 / per;  // threads a token, tokens a block
     const int p = (int)(threadIdx.x % per) * V;
-    uint64_t f[V];
+    uint32_t high[V], low[V];
     int ax[V];
+    bool one = true;  // all pairs go by the same axis
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        f[j] = (uint64_t)turns[p + j];
+        high[j] = (uint32_t)((uint64_t)turns[p + j] >> 32);
+        low[j] = (uint32_t)turns[p + j];
         ax[j] = axis ? axis[p + j] : 0;
         if ((unsigned)ax[j] >= (unsigned)axes) {
             raise_status(status, BSA_ERR_INDEX);
             ax[j] = 0;
         }
+        one = one && ax[j] == ax[0];
     }
     if ((int)threadIdx.x >= tokens * per) return;
     for (long long t = (long long)blockIdx.x * tokens + threadIdx.x / per; t < T; t += (long long)gridDim.x * tokens) {
         float c[V], s[V];
+        const int32_t* at = positions + t * axes;
+        const int32_t at0 = at[ax[0]];
 #pragma unroll
-        for (int j = 0; j < V; ++j) cos_sin(f[j] * (uint64_t)(int64_t)positions[t * axes + ax[j]], factor, c[j], s[j]);
-        const long long at = t * P + p;
+        for (int j = 0; j < V; ++j) cos_sin(high[j], low[j], one ? at0 : at[ax[j]], factor, c[j], s[j]);
+        const long long to = t * P + p;
         if constexpr (V == 4) {
-            *reinterpret_cast<float4*>(cos_out + at) = make_float4(c[0], c[1], c[2], c[3]);
-            *reinterpret_cast<float4*>(sin_out + at) = make_float4(s[0], s[1], s[2], s[3]);
+            *reinterpret_cast<float4*>(cos_out + to) = make_float4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<float4*>(sin_out + to) = make_float4(s[0], s[1], s[2], s[3]);
         } else {
-            cos_out[at] = c[0];
-            sin_out[at] = s[0];
+            cos_out[to] = c[0];
+            sin_out[to] = s[0];
         }
     }
 }
