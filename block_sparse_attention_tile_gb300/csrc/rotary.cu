@@ -63,12 +63,25 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const int32_t* __rest
         one = one && ax[j] == ax[0];
     }
     if ((int)threadIdx.x >= tokens * per) return;
-    for (long long t = (long long)blockIdx.x * tokens + threadIdx.x / per; t < T; t += (long long)gridDim.x * tokens) {
-        float c[V], s[V];
+    const long long stride = (long long)gridDim.x * tokens;
+    int32_t next[V];  // the next token's positions, read while this one's angles are taken
+    auto read = [&](long long t) {
+        if (t >= T) return;
         const int32_t* at = positions + t * axes;
-        const int32_t at0 = at[ax[0]];
+        next[0] = at[ax[0]];
 #pragma unroll
-        for (int j = 0; j < V; ++j) cos_sin(high[j], low[j], one ? at0 : at[ax[j]], factor, c[j], s[j]);
+        for (int j = 1; j < V; ++j) next[j] = one ? next[0] : at[ax[j]];
+    };
+    const long long first = (long long)blockIdx.x * tokens + threadIdx.x / per;
+    read(first);
+    for (long long t = first; t < T; t += stride) {
+        float c[V], s[V];
+        int32_t pos[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) pos[j] = next[j];
+        read(t + stride);
+#pragma unroll
+        for (int j = 0; j < V; ++j) cos_sin(high[j], low[j], pos[j], factor, c[j], s[j]);
         const long long to = t * P + p;
         if constexpr (V == 4) {
             *reinterpret_cast<float4*>(cos_out + to) = make_float4(c[0], c[1], c[2], c[3]);
@@ -201,7 +214,7 @@ bsa_status bsa_rotary_table(const int32_t* positions, int T, int axes, const int
     if (T == 0) return BSA_OK;
     const bool wide = P % 4 == 0 && (((uintptr_t)cos_out | (uintptr_t)sin_out) & 15) == 0;
     const int tokens = 256 / (wide ? P / 4 : P);
-    const unsigned grid = (unsigned)std::min<long long>(((long long)T + tokens - 1) / tokens, 152 * 16);
+    const unsigned grid = (unsigned)std::min<long long>(((long long)T + tokens - 1) / tokens, 152 * 5);
     cudaStream_t st = as_stream(stream);
     if (wide)
         rotary_table_kernel<4><<<grid, 256, 0, st>>>(positions, axes, turns, axis, P, factor, cos_out, sin_out, T,
