@@ -213,34 +213,45 @@ struct CrossPlan {
     int runs;     // way 2, long rows: equal runs of all keys instead
 };
 
-constexpr int kWant = 8, kLeast = 128;
-constexpr int kLongRow = 1024;  // keys
+constexpr int kAtOnce = 2 * 152;  // blocks of the 16-row kernels that run at once
+constexpr int kLongRow = 1024;    // keys
 
+// Which kernel, and how the keys are cut.  Only sizes that the host knows: a batch's average stands for its sequences.
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
     CrossPlan p{};
     const int G = HQ / H, Gt = cross_tc_heads(G);
     const long long rows = (packed_q ? (N + B - 1) / B : (long long)N) * G;  // of a sequence and KV head, on average
     const long long keys = packed_k ? (M + B - 1) / B : M;
-    long long items;
-    p.cluster = 1;
-    if (cross_tc_sizes(dtype, D) && rows <= (keys > kLongRow ? 16 : 31)) {
+    const long long few = row_tiles(B, N, G, packed_q, 16) * H;              // items of 16 rows
+    p.parts = p.cluster = 1;
+    // Up to 16 rows the 16-row kernels.  Short rows, inputs in L2: 64 requests of 4 rows over 700 states 16 us against the
+    // 256-row kernel's 23, 30 of 10 over 400 (D = 64) 7 against 15.  Long ones, L2 overwritten: 8 ragged requests of 1024 to
+    // 32768 keys 100 against 185, since equal runs balance what whole items do not.  Where all lengths are the same the
+    // 256-row kernel would be the faster (8 of 4096 keys 42 against 48, one of 131072 78 against 88), but the lengths are
+    // on the device.  17 to 31 rows are two tiles, which read the keys twice: only for short rows whose blocks all run at
+    // once (8 requests of 24 rows over 300 states 9 against 12; but 64 over 700 33 against 23, 8 over 4096 52 against 32).
+    if (cross_tc_sizes(dtype, D) && (rows <= 16 || (rows < 32 && keys <= kLongRow && few <= kAtOnce))) {
         p.way = 2;
-        items = row_tiles(B, N, G, packed_q, 16) * H;
-        // blocks of 128 keys or more, and no more of them than run at once (two an SM): 8 requests of 8 heads over up to
-        // 600 keys take 7.7 us in clusters of 4, 14.4 in clusters of 8
-        while (p.cluster < 8 && p.cluster * 128 < keys && 2 * p.cluster * items <= 2 * 152) p.cluster *= 2;
-        p.parts = 1;
-        // runs of four 64-key chunks or more
-        if (keys > kLongRow && items < 4 * 152)
-            p.runs = (int)std::min<long long>((D <= 64 ? 3 : 2) * 152, std::max<long long>(1, items * keys / 256));
+        // Clusters of blocks of 128 keys or more, no more blocks than run at once: 8 requests of 8 heads and 600 keys
+        // take 16.5 us in clusters of 4 (L2 overwritten), 17.5 in 2, 19.6 alone, 23.7 in 8
+        while (p.cluster < 8 && p.cluster * 128 < keys && 2 * p.cluster * few <= kAtOnce) p.cluster *= 2;
+        // Long rows: equal runs of four 64-key chunks or more (the 8 ragged requests: 100 us, in clusters of 8 124, whole
+        // 491); with rows enough to fill the card twice they are left whole (256 of 1500 keys x 16 heads, D = 64: 278 us
+        // against 323)
+        if (keys > kLongRow && few < 2 * kAtOnce)
+            p.runs = (int)std::min<long long>((D <= 64 ? 3 : 2) * 152, std::max<long long>(1, few * keys / 256));
     } else if (cross_tc_sizes(dtype, D)) {
         p.way = 1;
-        items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
+        // as many parts as leave every SM an item, of two key tiles or more: more of them cost more to start and to join than
+        // they balance (8 requests of 64 rows over 4096 states: 44 us with 2 parts, 47 with 4, 50 with 8, 54 whole)
+        const long long items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
         p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
     } else {
         p.way = dtype == BSA_F32 && !force_simt() ? 3 : 0;
-        items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
-        p.parts = (int)std::max<long long>(1, std::min<long long>({kWant * 152 / std::max(items, 1LL), (keys + kLeast - 1) / kLeast, 64}));
+        // several blocks an SM, of 128 keys or more (float32, 4096 x 4096 x 8 heads: 1495 us in 2 parts, 1685 whole,
+        // 1488 in 4)
+        const long long items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
+        p.parts = (int)std::max<long long>(1, std::min<long long>({8 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
     }
     return p;
 }
