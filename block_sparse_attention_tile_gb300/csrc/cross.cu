@@ -258,6 +258,7 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
 
 static bool cross_sizes_ok(int B, int N, int M, int HQ, int H, int D, bool packed_q) {
     if (B < 0 || N < 0 || M < 0 || HQ < 1 || H < 1 || HQ > 65535 || HQ % H || D < 1 || D > 128) return false;
+    if (M > INT_MAX / 2) return false;  // a tile may end past the last state
     const long long rows = (packed_q ? 1LL : std::max(B, 1)) * (long long)N;  // and with the heads of a KV head
     return rows <= INT_MAX && rows * (HQ / H) <= INT_MAX / 2 && B <= INT_MAX / 2;
 }

@@ -25,10 +25,10 @@
  *    that expired) are latched in a device status word; bsa_device_status()
  *    synchronises the stream, returns that status and clears it.
  *  - The tensor-core attention kernels (bsa_fwd_qouter, bsa_fwd_summary and
- *    bsa_fwd_qouter_tokens with bf16, D = 128, and bsa_fwd_cache_tokens with
- *    block lists of many rows) are persistent grids that take
- *    their work items from a counter pair the library keeps per (device,
- *    stream) in static device memory (64 streams per device; further streams
+ *    bsa_fwd_qouter_tokens with bf16, D = 128, bsa_fwd_cross with bf16, and
+ *    bsa_fwd_cache_tokens with block lists of many rows) are persistent grids
+ *    that take their work items from a counter pair the library keeps per
+ *    (device, stream) in static device memory (64 streams per device; further streams
  *    take a static schedule).  Launches on one stream run in order and each
  *    leaves its pair at zero.  A launch made while its stream is being
  *    captured into a CUDA graph takes the static schedule instead, so a
@@ -580,9 +580,9 @@ bsa_status bsa_fwd_cache_tokens(const void* q, bsa_dtype dtype, int T, int HQ, i
  * each token turn.  Pair i of token t turns by 2 pi times the fraction of
  *   positions[t, axis[i]] * turns[i] / 2^64,
  * turns being the frequency in units of 2^-64 turns a position (a frequency of f
- * radians is round(f / 2 pi * 2^64)): the product is exact, so a position of any size, negative ones
- * too, keeps its angle.  cos_out, sin_out [T, P] = factor * cos, factor * sin (factor: 1, or the
- * attention factor of a stretched context).
+ * radians is round(f / 2 pi * 2^64)): the product is exact, so a position of any
+ * size, negative ones too, keeps its angle.  cos_out, sin_out [T, P] = factor *
+ * cos, factor * sin (factor: 1, or the attention factor of a stretched context).
  * positions: [device] int32 [T, axes] (axes <= 8: one for text, t / y / x for a
  * video); turns: [device] int64 [P]; axis: [device] int32 [P], or NULL with one
  * axis (an axis outside [0, axes) latches BSA_ERR_INDEX and is read as 0);
@@ -648,10 +648,13 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * BSA_ERR_INDEX and counts as empty; a length outside [0, M] is clamped and latched.
  * strides: [host] int64 [5][3]: batch, token and head stride of q, k, v, out and
  * lse in elements (channels are adjacent; a batch stride is not used where the rows are packed; strides of 0
- * broadcast k and v).  lse: [device] float or NULL.  1 <= D <= 128, scale >= 0.
+ * broadcast k and v).  lse: [device] float or NULL.  1 <= D <= 128, scale >= 0,
+ * M < 2^30.
  * query_start, key_start, key_lens: [device] int32.
  * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
- * between calls.  Deterministic. */
+ * between calls.  Deterministic for the same sizes and
+ * flags.  bf16 takes the softmax's weights to bf16 before the product with V (so do the other bf16 kernels); float32
+ * keeps float32's accuracy, but an infinite element in a row that counts gives NaN. */
 /* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
  * tiles of 16 rows, 3 tensor cores in float32 (1 and 2: addresses and strides that are no multiples of 16 bytes take 0
  * all the same); -1 for sizes out of range. */

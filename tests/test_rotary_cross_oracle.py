@@ -188,3 +188,13 @@ def test_arguments_are_refused(bsa):
     # 2^30 padded rows with their heads are too many, the same tokens packed are not
     assert bsa.bsa_cross_way(torch.bfloat16, 4096, 65536, 64, 64, 4, 128) == -1
     assert bsa.bsa_cross_way(torch.bfloat16, 4096, 65536, 1 << 20, 64, 4, 128, True, True) >= 0
+
+
+def test_cross_sizes_whose_tiles_would_pass_32_bits_are_refused(bsa):
+    """A tile's end may lie past the last state; it has to stay within 32 bits."""
+    for dtype, D in ((torch.bfloat16, 64), (torch.bfloat16, 7), (torch.float32, 64)):
+        for packed in (False, True):
+            assert bsa.bsa_cross_way(dtype, 2, 1, 2 ** 30 - 1, 1, 1, D, packed, packed) >= 0
+            for M in (2 ** 30, 2 ** 31 - 1):
+                assert bsa.bsa_cross_way(dtype, 2, 1, M, 1, 1, D, packed, packed) == -1
+                assert bsa.bsa_cross_workspace(dtype, 2, 1, M, 1, 1, D, packed, packed) == 0
