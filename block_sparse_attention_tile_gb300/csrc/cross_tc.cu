@@ -15,7 +15,7 @@
 //   warps 4-7, 8-11  softmax of row tile 0 and 1, one row a thread: running maximum (O is rescaled only when it grows
 //               by more than 2^8) and sum, the weights back to TMEM as bf16.
 //   warps 12-15 output: O times 1 / sum to global memory while the softmax is at the next item.
-// The products bound it where the keys are many (16384 tokens x 16384 keys: 1600 TFLOP/s at D = 128, 82% of the measured
+// The products bound it where the keys are many (38912 tokens x 2 heads x 16384 keys: 1600 TFLOP/s at D = 128, 82% of the measured
 // matrix rate, and 1108 at D = 64, where a key's exponentials take as long as its products); where they are few (115200
 // tokens x 512 keys: 571 us, 371 of it products) the items' starts, outputs and changes of queries are the rest.
 // Every wait is bounded (2 s): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
