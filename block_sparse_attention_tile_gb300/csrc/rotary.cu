@@ -140,59 +140,96 @@ static void start_rotate(const Rotate& a, dim3 grid, cudaStream_t st) {
     else rotate_kernel<T, kLanes, false, false><<<grid, 256, 0, st>>>(a);
 }
 
-// Any D up to 256, any number of pairs, any strides: a warp a row, a channel a lane at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) rotate_any_kernel(const Rotate a, long long rows) {
-    const int lane = threadIdx.x & 31, heads = a.set[0].heads + a.set[1].heads;
-    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * 8) {
-        const long long tok = i / heads, b = tok / a.T, t = tok - b * a.T;
-        int h = (int)(i - tok * heads);
-        const int n = h >= a.set[0].heads;
-        if (n) h -= a.set[0].heads;
-        const RowSet& r = a.set[n];
-        const T* x = (const T*)r.x + b * r.xb + t * r.xt + h * r.xh;
-        T* y = (T*)r.y + b * r.yb + t * r.yt + h * r.yh;
-        const float *cs = a.cos + b * a.table_batch + t * a.P, *sn = a.sin + b * a.table_batch + t * a.P;
-        float norm = 1.f, out[8];
-        if (r.weight) {
-            float ss = 0.f;
-            for (int c = lane; c < a.D; c += 32) ss = fmaf(to_f32(x[c]), to_f32(x[c]), ss);
-            norm = rsqrtf(warp_sum(ss) / a.D + a.eps);
-        }
+// Any D up to 256, any number of pairs, any strides: a channel a lane at a time (kJ of them), a token's heads by a warp,
+// whose table entries, weights and partners' places stay in registers over them.  The rows of two heads are read before
+// the first of them is written (y may be x).  Its instructions bound it (issue slots 66%, L2 14%): 115200 tokens of
+// 24 + 24 heads of 128 bf16 channels, 63 pairs, with a norm take 1325 us, interleaved 1535 (a warp a row 3470 and 4145,
+// four heads at a time 1900 and 1970, at 64 registers 1545 and 1874), where the wide kernel takes 489 for 64 pairs;
+// float32, D = 64, 66% of the copy rate.  64 tokens of 64 + 4 heads take 5.2, and 4.4 with a warp a row: the host's call
+// is three times that.
+template <typename T, int kJ>
+__global__ void __launch_bounds__(256) rotate_any_kernel(const Rotate a) {
+    constexpr int kBatch = 2;
+    const int lane = threadIdx.x & 31;
+    const RowSet& r = a.set[blockIdx.y];
+    int other[kJ];
+    bool first[kJ];
+    float w[kJ], wo[kJ];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = lane + 32 * j;
-            if (c >= a.D) break;
-            const auto at = [&](int ch) { return r.weight ? to_f32(x[ch]) * (norm * r.weight[ch]) : to_f32(x[ch]); };
-            float v = at(c);
-            if (c < 2 * a.P) {
-                const bool first = a.interleaved ? !(c & 1) : c < a.P;
-                const int p = a.interleaved ? c >> 1 : first ? c : c - a.P;
-                const float o = at(a.interleaved ? c ^ 1 : first ? c + a.P : c - a.P), s = a.transpose ? -sn[p] : sn[p];
-                v = first ? __fsub_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, s)) : __fadd_rn(__fmul_rn(v, cs[p]), __fmul_rn(o, s));
+    for (int j = 0; j < kJ; ++j) {
+        const int ch = lane + 32 * j;
+        first[j] = a.interleaved ? !(ch & 1) : ch < a.P;
+        other[j] = ch >= 2 * a.P ? ch : a.interleaved ? ch ^ 1 : first[j] ? ch + a.P : ch - a.P;
+        w[j] = r.weight && ch < a.D ? r.weight[ch] : 1.f;
+        wo[j] = r.weight && ch < a.D ? r.weight[other[j]] : 1.f;
+    }
+    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < a.items; i += (long long)gridDim.x * 8) {
+        const long long tok = a.splits > 1 ? i / a.splits : i, b = tok < a.T ? 0 : tok / a.T, t = tok - b * a.T;
+        const int part = (int)(i - tok * a.splits);
+        const long long at = b * a.table_batch + t * a.P;
+        float c[kJ], s[kJ];  // s: with the sign of the sum, -fl(x s) being fl(x (-s))
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int ch = lane + 32 * j;
+            if (ch >= 2 * a.P) continue;
+            const int p = a.interleaved ? ch >> 1 : first[j] ? ch : ch - a.P;
+            c[j] = a.cos[at + p];
+            s[j] = first[j] != a.transpose ? -a.sin[at + p] : a.sin[at + p];
+        }
+        const int h0 = (int)((long long)r.heads * part / a.splits), h1 = (int)((long long)r.heads * (part + 1) / a.splits);
+        const T* x = (const T*)r.x + b * r.xb + t * r.xt;
+        T* y = (T*)r.y + b * r.yb + t * r.yt;
+        for (int h = h0; h < h1; h += kBatch) {
+            float v[kBatch][kJ], o[kBatch][kJ];
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    v[n][j] = o[n][j] = 0.f;
+                    if (h + n < h1 && lane + 32 * j < a.D) {
+                        v[n][j] = to_f32(x[(h + n) * r.xh + lane + 32 * j]);
+                        o[n][j] = to_f32(x[(h + n) * r.xh + other[j]]);
+                    }
+                }
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                if (h + n >= h1) break;
+                if (r.weight) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) ss = fmaf(v[n][j], v[n][j], ss);
+                    const float norm = rsqrtf(warp_sum(ss) / a.D + a.eps);
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) v[n][j] *= norm * w[j], o[n][j] *= norm * wo[j];
+                }
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int ch = lane + 32 * j;
+                    if (ch >= a.D) break;
+                    const float z = ch < 2 * a.P ? __fadd_rn(__fmul_rn(v[n][j], c[j]), __fmul_rn(o[n][j], s[j])) : v[n][j];
+                    y[(h + n) * r.yh + ch] = from_f32<T>(z);
+                }
             }
-            out[j] = v;
         }
-        __syncwarp();  // y may be x
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (lane + 32 * j < a.D) y[lane + 32 * j] = from_f32<T>(out[j]);
     }
 }
 
 template <typename T>
 static bsa_status launch_rotate(Rotate& a, long long tokens, bool wide, cudaStream_t st) {
-    const int heads = a.set[0].heads + a.set[1].heads;
     const auto blocks = [](long long warps) { return (unsigned)std::min<long long>((warps + 7) / 8, 152 * 64); };
-    if (!wide) {
-        rotate_any_kernel<T><<<blocks(tokens * heads), 256, 0, st>>>(a, tokens * heads);
-        return check_launch("rotate_any_kernel");
-    }
-    const int lanes = row_lanes(a.D), steps = (std::max(a.set[0].heads, a.set[1].heads) * lanes + 31) / 32;  // of a token
+    const int most = std::max(a.set[0].heads, a.set[1].heads), lanes = row_lanes(a.D);
+    const int steps = wide ? (most * lanes + 31) / 32 : (most + 1) / 2;  // of a token
     // a share of the heads to a warp where there are few tokens
     a.splits = (int)std::max<long long>(1, std::min<long long>(steps, 152 * 32 / std::max<long long>(tokens, 1)));
     a.items = tokens * a.splits;
     const dim3 grid(blocks(a.items), a.set[1].heads ? 2 : 1);
+    if (!wide) {
+        if (a.D <= 64) rotate_any_kernel<T, 2><<<grid, 256, 0, st>>>(a);
+        else if (a.D <= 128) rotate_any_kernel<T, 4><<<grid, 256, 0, st>>>(a);
+        else rotate_any_kernel<T, 8><<<grid, 256, 0, st>>>(a);
+        return check_launch("rotate_any_kernel");
+    }
     if (lanes == 4) start_rotate<T, 4>(a, grid, st);
     else if (lanes == 8) start_rotate<T, 8>(a, grid, st);
     else if (lanes == 16) start_rotate<T, 16>(a, grid, st);
