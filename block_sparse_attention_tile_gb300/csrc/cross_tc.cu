@@ -38,6 +38,13 @@ constexpr int kThreads = 512;
 constexpr int kMaxStages = 6;            // K and V tiles in flight, at most
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// The tensor cores cut off what they add to O: by up to 2^-23 of it at each of a key tile's eight products, which does not
+// average out over values of one sign (unsplit 2^20 keys came out 5e-3 short).  Every so many key tiles the sums are
+// therefore put aside, and those are added up rounded: 1e-4 at most, whatever the number of keys.  Only calls whose states
+// could be that long get the code for it, which makes the softmax's loop longer (D = 64, 6 x 4001 queries over up to 1024
+// states: 82 us with it, 78.5 without).
+constexpr int kAside = 128;
+static_assert((kAside & (kAside - 1)) == 0, "kAside is a mask");
 constexpr int kRegsLow = 64, kRegsHigh = 176, kRegsOut = 96, kRegsLaunch = 128;  // setmaxnreg (x 128 / 256 / 128 threads)
 static_assert(128 * kRegsLow + 256 * kRegsHigh + 128 * kRegsOut <= kThreads * kRegsLaunch, "register split exceeds the launch");
 constexpr uint32_t kHalf = kBN * 64 * 2;  // 128 rows x 64 channels
@@ -160,7 +167,7 @@ __device__ __forceinline__ RowAt row_at(const Cross& a, const Item& x, int at) {
     return p;
 }
 
-template <int HD>
+template <int HD, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
 cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const Params prm) {
@@ -442,7 +449,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (j >= 0) {
-                        issue_pv(w, vst, j > 0);
+                        issue_pv(w, vst, kLong ? (j & (kAside - 1)) != 0 : j > 0);
                         if (w == nw - 1) ptx::mma_commit(bar(BAR_EMPTY + vst));
                         if (!more) ptx::mma_commit(bar(BAR_OF + w));
                     }
@@ -478,6 +485,7 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       int su = 0, live = 0;  // S tiles, live items
       uint32_t r[16];
       float x[kBN];
+      [[maybe_unused]] float aside[kLong ? HD : 1];  // in local memory
       for (int it = 0;; ++it) {
         if (!warp_wait(bar(BAR_TFULL + it % kHeaders), (uint32_t)(it / kHeaders) & 1u, abort_flag, prm)) break;
         const Item* hd = hdr(it % kHeaders);
@@ -490,7 +498,9 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const int n = hd->t1 - hd->t0;
         int left = hd->keys - hd->t0 * kBN;  // keys from the current tile on
         float m_ref = -CUDART_INF_F, l = 0.f;
+        [[maybe_unused]] float m_aside = -CUDART_INF_F, l_aside = 0.f;
         bool ok = true;
+        [[maybe_unused]] const auto from_aside = [&] { return m_aside == -CUDART_INF_F ? 0.f : ptx::ex2(m_aside - m_ref); };
         for (int j = 0; j < n; ++j, left -= kBN) {
             const int nv = left;
             ok = warp_wait(bar(BAR_SF + w), (uint32_t)su & 1u, abort_flag, prm);
@@ -530,6 +540,19 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     ptx::tmem_wait_st();
                 }
             }
+            if (kLong && j > 0 && (j & (kAside - 1)) == 0) {  // the next product begins O anew
+                const float f = from_aside();
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                    ptx::tmem_ld16(tO + c * 16, r);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) aside[c * 16 + e] = __uint_as_float(r[e]) + (j == kAside ? 0.f : aside[c * 16 + e] * f);
+                }
+                l_aside = fmaf(l_aside, f, l);
+                l = 0.f;
+                m_aside = m_ref;
+            }
             const bool some = m_ref != -CUDART_INF_F;
             const float sc = some ? prm.scale_log2 : 1.f, ref = some ? m_ref : 0.f;
             const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
@@ -556,6 +579,22 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         if (!ok) break;
         if (n > 0) {
+            if (kLong && n > kAside) {
+                if (!warp_wait(bar(BAR_OF + w), (uint32_t)live & 1u, abort_flag, prm)) break;
+                ptx::tc_fence_after();
+                const float f = from_aside();
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                    ptx::tmem_ld16(tO + c * 16, r);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(fmaf(aside[c * 16 + e], f, __uint_as_float(r[e])));
+                    ptx::tmem_st16(tO + c * 16, r);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                l = fmaf(l_aside, f, l);
+            }
             // the output is another warpgroup's: it gets 1 / sum, once it has read the last item's
             if (live > 0 && !warp_wait(bar(BAR_OFREE + w), (uint32_t)(live - 1) & 1u, abort_flag, prm)) break;
             ++live;
@@ -703,25 +742,25 @@ static bool make_map(CUtensorMap* m, const void* ptr, int D, int heads, long lon
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD>
+template <int HD, bool kLong>
 static bsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& prm,
                          cudaStream_t st, bool* handled) {
     static int fits = 0;  // 0 unknown, 1 fits, -1 does not: setmaxnreg.inc would wait for registers
     if (!fits) {
         cudaFuncAttributes a;
-        fits = (cudaFuncGetAttributes(&a, cross_tc_kernel<HD>) == cudaSuccess &&
+        fits = (cudaFuncGetAttributes(&a, cross_tc_kernel<HD, kLong>) == cudaSuccess &&
                 a.numRegs * kThreads >= 128 * kRegsLow + 256 * kRegsHigh + 128 * kRegsOut) ? 1 : -1;
     }
     if (fits < 0) return BSA_OK;
     *handled = true;
-    cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(cross_tc_kernel<HD, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem<HD>::kBytes);
     if (e != cudaSuccess) return fail(BSA_ERR_CUDA, "cross attention attribute: %s", cudaGetErrorString(e));
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         return fail(BSA_ERR_CUDA, "cross attention: device query failed");
-    cross_tc_kernel<HD><<<std::min(prm.items, sms), kThreads, Smem<HD>::kBytes, st>>>(mq, mk, mv, prm);
+    cross_tc_kernel<HD, kLong><<<std::min(prm.items, sms), kThreads, Smem<HD>::kBytes, st>>>(mq, mk, mv, prm);
     return check_launch("cross_tc_kernel");
 }
 
@@ -763,7 +802,9 @@ bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled) {
     prm.sched = sched_counter(st);
     prm.stall = test_stall_tile();
     prm.wait_ns = prm.stall >= 0 ? 1000000ull : kWaitNs;
-    return a.D <= 64 ? launch<64>(mq, mk, mv, prm, st, handled) : launch<128>(mq, mk, mv, prm, st, handled);
+    const bool longs = ((a.M + kBN - 1) / kBN + a.parts - 1) / a.parts > kAside;  // key tiles that an item may have
+    if (a.D <= 64) return longs ? launch<64, true>(mq, mk, mv, prm, st, handled) : launch<64, false>(mq, mk, mv, prm, st, handled);
+    return longs ? launch<128, true>(mq, mk, mv, prm, st, handled) : launch<128, false>(mq, mk, mv, prm, st, handled);
 }
 
 }  // namespace bsa
