@@ -28,6 +28,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kRowTile = 16, kStep = 16, kWarps = 4;
 constexpr int kChunk = kStep * kWarps;
+// The tensor cores cut off what they add to a sum, which over values of one sign does not average out (outputs between 1 and 2
+// over 2^21 keys, 2^19 a warp, were 6e-3 off, 4e-3 of it the output's rounding): every so many steps a warp puts its sums
+// aside, into the shared memory that they are joined in, and those are added up rounded.
+constexpr int kAside = 1024;
 constexpr float kGrow = 8.f;  // log2 units: the running maximum is raised, and O rescaled, only when it grows by more
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -90,88 +94,105 @@ __device__ __forceinline__ void walk_keys(const Cross& a, int b, int h, int row0
         for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     read_k(t);
     read_v(t);
-    for (; t < t1; t += kWarps) {
-        float s[2][4] = {};
+    bool first = true;  // nothing put aside
+    for (int stop = min(t1, t0 + kAside * kWarps);; stop = min(t1, stop + kAside * kWarps)) {
+        for (; t < stop; t += kWarps) {
+            float s[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < kC; ++i)
+            for (int i = 0; i < kC; ++i)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                mma16816(s[u], qa[2 * i], kx[u][i].x, kx[u][i].y);
-                mma16816(s[u], qa[2 * i + 1], kx[u][i].z, kx[u][i].w);
+                for (int u = 0; u < 2; ++u) {
+                    mma16816(s[u], qa[2 * i], kx[u][i].x, kx[u][i].y);
+                    mma16816(s[u], qa[2 * i + 1], kx[u][i].z, kx[u][i].w);
+                }
+            read_k(t + kWarps);
+            if (t * kStep + kStep > m) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t * kStep + 8 * u + 2 * c + (e & 1) >= m) s[u][e] = -CUDART_INF_F;
             }
-        read_k(t + kWarps);
-        if (t * kStep + kStep > m) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t * kStep + 8 * u + 2 * c + (e & 1) >= m) s[u][e] = -CUDART_INF_F;
-        }
-        float now[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            now[r] = fmaxf(ref[r], x * scale);
-        }
-        if (__any_sync(0xffffffffu, now[0] > ref[0] + kGrow || now[1] > ref[1] + kGrow)) {
+            float now[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const bool up = now[r] > ref[r] + kGrow;  // the same in a row's four lanes
-                const float alpha = up ? ptx::ex2(ref[r] - now[r]) : 1.f;
-                if (up) ref[r] = now[r];
-                l[r] *= alpha;
+                float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                now[r] = fmaxf(ref[r], x * scale);
+            }
+            if (__any_sync(0xffffffffu, now[0] > ref[0] + kGrow || now[1] > ref[1] + kGrow)) {
 #pragma unroll
-                for (int j = 0; j < 8 * kV; ++j) {
-                    o[j][2 * r] *= alpha;
-                    o[j][2 * r + 1] *= alpha;
+                for (int r = 0; r < 2; ++r) {
+                    const bool up = now[r] > ref[r] + kGrow;  // the same in a row's four lanes
+                    const float alpha = up ? ptx::ex2(ref[r] - now[r]) : 1.f;
+                    if (up) ref[r] = now[r];
+                    l[r] *= alpha;
+#pragma unroll
+                    for (int j = 0; j < 8 * kV; ++j) {
+                        o[j][2 * r] *= alpha;
+                        o[j][2 * r + 1] *= alpha;
+                    }
                 }
             }
+            uint32_t p[4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float base = ref[r] == -CUDART_INF_F ? 0.f : ref[r];
+                float w[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) w[2 * u + e] = ptx::ex2(fmaf(s[u][2 * r + e], scale, -base));
+                l[r] += (w[0] + w[1]) + (w[2] + w[3]);
+                p[r] = ptx::pack_bf16x2(w[0], w[1]);
+                p[2 + r] = ptx::pack_bf16x2(w[2], w[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const uint32_t* x[4] = {&vx[0][i].x, &vx[1][i].x, &vx[2][i].x, &vx[3][i].x};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int sel = j & 1 ? 0x7632 : 0x5410;
+                    mma16816(o[8 * i + j], p, __byte_perm(x[0][j >> 1], x[1][j >> 1], sel), __byte_perm(x[2][j >> 1], x[3][j >> 1], sel));
+                }
+            }
+            read_v(t + kWarps);
         }
-        uint32_t p[4];
+
+        // the warps' parts: product j's columns 2c, 2c + 1 are channels 8 (2c) + j and 8 (2c + 1) + j of a run of 64
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const float base = ref[r] == -CUDART_INF_F ? 0.f : ref[r];
-            float w[4];
+            const int row = warp * kRowTile + g + 8 * r;
+            const float was = first ? -CUDART_INF_F : sm[row], f = was == -CUDART_INF_F ? 0.f : ptx::ex2(was - ref[r]);
+            __syncwarp();  // all have read what c = 0 writes
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            float* to = so + row * HD;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < kV; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) w[2 * u + e] = ptx::ex2(fmaf(s[u][2 * r + e], scale, -base));
-            l[r] += (w[0] + w[1]) + (w[2] + w[3]);
-            p[r] = ptx::pack_bf16x2(w[0], w[1]);
-            p[2 + r] = ptx::pack_bf16x2(w[2], w[3]);
-        }
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const uint32_t* x[4] = {&vx[0][i].x, &vx[1][i].x, &vx[2][i].x, &vx[3][i].x};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int sel = j & 1 ? 0x7632 : 0x5410;
-                mma16816(o[8 * i + j], p, __byte_perm(x[0][j >> 1], x[1][j >> 1], sel), __byte_perm(x[2][j >> 1], x[3][j >> 1], sel));
+                    for (int j = 0; j < 8; j += 4) {
+                        float4& at = *reinterpret_cast<float4*>(to + 64 * i + 8 * (2 * c + e) + j);
+                        const float4 x = first ? make_float4(0.f, 0.f, 0.f, 0.f) : at;
+                        at = make_float4(fmaf(x.x, f, o[8 * i + j][2 * r + e]), fmaf(x.y, f, o[8 * i + j + 1][2 * r + e]),
+                                         fmaf(x.z, f, o[8 * i + j + 2][2 * r + e]), fmaf(x.w, f, o[8 * i + j + 3][2 * r + e]));
+                    }
+            if (c == 0) {
+                sm[row] = ref[r];
+                sm[kWarps * kRowTile + row] = first ? l[r] : fmaf(sm[kWarps * kRowTile + row], f, l[r]);
             }
+            l[r] = 0.f;
         }
-        read_v(t + kWarps);
-    }
-
-    // the warps' parts: product j's columns 2c, 2c + 1 are channels 8 (2c) + j and 8 (2c + 1) + j of a run of 64
+        if (t >= t1) break;
+        first = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        float* to = so + (warp * kRowTile + g + 8 * r) * HD;
+        for (int j = 0; j < 8 * kV; ++j)
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int j = 0; j < 8; j += 4)
-                    *reinterpret_cast<float4*>(to + 64 * i + 8 * (2 * c + e) + j) =
-                        make_float4(o[8 * i + j][2 * r + e], o[8 * i + j + 1][2 * r + e], o[8 * i + j + 2][2 * r + e], o[8 * i + j + 3][2 * r + e]);
-        if (c == 0) {
-            sm[warp * kRowTile + g + 8 * r] = ref[r];
-            sm[(kWarps + warp) * kRowTile + g + 8 * r] = l[r];
-        }
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        __syncwarp();
     }
 }
 

@@ -77,3 +77,19 @@ def moving_maxima(pl, dtype, B, N, M, HQ, H, D):
 @pytest.mark.parametrize("D", [64, 128])
 def test_moving_maxima_256_rows(pl, D):
     moving_maxima(pl, BF16, 1, 19712, 40013, 1, 1, D)
+
+
+@pytest.mark.parametrize("HQ,D", [(1, 64), (4, 128)])
+@pytest.mark.parametrize("M", [1 << 19, (1 << 21) + 77])
+def test_unsplit_long_sums_16_rows(pl, HQ, D, M):
+    B = 640  # twice what runs at once: the rows are left whole, a quarter of the keys to a warp
+    assert pl.bsa.bsa_cross_way(BF16, B, 1, M, HQ, 1, D) == 2
+    assert pl.bsa.bsa_cross_workspace(BF16, B, 1, M, HQ, 1, D, False, False) == 0
+    out, mean = equal_keys(pl, BF16, B, 1, M, HQ, 1, D)
+    most = off(out, mean)
+    assert most <= 2.0 ** -8 + 2 * (2048 + M / 16384 + 8) * U
+
+
+@pytest.mark.parametrize("HQ,D", [(1, 64), (4, 128)])
+def test_moving_maxima_16_rows(pl, HQ, D):
+    moving_maxima(pl, BF16, 640, 1, 150013, HQ, 1, D)
