@@ -21,6 +21,10 @@ namespace bsa {
 namespace cross {
 
 constexpr int kFRows = 64, kFKeys = 32;  // the products take four column tiles of 8 at a time
+// Key tiles whose sums are added up in registers: equal terms, and so equal roundings, would take 2^19 keys 2e-4 off.  After
+// as many the sums are put aside, in the output's place, and those are added up (kLong, for calls whose states could be
+// that long: the code for it costs 2 to 5%).
+constexpr int kFAside = 128;
 
 struct Split { uint32_t hi, lo; };
 __device__ __forceinline__ Split split(float x) {
@@ -54,7 +58,7 @@ __device__ __forceinline__ void copy_in(float* dst, const float* src, bool on) {
 }
 
 // HD: channels padded to 64 or 128; kBytes: 16 where rows can be copied by 16 bytes, else 4.
-template <int HD, int kBytes>
+template <int HD, int kBytes, bool kLong>
 __global__ void __launch_bounds__(128, HD == 64 ? 3 : 2) cross_f32_kernel(const Cross a) {
     constexpr int ld = HD + 4, kN = kBytes / 4, kTile = kFKeys * ld;
     extern __shared__ __align__(16) float f32_smem[];
@@ -93,107 +97,129 @@ __global__ void __launch_bounds__(128, HD == 64 ? 3 : 2) cross_f32_kernel(const 
     fetch(t);
     const float scale = fmaxf(a.scale * kLog2e, 1.2e-38f);  // 0 would turn a masked -inf into NaN
     float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f}, o[HD / 8][4] = {};
-    for (; t < t1; ++t) {
-        fetch(t + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
-        const float *K = KV + (t & 1) * 2 * kTile, *V = K + kTile, *Q = Qs + (16 * warp) * ld;
-        float s[kFKeys / 8][4] = {};
+    float m_aside[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_aside[2] = {0.f, 0.f};
+    bool first = true;  // nothing put aside
+    for (int stop = kLong ? min(t1, t + kFAside) : t1;; stop = min(t1, stop + kFAside)) {
+        for (; t < stop; ++t) {
+            fetch(t + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            const float *K = KV + (t & 1) * 2 * kTile, *V = K + kTile, *Q = Qs + (16 * warp) * ld;
+            float s[kFKeys / 8][4] = {};
 #pragma unroll 4
-        for (int d = 0; d < HD; d += 8) {
-            const Split x[4] = {split(Q[g * ld + d + c]), split(Q[(g + 8) * ld + d + c]), split(Q[g * ld + d + c + 4]),
-                                split(Q[(g + 8) * ld + d + c + 4])};
-            Split y[4][2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) y[j][e] = split(K[(8 * j + g) * ld + d + c + 4 * e]);
-            mma3x4(s, x, y);
-        }
-        const int left = m - t * kFKeys;
-        Split p[kFKeys / 8][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float top = -CUDART_INF_F;
-#pragma unroll
-            for (int j = 0; j < kFKeys / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& x = s[j][2 * r + e];
-                    x = 8 * j + 2 * c + e < left ? x * scale : -CUDART_INF_F;
-                    top = fmaxf(top, x);
-                }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float now = fmaxf(mx[r], top), ref = now == -CUDART_INF_F ? 0.f : now, alpha = exp2f(mx[r] - ref);
-            mx[r] = now;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < kFKeys / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float w = exp2f(s[j][2 * r + e] - ref);
-                    sum += w;
-                    p[j][2 * e + r] = split(w);
-                }
-            l[r] = l[r] * alpha + sum;
-#pragma unroll
-            for (int j = 0; j < HD / 8; ++j) {
-                o[j][2 * r] *= alpha;
-                o[j][2 * r + 1] *= alpha;
-            }
-        }
-#pragma unroll
-        for (int j0 = 0; j0 < HD / 8; j0 += 4) {
-            float y[4][4] = {};
-#pragma unroll
-            for (int i = 0; i < kFKeys / 8; ++i) {
-                Split w[4][2];
+            for (int d = 0; d < HD; d += 8) {
+                const Split x[4] = {split(Q[g * ld + d + c]), split(Q[(g + 8) * ld + d + c]), split(Q[g * ld + d + c + 4]),
+                                    split(Q[(g + 8) * ld + d + c + 4])};
+                Split y[4][2];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) w[j][e] = split(V[(8 * i + 2 * c + e) * ld + 8 * (j0 + j) + g]);
-                mma3x4(y, p[i], w);
+                    for (int e = 0; e < 2; ++e) y[j][e] = split(K[(8 * j + g) * ld + d + c + 4 * e]);
+                mma3x4(s, x, y);
+            }
+            const int left = m - t * kFKeys;
+            Split p[kFKeys / 8][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int j = 0; j < kFKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float& x = s[j][2 * r + e];
+                        x = 8 * j + 2 * c + e < left ? x * scale : -CUDART_INF_F;
+                        top = fmaxf(top, x);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float now = fmaxf(mx[r], top), ref = now == -CUDART_INF_F ? 0.f : now, alpha = exp2f(mx[r] - ref);
+                mx[r] = now;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < kFKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float w = exp2f(s[j][2 * r + e] - ref);
+                        sum += w;
+                        p[j][2 * e + r] = split(w);
+                    }
+                l[r] = l[r] * alpha + sum;
+#pragma unroll
+                for (int j = 0; j < HD / 8; ++j) {
+                    o[j][2 * r] *= alpha;
+                    o[j][2 * r + 1] *= alpha;
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j0 = 0; j0 < HD / 8; j0 += 4) {
+                float y[4][4] = {};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[j0 + j][e] += y[j][e];
-        }
-        __syncthreads();
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                for (int i = 0; i < kFKeys / 8; ++i) {
+                    Split w[4][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const int at = 16 * warp + g + 8 * r;
-        if (at >= rows) continue;
-        const int rr = row0 + at, tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], lse = l[r] == 0.f ? -CUDART_INF_F : (mx[r] + log2f(l[r])) * kLn2;
-        float* to = (float*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
-        if (a.parts > 1) {
-            const long long row = ((long long)part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
-            to = a.part_out + row * a.D;
-            if (c == 0) a.part_lse[row] = lse;
-        } else if (c == 0 && a.lse) {
-            a.lse[qbat * a.lb + tok * a.lt + hq * a.lh] = lse;
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) w[j][e] = split(V[(8 * i + 2 * c + e) * ld + 8 * (j0 + j) + g]);
+                    mma3x4(y, p[i], w);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j0 + j][e] += y[j][e];
+            }
+            __syncthreads();
         }
+        const bool last = !kLong || t >= t1;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int at = 16 * warp + g + 8 * r;
+            if (at >= rows) continue;
+            const int rr = row0 + at, tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
+            const float f = m_aside[r] == -CUDART_INF_F ? 0.f : exp2f(m_aside[r] - mx[r]);
+            l_aside[r] = fmaf(l_aside[r], f, l[r]);
+            m_aside[r] = mx[r];
+            float* to = (float*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
+            float* to_lse = a.lse ? a.lse + qbat * a.lb + tok * a.lt + hq * a.lh : nullptr;
+            if (a.parts > 1) {
+                const long long row = ((long long)part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
+                to = a.part_out + row * a.D;
+                to_lse = a.part_lse + row;
+            }
+            const float inv = !last ? 1.f : l_aside[r] == 0.f ? 0.f : 1.f / l_aside[r];
+            if (last && c == 0 && to_lse) *to_lse = l_aside[r] == 0.f ? -CUDART_INF_F : (mx[r] + log2f(l_aside[r])) * kLn2;
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float* x = to + 8 * j + 2 * c + e;
+                    if (8 * j + 2 * c + e < a.D) *x = (!kLong || first ? o[j][2 * r + e] : fmaf(*x, f, o[j][2 * r + e])) * inv;
+                }
+        }
+        if (last) break;
+        first = false;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (8 * j + 2 * c + e < a.D) to[8 * j + 2 * c + e] = o[j][2 * r + e] * inv;
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int HD, int kBytes>
+template <int HD, int kBytes, bool kLong>
 static bsa_status launch_f32(const Cross& a, cudaStream_t st) {
     constexpr int kSmem = sizeof(float) * (HD + 4) * (kFRows + 4 * kFKeys);
-    cudaError_t e = cudaFuncSetAttribute(cross_f32_kernel<HD, kBytes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(cross_f32_kernel<HD, kBytes, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return fail(BSA_ERR_CUDA, "cross attention attribute: %s", cudaGetErrorString(e));
-    cross_f32_kernel<HD, kBytes><<<dim3((unsigned)a.tiles, a.H, a.parts), 128, kSmem, st>>>(a);
+    cross_f32_kernel<HD, kBytes, kLong><<<dim3((unsigned)a.tiles, a.H, a.parts), 128, kSmem, st>>>(a);
     return check_launch("cross_f32_kernel");
+}
+template <int HD, int kBytes>
+static bsa_status launch_f32(const Cross& a, cudaStream_t st) {
+    const int tiles = ((a.M + kFKeys - 1) / kFKeys + a.parts - 1) / a.parts;  // that an item may have
+    return tiles > kFAside ? launch_f32<HD, kBytes, true>(a, st) : launch_f32<HD, kBytes, false>(a, st);
 }
 
 }  // namespace cross

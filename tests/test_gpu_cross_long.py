@@ -93,3 +93,27 @@ def test_unsplit_long_sums_16_rows(pl, HQ, D, M):
 @pytest.mark.parametrize("HQ,D", [(1, 64), (4, 128)])
 def test_moving_maxima_16_rows(pl, HQ, D):
     moving_maxima(pl, BF16, 640, 1, 150013, HQ, 1, D)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("M", [1 << 17, 1 << 19])
+def test_unsplit_long_sums_float32(pl, D, M):
+    N = 39040
+    assert pl.bsa.bsa_cross_way(F32, 1, N, M, 1, 1, D) == 3 and pl.bsa.bsa_cross_workspace(F32, 1, N, M, 1, 1, D, False, False) == 0
+    out, mean = equal_keys(pl, F32, 1, N, M, 1, 1, D, 0.73)
+    most = off(out, mean)
+    assert most <= 0.73 * (24 + 128 + 2 * M / 4096 + 8) * U
+
+
+@pytest.mark.parametrize("D", [7, 64, 128])
+def test_long_sums_in_parts_float32(pl, D):
+    N, M = 100, (1 << 20) + 77
+    assert pl.bsa.bsa_cross_workspace(F32, 1, N, M, 1, 1, D, False, False) == 4 * 64 * N * (D + 1)  # 64 parts
+    out, mean = equal_keys(pl, F32, 1, N, M, 1, 1, D, 0.73)
+    most = off(out, mean)
+    assert most <= 0.73 * (24 + 128 + 2 * M / 64 / 4096 + 2 * 64 + 8) * U
+
+
+@pytest.mark.parametrize("N,HQ,H,D", [(39040, 1, 1, 64), (9760, 4, 1, 128), (100, 6, 2, 20)])
+def test_moving_maxima_float32(pl, N, HQ, H, D):
+    moving_maxima(pl, F32, 1, N, 10013 if N > 100 else 600013, HQ, H, D)
