@@ -5,8 +5,8 @@ with u = 2^-24 (a product with the tensor cores cuts its sum off: 2 u; an additi
 * 256-row and 16-row kernels: at most 1024 products join a sum before it is put aside, 2048 u; the sums put aside are
   added up rounded, M / 16384 of them; some 8 u for the weights' sum and the division; half a step of the output.
 * float32: 12 products a tile of 32 keys, 24 u; 128 tiles, 128 u; M / 4096 sums, each scaled and added, 2 u; 8 u.
-* CUDA cores: 1024 keys one after the other, 1024 u, and M / 1024 such sums, 2 u each; 8 u; the weights' own sum has the same
-  number of additions but for 64 keys at once: doubled; half a step of the output."""
+* CUDA cores: 64 keys one after the other, 64 u, and M / 64 such sums, u each; 8 u; the weights' own sum likewise: doubled;
+  half a step of the output."""
 
 import pytest
 import torch
@@ -117,3 +117,17 @@ def test_long_sums_in_parts_float32(pl, D):
 @pytest.mark.parametrize("N,HQ,H,D", [(39040, 1, 1, 64), (9760, 4, 1, 128), (100, 6, 2, 20)])
 def test_moving_maxima_float32(pl, N, HQ, H, D):
     moving_maxima(pl, F32, 1, N, 10013 if N > 100 else 600013, HQ, H, D)
+
+
+def test_unsplit_long_sums_cuda_cores(pl):
+    N, M, D = 39040, 1 << 18, 4
+    assert pl.bsa.bsa_cross_way(BF16, 1, N, M, 1, 1, D) == 0 and pl.bsa.bsa_cross_workspace(BF16, 1, N, M, 1, 1, D, False, False) == 0
+    out, mean = equal_keys(pl, BF16, 1, N, M, 1, 1, D, 0.73)
+    most = off(out, mean)
+    assert most <= 2.0 ** -9 + 0.73 * 2 * (64 + M / 64 + 8) * U
+
+
+@pytest.mark.parametrize("N,M,HQ,H,D", [(39040, 3013, 1, 1, 20), (700, 20013, 3, 1, 100), (3, 70000, 2, 2, 7)])
+def test_moving_maxima_cuda_cores(pl, N, M, HQ, H, D):
+    assert pl.bsa.bsa_cross_way(BF16, 1, N, M, HQ, H, D) == 0
+    moving_maxima(pl, BF16, 1, N, M, HQ, H, D)
