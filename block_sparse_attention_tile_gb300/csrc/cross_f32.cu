@@ -3,7 +3,9 @@
 // "VSA 实现详解：三维分块、均值路由与块稀疏 Attention" §6.5 for the online softmax in the log2 domain.
 //
 // An operand x is split into x = hi + lo, both rounded to tf32, and a product is lo hi + hi lo + hi hi (what is left out,
-// lo lo and lo's own roundings, is 3 x 2^-22 of it at most).  An infinity has no remainder and comes out as NaN.
+// lo lo and lo's own roundings, is 3 x 2^-22 of it at most).  Where hi is infinite (an infinity, or a value within 2^-12 of
+// the largest float) that is NaN: a block with NaN in its results takes its keys once more, with hi stopped at the largest
+// value (kSat; the conversion that does so costs 10% where all blocks use it), and an infinity is then one in lo alone.
 // A block holds 64 rows, 16 to a warp, against tiles of 32 keys that are copied two ahead of each other.  The weights of
 // keys 2c and 2c + 1, which a lane of quad c holds after the product with K, are its operands at k = c and c + 4 of the
 // product with V, whose rows are read in that order; a tile's weighted values are summed from zero and added to O
@@ -13,6 +15,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cross.cuh"
 #include "tc_ptx.cuh"
@@ -27,9 +30,11 @@ constexpr int kFRows = 64, kFKeys = 32;  // the products take four column tiles 
 constexpr int kFAside = 128;
 
 struct Split { uint32_t hi, lo; };
+template <bool kSat = false>
 __device__ __forceinline__ Split split(float x) {
     Split s;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(s.hi) : "f"(x));
+    if constexpr (kSat) asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(s.hi) : "f"(x));
+    else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(s.hi) : "f"(x));
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(s.lo) : "f"(x - __uint_as_float(s.hi)));
     return s;
 }
@@ -81,7 +86,6 @@ __global__ void __launch_bounds__(128, HD == 64 ? 3 : 2) cross_f32_kernel(const 
         copy_in<kBytes>(Qs + r * ld + d, on ? q + (q0 + t) * a.qt + (row0 + r - t * a.G) * a.qh + d : q, on);
     }
     const int nt = (m + kFKeys - 1) / kFKeys, t1 = (int)((long long)nt * (part + 1) / a.parts);
-    int t = (int)((long long)nt * part / a.parts);
     auto fetch = [&](int tile) {
         if (tile < t1) {
             float *K = KV + (tile & 1) * 2 * kTile, *V = K + kTile;
@@ -94,118 +98,129 @@ __global__ void __launch_bounds__(128, HD == 64 ? 3 : 2) cross_f32_kernel(const 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(t);
-    const float scale = fmaxf(a.scale * kLog2e, 1.2e-38f);  // 0 would turn a masked -inf into NaN
-    float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f}, o[HD / 8][4] = {};
-    float m_aside[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_aside[2] = {0.f, 0.f};
-    bool first = true;  // nothing put aside
-    for (int stop = kLong ? min(t1, t + kFAside) : t1;; stop = min(t1, stop + kFAside)) {
-        for (; t < stop; ++t) {
-            fetch(t + 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncthreads();
-            const float *K = KV + (t & 1) * 2 * kTile, *V = K + kTile, *Q = Qs + (16 * warp) * ld;
-            float s[kFKeys / 8][4] = {};
+    const auto pass = [&](auto sat) {  // whether there is a NaN among the thread's results
+        constexpr bool kSat = decltype(sat)::value;
+        int t = (int)((long long)nt * part / a.parts);
+        fetch(t);
+        const float scale = fmaxf(a.scale * kLog2e, 1.2e-38f);  // 0 would turn a masked -inf into NaN
+        float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f}, o[HD / 8][4] = {};
+        float m_aside[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_aside[2] = {0.f, 0.f};
+        bool first = true, bad = false;  // first: nothing put aside
+        for (int stop = kLong ? min(t1, t + kFAside) : t1;; stop = min(t1, stop + kFAside)) {
+            for (; t < stop; ++t) {
+                fetch(t + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                __syncthreads();
+                const float *K = KV + (t & 1) * 2 * kTile, *V = K + kTile, *Q = Qs + (16 * warp) * ld;
+                float s[kFKeys / 8][4] = {};
 #pragma unroll 4
-            for (int d = 0; d < HD; d += 8) {
-                const Split x[4] = {split(Q[g * ld + d + c]), split(Q[(g + 8) * ld + d + c]), split(Q[g * ld + d + c + 4]),
-                                    split(Q[(g + 8) * ld + d + c + 4])};
-                Split y[4][2];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) y[j][e] = split(K[(8 * j + g) * ld + d + c + 4 * e]);
-                mma3x4(s, x, y);
-            }
-            const int left = m - t * kFKeys;
-            Split p[kFKeys / 8][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float top = -CUDART_INF_F;
-#pragma unroll
-                for (int j = 0; j < kFKeys / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& x = s[j][2 * r + e];
-                        x = 8 * j + 2 * c + e < left ? x * scale : -CUDART_INF_F;
-                        top = fmaxf(top, x);
-                    }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float now = fmaxf(mx[r], top), ref = now == -CUDART_INF_F ? 0.f : now, alpha = exp2f(mx[r] - ref);
-                mx[r] = now;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < kFKeys / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float w = exp2f(s[j][2 * r + e] - ref);
-                        sum += w;
-                        p[j][2 * e + r] = split(w);
-                    }
-                l[r] = l[r] * alpha + sum;
-#pragma unroll
-                for (int j = 0; j < HD / 8; ++j) {
-                    o[j][2 * r] *= alpha;
-                    o[j][2 * r + 1] *= alpha;
-                }
-            }
-#pragma unroll
-            for (int j0 = 0; j0 < HD / 8; j0 += 4) {
-                float y[4][4] = {};
-#pragma unroll
-                for (int i = 0; i < kFKeys / 8; ++i) {
-                    Split w[4][2];
+                for (int d = 0; d < HD; d += 8) {
+                    const Split x[4] = {split<kSat>(Q[g * ld + d + c]), split<kSat>(Q[(g + 8) * ld + d + c]), split<kSat>(Q[g * ld + d + c + 4]),
+                                        split<kSat>(Q[(g + 8) * ld + d + c + 4])};
+                    Split y[4][2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) w[j][e] = split(V[(8 * i + 2 * c + e) * ld + 8 * (j0 + j) + g]);
-                    mma3x4(y, p[i], w);
+                        for (int e = 0; e < 2; ++e) y[j][e] = split<kSat>(K[(8 * j + g) * ld + d + c + 4 * e]);
+                    mma3x4(s, x, y);
+                }
+                const int left = m - t * kFKeys;
+                Split p[kFKeys / 8][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float top = -CUDART_INF_F;
+#pragma unroll
+                    for (int j = 0; j < kFKeys / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& x = s[j][2 * r + e];
+                            x = 8 * j + 2 * c + e < left ? x * scale : -CUDART_INF_F;
+                            top = fmaxf(top, x);
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float now = fmaxf(mx[r], top), ref = now == -CUDART_INF_F ? 0.f : now, alpha = exp2f(mx[r] - ref);
+                    mx[r] = now;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < kFKeys / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float w = exp2f(s[j][2 * r + e] - ref);
+                            if (kSat) w *= 0.5f;  // the largest float's two halves may add up to 2^128
+                            sum += w;
+                            p[j][2 * e + r] = split(w);
+                        }
+                    l[r] = l[r] * alpha + sum;
+#pragma unroll
+                    for (int j = 0; j < HD / 8; ++j) {
+                        o[j][2 * r] *= alpha;
+                        o[j][2 * r + 1] *= alpha;
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j0 = 0; j0 < HD / 8; j0 += 4) {
+                    float y[4][4] = {};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j0 + j][e] += y[j][e];
-            }
-            __syncthreads();
-        }
-        const bool last = !kLong || t >= t1;
+                    for (int i = 0; i < kFKeys / 8; ++i) {
+                        Split w[4][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            const int at = 16 * warp + g + 8 * r;
-            if (at >= rows) continue;
-            const int rr = row0 + at, tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
-            const float f = m_aside[r] == -CUDART_INF_F ? 0.f : exp2f(m_aside[r] - mx[r]);
-            l_aside[r] = fmaf(l_aside[r], f, l[r]);
-            m_aside[r] = mx[r];
-            float* to = (float*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
-            float* to_lse = a.lse ? a.lse + qbat * a.lb + tok * a.lt + hq * a.lh : nullptr;
-            if (a.parts > 1) {
-                const long long row = ((long long)part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
-                to = a.part_out + row * a.D;
-                to_lse = a.part_lse + row;
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) w[j][e] = split<kSat>(V[(8 * i + 2 * c + e) * ld + 8 * (j0 + j) + g]);
+                        mma3x4(y, p[i], w);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[j0 + j][e] += y[j][e];
+                }
+                __syncthreads();
             }
-            const float inv = !last ? 1.f : l_aside[r] == 0.f ? 0.f : 1.f / l_aside[r];
-            if (last && c == 0 && to_lse) *to_lse = l_aside[r] == 0.f ? -CUDART_INF_F : (mx[r] + log2f(l_aside[r])) * kLn2;
+            const bool last = !kLong || t >= t1;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                const int at = 16 * warp + g + 8 * r;
+                if (at >= rows) continue;
+                const int rr = row0 + at, tok = q0 + rr / a.G, hq = h * a.G + rr % a.G;
+                const float f = m_aside[r] == -CUDART_INF_F ? 0.f : exp2f(m_aside[r] - mx[r]);
+                l_aside[r] = fmaf(l_aside[r], f, l[r]);
+                m_aside[r] = mx[r];
+                float* to = (float*)a.out + qbat * a.ob + tok * a.ot + hq * a.oh;
+                float* to_lse = a.lse ? a.lse + qbat * a.lb + tok * a.lt + hq * a.lh : nullptr;
+                if (a.parts > 1) {
+                    const long long row = ((long long)part * (a.query_start ? a.N : (long long)a.B * a.N) + qbat * a.N + tok) * a.HQ + hq;
+                    to = a.part_out + row * a.D;
+                    to_lse = a.part_lse + row;
+                }
+                const float inv = !last ? 1.f : l_aside[r] == 0.f ? 0.f : 1.f / l_aside[r];
+                if (last && c == 0 && to_lse) *to_lse = l_aside[r] == 0.f ? -CUDART_INF_F : (mx[r] + log2f(kSat ? 2.f * l_aside[r] : l_aside[r])) * kLn2;
+                bad = bad || l_aside[r] != l_aside[r];
+#pragma unroll
+                for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float* x = to + 8 * j + 2 * c + e;
+                        if (8 * j + 2 * c + e >= a.D) continue;
+                        const float y = !kLong || first ? o[j][2 * r + e] : fmaf(*x, f, o[j][2 * r + e]);
+                        bad = bad || y != y;
+                        *x = y * inv;
+                    }
+            }
+            if (last) break;
+            first = false;
+            l[0] = l[1] = 0.f;
 #pragma unroll
             for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float* x = to + 8 * j + 2 * c + e;
-                    if (8 * j + 2 * c + e < a.D) *x = (!kLong || first ? o[j][2 * r + e] : fmaf(*x, f, o[j][2 * r + e])) * inv;
-                }
+                for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         }
-        if (last) break;
-        first = false;
-        l[0] = l[1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < HD / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        return bad;
+    };
+    if (__syncthreads_or(pass(std::false_type{}))) pass(std::true_type{});
 }
 
 template <int HD, int kBytes, bool kLong>

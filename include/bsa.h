@@ -654,7 +654,8 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
  * between calls.  Deterministic for the same sizes and
  * flags.  bf16 takes the softmax's weights to bf16 before the product with V (so do the other bf16 kernels); float32
- * keeps float32's accuracy, but an infinite element in a row that counts gives NaN. */
+ * keeps float32's accuracy; an infinity in a row that counts does what it does in float32, but against an element of
+ * 2^11 or more it may give NaN.  A block of rows that comes out with NaN is computed twice. */
 /* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
  * tiles of 16 rows, 3 tensor cores in float32 (1 and 2: addresses and strides that are no multiples of 16 bytes take 0
  * all the same); -1 for sizes out of range. */
