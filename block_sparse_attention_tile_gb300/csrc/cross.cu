@@ -223,6 +223,13 @@ struct CrossPlan {
 constexpr int kAtOnce = 2 * 152;  // blocks of the 16-row kernels that run at once
 constexpr int kLongRow = 1024;    // keys
 
+// Parts of the keys for the kernels of 64 rows an item: several blocks an SM, of 128 keys or more (float32, 4096 x 4096 x 8
+// heads: 1495 us in 2 parts, 1685 whole, 1488 in 4).
+static int key_parts(int B, int N, int M, int G, int H, bool packed_q, bool packed_k) {
+    const long long keys = packed_k ? (M + B - 1) / B : M, items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
+    return (int)std::max<long long>(1, std::min<long long>({8 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
+}
+
 // Which kernel, and how the keys are cut.  Only sizes that the host knows: a batch's average stands for its sequences.
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
     CrossPlan p{};
@@ -255,10 +262,7 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
         p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
     } else {
         p.way = dtype == BSA_F32 && !force_simt() ? 3 : 0;
-        // several blocks an SM, of 128 keys or more (float32, 4096 x 4096 x 8 heads: 1495 us in 2 parts, 1685 whole,
-        // 1488 in 4)
-        const long long items = row_tiles(B, N, G, packed_q, kSimtRows) * H;
-        p.parts = (int)std::max<long long>(1, std::min<long long>({8 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
+        p.parts = key_parts(B, N, M, G, H, packed_q, packed_k);
     }
     return p;
 }
@@ -343,9 +347,16 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
         rc = cross_rows(r, p.runs, st, &handled);
     }
     if (p.way == 3) rc = cross_f32(a, st), handled = true;
+    if (!handled && p.runs) {
+        // strides or addresses that the 16-row kernels do not take: as many parts as the runs' workspace holds (one token
+        // over 131072 states, 8 heads, D = 64: 0.8 ms in 64 parts, 18.6 whole)
+        a.parts = (int)std::max<size_t>(1, std::min<size_t>(key_parts(B, N, M, a.G, H, query_start != nullptr, key_start != nullptr),
+                                                            need / (sizeof(float) * (D + 1) * rows)));
+        a.part_lse = a.part_out + (size_t)a.parts * rows * D;
+    }
     if (!handled && rc == BSA_OK)
         rc = dtype == BSA_F32 ? launch_cross_simt<float>(a, st) : launch_cross_simt<__nv_bfloat16>(a, st);
-    if (rc != BSA_OK || p.parts == 1) return rc;  // runs join by themselves
+    if (rc != BSA_OK || a.parts == 1) return rc;  // runs join by themselves
     const dim3 grid((unsigned)row_tiles(B, N, a.G, query_start != nullptr, kJoinRows), H);
     if (dtype == BSA_F32) cross_join_kernel<float><<<grid, 32 * kJoinRows, 0, st>>>(a);
     else cross_join_kernel<__nv_bfloat16><<<grid, 32 * kJoinRows, 0, st>>>(a);
