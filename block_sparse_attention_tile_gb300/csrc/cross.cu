@@ -230,7 +230,9 @@ static int key_parts(int B, int N, int M, int G, int H, bool packed_q, bool pack
     return (int)std::max<long long>(1, std::min<long long>({8 * 152 / std::max(items, 1LL), (keys + 127) / 128, 64}));
 }
 
-// Which kernel, and how the keys are cut.  Only sizes that the host knows: a batch's average stands for its sequences.
+// Which kernel, and how the keys are cut.  Only sizes that the host knows: a batch's average stands for its sequences.  The
+// CUDA cores take the plan's cut where they stand in for its kernel (by BSA_FORCE_SIMT, or for strides and addresses), so
+// that the workspace does not depend on that.
 static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, bool packed_q, bool packed_k) {
     CrossPlan p{};
     const int G = HQ / H, Gt = cross_tc_heads(G);
@@ -261,7 +263,7 @@ static CrossPlan cross_plan(bsa_dtype dtype, int B, int N, int M, int HQ, int H,
         const long long items = row_tiles(B, N, Gt, packed_q, 256) * (HQ / Gt);
         p.parts = (int)std::max<long long>(1, std::min<long long>({152 / std::max(items, 1LL), (keys + 255) / 256, 64}));
     } else {
-        p.way = dtype == BSA_F32 && !force_simt() ? 3 : 0;
+        p.way = dtype == BSA_F32 ? 3 : 0;
         p.parts = key_parts(B, N, M, G, H, packed_q, packed_k);
     }
     return p;
@@ -305,7 +307,7 @@ size_t bsa_cross_workspace(bsa_dtype dtype, int B, int N, int M, int HQ, int H, 
 
 int bsa_cross_way(bsa_dtype dtype, int B, int N, int M, int HQ, int H, int D, int packed_queries, int packed_keys) {
     if ((dtype != BSA_F32 && dtype != BSA_BF16) || !cross_sizes_ok(B, N, M, HQ, H, D, packed_queries != 0) || B == 0 || N == 0) return -1;
-    return cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0).way;
+    return force_simt() ? 0 : cross_plan(dtype, B, N, M, HQ, H, D, packed_queries != 0, packed_keys != 0).way;
 }
 
 bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype dtype, int B, int N, int M, int HQ,
@@ -340,15 +342,16 @@ bsa_status bsa_fwd_cross(const void* q, const void* k, const void* v, bsa_dtype 
     cudaStream_t st = as_stream(stream);
     bsa_status rc = BSA_OK;
     bool handled = false;
-    if (p.way == 1) rc = cross_tc(a, st, &handled);
-    if (p.way == 2) {
+    const int way = force_simt() ? 0 : p.way;
+    if (way == 1) rc = cross_tc(a, st, &handled);
+    if (way == 2) {
         Cross r = a;
         r.parts = p.cluster;
         rc = cross_rows(r, p.runs, st, &handled);
     }
-    if (p.way == 3) rc = cross_f32(a, st), handled = true;
+    if (way == 3) rc = cross_f32(a, st), handled = true;
     if (!handled && p.runs) {
-        // strides or addresses that the 16-row kernels do not take: as many parts as the runs' workspace holds (one token
+        // in place of the 16-row kernels: as many parts as the runs' workspace holds (at an odd address, one token
         // over 131072 states, 8 heads, D = 64: 0.8 ms in 64 parts, 18.6 whole)
         a.parts = (int)std::max<size_t>(1, std::min<size_t>(key_parts(B, N, M, a.G, H, query_start != nullptr, key_start != nullptr),
                                                             need / (sizeof(float) * (D + 1) * rows)));

@@ -773,7 +773,7 @@ int cross_tc_heads(int G) {
 }
 
 // Whether the sizes suit the tensor-core kernel (strides and addresses are looked at at the launch).
-bool cross_tc_sizes(bsa_dtype dtype, int D) { return dtype == BSA_BF16 && D % 8 == 0 && !force_simt(); }
+bool cross_tc_sizes(bsa_dtype dtype, int D) { return dtype == BSA_BF16 && D % 8 == 0; }
 
 bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled) {
     using namespace cross;

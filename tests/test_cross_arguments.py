@@ -1,0 +1,28 @@
+"""Rotation and cross attention without a GPU: sizes that follow the kernel switch, and calls that are refused."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def pl():
+    from block_sparse_attention_tile_gb300.build import build
+    build()
+    from block_sparse_attention_tile_gb300 import pipeline
+    return pipeline
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [(1, 1, 20000, 8, 2, 64), (1, 500, 20000, 4, 4, 128), (8, 1, 600, 8, 8, 128), (1, 2, 9000, 2, 2, 60)])
+def test_cross_workspace_does_not_depend_on_the_switch(pl, monkeypatch, dtype, sizes):
+    """A size that the binding keeps holds after BSA_FORCE_SIMT changes: the library asks for the same one."""
+    def both():
+        return (pl.bsa.bsa_cross_workspace(dtype, *sizes, False, False),
+                pl.bsa._lib.bsa_cross_workspace(1 if dtype is torch.bfloat16 else 0, *sizes, 0, 0))
+    monkeypatch.delenv("BSA_FORCE_SIMT", raising=False)
+    cached, size = both()
+    assert cached == size
+    monkeypatch.setenv("BSA_FORCE_SIMT", "1")
+    assert both() == (size, size) and pl.bsa.bsa_cross_way(dtype, *sizes) == 0

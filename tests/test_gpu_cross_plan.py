@@ -53,3 +53,17 @@ def test_odd_addresses_few_rows_use_the_whole_card(pl):
     q, k = (off_by_one(rand(i, 1, n, H, 64, dtype=BF16)) for i, n in ((1, 1), (2, M)))
     q60, k60 = q[..., :60].contiguous(), k[..., :60].contiguous()
     assert median_ms(lambda: pl.cross_attention(q, k, k)) <= 4 * median_ms(lambda: pl.cross_attention(q60, k60, k60))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,N,M,HQ,H,D", [(3, 1, 2000, 8, 2, 128), (1, 70, 9000, 4, 4, 64), (2, 1, 500, 4, 4, 40), (640, 1, 1100, 1, 1, 64)])
+def test_the_switch_between_two_calls(pl, monkeypatch, dtype, B, N, M, HQ, H, D):
+    q, k, v = rand(1, B, N, HQ, D, dtype=dtype), rand(2, 1, M, H, D, dtype=dtype), rand(3, 1, M, H, D, dtype=dtype)
+    k, v = k.expand(B, M, H, D), v.expand(B, M, H, D)
+    rows = range(0, B, max(1, B // 5))
+    monkeypatch.delenv("BSA_FORCE_SIMT", raising=False)
+    for _ in range(2):
+        out, lse = pl.cross_attention(q, k, v)
+        for b in rows:
+            check_rows(out[b], lse[b], q[b], k[b], v[b], D ** -0.5, dtype)
+        monkeypatch.setenv("BSA_FORCE_SIMT", "1")
