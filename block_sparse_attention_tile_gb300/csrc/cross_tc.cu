@@ -18,7 +18,8 @@
 // The products bound it where the keys are many (38912 tokens x 2 heads x 16384 keys: 1600 TFLOP/s at D = 128, 82% of the measured
 // matrix rate, and 1108 at D = 64, where a key's exponentials take as long as its products); where they are few (115200
 // tokens x 512 keys: 571 us, 371 of it products) the items' starts, outputs and changes of queries are the rest.
-// Every wait is bounded (2 s): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
+// Every wait is bounded (2 s, and 20 us for each key tile that an item may have, some ten times what one takes: the waits for
+// an item's end last as long as the item): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math_constants.h>
@@ -36,7 +37,7 @@ constexpr int kBM = 128, kBN = 128;      // rows of a tile, keys of a tile
 constexpr int kRows = 2 * kBM;           // rows of an item
 constexpr int kThreads = 512;
 constexpr int kMaxStages = 6;            // K and V tiles in flight, at most
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull, kWaitTileNs = 20000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // The tensor cores cut off what they add to O: by up to 2^-23 of it at each of a key tile's eight products, which does not
 // average out over values of one sign (unsplit 2^20 keys came out 5e-3 short).  Every so many key tiles the sums are
@@ -801,8 +802,9 @@ bsa_status cross_tc(const Cross& a, cudaStream_t st, bool* handled) {
     prm.scale_log2 = std::max(a.scale * kLog2e, 1.2e-38f);
     prm.sched = sched_counter(st);
     prm.stall = test_stall_tile();
-    prm.wait_ns = prm.stall >= 0 ? 1000000ull : kWaitNs;
-    const bool longs = ((a.M + kBN - 1) / kBN + a.parts - 1) / a.parts > kAside;  // key tiles that an item may have
+    const int item_tiles = ((a.M + kBN - 1) / kBN + a.parts - 1) / a.parts;  // at most
+    prm.wait_ns = prm.stall >= 0 ? 1000000ull : kWaitNs + kWaitTileNs * (uint64_t)item_tiles;
+    const bool longs = item_tiles > kAside;
     if (a.D <= 64) return longs ? launch<64, true>(mq, mk, mv, prm, st, handled) : launch<64, false>(mq, mk, mv, prm, st, handled);
     return longs ? launch<128, true>(mq, mk, mv, prm, st, handled) : launch<128, false>(mq, mk, mv, prm, st, handled);
 }

@@ -131,3 +131,17 @@ def test_unsplit_long_sums_cuda_cores(pl):
 def test_moving_maxima_cuda_cores(pl, N, M, HQ, H, D):
     assert pl.bsa.bsa_cross_way(BF16, 1, N, M, HQ, H, D) == 0
     moving_maxima(pl, BF16, 1, N, M, HQ, H, D)
+
+
+def test_items_longer_than_two_seconds(pl):
+    """An item of 1.5 x 2^28 states (6.4 GB, K and V the same) takes the 256-row kernel some 3 s: its waits last as long."""
+    N, M, D = 19712, 3 << 27, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q, row = torch.randn(1, N, 1, D, generator=g, device=DEV).to(BF16), torch.randn(D, generator=g, device=DEV).to(BF16)
+    k = torch.empty(1, M, 1, D, dtype=BF16, device=DEV).copy_(row)
+    assert pl.bsa.bsa_cross_way(BF16, 1, N, M, 1, 1, D) == 1 and pl.bsa.bsa_cross_workspace(BF16, 1, N, M, 1, 1, D, False, False) == 0
+    out, lse = pl.cross_attention(q, k, k)
+    assert pl.bsa.bsa_device_status() == pl.bsa.BSA_OK
+    # equal keys: the output is their row, but for half a step, and what 2^15 sums that were put aside are off
+    most = float(((out.double() - row.double()) / row.double()).abs().max())
+    assert most <= 2.0 ** -8 + 2 * (2048 + M / 16384 + 8) * U
