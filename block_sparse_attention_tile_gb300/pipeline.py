@@ -465,7 +465,10 @@ def rotary_frequencies(channels, base=10000.0, sections=None, scaling=None, stre
 
 def rotary_table(positions, turns, axis=None, factor=1.0, out=None):
     """(cos, sin) float32 [T, P] of positions int32 [T] or [T, axes] and the frequencies of ``Rotary``."""
-    T, axes = positions.shape[0], positions.shape[1] if positions.dim() == 2 else 1
+    shape = positions.shape
+    if not 1 <= len(shape) <= 2 or turns.dim() != 1:
+        raise ValueError("positions [T] or [T, axes] and turns [P] are needed, got %s and %s" % (tuple(shape), tuple(turns.shape)))
+    T, axes = shape if len(shape) == 2 else (shape[0], 1)
     P = turns.shape[0]
     if axis is not None and axis.shape != turns.shape:
         raise ValueError("axis: one for each of %d frequencies is needed, got %s" % (P, tuple(axis.shape)))

@@ -26,3 +26,12 @@ def test_cross_workspace_does_not_depend_on_the_switch(pl, monkeypatch, dtype, s
     assert cached == size
     monkeypatch.setenv("BSA_FORCE_SIMT", "1")
     assert both() == (size, size) and pl.bsa.bsa_cross_way(dtype, *sizes) == 0
+
+
+@pytest.mark.parametrize("positions,turns,axis", [((4, 3, 2), (8,), None), ((), (8,), None), ((4,), (8, 2), None), ((4, 2), (8, 2), (8, 2))])
+def test_table_shapes_are_refused(pl, positions, turns, axis):
+    """Positions of a batch, [B, T, axes], were read as B tokens."""
+    i32 = torch.int32
+    with pytest.raises(ValueError, match=r"positions \[T\] or \[T, axes\]"):
+        pl.rotary_table(torch.zeros(positions, dtype=i32), torch.zeros(turns, dtype=torch.int64),
+                        None if axis is None else torch.zeros(axis, dtype=i32))
