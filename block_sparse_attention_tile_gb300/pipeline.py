@@ -551,11 +551,15 @@ def cross_attention(q, k, v, key_lens=None, query_start=None, key_start=None, sc
         raise ValueError("q %s, k %s, v %s: packed rows have three dimensions, padded ones four"
                          % (tuple(qshape), tuple(kshape), tuple(v.shape)))
     if packed_q:
+        if query_start.dim() != 1:
+            raise ValueError("query_start: [B + 1] is needed, got %s" % (tuple(query_start.shape),))
         B = query_start.shape[0] - 1
         N, HQ, D = qshape
     else:
         B, N, HQ, D = qshape
     M, H = kshape[-3], kshape[-2]
+    if packed_k and key_start.dim() != 1:
+        raise ValueError("key_start: [B + 1] is needed, got %s" % (tuple(key_start.shape),))
     if (packed_k and key_start.shape[0] - 1 != B) or (key_lens is not None and key_lens.shape != (B,)):
         raise ValueError("the states of %d sequences are needed" % B)
     if out is None:

@@ -35,3 +35,11 @@ def test_table_shapes_are_refused(pl, positions, turns, axis):
     with pytest.raises(ValueError, match=r"positions \[T\] or \[T, axes\]"):
         pl.rotary_table(torch.zeros(positions, dtype=i32), torch.zeros(turns, dtype=torch.int64),
                         None if axis is None else torch.zeros(axis, dtype=i32))
+
+
+@pytest.mark.parametrize("starts", [dict(query_start=(3, 2)), dict(query_start=()), dict(query_start=(3,), key_start=(3, 2))])
+def test_start_shapes_are_refused(pl, starts):
+    x = torch.zeros(4, 2, 16)
+    kw = {n: torch.zeros(s, dtype=torch.int32) for n, s in starts.items()}
+    with pytest.raises(ValueError, match="start"):
+        pl.cross_attention(x, x if "key_start" in kw else x[None].expand(2, 4, 2, 16), x if "key_start" in kw else x[None].expand(2, 4, 2, 16), **kw)
