@@ -274,6 +274,7 @@ bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleav
     BSA_REQUIRE(strides, "rotate: null strides");
     if (B == 0 || T == 0) return BSA_OK;
     BSA_REQUIRE(cos_table && sin_table && q && q_out && (H == 0 || (k && k_out)), "rotate: null pointer");
+    BSA_REQUIRE(table_batch_stride >= 0, "rotate: the table's batch stride must not be negative");
     BSA_REQUIRE(!transpose || (!q_weight && !k_weight), "rotate: the transposed rotation takes no norm");
     BSA_REQUIRE(!(q_weight || k_weight) || (eps >= 0.f && eps <= 1.f), "rotate: eps must lie in [0, 1]");
     Rotate a{};

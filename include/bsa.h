@@ -608,7 +608,7 @@ bsa_status bsa_rotary_table(const int32_t* positions, int T, int axes, const int
  * q_out may be q with the same strides, k_out likewise; otherwise outputs must not overlap
  * anything.  q_weight, k_weight: [device] float [D] or NULL.  cos_table, sin_table:
  * [device] float rows of P, token t of batch b at b * table_batch_stride + t * P
- * (a stride of 0: one table for the batch).  2 <= D <= 256, 2 P <= D.
+ * (a stride of 0: one table for the batch; none is negative).  2 <= D <= 256, 2 P <= D.
  * Wide loads where D is a multiple of 8, P of 4, and all addresses and strides of four
  * channels; a channel at a time otherwise. */
 bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleaved, int transpose,

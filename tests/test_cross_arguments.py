@@ -43,3 +43,15 @@ def test_start_shapes_are_refused(pl, starts):
     kw = {n: torch.zeros(s, dtype=torch.int32) for n, s in starts.items()}
     with pytest.raises(ValueError, match="start"):
         pl.cross_attention(x, x if "key_start" in kw else x[None].expand(2, 4, 2, 16), x if "key_start" in kw else x[None].expand(2, 4, 2, 16), **kw)
+
+
+def ints(*values):
+    return (ctypes.c_int64 * len(values))(*values)
+
+
+def test_rotate_refuses_a_negative_table_stride(pl):
+    """The binding counts the table's rows from it: a negative one let the kernel read ahead of the table."""
+    lib, st = pl.bsa._lib, ints(*[128, 32, 16] * 4)
+    call = lambda stride: lib.bsa_rotate(1, 2, 4, 16, 8, 0, 0, 16, 16, stride, 64, 2, None, 64, None, 0, None, None, st, 1e-6, None)  # noqa: E731
+    for stride in (-1, -32, -(1 << 40)):
+        assert call(stride) == pl.bsa.BSA_ERR_INVALID_ARG and "table" in pl.bsa.bsa_last_error()
