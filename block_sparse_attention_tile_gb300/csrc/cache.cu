@@ -787,6 +787,8 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
                 "rotated append: HQ out of range, or a query token's stride below HQ * D");
     BSA_REQUIRE(((uintptr_t)cache & 15) == 0, "rotated append: the cache must be 16-byte aligned");
     if (T == 0) return BSA_OK;
+    BSA_REQUIRE(!k_val || (k_val != k && k_val != v && v_val != k && v_val != v && k_val != v_val),
+                "rotated append: k_val and v_val must not overlap k, v or each other");
     const long long n_slots = (long long)n_pages * page_size;
     const int sh = log2i(page_size);
     cudaStream_t st = as_stream(stream);

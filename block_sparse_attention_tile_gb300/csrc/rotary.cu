@@ -290,6 +290,9 @@ bsa_status bsa_rotate(bsa_dtype dtype, int B, int T, int D, int P, int interleav
         const int64_t* s = strides + 6 * n;
         a.set[n] = RowSet{in[n], out[n], weight[n], s[0], s[1], s[2], s[3], s[4], s[5], heads[n]};
         if (!heads[n]) continue;
+        BSA_REQUIRE(in[n] != out[n] || ((B == 1 || s[0] == s[3]) && (T == 1 || s[1] == s[4]) && (heads[n] == 1 || s[2] == s[5])),
+                    "rotate: an output over its input needs the same strides, others must not overlap");
+        BSA_REQUIRE(H == 0 || (out[n] != in[1 - n] && out[0] != out[1]), "rotate: outputs must not overlap the other tensor");
         uintptr_t any = (uintptr_t)in[n] | (uintptr_t)out[n];
         for (int j = 0; j < 6; ++j) any |= (uintptr_t)(s[j] * size);
         wide = wide && (any & run) == 0 && ((uintptr_t)weight[n] & 15) == 0;

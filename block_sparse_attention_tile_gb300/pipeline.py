@@ -487,7 +487,7 @@ def rotate(q, k, cos, sin, interleaved=False, q_weight=None, k_weight=None, eps=
     of each sequence), after an RMS norm over each head's channels where there is a weight [D].  Any strides with
     adjacent channels.  Returns (q, k) as new tensors of the same layout, or heads first ([B, H, T, D], what the
     block-sparse stages read).  ``transpose``: the transposed rotation, which is the gradient's and takes a rotation
-    back.  ``out``: the two tensors to write instead of new ones, q and k themselves among them."""
+    back.  ``out``: the two tensors to write instead of new ones, q and k themselves among them (with their own strides)."""
     shape, flat = q.shape, q.dim() == 3
     B, T, HQ, D = (1, *shape) if flat else shape
     H, P = 0 if k is None else k.shape[-2], cos.shape[-1]

@@ -55,3 +55,25 @@ def test_rotate_refuses_a_negative_table_stride(pl):
     call = lambda stride: lib.bsa_rotate(1, 2, 4, 16, 8, 0, 0, 16, 16, stride, 64, 2, None, 64, None, 0, None, None, st, 1e-6, None)  # noqa: E731
     for stride in (-1, -32, -(1 << 40)):
         assert call(stride) == pl.bsa.BSA_ERR_INVALID_ARG and "table" in pl.bsa.bsa_last_error()
+
+
+def test_rotate_refuses_outputs_over_other_rows(pl):
+    """In place with other strides, or one output over the other tensor: rows were overwritten before they were read."""
+    lib, B, T, HQ, H, D = pl.bsa._lib, 2, 4, 2, 2, 16
+    rows, heads = (T * HQ * D, HQ * D, D), (T * HQ * D, D, T * D)  # batch, token, head: [B, T, H, D] and [B, H, T, D]
+    def call(q, q_out, k, k_out, q_in=rows, q_to=rows, k_in=rows, k_to=rows, T=T):  # noqa: E306
+        return lib.bsa_rotate(1, B, T, D, 8, 0, 0, 16, 16, 0, q, HQ, None, q_out, k, H, None, k_out, ints(*q_in, *q_to, *k_in, *k_to), 1e-6, None)
+    for kw in (dict(q=4096, q_out=4096, k=8192, k_out=12288, q_to=heads), dict(q=4096, q_out=8192, k=12288, k_out=12288, k_to=heads),
+               dict(q=4096, q_out=8192, k=8192, k_out=4096), dict(q=4096, q_out=4096, k=4096, k_out=8192),
+               dict(q=4096, q_out=8192, k=12288, k_out=8192), dict(q=4096, q_out=8192, k=12288, k_out=4096)):
+        assert call(**kw) == pl.bsa.BSA_ERR_INVALID_ARG and "overlap" in pl.bsa.bsa_last_error(), kw
+    assert call(4096, 4096, 8192, 8192, q_to=heads, T=0) == pl.bsa.BSA_OK
+
+
+def test_append_rotated_refuses_values_over_its_inputs(pl):
+    """A key's partner channels are read by another thread than the one that writes its value."""
+    def call(k=4096, v=8192, k_val=12288, v_val=16384):
+        return pl.bsa._lib.bsa_cache_append_rotated(k, v, 1, 4, 2, 64, 128, 128, 64, 4096 * 16, 4, 16, None, None, k_val, v_val, 16,
+                                                    16, 32, 0, None, 0, 0, None, None)
+    for kw in (dict(k_val=4096), dict(v_val=8192), dict(k_val=8192), dict(v_val=4096), dict(k_val=16384)):
+        assert call(**kw) == pl.bsa.BSA_ERR_INVALID_ARG and "overlap" in pl.bsa.bsa_last_error(), kw
