@@ -67,3 +67,61 @@ def test_the_switch_between_two_calls(pl, monkeypatch, dtype, B, N, M, HQ, H, D)
         for b in rows:
             check_rows(out[b], lse[b], q[b], k[b], v[b], D ** -0.5, dtype)
         monkeypatch.setenv("BSA_FORCE_SIMT", "1")
+
+
+def many(seed, B, most, empty=5):
+    """Mixed lengths, every `empty`-th sequence without any."""
+    n = np.random.default_rng(seed).integers(1, most + 1, B)
+    n[::empty] = 0
+    return n.tolist()
+
+
+def starts(x):
+    return torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("B", [33, 64, 70])
+@pytest.mark.parametrize("dtype,most,keys,HQ,H,D,way", [
+    (BF16, 400, 700, 4, 2, 64, 1), (BF16, 300, 300, 2, 2, 128, 1), (BF16, 90, 9000, 1, 1, 64, 1), (F32, 60, 300, 2, 1, 64, 3),
+    (F32, 3, 9000, 1, 1, 20, 3), (BF16, 40, 400, 3, 1, 50, 0), (BF16, 3, 9000, 1, 1, 60, 0)])
+def test_more_sequences_than_lanes(pl, B, dtype, most, keys, HQ, H, D, way):
+    """Packed and padded-ragged batches of more than 32 sequences, live and from a graph (whose schedule is fixed): the
+    256-row kernel, float32 and the CUDA cores, whole and in parts."""
+    n, m = many(B, B, most), many(B + 1, B, keys, 7)
+    T, M = sum(n), sum(m)
+    assert pl.bsa.bsa_cross_way(dtype, B, T + 3, M, HQ, H, D, True, True) == way
+    q, k, v = rand(1, T + 3, HQ, D, dtype=dtype), rand(2, M, H, D, dtype=dtype), rand(3, M, H, D, dtype=dtype)
+    qs, ks = starts(n), starts(m)
+
+    def check(out, lse):
+        for b in range(B):
+            r, c = slice(int(qs[b]), int(qs[b + 1])), slice(int(ks[b]), int(ks[b + 1]))
+            check_rows(out[r], lse[r], q[r], k[c], v[c], D ** -0.5, dtype)
+        assert bool((out[T:] == 7).all()) and bool((lse[T:] == 7).all())
+
+    def new():
+        return torch.full((T + 3, HQ, D), 7.0, dtype=dtype, device=DEV), torch.full((T + 3, HQ), 7.0, device=DEV)
+    out, lse = new()
+    pl.cross_attention(q, k, v, query_start=qs, key_start=ks, out=out, lse=lse)
+    check(out, lse)
+    again = new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pl.cross_attention(q, k, v, query_start=qs, key_start=ks, out=again[0], lse=again[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    # the states padded, NaN behind the lengths
+    kp, vp = (torch.full((B, max(m), H, D), float("nan"), dtype=dtype, device=DEV) for _ in range(2))
+    for b in range(B):
+        kp[b, :m[b]], vp[b, :m[b]] = k[ks[b]:ks[b + 1]], v[ks[b]:ks[b + 1]]
+    padded = new()
+    pl.cross_attention(q, kp, vp, query_start=qs, key_lens=torch.tensor(m, dtype=torch.int32, device=DEV), out=padded[0], lse=padded[1])
+    check(*padded)
+    # and the queries, as many of each
+    count = min(max(n), 40)
+    qp = rand(4, B, count, HQ, D, dtype=dtype)
+    o, z = pl.cross_attention(qp, kp, vp, key_lens=torch.tensor(m, dtype=torch.int32, device=DEV))
+    for b in range(0, B, 3):
+        c = slice(int(ks[b]), int(ks[b + 1]))
+        check_rows(o[b], z[b], qp[b], k[c], v[c], D ** -0.5, dtype)
