@@ -9,7 +9,7 @@
 // way; of V it reads 16 bytes at channels 8 g of the four keys 2c, 2c + 1, 2c + 8, 2c + 9 whose weights it holds, so
 // that channel 8 g + j is column g of product j.  The next 16 keys' reads go out as soon as a register is consumed:
 // 8 KB a warp are on their way, 64 KB an SM.
-// 8 ragged requests of 1024 to 32768 keys, 32 heads over 8, D = 128: 554 MB in 105 us, 78% of the copy rate; a warp waits for
+// 8 ragged requests of 1024 to 32768 keys, 32 heads over 8, D = 128: 554 MB in 105 to 108 us, 76 to 78% of the copy rate; a warp waits for
 // its reads most of the time, and 254 registers leave two blocks an SM.
 // The four warps of a block join their parts of the keys in shared memory.  Short rows: a cluster of up to 8 blocks an
 // item, which read each other's shared memory (one launch).  Long ones: equal runs and a join.

@@ -15,8 +15,9 @@
 //   warps 4-7, 8-11  softmax of row tile 0 and 1, one row a thread: running maximum (O is rescaled only when it grows
 //               by more than 2^8) and sum, the weights back to TMEM as bf16.
 //   warps 12-15 output: O times 1 / sum to global memory while the softmax is at the next item.
-// The products bound it where the keys are many (38912 tokens x 2 heads x 16384 keys: 1600 TFLOP/s at D = 128, 82% of the measured
-// matrix rate, and 1108 at D = 64, where a key's exponentials take as long as its products); where they are few (115200
+// The products bound it where the keys are many and D = 128 (38912 tokens x 2 heads x 16384 keys: 1600 TFLOP/s, 82% of the
+// measured matrix rate).  At D = 64 (1108 to 1131) neither they nor the exponentials do, the tensor pipe and the special function
+// unit being busy 47% of the time each: it is a key tile's chain of S, softmax, P and P V.  Where the keys are few (115200
 // tokens x 512 keys: 571 us, 371 of it products) the items' starts, outputs and changes of queries are the rest.
 // Every wait is bounded (2 s, and 20 us for each key tile that an item may have, some ten times what one takes: the waits for
 // an item's end last as long as the item): on expiry the CTA raises BSA_ERR_TIMEOUT, drains its copies and products, frees TMEM.
@@ -41,7 +42,7 @@ constexpr uint64_t kWaitNs = 2000000000ull, kWaitTileNs = 20000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // The tensor cores cut off what they add to O: by up to 2^-23 of it at each of a key tile's eight products, which does not
 // average out over values of one sign (unsplit 2^20 keys came out 5e-3 short).  Every so many key tiles the sums are
-// therefore put aside, and those are added up rounded: 1e-4 at most, whatever the number of keys.  Only calls whose states
+// therefore put aside, and those are added up rounded: 1.3e-4 at most for up to 2^20 keys.  Only calls whose states
 // could be that long get the code for it, which makes the softmax's loop longer (D = 64, 6 x 4001 queries over up to 1024
 // states: 82 us with it, 78.5 without).
 constexpr int kAside = 128;
@@ -222,7 +223,8 @@ cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
       if (warp == 3) {
         // Ragged batches of up to 32 sequences: a lane a sequence, the ones with the most keys first, so that the long
-        // items do not begin last (16 prompts of 1 to 511 tokens over 4096 to 64 states: 215 us, and 254 in their own order with tickets drawn early).
+        // items do not begin last (16 prompts of 1 to 511 tokens over 64 to 4096 states: 189 us, and 229 in their own order; in a
+        // graph 210 and 239).
         const bool sorted = prm.a.B <= 32 && (prm.a.query_start || prm.a.key_start || prm.a.key_lens);
         int sq0 = 0, sn = 0, sk0 = 0, sm_ = 0, sb = 0, stiles = 0, sends = 0;  // of the lane's sequence; sends: items up to its last
         if (sorted) {

@@ -18,8 +18,9 @@ namespace bsa {
 // and remainder, and only the remainder, an eighth of a turn at most, becomes a float.  Its sine and cosine are the
 // first five and six terms of their series: what is left out is below 2e-9 of the one and 1.2e-10 of the other.
 // A thread keeps the frequencies of four neighbouring pairs (of one, where P is no multiple of 4) and walks the
-// tokens, whose positions it reads one token ahead.  At 115200 tokens x 64 pairs, 59 MB of writes, it takes 13.6 us of
-// the 8.9 that the copy rate allows: the arithmetic, not the writes, fills the issue slots (73%).
+// tokens, whose positions it reads one token ahead.  At 115200 tokens x 64 pairs, 59 MB of writes, it takes 13.6 us
+// (16.3 with other outputs each time) of the 8.9 that the copy rate allows: the arithmetic, not the writes, fills the issue
+// slots (63 to 73%).
 __device__ __forceinline__ void cos_sin(uint32_t high, uint32_t low, int32_t pos, float factor, float& c, float& s) {
     // 2^-32 turns: the product's upper half, of an unsigned and a signed factor
     const uint32_t t = high * (uint32_t)pos + __umulhi(low, (uint32_t)pos) - (pos < 0 ? low : 0u);
