@@ -649,14 +649,16 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * strides: [host] int64 [5][3]: batch, token and head stride of q, k, v, out and
  * lse in elements (channels are adjacent; a batch stride is not used where the rows are packed; strides of 0
  * broadcast k and v).  lse: [device] float or NULL.  1 <= D <= 128, scale >= 0,
- * M < 2^30; a scale below 1e-38 is taken as 1e-38.  out and lse must not overlap k, v or each other.
+ * M < 2^30, and N (with padded queries B N) times HQ / H below 2^30.  A scale below 1e-38 may be taken as 1e-38.  out and lse
+ * must not overlap k, v or each other.
  * query_start, key_start, key_lens: [device] int32.
  * workspace: [device] bsa_cross_workspace bytes, 32-byte aligned, its contents meaningless
  * between calls.  Deterministic for the same sizes, flags,
  * strides and alignment of addresses.  Sums of terms of one sign over M states are off by 1.3e-4 + M 2^-37 of
- * themselves at most in bf16 (M 2^-29 on the CUDA cores), 1e-5 + M 2^-35 in float32.  bf16 takes the softmax's weights to bf16 before the product with V (so do the other bf16 kernels); float32
- * keeps float32's accuracy; an infinity in a row that counts does what it does in float32, but against an element of
- * 2^11 or more it may give NaN.  A block of rows that comes out with NaN is computed twice. */
+ * themselves at most in bf16 (M 2^-29 on the CUDA cores), 1e-5 + M 2^-35 in float32.  bf16 takes the softmax's
+ * weights to bf16 before the product with V (so do the other bf16 kernels); float32 keeps float32's accuracy; an
+ * infinity in a row that counts does what it does in float32, but against an element of 2^11 or more it may give
+ * NaN.  A block of rows that comes out with NaN is computed twice. */
 /* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
  * tiles of 16 rows, 3 tensor cores in float32 (1 and 2: addresses and strides that are no multiples of 16 bytes take 0
  * all the same); -1 for sizes out of range. */
