@@ -656,7 +656,8 @@ bsa_status bsa_cache_append_rotated(const void* k, const void* v, bsa_dtype dtyp
  * between calls.  Deterministic for the same sizes, flags,
  * strides and alignment of addresses.  Sums of terms of one sign over M states are off by 1.3e-4 + M 2^-37 of
  * themselves at most in bf16 (M 2^-29 on the CUDA cores), 1e-5 + M 2^-35 in float32.  bf16 takes the softmax's
- * weights to bf16 before the product with V (so do the other bf16 kernels); float32 keeps float32's accuracy; an
+ * weights to bf16 before the product with V (so do the other bf16 kernels), weights of up to 2^8 before the division, so
+ * that values of 2^119 or more may come out infinite; float32 keeps float32's accuracy; an
  * infinity in a row that counts does what it does in float32, but against an element of 2^11 or more it may give
  * NaN.  A block of rows that comes out with NaN is computed twice. */
 /* Which kernel a call of these sizes takes, for profiles and tests: 0 CUDA cores, 1 tensor cores, 2 tensor cores with
